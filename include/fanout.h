@@ -142,6 +142,58 @@ FANOUT_API int fanout_extend(int32_t *page_table, int32_t num_branches,
                 int32_t n_free, int32_t *n_used);
 
 /*
+ * fanout_fork_device -- fanout_fork / fanout_fork_cow on the device: lengths,
+ * free list and tables are device memory, ordered on `stream`. "AHBM Agentic
+ * Runtime Architecture", section 3.1 "Fan-out context structure".
+ *   prefix_pages  dev int32 [ceil(prefix_len / page_size)].
+ *   suffix_lens   dev int32 [B], B <= 4096 (FANOUT_EUNSUPPORTED above).
+ *   free_pages    dev int32 [n_free]; the call takes entries from *used_in on,
+ *                 branch 0 first.
+ *   used_in       dev int32 [1] or NULL (0): entries taken before this call.
+ *   used_out      dev int32 [1] or NULL, written: entries taken after it. Not
+ *                 the same word as used_in (FANOUT_EINVAL), so that a replayed
+ *                 call does the same again.
+ *   page_table    dev int32 [B][max_pages_per_branch], every entry written: the
+ *                 whole prefix pages, the branch's own pages (the copy of a
+ *                 partial prefix page first), then -1.
+ *   cow_pairs     dev int32 [B][2] or NULL: as fanout_fork_cow, written when
+ *                 prefix_len is not a multiple of page_size.
+ * What only the device can see -- a negative suffix, more than 2^31 - 1 tokens,
+ * a row too narrow, a free list too short, *used_in < 0 -- leaves the table and
+ * cow_pairs as they were, copies *used_in to *used_out and is reported by
+ * fanout_last_error() as FANOUT_EINVAL. No workspace, no host copy: the call can
+ * be captured (make the first call on a device outside a capture).
+ */
+FANOUT_API int fanout_fork_device(const int32_t *prefix_pages, int32_t prefix_len,
+                int32_t num_branches, const int32_t *suffix_lens, int32_t page_size,
+                const int32_t *free_pages, int32_t n_free, const int32_t *used_in,
+                int32_t *used_out, int32_t *page_table, int32_t max_pages_per_branch,
+                int32_t *cow_pairs, fanout_stream_t stream);
+
+/*
+ * fanout_extend_device -- fanout_extend on the device, and the slot map of the
+ * new tokens. Branch b grows by add_lens[b] tokens; the table entries it then
+ * needs are taken from the free list as in fanout_fork_device, and
+ *   slots[r] = page * page_size + pos % page_size
+ * for row r = token t of branch b (rows grouped by branch) at pos = prefix_len +
+ * suffix_lens[b] + t: where fanout_kv_append_q4 puts the row.
+ *   page_table    dev int32 [B][max_pages_per_branch], updated in place: only
+ *                 the new entries are written.
+ *   suffix_lens, add_lens  dev int32 [B], B <= 4096; suffix_lens BEFORE the growth.
+ *   slots         dev int64 [n_slots], 8-byte aligned; NULL with n_slots == 0:
+ *                 no map wanted. Rows behind the last token get -1 (a padded
+ *                 batch of fixed size). n_slots <= 2^31 - 1.
+ * Errors as fanout_fork_device (also a negative add_lens entry, or more new
+ * tokens than n_slots): the table is left as it was and every slot is -1. A
+ * negative page id gives slot -1 and the same report. Can be captured.
+ */
+FANOUT_API int fanout_extend_device(int32_t *page_table, int32_t num_branches,
+                int32_t max_pages_per_branch, int32_t prefix_len, const int32_t *suffix_lens,
+                const int32_t *add_lens, int32_t page_size, const int32_t *free_pages,
+                int32_t n_free, const int32_t *used_in, int32_t *used_out, int64_t *slots,
+                int64_t n_slots, fanout_stream_t stream);
+
+/*
  * fanout_kv_append -- write new K/V rows into the paged pools (device).
  * ADR-0060 section 0.5.1 precondition P3: the new tokens' post-RoPE K and V
  * are in the cache before attention runs. Row r of k_new / v_new is token t of
@@ -163,6 +215,52 @@ FANOUT_API int fanout_kv_append(const void *k_new, const void *v_new, void *k_pa
                 const int32_t *suffix_lens, const int32_t *add_lens, int32_t num_branches,
                 int32_t max_pages_per_branch, int32_t num_pages, int32_t H_kv, int32_t d,
                 int32_t page_size, fanout_stream_t stream);
+
+/*
+ * The 4-bit cache. A row of d = 128 values is 8 groups of 16; with the pool's
+ * scale gs (host float, 1e-30 .. 1e30) and a group's largest magnitude a,
+ *   group scale = e4m3(a / (6 gs)), saturating at 448;
+ *   code        = e2m1(x / (group scale * gs)): 0, .5, 1, 1.5, 2, 3, 4, 6, +-;
+ *   value       = e2m1(code) * (group scale * gs),
+ * quotients in fp32, roundings to nearest, ties to even; a group whose scale is
+ * 0 holds zeros. A pool is uint8 [num_pages][H_kv][page_size * 72]: of each
+ * (page, KV head) block the first page_size * 64 bytes are codes, 64 per token,
+ * the rest scales, 8 per token. Each little-endian 32-bit word of codes holds 8
+ * neighbouring values: 0, 2, 4, 6 in its low half (4 bits each, from bit 0, the
+ * sign highest), 1, 3, 5, 7 in its high half. Whole pages can be copied as bytes.
+ * A pool's bytes must come from fanout_kv_append_q4, or be any codes with scale
+ * bytes 0x00 .. 0x7e. page_size is 16, 32, 64 or 128.
+ */
+#define FANOUT_Q4_ROW_BYTES 72
+
+/*
+ * fanout_kv_append_q4 -- write new K/V rows into 4-bit pools (device).
+ *   k_new, v_new  dev bf16, row r of KV head h at [r * stride + h * d], 16-byte
+ *                 aligned; k_stride, v_stride: elements between rows, multiples
+ *                 of 8, at least H_kv * d (rows may be slices of wider ones).
+ *   slots         dev int64 [n_rows]: page * page_size + slot in the page (see
+ *                 fanout_extend_device). Negative: the row is skipped. At or
+ *                 past num_pages * page_size: skipped, and fanout_last_error()
+ *                 reports FANOUT_EINVAL. A slot given to two rows holds
+ *                 unspecified bytes of them.
+ * Infinities are held as the largest value of their group's scale; a NaN is held
+ * as 0 and reported as FANOUT_EINVAL, so no cached row can poison others. Can be
+ * captured (first call on a device outside a capture).
+ */
+FANOUT_API int fanout_kv_append_q4(const void *k_new, const void *v_new, int64_t k_stride,
+                int64_t v_stride, void *k_pages, void *v_pages, const int64_t *slots,
+                int32_t n_rows, int32_t num_pages, int32_t H_kv, int32_t d, int32_t page_size,
+                float k_scale, float v_scale, fanout_stream_t stream);
+
+/*
+ * fanout_kv_read_q4 -- the values that slots of 4-bit pools stand for, rounded to
+ * bf16, into k_out / v_out (strides as the appended rows'). A row whose slot is
+ * negative, or outside the pools (reported), is left as it was. Can be captured.
+ */
+FANOUT_API int fanout_kv_read_q4(const void *k_pages, const void *v_pages, const int64_t *slots,
+                int32_t n_rows, int32_t num_pages, int32_t H_kv, int32_t d, int32_t page_size,
+                float k_scale, float v_scale, void *k_out, void *v_out, int64_t k_stride,
+                int64_t v_stride, fanout_stream_t stream);
 
 /*
  * fanout_attn -- batched shared-prefix fan-out attention.
@@ -219,6 +317,46 @@ FANOUT_API int fanout_attn(const void *q, const void *k_pages, const void *v_pag
                 int32_t max_pages_per_branch, int32_t num_pages, int32_t H_q, int32_t H_kv,
                 int32_t d, int32_t page_size, float scale, int32_t causal, void *out,
                 int32_t out_dtype, float *lse, fanout_stream_t stream);
+
+/*
+ * fanout_attn_window -- fanout_attn, causal, with a sliding window and a few
+ * first tokens that stay visible: key j is visible to the token at pos iff
+ *   j <= pos and (j > pos - window or j < sinks).
+ *   window  >= 1 keys, the row's own among them; sinks >= 0.
+ * Arguments, layouts and limits otherwise as fanout_attn. Table entries of pages
+ * that hold no key a row of the call sees are never read, nor are the pages: a
+ * caller may have given them back. Of the prefix, row 0's entries must be good
+ * for every page that any branch sees. Keys that no row sees are never used,
+ * whatever they hold; a key that a row of the call sees must be finite. A page id
+ * outside [0, num_pages) that is read is reported as FANOUT_EINVAL by
+ * fanout_last_error() and leaves the results unspecified. FANOUT_EUNSUPPORTED,
+ * with nothing done, when `stream` is capturing: the plan on the device moves with
+ * the suffix lengths. Each stream keeps one plan for this call beside
+ * fanout_attn's, so layers may alternate; FANOUT_OPT_FUSED_MERGE does not apply.
+ */
+FANOUT_API int fanout_attn_window(const void *q, const void *k_pages, const void *v_pages,
+                const int32_t *page_table, int32_t prefix_len, const int32_t *suffix_lens,
+                const int32_t *q_rows_per_branch, int32_t num_branches,
+                int32_t max_pages_per_branch, int32_t num_pages, int32_t H_q, int32_t H_kv,
+                int32_t d, int32_t page_size, float scale, int32_t window, int32_t sinks,
+                void *out, int32_t out_dtype, float *lse, fanout_stream_t stream);
+
+/*
+ * fanout_attn_q4 -- fanout_attn over 4-bit pools: out = softmax(scale q K^T) V
+ * and lse over the values that the pools' bytes stand for (uint8 [num_pages][H_kv]
+ * [page_size * 72], 16-byte aligned, scales k_scale and v_scale).
+ *   window, sinks  0, 0: every key (up to pos with causal != 0); window >= 1
+ *                  needs causal and means what it does in fanout_attn_window.
+ *                  sinks without a window is FANOUT_EINVAL.
+ * Page ids, capturing and plans as fanout_attn_window.
+ */
+FANOUT_API int fanout_attn_q4(const void *q, const void *k_pages, const void *v_pages,
+                const int32_t *page_table, int32_t prefix_len, const int32_t *suffix_lens,
+                const int32_t *q_rows_per_branch, int32_t num_branches,
+                int32_t max_pages_per_branch, int32_t num_pages, int32_t H_q, int32_t H_kv,
+                int32_t d, int32_t page_size, float scale, int32_t causal, float k_scale,
+                float v_scale, int32_t window, int32_t sinks, void *out, int32_t out_dtype,
+                float *lse, fanout_stream_t stream);
 
 /*
  * fanout_lse_merge -- the log-sum-exp merge of split partials on its own

@@ -37,6 +37,20 @@ ABI = {
     "fanout_attn_noalloc": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32p, _i32p, _i32, _i32,
                                            _i32, _i32, _i32, _i32, _i32, _f32, _i32, _vp, _i32,
                                            _vp, _vp]),
+    "fanout_fork_device": (ctypes.c_int, [_vp, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp,
+                                          _i32, _vp, _vp]),
+    "fanout_extend_device": (ctypes.c_int, [_vp, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _i32, _vp,
+                                            _vp, _vp, _i64, _vp]),
+    "fanout_kv_append_q4": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _i32, _i32, _i32,
+                                           _i32, _i32, _f32, _f32, _vp]),
+    "fanout_kv_read_q4": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _f32, _f32,
+                                         _vp, _vp, _i64, _i64, _vp]),
+    "fanout_attn_window": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32p, _i32p, _i32, _i32,
+                                          _i32, _i32, _i32, _i32, _i32, _f32, _i32, _i32, _vp,
+                                          _i32, _vp, _vp]),
+    "fanout_attn_q4": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32p, _i32p, _i32, _i32, _i32,
+                                      _i32, _i32, _i32, _i32, _f32, _i32, _f32, _f32, _i32, _i32,
+                                      _vp, _i32, _vp, _vp]),
     "fanout_lse_merge": (ctypes.c_int, [_vp, _vp, _i32, _i64, _i32, _vp, _i32, _vp, _vp]),
     "fanout_last_error": (ctypes.c_int, [_vp]),
     "fanout_last_error_detail": (ctypes.c_int, [_vp, _i32p, _i32p]),
@@ -164,6 +178,189 @@ def kv_append(k_new, v_new, k_pages, v_pages, page_table, prefix_len: int, suffi
         int(k_pages.shape[3]), int(page_size), _stream_handle(stream)), "fanout_kv_append")
 
 
+def _on(dev, stream):
+    """(device guard, stream handle): `dev` current for a call on its tensors, and
+    its own current stream when none is given."""
+    import torch
+    handle = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream_handle(stream)
+    return torch.cuda.device(dev), handle
+
+
+def _dev_tensor(name: str, t, dtype, dev, shape=None, contiguous=True):
+    if not t.is_cuda or t.device != dev or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor on {dev}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
+
+
+def _opt_ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def fork_device(prefix_pages, prefix_len: int, suffix_lens, page_size: int, free_pages,
+                max_pages: int, used=None, out=None, want_cow: bool = True, stream=None):
+    """fork / fork_cow on the device: (tables [B, max_pages], cow_pairs, used).
+
+    prefix_pages, suffix_lens, free_pages: int32 CUDA tensors; `used` (int32 [1],
+    None: 0) counts the free-list entries already taken, the returned one those
+    taken after this call. cow_pairs (int32 [B, 2]) is None when the prefix ends
+    with its page or want_cow is false. What the lengths get wrong on the device
+    is reported by last_error() and leaves `out` as it was."""
+    import torch
+    dev, B = suffix_lens.device, int(suffix_lens.numel())
+    if page_size <= 0:
+        raise ValueError("page_size must be positive")
+    _dev_tensor("suffix_lens", suffix_lens, torch.int32, dev, (B,))
+    _dev_tensor("prefix_pages", prefix_pages, torch.int32, dev)
+    _dev_tensor("free_pages", free_pages, torch.int32, dev)
+    if prefix_pages.numel() < -(-int(prefix_len) // page_size):
+        raise ValueError("prefix_pages holds fewer pages than the prefix")
+    if used is not None:
+        _dev_tensor("used", used, torch.int32, dev, (1,))
+    if out is None:
+        out = torch.empty((B, int(max_pages)), dtype=torch.int32, device=dev)
+    _dev_tensor("out", out, torch.int32, dev, (B, int(max_pages)))
+    cow = None
+    if want_cow and prefix_len % page_size:
+        cow = torch.empty((B, 2), dtype=torch.int32, device=dev)
+    after = torch.empty((1,), dtype=torch.int32, device=dev)
+    guard, handle = _on(dev, stream)
+    with guard:
+        _check(load().fanout_fork_device(
+            prefix_pages.data_ptr(), int(prefix_len), B, suffix_lens.data_ptr(), int(page_size),
+            free_pages.data_ptr(), int(free_pages.numel()), _opt_ptr(used), after.data_ptr(),
+            out.data_ptr(), int(max_pages), _opt_ptr(cow), handle), "fanout_fork_device")
+    return out, cow, after
+
+
+def extend_device(page_table, prefix_len: int, suffix_lens, add_lens, page_size: int, free_pages,
+                  n_slots: int, used=None, slots=None, stream=None):
+    """extend on the device, page_table (int32 [B, max_pages]) in place: (slots, used).
+
+    slots (int64 [n_slots]) maps the new tokens' rows for kv_append_q4; rows
+    behind the last one get -1. `used` as in fork_device."""
+    import torch
+    dev = page_table.device
+    B, width = (int(x) for x in page_table.shape)
+    _dev_tensor("page_table", page_table, torch.int32, dev)
+    _dev_tensor("suffix_lens", suffix_lens, torch.int32, dev, (B,))
+    _dev_tensor("add_lens", add_lens, torch.int32, dev, (B,))
+    _dev_tensor("free_pages", free_pages, torch.int32, dev)
+    if used is not None:
+        _dev_tensor("used", used, torch.int32, dev, (1,))
+    if slots is None:
+        slots = torch.empty((int(n_slots),), dtype=torch.int64, device=dev)
+    _dev_tensor("slots", slots, torch.int64, dev, (int(n_slots),))
+    after = torch.empty((1,), dtype=torch.int32, device=dev)
+    guard, handle = _on(dev, stream)
+    with guard:
+        _check(load().fanout_extend_device(
+            page_table.data_ptr(), B, width, int(prefix_len), suffix_lens.data_ptr(),
+            add_lens.data_ptr(), int(page_size), free_pages.data_ptr(), int(free_pages.numel()),
+            _opt_ptr(used), after.data_ptr(), slots.data_ptr(), int(n_slots), handle),
+            "fanout_extend_device")
+    return slots, after
+
+
+# Bytes of one token and KV head in a 4-bit pool (FANOUT_Q4_ROW_BYTES in include/fanout.h).
+Q4_ROW_BYTES = 72
+
+
+def q4_pool(num_pages: int, h_kv: int, page_size: int, device="cuda"):
+    """A zeroed 4-bit pool: uint8 [num_pages, H_kv, page_size * 72]."""
+    import torch
+    return torch.zeros((int(num_pages), int(h_kv), int(page_size) * Q4_ROW_BYTES),
+                       dtype=torch.uint8, device=device)
+
+
+def _q4_pools(k_pages, v_pages, page_size: int, dev):
+    import torch
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        _dev_tensor(name, t, torch.uint8, dev)
+        if t.dim() != 3 or int(t.shape[2]) != int(page_size) * Q4_ROW_BYTES:
+            raise ValueError(f"{name} must be [num_pages, H_kv, page_size * {Q4_ROW_BYTES}]")
+    if k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages / v_pages differ in shape")
+    return int(k_pages.shape[0]), int(k_pages.shape[1])
+
+
+def _rows_of(name: str, t, n: int, h_kv: int, dev) -> int:
+    """Elements between the rows of a bf16 [n, H_kv, d] tensor whose heads are packed."""
+    import torch
+    _dev_tensor(name, t, torch.bfloat16, dev, contiguous=False)
+    if t.dim() != 3 or int(t.shape[0]) != n or int(t.shape[1]) != h_kv:
+        raise ValueError(f"{name} must be [{n}, {h_kv}, d]")
+    d = int(t.shape[2])
+    if n == 0:
+        return h_kv * d
+    if t.stride(2) != 1 or (h_kv > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: a row's heads must be packed")
+    return int(t.stride(0)) if n > 1 else h_kv * d
+
+
+def kv_append_q4(k_new, v_new, k_pages, v_pages, slots, page_size: int, k_scale: float = 1.0,
+                 v_scale: float = 1.0, stream=None) -> None:
+    """Write new K/V rows (bf16 [R, H_kv, 128], rows may be strided) into 4-bit
+    pools at `slots` (int64 [R]; negative: the row is skipped)."""
+    import torch
+    dev, n = k_pages.device, int(slots.numel())
+    num_pages, h_kv = _q4_pools(k_pages, v_pages, page_size, dev)
+    _dev_tensor("slots", slots, torch.int64, dev, (n,))
+    ks, vs = _rows_of("k_new", k_new, n, h_kv, dev), _rows_of("v_new", v_new, n, h_kv, dev)
+    if k_new.shape != v_new.shape:
+        raise ValueError("k_new / v_new differ in shape")
+    guard, handle = _on(dev, stream)
+    with guard:
+        _check(load().fanout_kv_append_q4(
+            k_new.data_ptr(), v_new.data_ptr(), ks, vs, k_pages.data_ptr(), v_pages.data_ptr(),
+            slots.data_ptr(), n, num_pages, h_kv, int(k_new.shape[2]), int(page_size),
+            float(k_scale), float(v_scale), handle), "fanout_kv_append_q4")
+
+
+def kv_read_q4(k_pages, v_pages, slots, page_size: int, k_scale: float = 1.0,
+               v_scale: float = 1.0, k_out=None, v_out=None, stream=None):
+    """The bf16 rows [R, H_kv, 128] that `slots` of 4-bit pools stand for: (k, v).
+    Rows with a negative slot are left as they were (undefined when allocated here)."""
+    import torch
+    dev, n = k_pages.device, int(slots.numel())
+    num_pages, h_kv = _q4_pools(k_pages, v_pages, page_size, dev)
+    _dev_tensor("slots", slots, torch.int64, dev, (n,))
+    if k_out is None:
+        k_out = torch.empty((n, h_kv, 128), dtype=torch.bfloat16, device=dev)
+    if v_out is None:
+        v_out = torch.empty((n, h_kv, 128), dtype=torch.bfloat16, device=dev)
+    ks, vs = _rows_of("k_out", k_out, n, h_kv, dev), _rows_of("v_out", v_out, n, h_kv, dev)
+    if k_out.shape != v_out.shape:
+        raise ValueError("k_out / v_out differ in shape")
+    guard, handle = _on(dev, stream)
+    with guard:
+        _check(load().fanout_kv_read_q4(
+            k_pages.data_ptr(), v_pages.data_ptr(), slots.data_ptr(), n, num_pages, h_kv,
+            int(k_out.shape[2]), int(page_size), float(k_scale), float(v_scale),
+            k_out.data_ptr(), v_out.data_ptr(), ks, vs, handle), "fanout_kv_read_q4")
+    return k_out, v_out
+
+
+def copy_pages_q4(k_pages, v_pages, pairs, page_size: int, stream=None) -> None:
+    """Copy whole pages of 4-bit pools for page pairs (int32 [n, 2] on the device):
+    the copy-on-write step of a fork whose prefix ends inside a page."""
+    import torch
+    dev = k_pages.device
+    num_pages, h_kv = _q4_pools(k_pages, v_pages, page_size, dev)
+    _dev_tensor("pairs", pairs, torch.int32, dev)
+    if pairs.dim() != 2 or int(pairs.shape[1]) != 2:
+        raise ValueError("pairs must be [n, 2]")
+    # a block of page_size * 72 bytes as page_size / 2 rows of 72 16-bit values
+    guard, handle = _on(dev, stream)
+    with guard:
+        _check(load().fanout_copy_pages(k_pages.data_ptr(), v_pages.data_ptr(), pairs.data_ptr(),
+                                        int(pairs.shape[0]), int(page_size) // 2, num_pages, h_kv,
+                                        Q4_ROW_BYTES, int(page_size) // 2, handle),
+               "fanout_copy_pages")
+
+
 def plan(suffix_lens, q_rows, prefix_len: int, h_q: int, h_kv: int, page_size: int,
          causal: bool, num_sms: int = 152) -> Tuple[np.ndarray, np.ndarray, int]:
     """The work plan fanout_attn would run: (units [n, 8], cta_first [n_cta+1], n_parts)."""
@@ -251,6 +448,79 @@ def attn(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens: Sequence
                          float(scale), int(bool(causal)), out.data_ptr(), odt[1],
                          lse.data_ptr() if lse is not None else None, _stream_handle(stream))
     _check(rc, "fanout_attn")
+    return out, lse
+
+
+def _attn_tensors(q, k_pages, v_pages, pool_dtype, page_table, suffix_lens, q_rows, h_q: int,
+                  page_size: int, out, lse, out_dtype: str, want_lse: bool):
+    """Checks and outputs the two calls below share: (suffix lens, q rows, d, out
+    dtype code, out, lse, max pages)."""
+    import torch
+    sl, tq = _i32arr(suffix_lens), _i32arr(q_rows)
+    if sl.ndim != 1 or sl.shape != tq.shape:
+        raise ValueError("suffix_lens and q_rows must be sequences of one length")
+    R, d, dev = int(tq.sum()), int(q.shape[-1]), q.device
+    if out_dtype not in ("f32", "bf16"):
+        raise ValueError("out_dtype must be 'f32' or 'bf16'")
+    dt, code = (torch.float32, OUT_F32) if out_dtype == "f32" else (torch.bfloat16, OUT_BF16)
+    _dev_tensor("q", q, torch.bfloat16, dev, (R, h_q, d))
+    _dev_tensor("page_table", page_table, torch.int32, dev)
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        _dev_tensor(name, t, pool_dtype, dev)
+    if page_table.dim() != 2 or int(page_table.shape[0]) != int(sl.shape[0]):
+        raise ValueError("page_table must be [num_branches, max_pages]")
+    if out is None:
+        out = torch.empty((R, h_q, d), dtype=dt, device=dev)
+    _dev_tensor("out", out, dt, dev, (R, h_q, d))
+    if lse is None and want_lse:
+        lse = torch.empty((R, h_q), dtype=torch.float32, device=dev)
+    if lse is not None:
+        _dev_tensor("lse", lse, torch.float32, dev, (R, h_q))
+    return sl, tq, d, code, out, lse, int(page_table.shape[1])
+
+
+def attn_window(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q_rows, h_q: int,
+                h_kv: int, page_size: int, scale: float, window: int, sinks: int = 0, out=None,
+                lse=None, out_dtype: str = "f32", want_lse: bool = True, stream=None):
+    """attn(), causal, where a row at pos sees keys j <= pos with j > pos - window
+    or j < sinks. Pages that no row sees may have been given back."""
+    import torch
+    sl, tq, d, code, out, lse, width = _attn_tensors(
+        q, k_pages, v_pages, torch.bfloat16, page_table, suffix_lens, q_rows, h_q, page_size, out,
+        lse, out_dtype, want_lse)
+    if k_pages.shape != v_pages.shape or tuple(k_pages.shape[1:]) != (h_kv, page_size, d):
+        raise ValueError("k_pages / v_pages must be [num_pages, H_kv, page, d]")
+    guard, handle = _on(q.device, stream)
+    with guard:
+        _check(load().fanout_attn_window(
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+            int(prefix_len), _ptr(sl), _ptr(tq), int(sl.shape[0]), width, int(k_pages.shape[0]),
+            int(h_q), int(h_kv), d, int(page_size), float(scale), int(window), int(sinks),
+            out.data_ptr(), code, _opt_ptr(lse), handle), "fanout_attn_window")
+    return out, lse
+
+
+def attn_q4(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q_rows, h_q: int,
+            h_kv: int, page_size: int, scale: float, causal: bool, k_scale: float = 1.0,
+            v_scale: float = 1.0, window: int = 0, sinks: int = 0, out=None, lse=None,
+            out_dtype: str = "f32", want_lse: bool = True, stream=None):
+    """attn() over 4-bit pools (uint8 [num_pages, H_kv, page_size * 72]); window and
+    sinks as in attn_window (0, 0: none)."""
+    import torch
+    sl, tq, d, code, out, lse, width = _attn_tensors(
+        q, k_pages, v_pages, torch.uint8, page_table, suffix_lens, q_rows, h_q, page_size, out,
+        lse, out_dtype, want_lse)
+    num_pages, heads = _q4_pools(k_pages, v_pages, page_size, q.device)
+    if heads != h_kv:
+        raise ValueError(f"pools hold {heads} KV heads, not {h_kv}")
+    guard, handle = _on(q.device, stream)
+    with guard:
+        _check(load().fanout_attn_q4(
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+            int(prefix_len), _ptr(sl), _ptr(tq), int(sl.shape[0]), width, num_pages, int(h_q),
+            int(h_kv), d, int(page_size), float(scale), int(bool(causal)), float(k_scale),
+            float(v_scale), int(window), int(sinks), out.data_ptr(), code, _opt_ptr(lse), handle),
+            "fanout_attn_q4")
     return out, lse
 
 

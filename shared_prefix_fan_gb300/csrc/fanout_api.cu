@@ -11,6 +11,8 @@
 #include <cstring>
 #include <map>
 #include <mutex>
+#include <new>
+#include <tuple>
 #include <utility>
 #include <vector>
 
@@ -30,7 +32,8 @@ unsigned long long g_wait_limit_ns = 1000000000ull;
 cudaEvent_t g_ev_before = nullptr;
 cudaEvent_t g_ev_after = nullptr;
 
-// One per (device, stream). Its mutex serialises the calls on that stream's
+// One per (device, stream, kind of attention): a model whose layers alternate
+// between kinds keeps each kind's plan. Its mutex serialises the calls on that stream's
 // workspace (plan cache, buffer, upload, launch); calls on other streams only
 // share g_mu for the map lookup and the option reads.
 struct Workspace {
@@ -43,7 +46,8 @@ struct Workspace {
     bool plan_ready = false;
     uint32_t epoch = 0;  // flag value of the last call (fused merge)
 };
-std::map<std::pair<int, cudaStream_t>, Workspace*> g_ws;
+enum AttnKind { kFull = 0, kWindow = 1, kQ4 = 2, kQ4Window = 3 };
+std::map<std::tuple<int, cudaStream_t, int>, Workspace*> g_ws;
 
 int status_from_cuda(cudaError_t e) {
     if (e == cudaSuccess) return FANOUT_OK;
@@ -78,6 +82,157 @@ int32_t current_fused_merge() {
 cudaError_t launch_stream_read(const void* buf, int64_t bytes, uint32_t* xor_out,
                                cudaStream_t stream);
 }  // namespace fanout
+
+namespace {
+
+// The call behind fanout_attn, fanout_attn_window and fanout_attn_q4: checks,
+// the (device, stream, kind) workspace, the plan, its upload and the launches.
+// window > 0 (causal only): rows see keys > pos - window and keys < sinks.
+int attn_call(AttnKind kind, const void* q, const void* k_pages, const void* v_pages,
+              const int32_t* page_table, int32_t prefix_len, const int32_t* suffix_lens,
+              const int32_t* q_rows_per_branch, int32_t num_branches,
+              int32_t max_pages_per_branch, int32_t num_pages, int32_t H_q, int32_t H_kv,
+              int32_t d, int32_t page_size, float scale, int32_t causal, int32_t window,
+              int32_t sinks, float k_scale, float v_scale, void* out, int32_t out_dtype,
+              float* lse, fanout_stream_t stream_) {
+    const bool rows = kind != kFull, q4 = kind == kQ4 || kind == kQ4Window;
+    int st = validate_shape(suffix_lens, q_rows_per_branch, num_branches, prefix_len, H_q, H_kv,
+                            d, page_size, causal);
+    if (st != FANOUT_OK) return st;
+    if (out_dtype != FANOUT_OUT_F32 && out_dtype != FANOUT_OUT_BF16) return FANOUT_EINVAL;
+    if (!(scale > 0.0f) || scale > 3.0e38f) return FANOUT_EINVAL;  // positive, finite
+    int64_t R = 0;
+    for (int32_t b = 0; b < num_branches; ++b) R += q_rows_per_branch[b];
+    if (R == 0) return FANOUT_OK;
+    st = validate_call(q, k_pages, v_pages, page_table, suffix_lens, num_branches, prefix_len,
+                       max_pages_per_branch, num_pages, page_size, scale, out_dtype, out);
+    if (st != FANOUT_OK) return st;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (rows) {
+        // A captured call would replay a plan that later calls on the stream move.
+        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+        const cudaError_t e = cudaStreamIsCapturing(stream, &cap);
+        if (e != cudaSuccess) return status_from_cuda(e);
+        if (cap != cudaStreamCaptureStatusNone) return FANOUT_EUNSUPPORTED;
+    }
+
+    int dev = 0;
+    cudaError_t ce = cudaGetDevice(&dev);
+    if (ce != cudaSuccess) return status_from_cuda(ce);
+
+    // Options and the workspace under the process-wide lock; everything after
+    // under the workspace's own lock only.
+    int64_t validate_table, fused_merge;
+    int32_t splits;
+    unsigned long long wait_limit_ns;
+    cudaEvent_t ev_before, ev_after;
+    int sms;
+    Workspace* ws;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        validate_table = g_validate_table;
+        fused_merge = g_fused_merge;
+        splits = static_cast<int32_t>(g_force_splits);
+        wait_limit_ns = g_wait_limit_ns;
+        ev_before = g_ev_before;
+        ev_after = g_ev_after;
+        sms = device_sms(dev);
+        Workspace*& slot = g_ws[{dev, stream, kind}];
+        if (!slot) slot = new Workspace();
+        ws = slot;
+    }
+    std::lock_guard<std::mutex> wlk(ws->mu);
+
+    if (validate_table) {
+        std::vector<int32_t> tab(static_cast<size_t>(num_branches) * max_pages_per_branch);
+        ce = cudaMemcpyAsync(tab.data(), page_table, tab.size() * sizeof(int32_t),
+                             cudaMemcpyDeviceToHost, stream);
+        if (ce == cudaSuccess) ce = cudaStreamSynchronize(stream);
+        if (ce != cudaSuccess) return status_from_cuda(ce);
+        const int32_t n_pre = prefix_len / page_size;
+        for (int32_t b = 0; b < num_branches; ++b) {
+            const int64_t n = (static_cast<int64_t>(prefix_len) + suffix_lens[b] + page_size - 1) / page_size;
+            for (int64_t i = 0; i < n; ++i) {
+                const int32_t v = tab[static_cast<size_t>(b) * max_pages_per_branch + i];
+                if (v < 0 || v >= num_pages) return FANOUT_EINVAL;
+                if (i < n_pre && v != tab[i]) return FANOUT_EINVAL;  // prefix must be shared
+            }
+        }
+    }
+
+    std::vector<int32_t> key = {prefix_len, num_branches, H_q, H_kv, page_size, causal, sms,
+                                splits, window, sinks};
+    key.insert(key.end(), suffix_lens, suffix_lens + num_branches);
+    key.insert(key.end(), q_rows_per_branch, q_rows_per_branch + num_branches);
+    // A call that differs from the cached plan's only in suffix lengths (a
+    // decode step) keeps the plan when every key range keeps its tile count:
+    // only the unit table moves (new range ends and causal positions).
+    const size_t fixed = 10;  // key entries before the suffix lengths
+    PlanInput in{suffix_lens, q_rows_per_branch, num_branches, prefix_len, H_q, H_kv,
+                 page_size, causal, sms, splits};
+    in.rows = rows;
+    in.window = window;
+    in.sinks = sinks;
+    if (q4) in.row_bytes = 2 * kQ4RowBytes;
+    bool patched = false;
+    if (ws->plan_ready && key != ws->key && key.size() == ws->key.size() &&
+        std::equal(key.begin(), key.begin() + fixed, ws->key.begin()) &&
+        std::equal(key.begin() + fixed + num_branches, key.end(),
+                   ws->key.begin() + fixed + num_branches)) {
+        if (patch_plan(in, ws->plan)) {
+            ce = cudaMemcpyAsync(static_cast<uint8_t*>(ws->buf) + ws->layout.units,
+                                 ws->plan.units.data(), ws->plan.units.size() * sizeof(Unit),
+                                 cudaMemcpyHostToDevice, stream);
+            if (ce == cudaSuccess && !ws->plan.tok_pos.empty())
+                ce = cudaMemcpyAsync(static_cast<uint8_t*>(ws->buf) + ws->layout.pos,
+                                     ws->plan.tok_pos.data(),
+                                     ws->plan.tok_pos.size() * sizeof(int32_t),
+                                     cudaMemcpyHostToDevice, stream);
+            if (ce != cudaSuccess) {
+                ws->plan_ready = false;
+                return status_from_cuda(ce);
+            }
+            ws->key = key;
+            patched = true;
+        }
+    }
+    if (!patched && (!ws->plan_ready || key != ws->key)) {
+        ws->plan_ready = false;
+        if ((st = build_plan(in, ws->plan)) != FANOUT_OK) return st;
+        ws->layout = plan_layout(ws->plan);
+        if (ws->layout.total > ws->cap) {
+            if (ws->buf) {
+                cudaStreamSynchronize(stream);
+                cudaFree(ws->buf);
+                ws->buf = nullptr;
+                ws->cap = 0;
+            }
+            ce = cudaMalloc(&ws->buf, ws->layout.total);
+            if (ce != cudaSuccess) {
+                ws->buf = nullptr;
+                return status_from_cuda(ce);
+            }
+            ws->cap = ws->layout.total;
+            // fused-merge flags start below every epoch a call can use
+            ce = cudaMemsetAsync(static_cast<uint8_t*>(ws->buf) + ws->layout.flags, 0,
+                                 kMaxFusedGrid * sizeof(uint32_t), stream);
+            if (ce != cudaSuccess) return status_from_cuda(ce);
+        }
+        ce = upload_plan(ws->plan, ws->layout, static_cast<uint8_t*>(ws->buf), stream);
+        if (ce != cudaSuccess) return status_from_cuda(ce);
+        ws->key = key;
+        ws->plan_ready = true;
+    }
+    if (++ws->epoch == 0) ws->epoch = 1;  // 0 is the flags' initial value
+    CallArgs a{q, k_pages, v_pages, page_table, max_pages_per_branch, num_pages, H_q, H_kv,
+               page_size, out_dtype == FANOUT_OUT_BF16, scale, out, lse, R, wait_limit_ns,
+               window, sinks, q4, k_scale, v_scale,
+               rows ? 0 : static_cast<int32_t>(fused_merge), ws->epoch};
+    return launch_plan(a, ws->plan, ws->layout, static_cast<uint8_t*>(ws->buf), stream,
+                       ev_before, ev_after);
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -351,124 +506,54 @@ int fanout_attn(const void* q, const void* k_pages, const void* v_pages,
                 const int32_t* q_rows_per_branch, int32_t num_branches,
                 int32_t max_pages_per_branch, int32_t num_pages, int32_t H_q, int32_t H_kv,
                 int32_t d, int32_t page_size, float scale, int32_t causal, void* out,
-                int32_t out_dtype, float* lse, fanout_stream_t stream_) {
-    int st = validate_shape(suffix_lens, q_rows_per_branch, num_branches, prefix_len, H_q, H_kv,
-                            d, page_size, causal);
-    if (st != FANOUT_OK) return st;
-    if (out_dtype != FANOUT_OUT_F32 && out_dtype != FANOUT_OUT_BF16) return FANOUT_EINVAL;
-    if (!(scale > 0.0f) || scale > 3.0e38f) return FANOUT_EINVAL;  // positive, finite
-    int64_t R = 0;
-    for (int32_t b = 0; b < num_branches; ++b) R += q_rows_per_branch[b];
-    if (R == 0) return FANOUT_OK;
-    st = validate_call(q, k_pages, v_pages, page_table, suffix_lens, num_branches, prefix_len,
-                       max_pages_per_branch, num_pages, page_size, scale, out_dtype, out);
-    if (st != FANOUT_OK) return st;
-    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-
-    int dev = 0;
-    cudaError_t ce = cudaGetDevice(&dev);
-    if (ce != cudaSuccess) return status_from_cuda(ce);
-
-    // Options and the workspace under the process-wide lock; everything after
-    // under the workspace's own lock only.
-    int64_t validate_table, fused_merge;
-    int32_t splits;
-    unsigned long long wait_limit_ns;
-    cudaEvent_t ev_before, ev_after;
-    int sms;
-    Workspace* ws;
-    {
-        std::lock_guard<std::mutex> lk(g_mu);
-        validate_table = g_validate_table;
-        fused_merge = g_fused_merge;
-        splits = static_cast<int32_t>(g_force_splits);
-        wait_limit_ns = g_wait_limit_ns;
-        ev_before = g_ev_before;
-        ev_after = g_ev_after;
-        sms = device_sms(dev);
-        Workspace*& slot = g_ws[{dev, stream}];
-        if (!slot) slot = new Workspace();
-        ws = slot;
+                int32_t out_dtype, float* lse, fanout_stream_t stream) {
+    try {
+        return attn_call(kFull, q, k_pages, v_pages, page_table, prefix_len, suffix_lens,
+                         q_rows_per_branch, num_branches, max_pages_per_branch, num_pages, H_q,
+                         H_kv, d, page_size, scale, causal, 0, 0, 1.f, 1.f, out, out_dtype, lse,
+                         stream);
+    } catch (const std::bad_alloc&) {
+        return FANOUT_ENOMEM;
     }
-    std::lock_guard<std::mutex> wlk(ws->mu);
+}
 
-    if (validate_table) {
-        std::vector<int32_t> tab(static_cast<size_t>(num_branches) * max_pages_per_branch);
-        ce = cudaMemcpyAsync(tab.data(), page_table, tab.size() * sizeof(int32_t),
-                             cudaMemcpyDeviceToHost, stream);
-        if (ce == cudaSuccess) ce = cudaStreamSynchronize(stream);
-        if (ce != cudaSuccess) return status_from_cuda(ce);
-        const int32_t n_pre = prefix_len / page_size;
-        for (int32_t b = 0; b < num_branches; ++b) {
-            const int64_t n = (static_cast<int64_t>(prefix_len) + suffix_lens[b] + page_size - 1) / page_size;
-            for (int64_t i = 0; i < n; ++i) {
-                const int32_t v = tab[static_cast<size_t>(b) * max_pages_per_branch + i];
-                if (v < 0 || v >= num_pages) return FANOUT_EINVAL;
-                if (i < n_pre && v != tab[i]) return FANOUT_EINVAL;  // prefix must be shared
-            }
-        }
+int fanout_attn_window(const void* q, const void* k_pages, const void* v_pages,
+                       const int32_t* page_table, int32_t prefix_len, const int32_t* suffix_lens,
+                       const int32_t* q_rows_per_branch, int32_t num_branches,
+                       int32_t max_pages_per_branch, int32_t num_pages, int32_t H_q,
+                       int32_t H_kv, int32_t d, int32_t page_size, float scale, int32_t window,
+                       int32_t sinks, void* out, int32_t out_dtype, float* lse,
+                       fanout_stream_t stream) {
+    if (window < 1 || sinks < 0) return FANOUT_EINVAL;
+    try {
+        return attn_call(kWindow, q, k_pages, v_pages, page_table, prefix_len, suffix_lens,
+                         q_rows_per_branch, num_branches, max_pages_per_branch, num_pages, H_q,
+                         H_kv, d, page_size, scale, 1, std::min(window, kNoCausal),
+                         std::min(sinks, kNoCausal), 1.f, 1.f, out, out_dtype, lse, stream);
+    } catch (const std::bad_alloc&) {
+        return FANOUT_ENOMEM;
     }
+}
 
-    std::vector<int32_t> key = {prefix_len, num_branches, H_q, H_kv, page_size, causal, sms,
-                                splits};
-    key.insert(key.end(), suffix_lens, suffix_lens + num_branches);
-    key.insert(key.end(), q_rows_per_branch, q_rows_per_branch + num_branches);
-    // A call that differs from the cached plan's only in suffix lengths (a
-    // decode step) keeps the plan when every key range keeps its tile count:
-    // only the unit table moves (new range ends and causal positions).
-    const size_t fixed = 8;  // key entries before the suffix lengths
-    const PlanInput in{suffix_lens, q_rows_per_branch, num_branches, prefix_len, H_q, H_kv,
-                       page_size, causal, sms, splits};
-    bool patched = false;
-    if (ws->plan_ready && key != ws->key && key.size() == ws->key.size() &&
-        std::equal(key.begin(), key.begin() + fixed, ws->key.begin()) &&
-        std::equal(key.begin() + fixed + num_branches, key.end(),
-                   ws->key.begin() + fixed + num_branches)) {
-        if (patch_plan(in, ws->plan)) {
-            ce = cudaMemcpyAsync(static_cast<uint8_t*>(ws->buf) + ws->layout.units,
-                                 ws->plan.units.data(), ws->plan.units.size() * sizeof(Unit),
-                                 cudaMemcpyHostToDevice, stream);
-            if (ce != cudaSuccess) {
-                ws->plan_ready = false;
-                return status_from_cuda(ce);
-            }
-            ws->key = key;
-            patched = true;
-        }
+int fanout_attn_q4(const void* q, const void* k_pages, const void* v_pages,
+                   const int32_t* page_table, int32_t prefix_len, const int32_t* suffix_lens,
+                   const int32_t* q_rows_per_branch, int32_t num_branches,
+                   int32_t max_pages_per_branch, int32_t num_pages, int32_t H_q, int32_t H_kv,
+                   int32_t d, int32_t page_size, float scale, int32_t causal, float k_scale,
+                   float v_scale, int32_t window, int32_t sinks, void* out, int32_t out_dtype,
+                   float* lse, fanout_stream_t stream) {
+    if (window < 0 || sinks < 0 || (window > 0 && !causal) || (window == 0 && sinks > 0))
+        return FANOUT_EINVAL;
+    if (!q4_scale_ok(k_scale) || !q4_scale_ok(v_scale)) return FANOUT_EINVAL;
+    try {
+        return attn_call(window > 0 ? kQ4Window : kQ4, q, k_pages, v_pages, page_table,
+                         prefix_len, suffix_lens, q_rows_per_branch, num_branches,
+                         max_pages_per_branch, num_pages, H_q, H_kv, d, page_size, scale, causal,
+                         std::min(window, kNoCausal), std::min(sinks, kNoCausal), k_scale,
+                         v_scale, out, out_dtype, lse, stream);
+    } catch (const std::bad_alloc&) {
+        return FANOUT_ENOMEM;
     }
-    if (!patched && (!ws->plan_ready || key != ws->key)) {
-        ws->plan_ready = false;
-        if ((st = build_plan(in, ws->plan)) != FANOUT_OK) return st;
-        ws->layout = plan_layout(ws->plan);
-        if (ws->layout.total > ws->cap) {
-            if (ws->buf) {
-                cudaStreamSynchronize(stream);
-                cudaFree(ws->buf);
-                ws->buf = nullptr;
-                ws->cap = 0;
-            }
-            ce = cudaMalloc(&ws->buf, ws->layout.total);
-            if (ce != cudaSuccess) {
-                ws->buf = nullptr;
-                return status_from_cuda(ce);
-            }
-            ws->cap = ws->layout.total;
-            // fused-merge flags start below every epoch a call can use
-            ce = cudaMemsetAsync(static_cast<uint8_t*>(ws->buf) + ws->layout.flags, 0,
-                                 kMaxFusedGrid * sizeof(uint32_t), stream);
-            if (ce != cudaSuccess) return status_from_cuda(ce);
-        }
-        ce = upload_plan(ws->plan, ws->layout, static_cast<uint8_t*>(ws->buf), stream);
-        if (ce != cudaSuccess) return status_from_cuda(ce);
-        ws->key = key;
-        ws->plan_ready = true;
-    }
-    if (++ws->epoch == 0) ws->epoch = 1;  // 0 is the flags' initial value
-    CallArgs a{q, k_pages, v_pages, page_table, max_pages_per_branch, num_pages, H_q, H_kv,
-               page_size, out_dtype == FANOUT_OUT_BF16, scale, out, lse, R, wait_limit_ns,
-               static_cast<int32_t>(fused_merge), ws->epoch};
-    return launch_plan(a, ws->plan, ws->layout, static_cast<uint8_t*>(ws->buf), stream,
-                       ev_before, ev_after);
 }
 
 int fanout_lse_merge(const float* part_o, const float* part_ml, int32_t n_parts, int64_t n_out,
@@ -552,7 +637,7 @@ int fanout_release(void) {
         Workspace* ws = kv.second;
         std::lock_guard<std::mutex> wlk(ws->mu);
         if (ws->buf) {
-            cudaSetDevice(kv.first.first);
+            cudaSetDevice(std::get<0>(kv.first));
             cudaDeviceSynchronize();
             cudaFree(ws->buf);
         }

@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -13,6 +14,7 @@ constexpr int kBM = 128;      // query rows per tile (tcgen05 M)
 constexpr int kBN = 128;      // keys per KV tile
 constexpr int kHD = 128;      // the head dimension the kernels handle
 constexpr int kNoCausal = 1 << 30;  // pos_base for units that need no causal mask
+constexpr int kNoWindow = 3 << 29;  // wider than any position; position - window - key fits 32 bits
 
 // One unit of split-KV work: the query rows of `n_tok` consecutive tokens
 // (times the G query heads of KV head `kv_head`) against keys
@@ -79,6 +81,14 @@ struct SplitParams {
     uint32_t epoch;
     uint32_t* flags;
     MergeParams merge;
+    // Row plans: token positions, the window, and where the shared keys end.
+    const int32_t* tok_pos;
+    int32_t window, sinks, split_at;
+    // 4-bit pools
+    const void* q;
+    const uint8_t* k_pool;
+    const uint8_t* v_pool;
+    float o_scale;  // V's scale over the power of two its widened values carry
 };
 
 // Paged KV append: per-branch row offsets and current suffix lengths travel in
@@ -90,11 +100,50 @@ struct AppendParams {
     int32_t suffix_len[kMaxAppendBranches];   // suffix length before the append
 };
 
+// Page tables and slot maps built on the device (tables.cu). Every pointer is
+// device memory.
+constexpr int kMaxTableBranches = 4096;  // two int32 offsets per branch in shared memory
+struct TableParams {
+    const int32_t* prefix_pages;  // fork
+    const int32_t* suffix_lens;
+    const int32_t* add_lens;  // extension
+    const int32_t* free_pages;
+    const int32_t* used_in;  // null: 0
+    int32_t* used_out;       // null: not reported
+    int32_t* page_table;
+    int32_t* cow_pairs;  // fork
+    int64_t* slots;      // extension
+    int32_t* err;
+    int64_t n_slots;
+    int32_t num_branches, prefix_len, page_size, n_free, max_pages;
+    int32_t extend;  // 0: a fork
+};
+
+// Rows into the 4-bit pools and back (kv_q4.cu).
+constexpr int kQ4RowBytes = 72;  // 64 bytes of codes, 8 scales
+struct Q4RowParams {
+    const __nv_bfloat16* k_rows;
+    const __nv_bfloat16* v_rows;
+    __nv_bfloat16* k_out;
+    __nv_bfloat16* v_out;
+    uint8_t* k_pool;
+    uint8_t* v_pool;
+    const int64_t* slots;
+    int32_t* err;
+    int64_t k_stride, v_stride;  // elements between rows
+    int64_t n_slots;             // num_pages * page_size
+    int32_t n_rows, H_kv, page_shift;
+    float k_scale, v_scale;
+};
+
 // Launchers (defined in the .cu files); return cudaError_t.
 // cooperative: launch with all CTAs co-resident (required when p.fused_merge).
 cudaError_t launch_split_attn(const SplitParams& p, const CUtensorMap& tm_q,
                               const CUtensorMap& tm_k, const CUtensorMap& tm_v, int grid,
                               bool cooperative, cudaStream_t stream);
+// Attention over 4-bit pools (row plans; never fused with the merge).
+cudaError_t launch_attn_q4(const SplitParams& p, const CUtensorMap& tm_q, int grid,
+                           cudaStream_t stream);
 cudaError_t launch_lse_merge(const MergeParams& p, cudaStream_t stream);
 cudaError_t err_word_ptr(int32_t** ptr);
 cudaError_t launch_copy_pages(void* k_pool, void* v_pool, const int32_t* pairs, int32_t n_pairs,
@@ -103,6 +152,8 @@ cudaError_t launch_copy_pages(void* k_pool, void* v_pool, const int32_t* pairs, 
 cudaError_t launch_kv_append(const void* k_new, const void* v_new, void* k_pool, void* v_pool,
                              const int32_t* page_table, const AppendParams& p, int32_t* err,
                              cudaStream_t stream);
+cudaError_t launch_tables(const TableParams& p, cudaStream_t stream);
+cudaError_t launch_q4_rows(const Q4RowParams& p, bool read, cudaStream_t stream);
 cudaError_t launch_wait_selftest(int32_t* err, unsigned long long limit_ns, cudaStream_t stream);
 
 }  // namespace fanout

@@ -163,6 +163,6 @@ extern "C" FANOUT_API int fanout_attn_noalloc(
     }
     CallArgs a{q, k_pages, v_pages, page_table, max_pages_per_branch, num_pages, H_q, H_kv,
                page_size, out_dtype == FANOUT_OUT_BF16, scale, out, lse, R, 1000000000ull,
-               current_fused_merge(), epoch};
+               0, 0, 0, 1.f, 1.f, current_fused_merge(), epoch};
     return launch_plan(a, plan, L, scratch, stream, nullptr, nullptr);
 }

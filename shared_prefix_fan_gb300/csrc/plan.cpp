@@ -13,6 +13,10 @@
 //     branch's private suffix [P, P + S_b) is a key range for tiles of that
 //     branch's rows only.
 //   * Otherwise every branch's tiles take its whole context [0, P + S_b).
+//   * Row plans (windowed or 4-bit attention) trim each range to the keys its
+//     rows see: it starts at the page of the first row's oldest key, and the
+//     first keys that stay visible are swept as extra tiles in front of it, so
+//     that a windowed row block is still one unit (make_row_ranges).
 //   Causal: a tile's key range ends after the last key its last token sees;
 //   tiles entirely in the future are never produced (ADR-0060 section 5.4).
 //
@@ -52,6 +56,11 @@ constexpr double kUnitOverhead1 = 3.0;
 constexpr double kMergePerPart = 2.0;  // write + read of one 128-row partial, in tile times
 constexpr double kMergeLaunch = 4.0;   // the extra merge launch, in tile times
 
+// pos_base and key_begin of a piece of a range: the first keys of a row plan's
+// range go with its first piece only, which also starts behind its hidden keys.
+inline int32_t piece_pos(const Range& r, bool first) { return r.rows && !first ? 0 : r.pos_base; }
+inline int32_t piece_begin(const Range& r, int32_t k_lo) { return k_lo == r.lo ? k_lo + r.front : k_lo; }
+
 struct Cand {
     std::vector<Unit> units;   // in assignment order
     std::vector<int64_t> work;
@@ -80,9 +89,9 @@ void make_candidate(const std::vector<Range>& ranges, int64_t chunk, int32_t for
             const int64_t t_lo = ch * nkt / nch, t_hi = (ch + 1) * nkt / nch;
             const int32_t k_lo = r.lo + static_cast<int32_t>(t_lo) * kBN;
             const int32_t k_hi = std::min<int32_t>(r.hi, r.lo + static_cast<int32_t>(t_hi) * kBN);
-            all.push_back({t_hi - t_lo,
-                           Unit{r.kv_head, r.branch, r.tok_begin, r.n_tok, k_lo, k_hi, r.pos_base,
-                                0},
+            all.push_back({t_hi - t_lo + (ch == 0 ? r.first_tiles : 0),
+                           Unit{r.kv_head, r.branch, r.tok_begin, r.n_tok, piece_begin(r, k_lo), k_hi,
+                                piece_pos(r, ch == 0), 0},
                            r.complete && nch == 1, static_cast<int32_t>(ri)});
         }
     }
@@ -130,7 +139,7 @@ double candidate_cost_bound(const std::vector<Range>& ranges, int64_t chunk, int
         nch = std::max<int64_t>(1, std::min(nch, nkt));
         for (int64_t ch = 0; ch < nch; ++ch)
             max_w = std::max(max_w, (ch + 1) * nkt / nch - ch * nkt / nch);
-        total += nkt;
+        total += nkt + r.first_tiles;
         n += nch;
         if (!(r.complete && nch == 1)) n_parts += nch;
     }
@@ -175,8 +184,8 @@ void make_streamk(const std::vector<Range>& ranges, int32_t max_cta, double unit
             const int32_t k_lo = r.lo + static_cast<int32_t>(t) * kBN;
             const int32_t k_hi = std::min<int32_t>(r.hi, r.lo + static_cast<int32_t>(t + take) * kBN);
             const bool whole = r.complete && take == nkt;
-            c.units.push_back(Unit{r.kv_head, r.branch, r.tok_begin, r.n_tok, k_lo, k_hi, r.pos_base,
-                                   whole ? -1 : 0});
+            c.units.push_back(Unit{r.kv_head, r.branch, r.tok_begin, r.n_tok, piece_begin(r, k_lo), k_hi,
+                                   piece_pos(r, t == 0), whole ? -1 : 0});
             if (!whole) ++n_parts;
             c.work.push_back(take);
             c.cta_of.push_back(cta);
@@ -252,7 +261,8 @@ void make_lpt_cut(const std::vector<Range>& ranges, int32_t max_cta, double unit
         const Range& r = ranges[pc.range];
         const int32_t k_lo = r.lo + static_cast<int32_t>(pc.t_lo) * kBN;
         const int32_t k_hi = std::min<int32_t>(r.hi, r.lo + static_cast<int32_t>(pc.t_lo + take) * kBN);
-        c.units.push_back(Unit{r.kv_head, r.branch, r.tok_begin, r.n_tok, k_lo, k_hi, r.pos_base, 0});
+        c.units.push_back(Unit{r.kv_head, r.branch, r.tok_begin, r.n_tok, piece_begin(r, k_lo), k_hi,
+                               piece_pos(r, pc.t_lo == 0), 0});
         c.work.push_back(take);
         c.cta_of.push_back(s.second);
         range_of.push_back(pc.range);
@@ -333,6 +343,88 @@ void make_ranges(const PlanInput& in, std::vector<Range>& ranges, int32_t& R, in
     }
 }
 
+// make_ranges for a row plan: every token's position in tok_pos, and ranges
+// trimmed to what a window leaves visible. A range is [lo, hi) with lo rounded
+// down to a page (the page of the first row's oldest visible key; pages before
+// it may have been given back and are never read), preceded by the first keys
+// [base, pos_base) as tiles of their own unless lo already reaches them. The
+// shared range exists when some window reaches into the prefix; otherwise each
+// branch's rows sweep the first keys themselves and are written directly.
+void make_row_ranges(const PlanInput& in, std::vector<Range>& ranges, int32_t& R, int32_t& nq,
+                     int32_t& tpt_tile, std::vector<int32_t>& tok_pos, int32_t& split_at) {
+    ranges.clear();
+    const int32_t B = in.num_branches, ps = in.page_size, W = in.window;
+    const int32_t tail = in.prefix_len % ps;
+    const int32_t P = in.prefix_len - tail;  // see make_ranges
+    const int32_t G = in.H_q / in.H_kv;
+    std::vector<int32_t> tok0(B + 1, 0);
+    int active = 0;
+    int32_t max_t = 0;
+    for (int32_t b = 0; b < B; ++b) {
+        tok0[b + 1] = tok0[b] + in.q_rows[b];
+        if (in.q_rows[b] > 0) ++active;
+        max_t = std::max(max_t, in.q_rows[b]);
+    }
+    R = tok0[B];
+    tok_pos.assign(R, kNoCausal);
+    auto oldest = [&](int32_t t) { return W > 0 ? std::max(0, tok_pos[t] - W + 1) : 0; };
+    bool reaches = false;  // some row's window holds shared keys
+    for (int32_t b = 0; b < B; ++b)
+        for (int32_t t = tok0[b]; t < tok0[b + 1]; ++t) {
+            if (in.causal) tok_pos[t] = P + in.suffix_lens[b] + tail - tok0[b + 1] + t;
+            reaches = reaches || oldest(t) < P;
+        }
+    const bool shared = active >= 2 && P > 0 && reaches;
+    split_at = shared ? P : 0;
+    const int64_t block_rows = static_cast<int64_t>(shared ? R : max_t) * G;
+    nq = block_rows > kBM ? 2 : 1;
+    tpt_tile = kBM / G;
+    const int32_t tpt = tpt_tile * nq;
+    // keys [lo, hi) and first keys [base, last_first) of one run of tokens
+    auto emit = [&](int32_t h, int32_t b, int32_t t, int32_t n, int32_t base, int32_t lo,
+                    int32_t hi, int32_t last_first, bool complete) {
+        const int32_t oldest_key = std::max(base, lo);
+        lo = oldest_key / ps * ps;
+        Range r{h, b, t, n, lo, hi, 0, complete, true, oldest_key - lo, 0};
+        const bool first = last_first > base;
+        if (lo >= hi) {
+            if (!first) return false;
+            r.lo = base;
+            r.hi = last_first;
+            r.front = 0;
+        } else if (first && oldest_key <= last_first) {
+            r.lo = base;  // no hidden key between the two
+            r.front = 0;
+        } else if (first) {
+            r.pos_base = last_first;
+            r.first_tiles = static_cast<int32_t>(cdiv(last_first - base, kBN));
+        }
+        ranges.push_back(r);
+        return true;
+    };
+    std::vector<char> in_shared(R, 0);
+    for (int32_t h = 0; h < in.H_kv; ++h) {
+        for (int32_t t = 0; shared && t < R; t += tpt) {
+            const int32_t n = std::min(tpt, R - t);
+            int32_t lo = P;
+            for (int32_t i = t; i < t + n; ++i) lo = std::min(lo, oldest(i));
+            if (emit(h, 0, t, n, 0, lo, P, W > 0 ? std::min(in.sinks, P) : 0, false))
+                std::fill(in_shared.begin() + t, in_shared.begin() + t + n, 1);
+        }
+        for (int32_t b = 0; b < B; ++b) {
+            const int32_t end = P + in.suffix_lens[b] + tail, base = split_at;
+            for (int32_t t = tok0[b]; t < tok0[b + 1]; t += tpt) {
+                const int32_t n = std::min(tpt, tok0[b + 1] - t);
+                const int32_t hi = in.causal ? std::min(end, tok_pos[t + n - 1] + 1) : end;
+                bool complete = true;
+                for (int32_t i = t; i < t + n; ++i) complete = complete && !in_shared[i];
+                emit(h, b, t, n, base, oldest(t), hi, W > 0 ? std::min(in.sinks, hi) : 0,
+                     complete);
+            }
+        }
+    }
+}
+
 }  // namespace
 
 int build_plan(const PlanInput& in, Plan& plan) {
@@ -340,7 +432,10 @@ int build_plan(const PlanInput& in, Plan& plan) {
     const int32_t B = in.num_branches;
     std::vector<Range> ranges;
     int32_t R = 0;
-    make_ranges(in, ranges, R, plan.nq, plan.tpt);
+    if (in.rows)
+        make_row_ranges(in, ranges, R, plan.nq, plan.tpt, plan.tok_pos, plan.split_at);
+    else
+        make_ranges(in, ranges, R, plan.nq, plan.tpt);
     plan.R = R;
     if (R == 0) return 0;
     const int32_t G = in.H_q / in.H_kv;
@@ -394,7 +489,13 @@ int build_plan(const PlanInput& in, Plan& plan) {
         // equal-chunk plan are what keeps a large shared prefix in L2).
         int64_t kv_tokens = P;
         for (int32_t b = 0; b < B; ++b) kv_tokens += S_eff[b];
-        const int64_t kv_bytes = kv_tokens * in.H_kv * kHD * 2 * 2;
+        if (in.rows) {  // no more than what the ranges read
+            int64_t read = 0;
+            for (const Range& r : ranges)
+                if (r.kv_head == 0) read += r.hi - r.lo;
+            kv_tokens = std::min(kv_tokens, read);
+        }
+        const int64_t kv_bytes = kv_tokens * in.H_kv * in.row_bytes;
         if (kv_bytes <= (100LL << 20)) {
             make_streamk(ranges, max_cta, ovh, cand);
             if (cand.cost < best.cost * 0.97) std::swap(best, cand);
@@ -458,8 +559,11 @@ int build_plan(const PlanInput& in, Plan& plan) {
 bool patch_plan(const PlanInput& in, Plan& plan) {
     if (plan.units.empty() || plan.unit_range.size() != plan.units.size()) return false;
     std::vector<Range> ranges;
-    int32_t R = 0, nq = 0, tpt = 0;
-    make_ranges(in, ranges, R, nq, tpt);
+    int32_t R = 0, nq = 0, tpt = 0, split_at = 0;
+    std::vector<int32_t> tok_pos;
+    if (in.rows) make_row_ranges(in, ranges, R, nq, tpt, tok_pos, split_at);
+    else make_ranges(in, ranges, R, nq, tpt);
+    if (split_at != plan.split_at) return false;
     if (R != plan.R || nq != plan.nq || tpt != plan.tpt || ranges.size() != plan.ranges.size())
         return false;
     for (size_t i = 0; i < ranges.size(); ++i) {
@@ -467,7 +571,8 @@ bool patch_plan(const PlanInput& in, Plan& plan) {
         const Range& o = plan.ranges[i];
         if (a.kv_head != o.kv_head || a.branch != o.branch || a.tok_begin != o.tok_begin ||
             a.n_tok != o.n_tok || a.lo != o.lo || a.complete != o.complete ||
-            (a.pos_base == kNoCausal) != (o.pos_base == kNoCausal) ||
+            (in.rows ? a.pos_base != o.pos_base
+                     : (a.pos_base == kNoCausal) != (o.pos_base == kNoCausal)) ||
             cdiv(a.hi - a.lo, kBN) != cdiv(o.hi - o.lo, kBN))
             return false;
     }
@@ -476,9 +581,11 @@ bool patch_plan(const PlanInput& in, Plan& plan) {
         const Range& o = plan.ranges[plan.unit_range[k]];
         const Range& a = ranges[plan.unit_range[k]];
         if (u.key_end == o.hi) u.key_end = a.hi;  // the range's last unit
-        u.pos_base = a.pos_base;
+        if (in.rows && u.key_begin == o.lo + o.front) u.key_begin = a.lo + a.front;  // its first
+        if (!in.rows) u.pos_base = a.pos_base;
     }
     plan.ranges = ranges;
+    plan.tok_pos = tok_pos;
     return true;
 }
 

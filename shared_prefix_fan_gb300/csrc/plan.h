@@ -18,13 +18,24 @@ struct PlanInput {
     int32_t num_sms;       // persistent CTAs: at most one per SM
     int32_t force_splits;  // >0: cut every key range into this many chunks
     int32_t tail_cuts = 1; // 0: never cut a direct range to even out the last wave
+    // Row plans (windowed or 4-bit attention): every token's position goes to the
+    // device (Plan::tok_pos), and a unit may sweep some first keys before its own
+    // range (Unit::pos_base, see there).
+    int32_t rows = 0;
+    int32_t window = 0;    // > 0: a row at pos sees keys > pos - window ...
+    int32_t sinks = 0;     // ... and keys < sinks
+    int32_t row_bytes = 2 * 2 * kHD;  // K and V of one token and KV head
 };
 
 // A key range of the plan: the rows of n_tok tokens from tok_begin (one KV
 // head) against keys [lo, hi) of a branch (branch 0 for the shared prefix).
+// In a row plan pos_base is the end of the first keys swept before lo (0: none).
 struct PlanRange {
     int32_t kv_head, branch, tok_begin, n_tok, lo, hi, pos_base;
     bool complete;  // covers every visible key of its rows (no other range does)
+    bool rows = false;       // of a row plan (lo is then a page's first key)
+    int32_t front = 0;       // keys from lo on that no row sees: its first unit begins behind them
+    int32_t first_tiles = 0; // 128-key tiles of its first keys
 };
 
 struct Plan {
@@ -41,6 +52,8 @@ struct Plan {
     int32_t tpt = 0;                 // tokens per 128-row query tile
     int32_t nq = 1;                  // query tiles per unit (1 or 2)
     bool need_merge = false;
+    std::vector<int32_t> tok_pos;    // row plans: absolute position of every token
+    int32_t split_at = 0;            // keys below are the shared range's (0: no shared range)
     std::vector<PlanRange> ranges;   // the key ranges the units were cut from
     std::vector<int32_t> unit_range; // per unit: its range
     int32_t n_cta() const { return cta_first.empty() ? 0 : static_cast<int32_t>(cta_first.size()) - 1; }
@@ -69,8 +82,11 @@ struct CallArgs {
     float* lse;
     int64_t R;
     unsigned long long wait_limit_ns;
-    int32_t fused_merge;  // 1: merge inside the attention kernel when the grid fits
-    uint32_t epoch;       // this call's flag value (never 0; distinct from the last call's)
+    int32_t window, sinks;   // see PlanInput
+    int32_t q4;              // 1: 4-bit pools
+    float k_scale, v_scale;  // their scales
+    int32_t fused_merge;     // 1: merge inside the attention kernel when the grid fits
+    uint32_t epoch;          // this call's flag value (never 0; distinct from the last call's)
 };
 
 // Device layout of a plan inside one scratch buffer.
@@ -79,7 +95,7 @@ struct CallArgs {
 constexpr size_t kSinkBytes = 1024;
 
 struct Layout {
-    size_t flags, sink, units, cta, mcnt, ment, mkeys, ml, o, total;
+    size_t flags, sink, units, cta, pos, mcnt, ment, mkeys, ml, o, total;
 };
 Layout plan_layout(const Plan& pl);
 // Copies the plan's tables into `base` (device) on `stream`.
@@ -98,5 +114,7 @@ int validate_call(const void* q, const void* k, const void* v, const int32_t* pa
                   const int32_t* suffix_lens, int32_t B, int32_t P, int32_t max_pages,
                   int32_t num_pages, int32_t page_size, float scale, int32_t out_dtype,
                   const void* out);
+// Whether a 4-bit pool's scale is in the supported range.
+bool q4_scale_ok(float gs);
 
 }  // namespace fanout

@@ -119,6 +119,8 @@ Layout plan_layout(const Plan& pl) {
     off = align256(off + pl.units.size() * sizeof(Unit));
     L.cta = off;
     off = align256(off + pl.cta_first.size() * sizeof(int32_t));
+    L.pos = off;
+    off = align256(off + pl.tok_pos.size() * sizeof(int32_t));
     L.mcnt = off;
     off = align256(off + pl.merge_cnt.size() * sizeof(int32_t));
     L.ment = off;
@@ -140,6 +142,9 @@ cudaError_t upload_plan(const Plan& pl, const Layout& L, uint8_t* base, cudaStre
     if (e == cudaSuccess)
         e = cudaMemcpyAsync(base + L.cta, pl.cta_first.data(),
                             pl.cta_first.size() * sizeof(int32_t), cudaMemcpyHostToDevice, stream);
+    if (e == cudaSuccess && !pl.tok_pos.empty())
+        e = cudaMemcpyAsync(base + L.pos, pl.tok_pos.data(), pl.tok_pos.size() * sizeof(int32_t),
+                            cudaMemcpyHostToDevice, stream);
     if (e == cudaSuccess && !pl.merge_cnt.empty())
         e = cudaMemcpyAsync(base + L.mcnt, pl.merge_cnt.data(),
                             pl.merge_cnt.size() * sizeof(int32_t), cudaMemcpyHostToDevice, stream);
@@ -160,8 +165,10 @@ int launch_plan(const CallArgs& a, const Plan& pl, const Layout& L, uint8_t* bas
     const int64_t pool_rows = static_cast<int64_t>(a.num_pages) * a.H_kv * a.page_size;
     int st;
     if ((st = map_q(&tm_q, a.q, a.R, a.H_q, G, pl.tpt)) != FANOUT_OK) return st;
-    if ((st = map_pool(&tm_k, a.k, pool_rows, a.page_size)) != FANOUT_OK) return st;
-    if ((st = map_pool(&tm_v, a.v, pool_rows, a.page_size)) != FANOUT_OK) return st;
+    if (!a.q4) {
+        if ((st = map_pool(&tm_k, a.k, pool_rows, a.page_size)) != FANOUT_OK) return st;
+        if ((st = map_pool(&tm_v, a.v, pool_rows, a.page_size)) != FANOUT_OK) return st;
+    }
     int32_t* err = nullptr;
     cudaError_t ce = err_word_ptr(&err);
     if (ce != cudaSuccess) return status_of(ce);
@@ -187,6 +194,15 @@ int launch_plan(const CallArgs& a, const Plan& pl, const Layout& L, uint8_t* bas
     p.nq = pl.nq;
     p.out_bf16 = a.out_bf16;
     p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.tok_pos = pl.tok_pos.empty() ? nullptr : reinterpret_cast<const int32_t*>(base + L.pos);
+    p.window = a.window > 0 ? a.window : kNoWindow;
+    p.sinks = a.sinks;
+    p.split_at = pl.split_at;
+    p.q = a.q;
+    p.k_pool = static_cast<const uint8_t*>(a.k);
+    p.v_pool = static_cast<const uint8_t*>(a.v);
+    p.o_scale = a.v_scale;
+    if (a.q4) p.scale_log2 *= a.k_scale;
     p.wait_limit_ns = a.wait_limit_ns;
     MergeParams& m = p.merge;
     m.part_o = p.part_o;
@@ -216,7 +232,8 @@ int launch_plan(const CallArgs& a, const Plan& pl, const Layout& L, uint8_t* bas
 
     if (ev_before) cudaEventRecord(ev_before, stream);
     p.fused_merge = fuse ? 1 : 0;
-    ce = launch_split_attn(p, tm_q, tm_k, tm_v, pl.n_cta(), fuse, stream);
+    ce = a.q4 ? launch_attn_q4(p, tm_q, pl.n_cta(), stream)
+              : launch_split_attn(p, tm_q, tm_k, tm_v, pl.n_cta(), fuse, stream);
     if (ce != cudaSuccess && fuse) {
         (void)cudaGetLastError();  // refused as a cooperative launch: merge separately
         p.fused_merge = 0;
