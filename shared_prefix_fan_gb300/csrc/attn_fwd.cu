@@ -622,8 +622,12 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
         const Unit u = p.units[dry ? ui_first : ui];
         const int n_tiles = dry ? 0 : unit_tiles<ROWS>(p, u);
         if (!dry && (n_tiles <= 0 || x >= unit_nq<NQ>(u, p.tpt))) continue;
-        const int urow = kBM * x + row;  // row within the unit
-        const bool row_valid = dry ? (lane == 0 && quarter == 0) : urow < u.n_tok * p.G;
+        // row within the unit: tile x holds its tokens x * tpt .. (128 / G of them, so
+        // a G that does not divide 128 leaves the tile's last rows empty)
+        const int urow = kBM * x + row;
+        const int tile_tok = x * p.tpt;
+        const bool row_valid =
+            dry ? (lane == 0 && quarter == 0) : row < min(p.tpt, u.n_tok - tile_tok) * p.G;
         if (lane == 0)
             ptx::st_shared_v4(slot, static_cast<uint32_t>(u.tok_begin), static_cast<uint32_t>(u.kv_head),
                               static_cast<uint32_t>(u.part), 0u);
@@ -632,11 +636,11 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
         // Only the key start and this row's visible end stay live through the
         // tile loop (registers).
         const int key_begin = ROWS ? range_begin(u, p.page_size) : u.key_begin;
-        const int vis_end = ROWS ? 0 : row_valid ? min(u.key_end, u.pos_base + u.tok_begin + urow / p.G + 1) : 0;
+        const int vis_end = ROWS ? 0 : row_valid ? min(u.key_end, u.pos_base + u.tok_begin + tile_tok + row / p.G + 1) : 0;
         // a row plan's row sees keys [lo, pos] and keys < sinks, of this tile's run
         const int n_first = ROWS ? first_tiles(u, p.split_at) : 0;
         const int run_begin = ROWS ? first_begin(u, p.split_at) : 0;
-        const int row_end = ROWS && row_valid && !dry ? p.tok_pos[u.tok_begin + urow / p.G] + 1 : 0;
+        const int row_end = ROWS && row_valid && !dry ? p.tok_pos[u.tok_begin + tile_tok + row / p.G] + 1 : 0;
         float m_ref = -INFINITY, l_run = 0.f;
         for (int j = 0; j < n_tiles; ++j, ++jt) {
             const int kt = ROWS && j < n_first ? run_begin + j * kBN
@@ -760,8 +764,8 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
         if (active) {
             const uint4 f = ptx::ld_shared_v4(slot);
             const int e_part = static_cast<int>(f.z);
-            const int tok = static_cast<int>(f.x) + urow / p.G;
-            const int hq = static_cast<int>(f.y) * p.G + urow % p.G;
+            const int tok = static_cast<int>(f.x) + x * p.tpt + row / p.G;
+            const int hq = static_cast<int>(f.y) * p.G + row % p.G;
             const int64_t orow = dry ? 0 : static_cast<int64_t>(tok) * p.H_q + hq;
             const int64_t prow = dry ? 0 : static_cast<int64_t>(e_part) * rows_per_part + urow;
             void* const out_base = dry ? static_cast<void*>(p.sink) : p.out;

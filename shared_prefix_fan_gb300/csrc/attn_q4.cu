@@ -85,7 +85,9 @@ __global__ void __launch_bounds__(32 * kWarps) attn_q4_kernel(const SplitParams 
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] *= p.o_scale;
             if (u.part >= 0) {
-                const int64_t prow = static_cast<int64_t>(u.part) * (kBM * p.nq) + row;
+                const int i = row / p.G;
+                const int64_t prow = static_cast<int64_t>(u.part) * (kBM * p.nq) +
+                                     i / p.tpt * kBM + i % p.tpt * p.G + row % p.G;
                 reinterpret_cast<float4*>(p.part_o + prow * kHD)[lane] =
                     make_float4(o[0], o[1], o[2], o[3]);
                 if (lane == 0) p.part_ml[prow] = make_float2(m, l);

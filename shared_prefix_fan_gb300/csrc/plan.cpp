@@ -542,7 +542,8 @@ int build_plan(const PlanInput& in, Plan& plan) {
                     const size_t key = static_cast<size_t>(t) * in.H_kv + u.kv_head;
                     const size_t e = key * stride + fill_e[key]++;
                     plan.merge_ent[2 * e] = u.part;
-                    plan.merge_ent[2 * e + 1] = (t - u.tok_begin) * G;  // first row of t in u
+                    const int32_t i = t - u.tok_begin;  // first row of its t-th token
+                    plan.merge_ent[2 * e + 1] = i / plan.tpt * kBM + i % plan.tpt * G;
                 }
         // a (token, head) covered by a single direct unit has count 0; when
         // some are, the merge visits only the keys listed here
