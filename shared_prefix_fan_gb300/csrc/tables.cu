@@ -105,8 +105,8 @@ __device__ bool scan_branches(const TableParams& p, Scan& sm, int32_t& used, int
     int64_t row = block_scan(nr, sm.part[1], rows);
     if (!ok) sm.bad = 1;
     __syncthreads();
-    if (sm.bad || used < 0 || used + pages > p.n_free || (p.slots && rows > p.n_slots) ||
-        rows > kMaxTokens)
+    if (sm.bad || used < 0 || (pages > 0 && used + pages > p.n_free) ||
+        (p.slots && rows > p.n_slots) || rows > kMaxTokens)
         return false;
     for (int b = b0; b < b1; ++b) {  // lengths again: cheaper than keeping them
         int32_t held, need, r;
