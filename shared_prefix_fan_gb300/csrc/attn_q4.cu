@@ -1,13 +1,44 @@
-// attn_q4.cu -- fan-out attention over a cache held in 4 bits.
+// attn_q4.cu -- fan-out attention over a cache held in 4 bits, for sm_103a.
 //
 // The rows of a cache (kv_q4.cu) are e2m1 codes with one e4m3 scale per 16
-// values; out = softmax(scale q K^T) V over the values they stand for.
+// values; out = softmax(scale q K^T) V over the values they stand for. Units,
+// tiles and the online softmax are those of attn_fwd.cu (128 query rows x 128
+// keys, base 2, the reference maximum m raised only when a row's maximum passes
+// it by 2^8); positions, windows and first keys are those of its row plans.
 //
-// One warp per query row (token, head): every lane holds 4 of the 128
-// dimensions, keys are swept one by one with the online softmax (running
-// maximum m and sum l in base 2, O rescaled when m moves), split over the
-// planner's units and merged from their partials (m, l, O).
+// The tensor core gets 16-bit tiles that hold the cached values exactly: a code
+// has 2 significant bits, a group scale 4, their product 6.
+//   K: bf16 (q's type), value * 2^-8;    S = Q K^T from shared memory.
+//   V: f16, value * 2^-7;                O += P V with P from TMEM as f16,
+// P = 2^(x - m + 7): at most 2^15, and below 2^-21 of the row's reference its
+// step is 2^-31 of it, so P's rounding is f16's half step of 2^-11 (bf16, as for
+// bf16 pools, would be 2^-8). The powers of two go into the softmax scale and
+// cancel between P and V; pool scales go into the softmax scale and the output.
+//
+// Widening needs no conversion instruction: with a 16-bit float's sign at bit 15
+// and its lowest exponent bits and highest mantissa bit right below (bits 8..6 in
+// bf16, 11..9 in f16), a code's three magnitude bits put there are its value
+// times 2^-126 (2^-14), subnormals included; so are an e4m3 scale's bits, times
+// 2^-120 (2^-8). Two shifts and two logic operations bring a pair of codes there,
+// one packed product applies the scale.
+//
+// GB300 mapping, one persistent CTA per SM, 18 warps:
+//   warp 0      producer: page blocks by cp.async.bulk into a ring of raw tiles
+//               (9 KB: 128 rows of 72 bytes), Q by TMA when its buffer is free;
+//   warp 1      TMEM owner and single-thread tcgen05 issuer;
+//   warps 2-9   two softmax groups of 4 warps, thread = row;
+//   warps 10-17 widen raw tiles into the swizzled 16-bit ring (4 warps the K
+//               tiles, 4 the V tiles), rows that no row of the unit sees as zeros.
+// A unit of two query tiles gives each group one of them. A unit of one query
+// tile (decode) is split over the groups by keys instead: tile t goes to group
+// t mod 2, each with its own S, (m, l) and O in TMEM, and the two are joined at
+// the unit's end (64 columns of O each), so that two tiles' softmaxes overlap.
+// TMEM: S_0 = 0, S_1 = 128, O_0 = 256, O_1 = 384 (512 columns).
+// Every wait is bounded, as in attn_fwd.cu.
 #include <cuda_bf16.h>
+
+#include <atomic>
+#include <mutex>
 
 #include "fanout_internal.h"
 #include "ptx_sm100.cuh"
@@ -16,103 +47,804 @@
 namespace fanout {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kTileBytes = kBN * kHD * 2;   // one widened K or V tile
+constexpr int kHalfBytes = kTileBytes / 2;  // 128 rows x 64 columns (128 B rows)
+constexpr int kQBytes = kBM * kHD * 2;
+constexpr int kRawBytes = kBN * kQ4RowBytes;
+constexpr float kRescaleLog2 = 8.0f;  // lazy rescale threshold (base-2 units)
+constexpr float kLiftLog2 = 7.0f;     // P is 2^7 times the probability's numerator
+constexpr int kErrTimeout = 5;        // FANOUT_ETIMEOUT
+constexpr int kGroupWarps = 4;
+constexpr int kWarpSoftmax = 2;   // first softmax warp
+constexpr int kWarpWiden = 10;    // first widening warp
+constexpr int kThreads = 32 * 18;
 
-__device__ __forceinline__ float e2m1_f32(uint32_t code) {
-    const uint32_t m = code & 7u;
-    const float a = m < 4 ? 0.5f * static_cast<float>(m)
-                          : static_cast<float>((2u + (m & 1u)) << ((m >> 1) - 2u));
-    return (code & 8u) ? -a : a;
-}
-__device__ __forceinline__ float e4m3_f32(uint32_t byte) {
-    uint32_t h2;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(byte)));
-    float f;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}"
-        : "=f"(f)
-        : "r"(h2));
-    return f;
-}
+template <int NQ>
+struct Cfg {
+    static constexpr int kStages = 4;            // widened tiles
+    static constexpr int kRaw = NQ == 1 ? 6 : 3;  // raw tiles
+    static constexpr int kSmemQ = 0;
+    static constexpr int kSmemRing = NQ * kQBytes;
+    static constexpr int kSmemRaw = kSmemRing + kStages * kTileBytes;
+    static constexpr int kSmemBar = kSmemRaw + kRaw * kRawBytes;
+    static constexpr int BAR_FULL = 0;
+    static constexpr int BAR_EMPTY = kStages;
+    static constexpr int BAR_RFULL = 2 * kStages;
+    static constexpr int BAR_REMPTY = BAR_RFULL + kRaw;
+    static constexpr int BAR_QFULL = BAR_REMPTY + kRaw;  // + x
+    static constexpr int BAR_QFREE = BAR_QFULL + NQ;     // + x
+    static constexpr int BAR_OFREE = BAR_QFREE + NQ;
+    static constexpr int BAR_DRAIN = BAR_OFREE + 1;
+    static constexpr int BAR_GROUP = BAR_DRAIN + 1;  // + 4 x + {SFULL, PFULL, ODONE, JOIN}
+    static constexpr int kNumBars = BAR_GROUP + 8;
+    static constexpr int kSmemMisc = kSmemBar + kNumBars * 8;
+    static constexpr int kSmemJoin = (kSmemMisc + 16 + 15) & ~15;  // float2 [2][2][128]
+    static constexpr int kSmemTotal = kSmemJoin + 2 * 2 * kBM * 8;
+    static constexpr int kSmemAlloc = kSmemTotal + 1024;  // base aligned up to 1024 B
+    static_assert(kSmemAlloc <= 232448, "shared memory per CTA");
+    static_assert(kSmemBar % 16 == 0 && kSmemRaw % 128 == 0, "shared-memory alignment");
+};
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256;
+enum { SFULL = 0, PFULL = 1, ODONE = 2, JOIN = 3 };
 
-// This lane's 4 values (dimensions 4 lane ..) of token slot `slot` of a block.
-__device__ __forceinline__ void load4(const uint8_t* block, int page_size, int slot, int lane,
-                                      float (&x)[4]) {
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(block + slot * 64) + (lane >> 1));
-    const float s = e4m3_f32(__ldg(block + page_size * 64 + slot * 8 + (lane >> 2)));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int e = 4 * (lane & 1) + i;
-        x[i] = e2m1_f32((w >> (16 * (e & 1) + 4 * (e >> 1))) & 15u) * s;
+constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(kBM, kBN, false, false);
+constexpr uint32_t kIdescPV = ptx::idesc_f16_f32(kBM, kHD, false, true);
+
+template <int NQ>
+struct Smem {
+    using C = Cfg<NQ>;
+    uint32_t base;  // shared-window address of the 1024-aligned base
+    uint8_t* ptr;   // generic pointer to the same place
+    __device__ uint32_t bar(int i) const { return base + C::kSmemBar + 8u * i; }
+    __device__ uint32_t gbar(int x, int which) const { return bar(C::BAR_GROUP + 4 * x + which); }
+    __device__ uint32_t* tmem_slot() const { return reinterpret_cast<uint32_t*>(ptr + C::kSmemMisc); }
+    __device__ volatile int* abort_flag() const {
+        return reinterpret_cast<volatile int*>(ptr + C::kSmemMisc + 4);
+    }
+    __device__ uint32_t tile(uint32_t pos) const {
+        return base + C::kSmemRing + (pos % C::kStages) * kTileBytes;
+    }
+};
+
+__device__ __forceinline__ void record_timeout(const SplitParams& p, volatile int* abort_flag,
+                                               int site) {
+    *abort_flag = 1;
+    if (atomicCAS(p.err, 0, kErrTimeout) == 0) {
+        p.err[1] = site;
+        p.err[2] = static_cast<int32_t>(blockIdx.x);
     }
 }
 
-__global__ void __launch_bounds__(32 * kWarps) attn_q4_kernel(const SplitParams p) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Wait of a whole warp (every lane returns the same).
+template <int NQ>
+__device__ __forceinline__ bool warp_wait(const SplitParams& p, const Smem<NQ>& sm, uint32_t bar,
+                                          uint32_t parity, int site) {
+    const bool w = ptx::mbar_wait(bar, parity, p.wait_limit_ns, sm.abort_flag());
+    if (__all_sync(0xffffffffu, w)) return true;
+    record_timeout(p, sm.abort_flag(), site);
+    return false;
+}
+
+// Query tiles of a unit.
+template <int NQ>
+__device__ __forceinline__ int unit_nq(const Unit& u, int tpt) {
+    return (NQ == 2 && u.n_tok > tpt) ? 2 : 1;
+}
+
+// The tiles of a unit, in sweep order: its first keys, then its own range.
+struct Tiles {
+    int n_first, first_begin, first_end, begin, end, key_begin, n;
+    __device__ Tiles(const SplitParams& p, const Unit& u)
+        : n_first(first_tiles(u, p.split_at)),
+          first_begin(fanout::first_begin(u, p.split_at)),
+          first_end(u.pos_base),
+          begin(range_begin(u, p.page_size)),
+          end(u.key_end),
+          key_begin(u.key_begin),
+          n(n_first + (end - begin + kBN - 1) / kBN) {}
+    // first key, one past the last key, first key that some row sees
+    __device__ __forceinline__ void tile(int j, int& kt, int& last, int& front) const {
+        const bool f = j < n_first;
+        kt = f ? first_begin + j * kBN : begin + (j - n_first) * kBN;
+        last = min(kt + kBN, f ? first_end : end);
+        front = f ? 0 : max(0, key_begin - kt);
+    }
+};
+
+// ------------------------------------------------------------------ producer
+template <int NQ>
+__device__ void producer_warp(const SplitParams& p, const Smem<NQ>& sm, const CUtensorMap* tm_q) {
+    using C = Cfg<NQ>;
+    const int lane = threadIdx.x & 31;
+    volatile int* abort = sm.abort_flag();
     const int ps = p.page_size;
-    for (int ui = p.cta_first[blockIdx.x]; ui < p.cta_first[blockIdx.x + 1]; ++ui) {
+    const int64_t block = static_cast<int64_t>(ps) * kQ4RowBytes;
+    uint32_t it = 0;                // raw tiles issued
+    uint32_t q_loads[NQ] = {};      // loads of each Q buffer so far
+    bool ok = true;
+
+    // Q tile x of unit u into its buffer, whose last S products have completed.
+    auto load_q = [&](const Unit& u, int x) {
+        if (lane == 0) {
+            const uint32_t qb = sm.bar(C::BAR_QFULL + x);
+            const int box_bytes = p.G * p.tpt * 128;  // one half of one query tile
+            ptx::mbar_arrive_expect_tx(qb, static_cast<uint32_t>(2 * box_bytes));
+            const uint32_t dst = sm.base + C::kSmemQ + x * kQBytes;
+            const int y = u.kv_head * p.G, z = u.tok_begin + x * p.tpt;
+            ptx::tma_load_3d(dst, tm_q, qb, 0, y, z);
+            ptx::tma_load_3d(dst + kHalfBytes, tm_q, qb, 64, y, z);
+        }
+    };
+    auto q_free = [&](int x) {
+        return q_loads[x] == 0 ||
+               ptx::mbar_test_wait(sm.bar(C::BAR_QFREE + x), (q_loads[x] - 1) & 1u);
+    };
+
+    const int ui_end = p.cta_first[blockIdx.x + 1];
+    for (int ui = p.cta_first[blockIdx.x]; ui < ui_end && ok; ++ui) {
         const Unit u = p.units[ui];
-        const int32_t* table = p.page_table + static_cast<int64_t>(u.branch) * p.max_pages;
-        for (int row = warp; row < u.n_tok * p.G; row += kWarps) {
-            const int tok = u.tok_begin + row / p.G, hq = u.kv_head * p.G + row % p.G;
-            const int64_t orow = static_cast<int64_t>(tok) * p.H_q + hq;
-            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + orow * kHD + 4 * lane;
-            float qf[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) qf[i] = __bfloat162float(q[i]) * p.scale_log2;
-            const int pos = p.tok_pos[tok];
-            const int lo = pos - p.window + 1;
-            for (int run = u.pos_base > 0 ? 0 : 1; run < 2; ++run) {
-                const int begin = run == 0 ? first_begin(u, p.split_at) : u.key_begin;
-                const int end = min(run == 0 ? u.pos_base : u.key_end, pos + 1);
-                const int sinks = run == 0 || u.pos_base == 0 ? p.sinks : 0;
-                for (int j = begin; j < end; ++j) {
-                    if (j < lo && j >= sinks) continue;
-                    const int64_t page = checked_page(p, table[j / ps]);
-                    const int64_t block = (page * p.H_kv + u.kv_head) * (ps * kQ4RowBytes);
-                    float k[4], v[4];
-                    load4(p.k_pool + block, ps, j % ps, lane, k);
-                    load4(p.v_pool + block, ps, j % ps, lane, v);
-                    float s = k[0] * qf[0] + k[1] * qf[1] + k[2] * qf[2] + k[3] * qf[3];
-                    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-                    const float m_new = fmaxf(m, s);
-                    const float corr = ptx::ex2(m - m_new), e = ptx::ex2(s - m_new);
-                    l = l * corr + e;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[i] = o[i] * corr + e * v[i];
-                    m = m_new;
+        const Tiles tl(p, u);
+        const int nq = unit_nq<NQ>(u, p.tpt);
+        if (lane == 0 && ui + 1 < ui_end) {  // the next unit's Q into L2
+            const Unit un = p.units[ui + 1];
+            for (int x = 0; x < unit_nq<NQ>(un, p.tpt); ++x) {
+                const int y = un.kv_head * p.G, z = un.tok_begin + x * p.tpt;
+                ptx::tma_prefetch_3d(tm_q, 0, y, z);
+                ptx::tma_prefetch_3d(tm_q, 64, y, z);
+            }
+        }
+        // The unit's Q waits for the previous unit's last S products while its
+        // raw tiles already flow: Q goes out as soon as its buffer is seen free.
+        int q_next = 0;
+        auto try_q = [&]() {
+            while (q_next < nq && __shfl_sync(0xffffffffu, q_free(q_next), 0)) {
+                load_q(u, q_next);
+                ++q_loads[q_next];
+                ++q_next;
+            }
+        };
+        // Waits for a condition of this warp, sending Q when it can.
+        auto wait_for = [&](auto cond, int site) {
+            uint64_t t0 = 0;
+            for (uint32_t i = 0;; ++i) {
+                try_q();
+                if (__shfl_sync(0xffffffffu, cond(), 0)) return true;
+                if ((i & 15u) == 15u) {
+                    const uint64_t now = ptx::globaltimer_ns();
+                    if (t0 == 0) t0 = now;
+                    const bool over = *abort || now - t0 > p.wait_limit_ns;
+                    if (__shfl_sync(0xffffffffu, over, 0)) {
+                        if (lane == 0) record_timeout(p, abort, site);
+                        return false;
+                    }
                 }
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] *= p.o_scale;
-            if (u.part >= 0) {
-                const int i = row / p.G;
-                const int64_t prow = static_cast<int64_t>(u.part) * (kBM * p.nq) +
-                                     i / p.tpt * kBM + i % p.tpt * p.G + row % p.G;
-                reinterpret_cast<float4*>(p.part_o + prow * kHD)[lane] =
-                    make_float4(o[0], o[1], o[2], o[3]);
-                if (lane == 0) p.part_ml[prow] = make_float2(m, l);
-                continue;
+        };
+        const int32_t* table = p.page_table + static_cast<int64_t>(u.branch) * p.max_pages;
+        for (int run = tl.n_first > 0 ? 0 : 1; run < 2 && ok; ++run) {
+            const int begin = run == 0 ? tl.first_begin : tl.begin;
+            const int end = run == 0 ? tl.first_end : tl.end;
+            const int n_tiles = (end - begin + kBN - 1) / kBN;
+            const int n_pages = (end - begin + ps - 1) / ps;
+            const int ppt = kBN / ps;  // pages per tile: 1, 2, 4 or 8 (divides 32)
+            // page ids, 32 per window, loaded one window ahead
+            auto load_window = [&](int w) -> int {
+                const int idx = w * 32 + lane;
+                return idx < n_pages ? __ldg(table + begin / ps + idx) : 0;
+            };
+            int win = 0, win_cur = load_window(0), win_nxt = load_window(1);
+            for (int j = 0; j < n_tiles && ok; ++j) {
+                const int n_pg = min(ppt, n_pages - j * ppt);
+                if (((j * ppt) >> 5) != win) {
+                    win = (j * ppt) >> 5;
+                    win_cur = win_nxt;
+                    win_nxt = load_window(win + 1);
+                }
+                const int page = __shfl_sync(0xffffffffu, win_cur, ((j * ppt) & 31) + (lane & 7));
+                int64_t src = 0;
+                if (lane < n_pg)
+                    src = (static_cast<int64_t>(checked_page(p, page)) * p.H_kv + u.kv_head) * block;
+                for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
+                    const uint32_t s = it % C::kRaw, par = (it / C::kRaw) & 1u;
+                    const uint32_t empty = sm.bar(C::BAR_REMPTY + s), full = sm.bar(C::BAR_RFULL + s);
+                    ok = wait_for([&] { return ptx::mbar_test_wait(empty, par ^ 1u); }, 2);
+                    if (!ok) break;
+                    if (lane == 0)
+                        ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(n_pg) *
+                                                             static_cast<uint32_t>(block));
+                    __syncwarp();
+                    if (lane < n_pg)
+                        ptx::bulk_load(sm.base + C::kSmemRaw + s * kRawBytes +
+                                           lane * static_cast<uint32_t>(block),
+                                       (kv == 0 ? p.k_pool : p.v_pool) + src,
+                                       static_cast<uint32_t>(block), full);
+                }
             }
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            if (p.out_bf16)
-                reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + orow * kHD)[lane] =
-                    make_uint2(ptx::pack_bf16x2(o[0] * inv, o[1] * inv),
-                               ptx::pack_bf16x2(o[2] * inv, o[3] * inv));
-            else
-                reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow * kHD)[lane] =
-                    make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
-            if (p.lse && lane == 0) p.lse[orow] = (m + __log2f(l)) * 0.69314718055994531f;
+        }
+        if (ok && q_next < nq) ok = wait_for([&] { return q_next == nq; }, 1);
+    }
+    // (see attn_fwd.cu: the merge grid may start once every copy is issued)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (!ok && lane == 0) {
+        // Drain: every copy this warp started must land before the CTA exits.
+        const uint32_t n = it < C::kRaw ? it : C::kRaw;
+        for (uint32_t i = it - n; i != it; ++i)
+            ptx::mbar_wait(sm.bar(C::BAR_RFULL + i % C::kRaw), (i / C::kRaw) & 1u, p.wait_limit_ns,
+                           nullptr);
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+            if (q_loads[x] > 0)
+                ptx::mbar_wait(sm.bar(C::BAR_QFULL + x), (q_loads[x] - 1) & 1u, p.wait_limit_ns,
+                               nullptr);
+    }
+}
+
+// ------------------------------------------------------------------ widening
+// Four pairs of neighbouring values of a code word, as 16-bit floats without
+// their scale: sign to bit 15 and magnitude bits to kMag's place of each half.
+template <bool IS_V>
+__device__ __forceinline__ void widen_word(uint32_t w, uint32_t scale, uint32_t (&out)[4]) {
+    constexpr uint32_t kSign = 0x80008000u;
+    constexpr uint32_t kMag = IS_V ? 0x0E000E00u : 0x01C001C0u;
+    constexpr int kUp = IS_V ? 9 : 6;  // left shift of code 0's magnitude
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int sh = kUp - 4 * j;
+        const uint32_t mag = sh >= 0 ? w << sh : w >> -sh;
+        out[j] = ((w << (12 - 4 * j)) & kSign) | (mag & kMag);
+        out[j] = IS_V ? ptx::mul_f16x2(out[j], scale) : ptx::mul_bf16x2(out[j], scale);
+    }
+}
+// A group's scale (e4m3 byte) in both halves: K: times 2^118 (the codes carry
+// 2^-126, the tile 2^-8), in two exact products; V: times 2^7 (2^-14, 2^-7).
+template <bool IS_V>
+__device__ __forceinline__ uint32_t widen_scale(uint32_t byte) {
+    if (IS_V) return ptx::mul_f16x2(((byte & 0x7fu) << 7) * 0x00010001u, 0x78007800u);
+    const uint32_t s = ((byte & 0x7fu) << 4) * 0x00010001u;
+    return ptx::mul_bf16x2(ptx::mul_bf16x2(s, 0x7F007F00u), 0x77007700u);
+}
+
+// Four warps widen every K (or V) tile. A lane takes 16 bytes of codes (32
+// values, two groups) of a row: 8 rows per step and warp, loads without bank
+// conflicts; lanes of the upper 64 columns store their words in the order 2, 3,
+// 0, 1, so that the 8 lanes of a store phase cover all 8 sixteen-byte columns.
+template <int NQ, bool IS_V>
+__device__ void widen_warp(const SplitParams& p, const Smem<NQ>& sm, int w) {
+    using C = Cfg<NQ>;
+    const int lane = threadIdx.x & 31;
+    const int ps = p.page_size, ps_shift = 31 - __clz(ps), piece = lane & 3;
+    const bool upper = piece >= 2;
+    uint32_t it = IS_V ? 1u : 0u;  // ring position of this warp's next tile
+    const int ui_end = p.cta_first[blockIdx.x + 1];
+    for (int ui = p.cta_first[blockIdx.x]; ui < ui_end; ++ui) {
+        const Unit u = p.units[ui];
+        const Tiles tl(p, u);
+        for (int j = 0; j < tl.n; ++j, it += 2) {
+            int kt, last, front;
+            tl.tile(j, kt, last, front);
+            const uint32_t rs = it % C::kRaw, stage = it % C::kStages;
+            if (!warp_wait<NQ>(p, sm, sm.bar(C::BAR_RFULL + rs), (it / C::kRaw) & 1u, 40)) return;
+            if (!warp_wait<NQ>(p, sm, sm.bar(C::BAR_EMPTY + stage), ((it / C::kStages) & 1u) ^ 1u, 41))
+                return;
+            const uint32_t raw = sm.base + C::kSmemRaw + rs * kRawBytes;
+            const uint32_t dst = sm.tile(it) + (piece >> 1) * kHalfBytes;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = w * 32 + i * 8 + (lane >> 2);
+                const bool seen = r >= front && kt + r < last;
+                uint4 c = make_uint4(0u, 0u, 0u, 0u);
+                uint32_t sc = 0;
+                if (seen) {
+                    const int pg = r >> ps_shift, slot = r & (ps - 1);
+                    const uint32_t at = raw + pg * ps * kQ4RowBytes;
+                    c = ptx::ld_shared_v4(at + slot * 64 + piece * 16);
+                    sc = ptx::ld_shared_u16(at + ps * 64 + slot * 8 + piece * 2);
+                }
+                const uint32_t s0 = widen_scale<IS_V>(upper ? sc >> 8 : sc);
+                const uint32_t s1 = widen_scale<IS_V>(upper ? sc : sc >> 8);
+                const uint32_t word[4] = {upper ? c.z : c.x, upper ? c.w : c.y, upper ? c.x : c.z,
+                                          upper ? c.y : c.w};
+                const uint32_t row = dst + r * 128;
+                const uint32_t col = static_cast<uint32_t>(((piece & 1) * 4) ^ (upper ? 2 : 0) ^ (r & 7)) << 4;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t o[4];
+                    widen_word<IS_V>(word[k], k < 2 ? s0 : s1, o);
+                    ptx::st_shared_v4(row + (col ^ (k << 4)), o[0], o[1], o[2], o[3]);
+                }
+            }
+            ptx::fence_proxy_async_smem();  // the MMAs read the tile
+            __syncwarp();
+            if (lane == 0) {
+                ptx::mbar_arrive(sm.bar(C::BAR_FULL + stage));
+                ptx::mbar_arrive(sm.bar(C::BAR_REMPTY + rs));
+            }
         }
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ------------------------------------------------------------------ MMA issuer
+// Descriptors: see attn_fwd.cu (the same tile layouts).
+__device__ __forceinline__ uint64_t kmajor_step(int kk) {
+    return static_cast<uint64_t>((kk >> 2) * (kHalfBytes >> 4) + (kk & 3) * 2);
+}
+
+// One P.V product: group x's P of its t-th tile times the V tile at ring position
+// pos. first: the group's first product of unit k (O is overwritten; both groups
+// must have read the previous unit's O).
+struct PvOp {
+    int x;
+    uint32_t t;
+    bool first;
+    int k;
+    uint32_t pos;
+};
+
+template <int NQ>
+struct Issuer {
+    using C = Cfg<NQ>;
+    const SplitParams& p;
+    const Smem<NQ>& sm;
+    uint32_t tmem;
+    bool issued_any = false;
+
+    __device__ bool wait(uint32_t bar, uint32_t parity, int site) {
+        if (ptx::mbar_wait(bar, parity, p.wait_limit_ns, sm.abort_flag())) return true;
+        record_timeout(p, sm.abort_flag(), site);
+        return false;
+    }
+    __device__ bool wait_full(uint32_t pos, int site) {
+        return wait(sm.bar(C::BAR_FULL + pos % C::kStages), (pos / C::kStages) & 1u, site);
+    }
+    __device__ void release(uint32_t pos) { ptx::mma_commit(sm.bar(C::BAR_EMPTY + pos % C::kStages)); }
+    // S of group x = Q tile qx times the K tile at pos.
+    __device__ void issue_s(int x, int qx, uint32_t pos) {
+        ptx::tc_fence_after();
+        const uint64_t dq = ptx::sdesc_sw128(sm.base + C::kSmemQ + qx * kQBytes, 16, 1024);
+        const uint64_t dk = ptx::sdesc_sw128(sm.tile(pos), 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kHD / 16; ++kk)
+            ptx::mma_bf16_ss(tmem + 128u * x, dq + kmajor_step(kk), dk + kmajor_step(kk), kIdescQK,
+                             kk > 0);
+        ptx::mma_commit(sm.gbar(x, SFULL));
+        issued_any = true;
+    }
+    __device__ bool issue_pv(const PvOp& op) {
+        if (!wait(sm.gbar(op.x, PFULL), op.t & 1u, 14)) return false;
+        if (op.first && op.k > 0 && !wait(sm.bar(C::BAR_OFREE), (op.k - 1) & 1, 15)) return false;
+        ptx::tc_fence_after();
+        const uint32_t a = tmem + 128u * op.x;  // P: 64 columns of f16 pairs
+        const uint32_t d = tmem + kColO + 128u * op.x;
+        const uint64_t dv = ptx::sdesc_sw128(sm.tile(op.pos), kHalfBytes, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kBN / 16; ++kk)
+            ptx::mma_bf16_ts(d, a + 8u * kk, dv + 128u * kk, kIdescPV, (!op.first || kk > 0) ? 1u : 0u);
+        ptx::mma_commit(sm.gbar(op.x, ODONE));
+        return true;
+    }
+    // The held P.V of a unit of one query tile, if any.
+    __device__ bool issue_held(const PvOp& op, bool& held) {
+        if (!held) return true;
+        held = false;
+        if (!wait_full(op.pos, 13) || !issue_pv(op)) return false;
+        release(op.pos);
+        return true;
+    }
+};
+
+// Two query tiles per unit: S_0(j), P.V_1(j-1), S_1(j), P.V_0(j). One query tile:
+// S(t) into group t mod 2's buffer, then P.V(t-1) of the other group; a unit's
+// last P.V is held until the next such unit's first S is issued. An S that
+// reuses the TMEM of an earlier P is always issued after that P's product.
+template <int NQ>
+__device__ void mma_thread(const SplitParams& p, const Smem<NQ>& sm, uint32_t tmem) {
+    using C = Cfg<NQ>;
+    Issuer<NQ> is{p, sm, tmem};
+    bool ok = true;
+    uint32_t pos = 0;           // ring position of the unit's K_0 (K_j at pos + 2j, V_j behind it)
+    uint32_t jt[2] = {0, 0};    // tiles each softmax group got before
+    uint32_t qu[2] = {0, 0};    // loads of each Q buffer consumed
+    int nx = 0;                 // group of the next one-query-tile unit's first tile
+    PvOp pend{0, 0, false, 0, 0};
+    bool held = false;
+    int k = 0;
+    const int ui_end = p.cta_first[blockIdx.x + 1];
+    for (int ui = p.cta_first[blockIdx.x]; ui < ui_end && ok; ++ui, ++k) {
+        const Unit u = p.units[ui];
+        const int n = Tiles(p, u).n;
+        if (unit_nq<NQ>(u, p.tpt) == 2) {
+            if (!(ok = is.issue_held(pend, held))) break;
+            if (!(ok = is.wait(sm.bar(C::BAR_QFULL), qu[0] & 1u, 10) &&
+                       is.wait(sm.bar(C::BAR_QFULL + NQ - 1), qu[1] & 1u, 10)))
+                break;
+            for (int j = 0; j <= n && ok; ++j) {
+                const uint32_t posK = pos + 2u * j, posV = posK + 1u, posVp = posK - 1u;
+                if (j < n) {
+                    if (!(ok = is.wait_full(posK, 11))) break;
+                    is.issue_s(0, 0, posK);
+                    if (j == n - 1) ptx::mma_commit(sm.bar(C::BAR_QFREE));
+                }
+                if (j > 0) {
+                    if (!(ok = is.issue_pv(PvOp{1, jt[1] + j - 1, j == 1, k, posVp}))) break;
+                    is.release(posVp);
+                }
+                if (j < n) {
+                    is.issue_s(1, NQ - 1, posK);
+                    is.release(posK);
+                    if (j == n - 1) ptx::mma_commit(sm.bar(C::BAR_QFREE + NQ - 1));
+                    if (!(ok = is.wait_full(posV, 13))) break;
+                    if (!(ok = is.issue_pv(PvOp{0, jt[0] + j, j == 0, k, posV}))) break;
+                }
+            }
+            if (!ok) break;
+            jt[0] += n;
+            jt[1] += n;
+            ++qu[0];
+            ++qu[1];
+        } else {
+            if (held && !ptx::mbar_test_wait(sm.bar(C::BAR_QFULL), qu[0] & 1u) &&
+                !(ok = is.issue_held(pend, held)))
+                break;
+            for (int j = 0; j < n && ok; ++j) {
+                const uint32_t posK = pos + 2u * j;
+                const int x = (nx + j) & 1;
+                if (!(ok = is.wait_full(posK, 11))) break;
+                if (j == 0 && !(ok = is.wait(sm.bar(C::BAR_QFULL), qu[0] & 1u, 10))) break;
+                is.issue_s(x, 0, posK);
+                is.release(posK);
+                if (j == n - 1) ptx::mma_commit(sm.bar(C::BAR_QFREE));
+                if (!(ok = is.issue_held(pend, held))) break;
+                const uint32_t t = x == 0 ? jt[0]++ : jt[1]++;
+                pend = PvOp{x, t, j < 2, k, posK + 1u};
+                held = true;
+            }
+            if (!ok) break;
+            nx = (nx + n) & 1;
+            ++qu[0];
+        }
+        pos += 2u * n;
+    }
+    if (ok) ok = is.issue_held(pend, held);
+    if (!ok && is.issued_any) {
+        ptx::mma_commit(sm.bar(C::BAR_DRAIN));
+        ptx::mbar_wait(sm.bar(C::BAR_DRAIN), 0, p.wait_limit_ns, nullptr);
+    }
+}
+
+// ------------------------------------------------------------------ softmax
+__device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&a)[32], uint32_t (&b)[32]) {
+    ptx::tmem_ld32(taddr, a);
+    ptx::tmem_ld32(taddr + 32, b);
+    ptx::tmem_ld_wait(a);
+    ptx::reg_touch(b);
+}
+
+// What of a tile a row sees: columns below lim, and not [sink, lo).
+struct Seen {
+    int lim, lo, sink;
+    __device__ __forceinline__ void mask(uint32_t (&s)[32], int c0) const {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            if (c0 + c >= lim || (c0 + c < lo && c0 + c >= sink)) s[c] = __float_as_uint(-INFINITY);
+    }
+};
+
+__device__ __forceinline__ float max32(const uint32_t (&s)[32], float m) {
+    float a = m, b = __uint_as_float(s[1]);
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+        a = ptx::fmax3(a, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+        b = ptx::fmax3(b, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+    }
+    return fmaxf(a, b);
+}
+
+// P of 32 columns to TMEM (16 columns of f16 pairs), their sum added to l.
+__device__ __forceinline__ void exp32(const uint32_t (&s)[32], uint32_t taddr, uint64_t sl2,
+                                      uint64_t negm, uint64_t (&l)[2]) {
+    uint32_t packed[16];
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+        const uint64_t t = ptx::fma_f32x2(
+            ptx::f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sl2, negm);
+        const float e0 = ptx::ex2(ptx::lo_f32(t)), e1 = ptx::ex2(ptx::hi_f32(t));
+        l[(c >> 1) & 1] = ptx::add_f32x2(l[(c >> 1) & 1], ptx::f32x2(e0, e1));
+        packed[c >> 1] = ptx::pack_f16x2(e0, e1);
+    }
+    ptx::tmem_st16(taddr, packed);
+}
+
+// 32 columns of a finished row: to out (direct) or to its partial block.
+__device__ __forceinline__ void store32(const SplitParams& p, const uint32_t (&r)[32], bool direct,
+                                        int64_t orow, int64_t prow, int c0) {
+    if (direct && p.out_bf16) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * kHD + c0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            dst[i] = make_uint4(
+                ptx::pack_bf16x2(__uint_as_float(r[8 * i]), __uint_as_float(r[8 * i + 1])),
+                ptx::pack_bf16x2(__uint_as_float(r[8 * i + 2]), __uint_as_float(r[8 * i + 3])),
+                ptx::pack_bf16x2(__uint_as_float(r[8 * i + 4]), __uint_as_float(r[8 * i + 5])),
+                ptx::pack_bf16x2(__uint_as_float(r[8 * i + 6]), __uint_as_float(r[8 * i + 7])));
+    } else if (direct) {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow * kHD + c0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            dst[i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
+                                 __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
+    } else {
+        float* dst = p.part_o + prow * kHD + c0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ptx::st_global_v8(dst + 8 * i, r + 8 * i);
+    }
+}
+
+// Group x: thread i owns row i of the group's query tile (TMEM lane i).
+template <int NQ>
+__device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t tmem, int x) {
+    using C = Cfg<NQ>;
+    const int lane = threadIdx.x & 31;
+    const int quarter = (threadIdx.x >> 5) & 3;  // TMEM lane quarter this warp may access
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t colS = lane_addr + 128u * x, colO = lane_addr + kColO + 128u * x;
+    const float sl2 = p.scale_log2;
+    const uint64_t sl2p = ptx::f32x2(sl2, sl2);
+    uint32_t jt = 0, jt_other = 0;  // tiles this group and the other got
+    int nx = 0;
+    int kj = 0;  // joined (one-query-tile) units so far
+    const int ui_end = p.cta_first[blockIdx.x + 1];
+    for (int ui = p.cta_first[blockIdx.x]; ui < ui_end; ++ui) {
+        const Unit u = p.units[ui];
+        const Tiles tl(p, u);
+        const bool pair = unit_nq<NQ>(u, p.tpt) == 2;
+        const int tile_tok = pair ? x * p.tpt : 0;
+        const bool row_valid = row < min(p.tpt, u.n_tok - tile_tok) * p.G;
+        const bool active = __any_sync(0xffffffffu, row_valid);
+        const int tok = u.tok_begin + tile_tok + row / p.G;
+        const int row_end = row_valid ? p.tok_pos[tok] + 1 : 0;
+        const int j0 = pair ? 0 : (x - nx) & 1, dj = pair ? 1 : 2;
+        float m_ref = -INFINITY, l_run = 0.f;
+        for (int j = j0; j < tl.n; j += dj, ++jt) {
+            int kt, last, front;
+            tl.tile(j, kt, last, front);
+            const bool f = j < tl.n_first;
+            // (a run of first keys before the range leaves none of them to it)
+            const Seen see{min(row_end, last) - kt, row_end - p.window - kt,
+                           f || tl.n_first == 0 ? p.sinks - kt : 0};
+            const bool full = __all_sync(
+                0xffffffffu, see.lim >= kBN && (see.lo <= 0 || see.sink >= kBN));
+            if (!warp_wait<NQ>(p, sm, sm.gbar(x, SFULL), jt & 1u, 20)) return;
+            ptx::tc_fence_after();
+            float corr = 1.f;
+            if (active) {
+                uint32_t s0[32], s1[32];
+                // the row's maximum: columns 64.. first, 0.. stay in registers
+                load64(colS + 64, s0, s1);
+                if (!full) {
+                    see.mask(s0, 64);
+                    see.mask(s1, 96);
+                }
+                float mx = max32(s1, max32(s0, -INFINITY));
+                load64(colS, s0, s1);
+                if (!full) {
+                    see.mask(s0, 0);
+                    see.mask(s1, 32);
+                }
+                mx = max32(s1, max32(s0, mx)) * sl2;  // scale > 0: max commutes with scaling
+                if (mx > m_ref + kRescaleLog2) {
+                    corr = (m_ref == -INFINITY) ? 0.f : ptx::ex2(m_ref - mx);
+                    m_ref = mx;
+                }
+                const float neg = kLiftLog2 - ((m_ref == -INFINITY) ? 0.f : m_ref);
+                const uint64_t negm = ptx::f32x2(neg, neg);
+                uint64_t l[2] = {0ull, 0ull};
+                exp32(s0, colS, sl2p, negm, l);
+                exp32(s1, colS + 16, sl2p, negm, l);
+                load64(colS + 64, s0, s1);
+                if (!full) {
+                    see.mask(s0, 64);
+                    see.mask(s1, 96);
+                }
+                exp32(s0, colS + 32, sl2p, negm, l);
+                exp32(s1, colS + 48, sl2p, negm, l);
+                const uint64_t sum = ptx::add_f32x2(l[0], l[1]);
+                l_run = l_run * corr + (ptx::lo_f32(sum) + ptx::hi_f32(sum));
+            }
+            // O is rescaled in place: this S was issued after the group's previous
+            // product, so that one has completed.
+            if (j > j0 && __any_sync(0xffffffffu, corr != 1.f)) {
+                uint32_t r[32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    ptx::tmem_ld32(colO + 32 * c, r);
+                    ptx::tmem_ld_wait(r);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * corr);
+                    ptx::tmem_st32(colO + 32 * c, r);
+                }
+            }
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(sm.gbar(x, PFULL));
+        }
+        l_run *= 0.0078125f;  // 2^-7: the lift of P
+        const bool direct = u.part < 0;
+        const int64_t orow = static_cast<int64_t>(tok) * p.H_q + u.kv_head * p.G + row % p.G;
+        const int64_t prow = static_cast<int64_t>(u.part) * (kBM * NQ) + (pair ? kBM * x : 0) + row;
+        float m_out = m_ref, l_out = l_run;
+        if (pair) {
+            jt_other += tl.n;
+            if (!warp_wait<NQ>(p, sm, sm.gbar(x, ODONE), (jt - 1) & 1u, 22)) return;
+            ptx::tc_fence_after();
+            if (active) {
+                const float w = p.o_scale * (direct ? (l_run > 0.f ? 1.f / l_run : 0.f) : 1.f);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t r[32];
+                    __syncwarp();
+                    ptx::tmem_ld32(colO + 32 * c, r);
+                    ptx::tmem_ld_wait(r);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * w);
+                    if (row_valid) store32(p, r, direct, orow, prow, 32 * c);
+                }
+            }
+        } else {
+            // Join the groups: exchange (m, l), then each combines 64 columns.
+            float2* join = reinterpret_cast<float2*>(sm.ptr + C::kSmemJoin) + (kj & 1) * 2 * kBM;
+            join[x * kBM + row] = make_float2(m_ref, l_run);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(sm.gbar(x, JOIN));
+            const int n_other = (tl.n + j0) >> 1;  // tiles of the other parity
+            const int n_mine = tl.n - n_other;
+            jt_other += n_other;
+            if (!warp_wait<NQ>(p, sm, sm.gbar(x ^ 1, JOIN), kj & 1, 23)) return;
+            ++kj;
+            if (n_mine > 0 && !warp_wait<NQ>(p, sm, sm.gbar(x, ODONE), (jt - 1) & 1u, 22)) return;
+            if (n_other > 0 && !warp_wait<NQ>(p, sm, sm.gbar(x ^ 1, ODONE), (jt_other - 1) & 1u, 24))
+                return;
+            ptx::tc_fence_after();
+            nx = (nx + tl.n) & 1;
+            if (active) {
+                const float2 other = join[(x ^ 1) * kBM + row];
+                const float m_a = l_run > 0.f ? m_ref : -INFINITY;
+                const float m_b = other.y > 0.f ? other.x : -INFINITY;
+                m_out = fmaxf(m_a, m_b);
+                float wa = m_a == -INFINITY ? 0.f : ptx::ex2(m_a - m_out);
+                float wb = m_b == -INFINITY ? 0.f : ptx::ex2(m_b - m_out);
+                l_out = wa * l_run + wb * other.y;
+                const float w = p.o_scale * (direct ? (l_out > 0.f ? 1.f / l_out : 0.f) : 1.f);
+                wa *= w;
+                wb *= w;
+                const uint32_t oa = lane_addr + kColO + 128u * x + 64u * x;
+                const uint32_t ob = lane_addr + kColO + 128u * (x ^ 1) + 64u * x;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t a[32], b[32];
+                    __syncwarp();
+                    ptx::tmem_ld32(oa + 32 * c, a);
+                    ptx::tmem_ld32(ob + 32 * c, b);
+                    ptx::tmem_ld_wait(a);
+                    ptx::reg_touch(b);
+                    // a group without a visible key may never have written its O
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        a[i] = __float_as_uint((wa != 0.f ? wa * __uint_as_float(a[i]) : 0.f) +
+                                               (wb != 0.f ? wb * __uint_as_float(b[i]) : 0.f));
+                    if (row_valid) store32(p, a, direct, orow, prow, 64 * x + 32 * c);
+                }
+            }
+        }
+        if (row_valid && (pair || x == 0)) {
+            if (!direct) p.part_ml[prow] = make_float2(m_out, l_out);
+            else if (p.lse) p.lse[orow] = (m_out + __log2f(l_out)) * 0.69314718055994531f;
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(sm.bar(C::BAR_OFREE));
+    }
+}
+
+template <int NQ>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_q4_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ CUtensorMap tm_q) {
+    using C = Cfg<NQ>;
+    extern __shared__ uint8_t smem_raw[];
+    Smem<NQ> sm;
+    {
+        const uint32_t raw = ptx::smem_u32(smem_raw);
+        const uint32_t aligned = (raw + 1023u) & ~1023u;
+        sm.base = aligned;
+        sm.ptr = smem_raw + (aligned - raw);
+    }
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            ptx::mbar_init(sm.bar(C::BAR_FULL + s), kGroupWarps);
+            ptx::mbar_init(sm.bar(C::BAR_EMPTY + s), 1);
+        }
+        for (int s = 0; s < C::kRaw; ++s) {
+            ptx::mbar_init(sm.bar(C::BAR_RFULL + s), 1);
+            ptx::mbar_init(sm.bar(C::BAR_REMPTY + s), kGroupWarps);
+        }
+        for (int x = 0; x < NQ; ++x) {
+            ptx::mbar_init(sm.bar(C::BAR_QFULL + x), 1);
+            ptx::mbar_init(sm.bar(C::BAR_QFREE + x), 1);
+        }
+        ptx::mbar_init(sm.bar(C::BAR_OFREE), 2 * kGroupWarps);
+        ptx::mbar_init(sm.bar(C::BAR_DRAIN), 1);
+        for (int x = 0; x < 2; ++x) {
+            ptx::mbar_init(sm.gbar(x, SFULL), 1);
+            ptx::mbar_init(sm.gbar(x, PFULL), kGroupWarps);
+            ptx::mbar_init(sm.gbar(x, ODONE), 1);
+            ptx::mbar_init(sm.gbar(x, JOIN), kGroupWarps);
+        }
+        *sm.abort_flag() = 0;
+        ptx::fence_barrier_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (warp == 0 && lane == 0) ptx::prefetch_tmap(&tm_q);
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(sm.tmem_slot()), kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *sm.tmem_slot();
+
+    if (warp == 0) {
+        producer_warp<NQ>(p, sm, &tm_q);
+    } else if (warp == 1) {
+        if (lane == 0) mma_thread<NQ>(p, sm, tmem);
+        __syncwarp();
+    } else if (warp < kWarpWiden) {
+        softmax_group<NQ>(p, sm, tmem, (warp - kWarpSoftmax) / kGroupWarps);
+    } else if (warp < kWarpWiden + kGroupWarps) {
+        widen_warp<NQ, false>(p, sm, warp - kWarpWiden);
+    } else {
+        widen_warp<NQ, true>(p, sm, warp - kWarpWiden - kGroupWarps);
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int NQ>
+cudaError_t launch_nq(const SplitParams& p, const CUtensorMap& tm_q, int grid, cudaStream_t stream) {
+    // The shared-memory attribute is set once per device (see attn_fwd.cu).
+    static std::atomic<bool> attr_set[64];
+    static std::mutex attr_mu;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < 64;
+    if (!known || !attr_set[dev].load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> lk(attr_mu);
+        if (!known || !attr_set[dev].load(std::memory_order_relaxed)) {
+            e = cudaFuncSetAttribute(attn_q4_kernel<NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     Cfg<NQ>::kSmemAlloc);
+            if (e != cudaSuccess) return e;
+            if (known) attr_set[dev].store(true, std::memory_order_release);
+        }
+    }
+    attn_q4_kernel<NQ><<<grid, kThreads, Cfg<NQ>::kSmemAlloc, stream>>>(p, tm_q);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attn_q4(const SplitParams& p, const CUtensorMap& /*tm_q*/, int grid,
+cudaError_t launch_attn_q4(const SplitParams& p, const CUtensorMap& tm_q, int grid,
                            cudaStream_t stream) {
-    attn_q4_kernel<<<grid, 32 * kWarps, 0, stream>>>(p);
-    return cudaGetLastError();
+    return p.nq == 2 ? launch_nq<2>(p, tm_q, grid, stream) : launch_nq<1>(p, tm_q, grid, stream);
 }
 
 }  // namespace fanout

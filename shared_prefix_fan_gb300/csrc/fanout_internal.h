@@ -85,10 +85,9 @@ struct SplitParams {
     const int32_t* tok_pos;
     int32_t window, sinks, split_at;
     // 4-bit pools
-    const void* q;
     const uint8_t* k_pool;
     const uint8_t* v_pool;
-    float o_scale;  // V's scale over the power of two its widened values carry
+    float o_scale;  // V's scale
 };
 
 // Paged KV append: per-branch row offsets and current suffix lengths travel in

@@ -198,11 +198,10 @@ int launch_plan(const CallArgs& a, const Plan& pl, const Layout& L, uint8_t* bas
     p.window = a.window > 0 ? a.window : kNoWindow;
     p.sinks = a.sinks;
     p.split_at = pl.split_at;
-    p.q = a.q;
     p.k_pool = static_cast<const uint8_t*>(a.k);
     p.v_pool = static_cast<const uint8_t*>(a.v);
     p.o_scale = a.v_scale;
-    if (a.q4) p.scale_log2 *= a.k_scale;
+    if (a.q4) p.scale_log2 *= a.k_scale * 256.0f;  // the widened K tiles carry 2^-8
     p.wait_limit_ns = a.wait_limit_ns;
     MergeParams& m = p.merge;
     m.part_o = p.part_o;

@@ -94,12 +94,13 @@ def extend(table, P, S, A, page, free, used, n_slots):
 
 def attention(q, k, v, table, P, S, T, page, scale, causal=True, window=0, sinks=0):
     """q [R, H_q, 128], k / v [pages, H_kv, page, 128], all float64. Returns (out,
-    lse, A, E): A = sum p |v| / sum p per output, E = the largest scale * sum
-    |q k| of a visible key per (row, head): what the error bounds scale with."""
+    lse, A, E, V): A = sum p |v| / sum p per output, E = the largest scale * sum
+    |q k| of a visible key per (row, head), V = sum |v| over the visible keys: what
+    the error bounds scale with."""
     R, hq, d = q.shape
     hkv = k.shape[1]
     G = hq // hkv
-    out, A = np.zeros((R, hq, d)), np.zeros((R, hq, d))
+    out, A, V = np.zeros((R, hq, d)), np.zeros((R, hq, d)), np.zeros((R, hq, d))
     lse, E = np.full((R, hq), -np.inf), np.zeros((R, hq))
     r = 0
     for b, (s, t) in enumerate(zip(S, T)):
@@ -122,9 +123,10 @@ def attention(q, k, v, table, P, S, T, page, scale, causal=True, window=0, sinks
                 l = p.sum(-1, keepdims=True)
                 out[r, h * G:(h + 1) * G] = p @ vv / l
                 A[r, h * G:(h + 1) * G] = p @ np.abs(vv) / l
+                V[r, h * G:(h + 1) * G] = np.abs(vv).sum(0)
                 lse[r, h * G:(h + 1) * G] = (m + np.log(l))[:, 0]
             r += 1
-    return out, lse, A, E
+    return out, lse, A, E, V
 
 
 def check_attention(out, lse, ref, p_step, what=""):
@@ -133,14 +135,17 @@ def check_attention(out, lse, ref, p_step, what=""):
       2^-23 * sum |q k| * scale =: e (2^-23: an accumulator may truncate), and its
       scaling, subtraction and ex2 add at most 2^-20 relative to every p while
       |x - m| stays below 64; p and the sum of p each move by that: 2 (e + 2^-20);
-    - p is rounded once to p_step for the product with V, relative to A;
+    - p is rounded once to p_step for the product with V, relative to A; as f16
+      (p_step 2^-11) it carries a factor 2^7 and f16's smallest step is 2^-24, so a
+      small p is off by up to 2^-25 / 2^7 = 2^-32 of the row's reference, where the
+      sum of p is at least 1 (the key that set the reference has p = 1): 2^-32 V;
     - sums of p and of p v, rescales and the merge of partials: 2^-16 covers
       fewer than 128 fp32 additions per tile and a few per merge;
     - the output's own rounding: half a step of its type, relative to it."""
-    o64, l64, A, E = ref
+    o64, l64, A, E, V = ref
     e = 128 * 2.0 ** -23 * E
     rel = 2 * (e + 2.0 ** -20) + p_step + 2.0 ** -16
-    tol = A * rel[..., None]
+    tol = A * rel[..., None] + (2.0 ** -32 * V if p_step == 2.0 ** -11 else 0.0)
     step = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}[out.dtype]
     tol = tol + step * (np.abs(o64) + tol)
     d = np.abs(out.double().cpu().numpy() - o64)

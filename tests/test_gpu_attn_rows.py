@@ -12,7 +12,7 @@ from .gpu_helpers import ensure_lib
 
 pytestmark = pytest.mark.gpu
 # half a step of the type P is rounded to for the product with V
-P_STEP = {False: 2.0 ** -8, True: 2.0 ** -8}
+P_STEP = {False: 2.0 ** -8, True: 2.0 ** -11}
 
 
 @pytest.fixture(scope="module", autouse=True)
