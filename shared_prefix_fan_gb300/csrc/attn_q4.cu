@@ -6,29 +6,34 @@
 // keys, base 2, the reference maximum m raised only when a row's maximum passes
 // it by 2^8); positions, windows and first keys are those of its row plans.
 //
-// The tensor core gets 16-bit tiles that hold the cached values exactly: a code
-// has 2 significant bits, a group scale 4, their product 6.
-//   K: bf16 (q's type), value * 2^-8;    S = Q K^T from shared memory.
-//   V: f16, value * 2^-7;                O += P V with P from TMEM as f16,
-// P = 2^(x - m + 7): at most 2^15, and below 2^-21 of the row's reference its
-// step is 2^-31 of it, so P's rounding is f16's half step of 2^-11 (bf16, as for
-// bf16 pools, would be 2^-8). The powers of two go into the softmax scale and
-// cancel between P and V; pool scales go into the softmax scale and the output.
+// The tensor core gets f16 tiles that hold the cached values exactly: a code has 2
+// significant bits and a group scale 4, their product 6, and it lies between 2^-10
+// and 2688.
+//   S = Q K^T from shared memory, Q as f16 too: its rows are scaled by the power
+//   of two that brings their largest element into [2^14, 2^15) (undone in the
+//   row's softmax scale), so bf16's 8 bits fit f16's 11, and only elements below
+//   2^-28 of the row's largest lose bits;
+//   O += P V with P from TMEM, P = 2^(x - m + 7): at most 2^15, and its rounding is
+//   f16's half step of 2^-11 (bf16's, as for bf16 pools, would be 2^-8); a P below
+//   2^-21 of the row's reference has a step of 2^-31 of it. The 2^7 is taken out
+//   of l and of the output, where V's pool scale goes too (K's: softmax scale).
 //
-// Widening needs no conversion instruction: with a 16-bit float's sign at bit 15
-// and its lowest exponent bits and highest mantissa bit right below (bits 8..6 in
-// bf16, 11..9 in f16), a code's three magnitude bits put there are its value
-// times 2^-126 (2^-14), subnormals included; so are an e4m3 scale's bits, times
-// 2^-120 (2^-8). Two shifts and two logic operations bring a pair of codes there,
-// one packed product applies the scale.
+// Widening is one conversion (a byte of two codes to an f16 pair) and one packed
+// product per two values: both run at 64 lanes a cycle and SM (measured), so a K
+// and a V tile take 256 cycles of either pipe, under the 1024 their four (two for
+// a single query tile) products take on the tensor core. Bit tricks on bf16 tiles
+// instead took 2.5 times the instructions: a prefill step was 2.1 times slower.
+// The codes of a word come out as values 0 2 4 6 1 3 5 7 of its 8; K and Q keep
+// that order (it is summed over), V's columns are put back when O is stored.
 //
-// GB300 mapping, one persistent CTA per SM, 18 warps:
+// GB300 mapping, one persistent CTA per SM, 16 warps:
 //   warp 0      producer: page blocks by cp.async.bulk into a ring of raw tiles
 //               (9 KB: 128 rows of 72 bytes), Q by TMA when its buffer is free;
 //   warp 1      TMEM owner and single-thread tcgen05 issuer;
-//   warps 2-9   two softmax groups of 4 warps, thread = row;
-//   warps 10-17 widen raw tiles into the swizzled 16-bit ring (4 warps the K
-//               tiles, 4 the V tiles), rows that no row of the unit sees as zeros.
+//   warps 2-3   turn Q tiles into scaled f16, in place;
+//   warps 4-11  two softmax groups of 4 warps, thread = row;
+//   warps 12-15 widen raw tiles into the swizzled f16 ring, rows that no row of
+//               the unit sees as zeros.
 // A unit of two query tiles gives each group one of them. A unit of one query
 // tile (decode) is split over the groups by keys instead: tile t goes to group
 // t mod 2, each with its own S, (m, l) and O in TMEM, and the two are joined at
@@ -55,9 +60,12 @@ constexpr float kRescaleLog2 = 8.0f;  // lazy rescale threshold (base-2 units)
 constexpr float kLiftLog2 = 7.0f;     // P is 2^7 times the probability's numerator
 constexpr int kErrTimeout = 5;        // FANOUT_ETIMEOUT
 constexpr int kGroupWarps = 4;
-constexpr int kWarpSoftmax = 2;   // first softmax warp
-constexpr int kWarpWiden = 10;    // first widening warp
-constexpr int kThreads = 32 * 18;
+constexpr int kWarpQ = 2;        // first warp of the Q conversion
+constexpr int kQWarps = 2;
+constexpr int kWarpSoftmax = 4;  // first softmax warp
+constexpr int kWarpWiden = 12;   // first widening warp
+constexpr int kThreads = 32 * 16;
+constexpr int kFacBufs = 4;      // units whose row factors are held
 
 template <int NQ>
 struct Cfg {
@@ -73,13 +81,15 @@ struct Cfg {
     static constexpr int BAR_REMPTY = BAR_RFULL + kRaw;
     static constexpr int BAR_QFULL = BAR_REMPTY + kRaw;  // + x
     static constexpr int BAR_QFREE = BAR_QFULL + NQ;     // + x
-    static constexpr int BAR_OFREE = BAR_QFREE + NQ;
+    static constexpr int BAR_QREADY = BAR_QFREE + NQ;    // + x
+    static constexpr int BAR_OFREE = BAR_QREADY + NQ;
     static constexpr int BAR_DRAIN = BAR_OFREE + 1;
     static constexpr int BAR_GROUP = BAR_DRAIN + 1;  // + 4 x + {SFULL, PFULL, ODONE, JOIN}
     static constexpr int kNumBars = BAR_GROUP + 8;
     static constexpr int kSmemMisc = kSmemBar + kNumBars * 8;
     static constexpr int kSmemJoin = (kSmemMisc + 16 + 15) & ~15;  // float2 [2][2][128]
-    static constexpr int kSmemTotal = kSmemJoin + 2 * 2 * kBM * 8;
+    static constexpr int kSmemFac = kSmemJoin + 2 * 2 * kBM * 8;  // uint8 [kFacBufs][NQ][128]
+    static constexpr int kSmemTotal = kSmemFac + kFacBufs * NQ * kBM;
     static constexpr int kSmemAlloc = kSmemTotal + 1024;  // base aligned up to 1024 B
     static_assert(kSmemAlloc <= 232448, "shared memory per CTA");
     static_assert(kSmemBar % 16 == 0 && kSmemRaw % 128 == 0, "shared-memory alignment");
@@ -88,7 +98,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;
 enum { SFULL = 0, PFULL = 1, ODONE = 2, JOIN = 3 };
 
-constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(kBM, kBN, false, false);
+constexpr uint32_t kIdescQK = ptx::idesc_f16_f32(kBM, kBN, false, false);
 constexpr uint32_t kIdescPV = ptx::idesc_f16_f32(kBM, kHD, false, true);
 
 template <int NQ>
@@ -104,6 +114,11 @@ struct Smem {
     }
     __device__ uint32_t tile(uint32_t pos) const {
         return base + C::kSmemRing + (pos % C::kStages) * kTileBytes;
+    }
+    // Exponent of the power of two that row `row` of the n-th load of Q buffer x
+    // was multiplied with, plus 127 (a byte).
+    __device__ uint8_t* fac(uint32_t n, int x, int row) const {
+        return ptr + C::kSmemFac + ((n % kFacBufs) * NQ + x) * kBM + row;
     }
 };
 
@@ -280,77 +295,121 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ>& sm, const CU
     }
 }
 
-// ------------------------------------------------------------------ widening
-// Four pairs of neighbouring values of a code word, as 16-bit floats without
-// their scale: sign to bit 15 and magnitude bits to kMag's place of each half.
-template <bool IS_V>
-__device__ __forceinline__ void widen_word(uint32_t w, uint32_t scale, uint32_t (&out)[4]) {
-    constexpr uint32_t kSign = 0x80008000u;
-    constexpr uint32_t kMag = IS_V ? 0x0E000E00u : 0x01C001C0u;
-    constexpr int kUp = IS_V ? 9 : 6;  // left shift of code 0's magnitude
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int sh = kUp - 4 * j;
-        const uint32_t mag = sh >= 0 ? w << sh : w >> -sh;
-        out[j] = ((w << (12 - 4 * j)) & kSign) | (mag & kMag);
-        out[j] = IS_V ? ptx::mul_f16x2(out[j], scale) : ptx::mul_bf16x2(out[j], scale);
+// ------------------------------------------------------------------ Q to f16
+// Two warps turn the rows of a loaded Q tile into f16 in place: a thread finds its
+// row's largest exponent, scales by a power of two and stores the 8 values of each
+// 16-byte piece in the order the widened K tiles have. Rows behind the unit's last
+// are left as they are (their scores are never used).
+template <int NQ>
+__device__ void q_warp(const SplitParams& p, const Smem<NQ>& sm, int w) {
+    using C = Cfg<NQ>;
+    const int lane = threadIdx.x & 31;
+    uint32_t loads[2] = {0, 0};
+    const int ui_end = p.cta_first[blockIdx.x + 1];
+    for (int ui = p.cta_first[blockIdx.x]; ui < ui_end; ++ui) {
+        const Unit u = p.units[ui];
+        const int nq = unit_nq<NQ>(u, p.tpt);
+        for (int x = 0; x < nq; ++x) {
+            const uint32_t n = x == 0 ? loads[0]++ : loads[1]++;
+            if (!warp_wait<NQ>(p, sm, sm.bar(C::BAR_QFULL + x), n & 1u, 50)) return;
+            const int rows = min(p.tpt, u.n_tok - x * p.tpt) * p.G;
+            for (int row = w * 32 + lane; row < rows; row += 32 * kQWarps) {
+                const uint32_t at = sm.base + C::kSmemQ + x * kQBytes + row * 128;
+                const uint32_t swz = static_cast<uint32_t>(row & 7) << 4;
+                uint32_t top = 0;
+#pragma unroll 4
+                for (int c = 0; c < 16; ++c) {
+                    const uint4 v = ptx::ld_shared_v4(at + (c >> 3) * kHalfBytes + (((c & 7) << 4) ^ swz));
+                    top = ptx::max_abs_bf16x2(ptx::max_abs_bf16x2(top, v.x), v.y);
+                    top = ptx::max_abs_bf16x2(ptx::max_abs_bf16x2(top, v.z), v.w);
+                }
+                const int e = max((top >> 7) & 0xff, (top >> 23) & 0xff);
+                // largest element to [2^14, 2^15); infinities stay, tiny rows at most 2^100
+                const int k = e == 255 ? 0 : min(141 - e, 100);
+                const float f = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+#pragma unroll 2
+                for (int c = 0; c < 16; ++c) {
+                    const uint32_t a = at + (c >> 3) * kHalfBytes + (((c & 7) << 4) ^ swz);
+                    const uint4 v = ptx::ld_shared_v4(a);
+                    auto lo = [f](uint32_t b) { return __uint_as_float(b << 16) * f; };
+                    auto hi = [f](uint32_t b) { return __uint_as_float(b & 0xffff0000u) * f; };
+                    ptx::st_shared_v4(a, ptx::pack_f16x2(lo(v.x), lo(v.y)),
+                                      ptx::pack_f16x2(lo(v.z), lo(v.w)),
+                                      ptx::pack_f16x2(hi(v.x), hi(v.y)),
+                                      ptx::pack_f16x2(hi(v.z), hi(v.w)));
+                }
+                *sm.fac(n, x, row) = static_cast<uint8_t>(k + 127);
+            }
+            ptx::fence_proxy_async_smem();  // the MMAs read the tile
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(sm.bar(C::BAR_QREADY + x));
+        }
     }
 }
-// A group's scale (e4m3 byte) in both halves: K: times 2^118 (the codes carry
-// 2^-126, the tile 2^-8), in two exact products; V: times 2^7 (2^-14, 2^-7).
-template <bool IS_V>
-__device__ __forceinline__ uint32_t widen_scale(uint32_t byte) {
-    if (IS_V) return ptx::mul_f16x2(((byte & 0x7fu) << 7) * 0x00010001u, 0x78007800u);
-    const uint32_t s = ((byte & 0x7fu) << 4) * 0x00010001u;
-    return ptx::mul_bf16x2(ptx::mul_bf16x2(s, 0x7F007F00u), 0x77007700u);
+
+// ------------------------------------------------------------------ widening
+// Eight codes to eight f16 values (0 2 4 6 1 3 5 7) times their group's scale.
+__device__ __forceinline__ void widen_word(uint32_t w, uint32_t scale, uint32_t (&o)[4]) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = ptx::mul_f16x2(o[i], scale);
 }
 
-// Four warps widen every K (or V) tile. A lane takes 16 bytes of codes (32
+// Four warps widen every tile, 32 rows each. A lane takes 16 bytes of codes (32
 // values, two groups) of a row: 8 rows per step and warp, loads without bank
 // conflicts; lanes of the upper 64 columns store their words in the order 2, 3,
 // 0, 1, so that the 8 lanes of a store phase cover all 8 sixteen-byte columns.
-template <int NQ, bool IS_V>
+template <int NQ>
 __device__ void widen_warp(const SplitParams& p, const Smem<NQ>& sm, int w) {
     using C = Cfg<NQ>;
     const int lane = threadIdx.x & 31;
     const int ps = p.page_size, ps_shift = 31 - __clz(ps), piece = lane & 3;
     const bool upper = piece >= 2;
-    uint32_t it = IS_V ? 1u : 0u;  // ring position of this warp's next tile
+    const int row0 = w * 32 + (lane >> 2);
+    // byte of the first (second) stored pair of words' scale in the two loaded
+    const uint32_t sel0 = upper ? 0x3232u : 0x1010u, sel1 = upper ? 0x1010u : 0x3232u;
+    uint32_t it = 0;  // ring position of the next tile
     const int ui_end = p.cta_first[blockIdx.x + 1];
     for (int ui = p.cta_first[blockIdx.x]; ui < ui_end; ++ui) {
         const Unit u = p.units[ui];
         const Tiles tl(p, u);
-        for (int j = 0; j < tl.n; ++j, it += 2) {
+        for (int j2 = 0; j2 < 2 * tl.n; ++j2, ++it) {  // K, then V of each tile
             int kt, last, front;
-            tl.tile(j, kt, last, front);
+            tl.tile(j2 >> 1, kt, last, front);
             const uint32_t rs = it % C::kRaw, stage = it % C::kStages;
             if (!warp_wait<NQ>(p, sm, sm.bar(C::BAR_RFULL + rs), (it / C::kRaw) & 1u, 40)) return;
             if (!warp_wait<NQ>(p, sm, sm.bar(C::BAR_EMPTY + stage), ((it / C::kStages) & 1u) ^ 1u, 41))
                 return;
             const uint32_t raw = sm.base + C::kSmemRaw + rs * kRawBytes;
             const uint32_t dst = sm.tile(it) + (piece >> 1) * kHalfBytes;
-#pragma unroll
+#pragma unroll 2
             for (int i = 0; i < 4; ++i) {
-                const int r = w * 32 + i * 8 + (lane >> 2);
-                const bool seen = r >= front && kt + r < last;
+                const int r = row0 + i * 8;
                 uint4 c = make_uint4(0u, 0u, 0u, 0u);
                 uint32_t sc = 0;
-                if (seen) {
+                if (r >= front && kt + r < last) {
                     const int pg = r >> ps_shift, slot = r & (ps - 1);
-                    const uint32_t at = raw + pg * ps * kQ4RowBytes;
+                    const uint32_t at = raw + (pg << ps_shift) * kQ4RowBytes;
                     c = ptx::ld_shared_v4(at + slot * 64 + piece * 16);
-                    sc = ptx::ld_shared_u16(at + ps * 64 + slot * 8 + piece * 2);
+                    sc = ptx::f16x2_of_e4m3x2(ptx::ld_shared_u16(at + ps * 64 + slot * 8 + piece * 2));
                 }
-                const uint32_t s0 = widen_scale<IS_V>(upper ? sc >> 8 : sc);
-                const uint32_t s1 = widen_scale<IS_V>(upper ? sc : sc >> 8);
+                const uint32_t s0 = __byte_perm(sc, 0u, sel0), s1 = __byte_perm(sc, 0u, sel1);
                 const uint32_t word[4] = {upper ? c.z : c.x, upper ? c.w : c.y, upper ? c.x : c.z,
                                           upper ? c.y : c.w};
                 const uint32_t row = dst + r * 128;
-                const uint32_t col = static_cast<uint32_t>(((piece & 1) * 4) ^ (upper ? 2 : 0) ^ (r & 7)) << 4;
+                const uint32_t col =
+                    static_cast<uint32_t>(((piece & 1) * 4) ^ (upper ? 2 : 0) ^ (r & 7)) << 4;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint32_t o[4];
-                    widen_word<IS_V>(word[k], k < 2 ? s0 : s1, o);
+                    widen_word(word[k], k < 2 ? s0 : s1, o);
                     ptx::st_shared_v4(row + (col ^ (k << 4)), o[0], o[1], o[2], o[3]);
                 }
             }
@@ -455,8 +514,8 @@ __device__ void mma_thread(const SplitParams& p, const Smem<NQ>& sm, uint32_t tm
         const int n = Tiles(p, u).n;
         if (unit_nq<NQ>(u, p.tpt) == 2) {
             if (!(ok = is.issue_held(pend, held))) break;
-            if (!(ok = is.wait(sm.bar(C::BAR_QFULL), qu[0] & 1u, 10) &&
-                       is.wait(sm.bar(C::BAR_QFULL + NQ - 1), qu[1] & 1u, 10)))
+            if (!(ok = is.wait(sm.bar(C::BAR_QREADY), qu[0] & 1u, 10) &&
+                       is.wait(sm.bar(C::BAR_QREADY + NQ - 1), qu[1] & 1u, 10)))
                 break;
             for (int j = 0; j <= n && ok; ++j) {
                 const uint32_t posK = pos + 2u * j, posV = posK + 1u, posVp = posK - 1u;
@@ -483,14 +542,14 @@ __device__ void mma_thread(const SplitParams& p, const Smem<NQ>& sm, uint32_t tm
             ++qu[0];
             ++qu[1];
         } else {
-            if (held && !ptx::mbar_test_wait(sm.bar(C::BAR_QFULL), qu[0] & 1u) &&
+            if (held && !ptx::mbar_test_wait(sm.bar(C::BAR_QREADY), qu[0] & 1u) &&
                 !(ok = is.issue_held(pend, held)))
                 break;
             for (int j = 0; j < n && ok; ++j) {
                 const uint32_t posK = pos + 2u * j;
                 const int x = (nx + j) & 1;
                 if (!(ok = is.wait_full(posK, 11))) break;
-                if (j == 0 && !(ok = is.wait(sm.bar(C::BAR_QFULL), qu[0] & 1u, 10))) break;
+                if (j == 0 && !(ok = is.wait(sm.bar(C::BAR_QREADY), qu[0] & 1u, 10))) break;
                 is.issue_s(x, 0, posK);
                 is.release(posK);
                 if (j == n - 1) ptx::mma_commit(sm.bar(C::BAR_QFREE));
@@ -520,15 +579,23 @@ __device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&a)[32], uint32
     ptx::reg_touch(b);
 }
 
-// What of a tile a row sees: columns below lim, and not [sink, lo).
-struct Seen {
-    int lim, lo, sink;
-    __device__ __forceinline__ void mask(uint32_t (&s)[32], int c0) const {
+// Scores a row does not see become -inf in TMEM (tiles at a mask's border only,
+// so that the common path carries no masks): it sees columns below lim, and not
+// [sink, lo).
+__device__ __forceinline__ void mask_tile(uint32_t taddr, int lim, int lo, int sink) {
+    uint32_t s[32];
+#pragma unroll 1
+    for (int c0 = 0; c0 < kBN; c0 += 32) {
+        __syncwarp();
+        ptx::tmem_ld32(taddr + c0, s);
+        ptx::tmem_ld_wait(s);
 #pragma unroll
         for (int c = 0; c < 32; ++c)
             if (c0 + c >= lim || (c0 + c < lo && c0 + c >= sink)) s[c] = __float_as_uint(-INFINITY);
+        ptx::tmem_st32(taddr + c0, s);
     }
-};
+    ptx::tmem_st_wait();
+}
 
 __device__ __forceinline__ float max32(const uint32_t (&s)[32], float m) {
     float a = m, b = __uint_as_float(s[1]);
@@ -555,28 +622,37 @@ __device__ __forceinline__ void exp32(const uint32_t (&s)[32], uint32_t taddr, u
     ptx::tmem_st16(taddr, packed);
 }
 
-// 32 columns of a finished row: to out (direct) or to its partial block.
+// 32 columns of a finished row, put back into their order (each 8 hold values 0 2
+// 4 6 1 3 5 7): to out (direct) or to its partial block.
 __device__ __forceinline__ void store32(const SplitParams& p, const uint32_t (&r)[32], bool direct,
                                         int64_t orow, int64_t prow, int c0) {
+    auto at = [](int d) { return (d & ~7) + (d & 1) * 4 + ((d & 7) >> 1); };
     if (direct && p.out_bf16) {
         uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * kHD + c0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            dst[i] = make_uint4(
-                ptx::pack_bf16x2(__uint_as_float(r[8 * i]), __uint_as_float(r[8 * i + 1])),
-                ptx::pack_bf16x2(__uint_as_float(r[8 * i + 2]), __uint_as_float(r[8 * i + 3])),
-                ptx::pack_bf16x2(__uint_as_float(r[8 * i + 4]), __uint_as_float(r[8 * i + 5])),
-                ptx::pack_bf16x2(__uint_as_float(r[8 * i + 6]), __uint_as_float(r[8 * i + 7])));
+        for (int i = 0; i < 4; ++i) {
+            uint32_t v[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                v[h] = ptx::pack_bf16x2(__uint_as_float(r[at(8 * i + 2 * h)]),
+                                        __uint_as_float(r[at(8 * i + 2 * h + 1)]));
+            dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
+        }
     } else if (direct) {
         float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow * kHD + c0);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
-                                 __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
+            dst[i] = make_float4(__uint_as_float(r[at(4 * i)]), __uint_as_float(r[at(4 * i + 1)]),
+                                 __uint_as_float(r[at(4 * i + 2)]), __uint_as_float(r[at(4 * i + 3)]));
     } else {
         float* dst = p.part_o + prow * kHD + c0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ptx::st_global_v8(dst + 8 * i, r + 8 * i);
+        for (int i = 0; i < 4; ++i) {
+            uint32_t v[8];
+#pragma unroll
+            for (int h = 0; h < 8; ++h) v[h] = r[at(8 * i + h)];
+            ptx::st_global_v8(dst + 8 * i, v);
+        }
     }
 }
 
@@ -589,8 +665,7 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
     const int row = quarter * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t colS = lane_addr + 128u * x, colO = lane_addr + kColO + 128u * x;
-    const float sl2 = p.scale_log2;
-    const uint64_t sl2p = ptx::f32x2(sl2, sl2);
+    uint32_t n_load[2] = {0, 0};  // loads of each Q buffer before this unit
     uint32_t jt = 0, jt_other = 0;  // tiles this group and the other got
     int nx = 0;
     int kj = 0;  // joined (one-query-tile) units so far
@@ -606,32 +681,38 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
         const int row_end = row_valid ? p.tok_pos[tok] + 1 : 0;
         const int j0 = pair ? 0 : (x - nx) & 1, dj = pair ? 1 : 2;
         float m_ref = -INFINITY, l_run = 0.f;
+        // the softmax scale, with the power of two that the row of Q carries
+        const int xq = pair ? x : 0;
+        const uint32_t load = xq == 0 ? n_load[0] : n_load[1];
+        ++n_load[0];
+        if (pair) ++n_load[1];
+        float sl2 = p.scale_log2;
+        if (j0 < tl.n) {
+            if (!warp_wait<NQ>(p, sm, sm.bar(C::BAR_QREADY + xq * (NQ - 1)), load & 1u, 25)) return;
+            if (row_valid) {
+                const int k = static_cast<int>(*sm.fac(load, xq, row)) - 127;
+                sl2 *= __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+            }
+        }
+        const uint64_t sl2p = ptx::f32x2(sl2, sl2);
         for (int j = j0; j < tl.n; j += dj, ++jt) {
             int kt, last, front;
             tl.tile(j, kt, last, front);
             const bool f = j < tl.n_first;
             // (a run of first keys before the range leaves none of them to it)
-            const Seen see{min(row_end, last) - kt, row_end - p.window - kt,
-                           f || tl.n_first == 0 ? p.sinks - kt : 0};
-            const bool full = __all_sync(
-                0xffffffffu, see.lim >= kBN && (see.lo <= 0 || see.sink >= kBN));
+            const int lim = min(row_end, last) - kt, lo = row_end - p.window - kt;
+            const int sink = f || tl.n_first == 0 ? p.sinks - kt : 0;
+            const bool full = __all_sync(0xffffffffu, lim >= kBN && (lo <= 0 || sink >= kBN));
             if (!warp_wait<NQ>(p, sm, sm.gbar(x, SFULL), jt & 1u, 20)) return;
             ptx::tc_fence_after();
             float corr = 1.f;
             if (active) {
                 uint32_t s0[32], s1[32];
                 // the row's maximum: columns 64.. first, 0.. stay in registers
+                if (!full) mask_tile(colS, lim, lo, sink);
                 load64(colS + 64, s0, s1);
-                if (!full) {
-                    see.mask(s0, 64);
-                    see.mask(s1, 96);
-                }
                 float mx = max32(s1, max32(s0, -INFINITY));
                 load64(colS, s0, s1);
-                if (!full) {
-                    see.mask(s0, 0);
-                    see.mask(s1, 32);
-                }
                 mx = max32(s1, max32(s0, mx)) * sl2;  // scale > 0: max commutes with scaling
                 if (mx > m_ref + kRescaleLog2) {
                     corr = (m_ref == -INFINITY) ? 0.f : ptx::ex2(m_ref - mx);
@@ -643,10 +724,6 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
                 exp32(s0, colS, sl2p, negm, l);
                 exp32(s1, colS + 16, sl2p, negm, l);
                 load64(colS + 64, s0, s1);
-                if (!full) {
-                    see.mask(s0, 64);
-                    see.mask(s1, 96);
-                }
                 exp32(s0, colS + 32, sl2p, negm, l);
                 exp32(s1, colS + 48, sl2p, negm, l);
                 const uint64_t sum = ptx::add_f32x2(l[0], l[1]);
@@ -656,8 +733,9 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
             // product, so that one has completed.
             if (j > j0 && __any_sync(0xffffffffu, corr != 1.f)) {
                 uint32_t r[32];
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
+                    __syncwarp();
                     ptx::tmem_ld32(colO + 32 * c, r);
                     ptx::tmem_ld_wait(r);
 #pragma unroll
@@ -680,8 +758,8 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
             if (!warp_wait<NQ>(p, sm, sm.gbar(x, ODONE), (jt - 1) & 1u, 22)) return;
             ptx::tc_fence_after();
             if (active) {
-                const float w = p.o_scale * (direct ? (l_run > 0.f ? 1.f / l_run : 0.f) : 1.f);
-#pragma unroll
+                const float w = p.o_scale * 0.0078125f * (direct ? (l_run > 0.f ? 1.f / l_run : 0.f) : 1.f);
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t r[32];
                     __syncwarp();
@@ -716,12 +794,12 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
                 float wa = m_a == -INFINITY ? 0.f : ptx::ex2(m_a - m_out);
                 float wb = m_b == -INFINITY ? 0.f : ptx::ex2(m_b - m_out);
                 l_out = wa * l_run + wb * other.y;
-                const float w = p.o_scale * (direct ? (l_out > 0.f ? 1.f / l_out : 0.f) : 1.f);
+                const float w = p.o_scale * 0.0078125f * (direct ? (l_out > 0.f ? 1.f / l_out : 0.f) : 1.f);
                 wa *= w;
                 wb *= w;
                 const uint32_t oa = lane_addr + kColO + 128u * x + 64u * x;
                 const uint32_t ob = lane_addr + kColO + 128u * (x ^ 1) + 64u * x;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 2; ++c) {
                     uint32_t a[32], b[32];
                     __syncwarp();
@@ -774,6 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < NQ; ++x) {
             ptx::mbar_init(sm.bar(C::BAR_QFULL + x), 1);
             ptx::mbar_init(sm.bar(C::BAR_QFREE + x), 1);
+            ptx::mbar_init(sm.bar(C::BAR_QREADY + x), kQWarps);
         }
         ptx::mbar_init(sm.bar(C::BAR_OFREE), 2 * kGroupWarps);
         ptx::mbar_init(sm.bar(C::BAR_DRAIN), 1);
@@ -802,12 +881,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         if (lane == 0) mma_thread<NQ>(p, sm, tmem);
         __syncwarp();
+    } else if (warp < kWarpSoftmax) {
+        q_warp<NQ>(p, sm, warp - kWarpQ);
     } else if (warp < kWarpWiden) {
         softmax_group<NQ>(p, sm, tmem, (warp - kWarpSoftmax) / kGroupWarps);
-    } else if (warp < kWarpWiden + kGroupWarps) {
-        widen_warp<NQ, false>(p, sm, warp - kWarpWiden);
     } else {
-        widen_warp<NQ, true>(p, sm, warp - kWarpWiden - kGroupWarps);
+        widen_warp<NQ>(p, sm, warp - kWarpWiden);
     }
 
     ptx::tc_fence_before();

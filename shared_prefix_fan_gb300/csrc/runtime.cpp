@@ -201,7 +201,7 @@ int launch_plan(const CallArgs& a, const Plan& pl, const Layout& L, uint8_t* bas
     p.k_pool = static_cast<const uint8_t*>(a.k);
     p.v_pool = static_cast<const uint8_t*>(a.v);
     p.o_scale = a.v_scale;
-    if (a.q4) p.scale_log2 *= a.k_scale * 256.0f;  // the widened K tiles carry 2^-8
+    if (a.q4) p.scale_log2 *= a.k_scale;
     p.wait_limit_ns = a.wait_limit_ns;
     MergeParams& m = p.merge;
     m.part_o = p.part_o;
