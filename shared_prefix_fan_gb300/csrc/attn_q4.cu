@@ -26,14 +26,16 @@
 // The codes of a word come out as values 0 2 4 6 1 3 5 7 of its 8; K and Q keep
 // that order (it is summed over), V's columns are put back when O is stored.
 //
-// GB300 mapping, one persistent CTA per SM, 16 warps:
+// GB300 mapping, one persistent CTA per SM, 20 warps:
 //   warp 0      producer: page blocks by cp.async.bulk into a ring of raw tiles
 //               (9 KB: 128 rows of 72 bytes), Q by TMA when its buffer is free;
 //   warp 1      TMEM owner and single-thread tcgen05 issuer;
 //   warps 2-3   turn Q tiles into scaled f16, in place;
 //   warps 4-11  two softmax groups of 4 warps, thread = row;
-//   warps 12-15 widen raw tiles into the swizzled f16 ring, rows that no row of
-//               the unit sees as zeros.
+//   warps 12-19 widen raw tiles into the swizzled f16 ring (4 warps the K tiles, 4
+//               the V tiles), rows that no row of the unit sees as zeros. With 4
+//               warps for both, a decode step waited for them: 35 us, not 15.
+// Registers (launched with 96 a thread): softmax warps 136, widening 56.
 // A unit of two query tiles gives each group one of them. A unit of one query
 // tile (decode) is split over the groups by keys instead: tile t goes to group
 // t mod 2, each with its own S, (m, l) and O in TMEM, and the two are joined at
@@ -64,13 +66,21 @@ constexpr int kWarpQ = 2;        // first warp of the Q conversion
 constexpr int kQWarps = 2;
 constexpr int kWarpSoftmax = 4;  // first softmax warp
 constexpr int kWarpWiden = 12;   // first widening warp
-constexpr int kThreads = 32 * 16;
+constexpr int kThreads = 32 * 20;
+// 96 * 640 = 61440 registers at launch >= 136 * 256 + 56 * 256 + 96 * 128
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 136, kRegsWiden = 56;
+static_assert(kRegsSoftmax * 256 + kRegsWiden * 256 + kRegsLaunch * 128 <= kRegsLaunch * kThreads,
+              "register split");
 constexpr int kFacBufs = 4;      // units whose row factors are held
 
 template <int NQ>
 struct Cfg {
     static constexpr int kStages = 4;            // widened tiles
-    static constexpr int kRaw = NQ == 1 ? 6 : 3;  // raw tiles
+    static constexpr int kRaw = NQ == 1 ? 6 : 2;  // raw tiles
+    // K tiles take the even and V tiles the odd ring positions, and the warps that
+    // widen one kind wait for its stages only: with an odd ring a stage would change
+    // kind, and a warp could take the phase before last of its barrier for the last.
+    static_assert(kStages % 2 == 0 && kRaw % 2 == 0, "rings of K/V pairs");
     static constexpr int kSmemQ = 0;
     static constexpr int kSmemRing = NQ * kQBytes;
     static constexpr int kSmemRaw = kSmemRing + kStages * kTileBytes;
@@ -84,8 +94,8 @@ struct Cfg {
     static constexpr int BAR_QREADY = BAR_QFREE + NQ;    // + x
     static constexpr int BAR_OFREE = BAR_QREADY + NQ;
     static constexpr int BAR_DRAIN = BAR_OFREE + 1;
-    static constexpr int BAR_GROUP = BAR_DRAIN + 1;  // + 4 x + {SFULL, PFULL, ODONE, JOIN}
-    static constexpr int kNumBars = BAR_GROUP + 8;
+    static constexpr int BAR_GROUP = BAR_DRAIN + 1;  // + 5 x + {SFULL, PFULL, ODONE, JOIN, JOIN + 1}
+    static constexpr int kNumBars = BAR_GROUP + 10;
     static constexpr int kSmemMisc = kSmemBar + kNumBars * 8;
     static constexpr int kSmemJoin = (kSmemMisc + 16 + 15) & ~15;  // float2 [2][2][128]
     static constexpr int kSmemFac = kSmemJoin + 2 * 2 * kBM * 8;  // uint8 [kFacBufs][NQ][128]
@@ -107,7 +117,7 @@ struct Smem {
     uint32_t base;  // shared-window address of the 1024-aligned base
     uint8_t* ptr;   // generic pointer to the same place
     __device__ uint32_t bar(int i) const { return base + C::kSmemBar + 8u * i; }
-    __device__ uint32_t gbar(int x, int which) const { return bar(C::BAR_GROUP + 4 * x + which); }
+    __device__ uint32_t gbar(int x, int which) const { return bar(C::BAR_GROUP + 5 * x + which); }
     __device__ uint32_t* tmem_slot() const { return reinterpret_cast<uint32_t*>(ptr + C::kSmemMisc); }
     __device__ volatile int* abort_flag() const {
         return reinterpret_cast<volatile int*>(ptr + C::kSmemMisc + 4);
@@ -316,28 +326,33 @@ __device__ void q_warp(const SplitParams& p, const Smem<NQ>& sm, int w) {
             for (int row = w * 32 + lane; row < rows; row += 32 * kQWarps) {
                 const uint32_t at = sm.base + C::kSmemQ + x * kQBytes + row * 128;
                 const uint32_t swz = static_cast<uint32_t>(row & 7) << 4;
-                uint32_t top = 0;
-#pragma unroll 4
+                uint4 v[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    v[c] = ptx::ld_shared_v4(at + (c >> 3) * kHalfBytes + (((c & 7) << 4) ^ swz));
+                uint32_t top[4] = {0, 0, 0, 0};
+#pragma unroll
                 for (int c = 0; c < 16; ++c) {
-                    const uint4 v = ptx::ld_shared_v4(at + (c >> 3) * kHalfBytes + (((c & 7) << 4) ^ swz));
-                    top = ptx::max_abs_bf16x2(ptx::max_abs_bf16x2(top, v.x), v.y);
-                    top = ptx::max_abs_bf16x2(ptx::max_abs_bf16x2(top, v.z), v.w);
+                    top[0] = ptx::max_abs_bf16x2(top[0], v[c].x);
+                    top[1] = ptx::max_abs_bf16x2(top[1], v[c].y);
+                    top[2] = ptx::max_abs_bf16x2(top[2], v[c].z);
+                    top[3] = ptx::max_abs_bf16x2(top[3], v[c].w);
                 }
-                const int e = max((top >> 7) & 0xff, (top >> 23) & 0xff);
+                const uint32_t t = ptx::max_abs_bf16x2(ptx::max_abs_bf16x2(top[0], top[1]),
+                                                       ptx::max_abs_bf16x2(top[2], top[3]));
+                const int e = max((t >> 7) & 0xff, (t >> 23) & 0xff);
                 // largest element to [2^14, 2^15); infinities stay, tiny rows at most 2^100
                 const int k = e == 255 ? 0 : min(141 - e, 100);
                 const float f = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-#pragma unroll 2
-                for (int c = 0; c < 16; ++c) {
-                    const uint32_t a = at + (c >> 3) * kHalfBytes + (((c & 7) << 4) ^ swz);
-                    const uint4 v = ptx::ld_shared_v4(a);
-                    auto lo = [f](uint32_t b) { return __uint_as_float(b << 16) * f; };
-                    auto hi = [f](uint32_t b) { return __uint_as_float(b & 0xffff0000u) * f; };
-                    ptx::st_shared_v4(a, ptx::pack_f16x2(lo(v.x), lo(v.y)),
-                                      ptx::pack_f16x2(lo(v.z), lo(v.w)),
-                                      ptx::pack_f16x2(hi(v.x), hi(v.y)),
-                                      ptx::pack_f16x2(hi(v.z), hi(v.w)));
-                }
+                auto lo = [f](uint32_t b) { return __uint_as_float(b << 16) * f; };
+                auto hi = [f](uint32_t b) { return __uint_as_float(b & 0xffff0000u) * f; };
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    ptx::st_shared_v4(at + (c >> 3) * kHalfBytes + (((c & 7) << 4) ^ swz),
+                                      ptx::pack_f16x2(lo(v[c].x), lo(v[c].y)),
+                                      ptx::pack_f16x2(lo(v[c].z), lo(v[c].w)),
+                                      ptx::pack_f16x2(hi(v[c].x), hi(v[c].y)),
+                                      ptx::pack_f16x2(hi(v[c].z), hi(v[c].w)));
                 *sm.fac(n, x, row) = static_cast<uint8_t>(k + 127);
             }
             ptx::fence_proxy_async_smem();  // the MMAs read the tile
@@ -362,63 +377,73 @@ __device__ __forceinline__ void widen_word(uint32_t w, uint32_t scale, uint32_t 
     for (int i = 0; i < 4; ++i) o[i] = ptx::mul_f16x2(o[i], scale);
 }
 
-// Four warps widen every tile, 32 rows each. A lane takes 16 bytes of codes (32
-// values, two groups) of a row: 8 rows per step and warp, loads without bank
-// conflicts; lanes of the upper 64 columns store their words in the order 2, 3,
-// 0, 1, so that the 8 lanes of a store phase cover all 8 sixteen-byte columns.
+// Four warps widen every K (V) tile, 32 rows each. A lane takes 16 bytes of codes
+// (32 values, two groups) of a row, 4 rows in all, loaded before any is widened;
+// loads are without bank conflicts, and lanes of the upper 64 columns store their
+// words in the order 2, 3, 0, 1, so that the 8 lanes of a store phase cover all 8
+// sixteen-byte columns. A row that no row of the unit sees gets scale 0 (codes are
+// finite whatever they are).
 template <int NQ>
-__device__ void widen_warp(const SplitParams& p, const Smem<NQ>& sm, int w) {
+__device__ void widen_warp(const SplitParams& p, const Smem<NQ>& sm, int w, bool is_v) {
     using C = Cfg<NQ>;
     const int lane = threadIdx.x & 31;
     const int ps = p.page_size, ps_shift = 31 - __clz(ps), piece = lane & 3;
     const bool upper = piece >= 2;
     const int row0 = w * 32 + (lane >> 2);
-    // byte of the first (second) stored pair of words' scale in the two loaded
+    // scale of the first (second) stored pair of words, of the two loaded
     const uint32_t sel0 = upper ? 0x3232u : 0x1010u, sel1 = upper ? 0x1010u : 0x3232u;
-    uint32_t it = 0;  // ring position of the next tile
+    uint32_t code_at[4], scale_at[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = row0 + 8 * i, slot = r & (ps - 1);
+        const uint32_t block = (r - slot) * kQ4RowBytes;
+        code_at[i] = block + slot * 64 + piece * 16;
+        scale_at[i] = block + ps * 64 + slot * 8 + piece * 2;
+    }
+    const uint32_t row_at = (piece >> 1) * kHalfBytes + row0 * 128;
+    const uint32_t col =
+        static_cast<uint32_t>(((piece & 1) * 4) ^ (upper ? 2 : 0) ^ (row0 & 7)) << 4;
+    uint32_t it = is_v ? 1u : 0u;  // ring position of these warps' next tile
     const int ui_end = p.cta_first[blockIdx.x + 1];
     for (int ui = p.cta_first[blockIdx.x]; ui < ui_end; ++ui) {
         const Unit u = p.units[ui];
         const Tiles tl(p, u);
-        for (int j2 = 0; j2 < 2 * tl.n; ++j2, ++it) {  // K, then V of each tile
+        for (int j = 0; j < tl.n; ++j, it += 2) {
             int kt, last, front;
-            tl.tile(j2 >> 1, kt, last, front);
+            tl.tile(j, kt, last, front);
             const uint32_t rs = it % C::kRaw, stage = it % C::kStages;
             if (!warp_wait<NQ>(p, sm, sm.bar(C::BAR_RFULL + rs), (it / C::kRaw) & 1u, 40)) return;
+            const uint32_t raw = sm.base + C::kSmemRaw + rs * kRawBytes;
+            uint4 c[4];
+            uint32_t sc[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                c[i] = ptx::ld_shared_v4(raw + code_at[i]);
+                const int r = row0 + 8 * i;
+                sc[i] = ptx::ld_shared_u16(raw + scale_at[i]);
+                if (r < front || kt + r >= last) sc[i] = 0;
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(sm.bar(C::BAR_REMPTY + rs));  // in registers now
             if (!warp_wait<NQ>(p, sm, sm.bar(C::BAR_EMPTY + stage), ((it / C::kStages) & 1u) ^ 1u, 41))
                 return;
-            const uint32_t raw = sm.base + C::kSmemRaw + rs * kRawBytes;
-            const uint32_t dst = sm.tile(it) + (piece >> 1) * kHalfBytes;
-#pragma unroll 2
+            const uint32_t dst = sm.tile(it) + row_at;
+#pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = row0 + i * 8;
-                uint4 c = make_uint4(0u, 0u, 0u, 0u);
-                uint32_t sc = 0;
-                if (r >= front && kt + r < last) {
-                    const int pg = r >> ps_shift, slot = r & (ps - 1);
-                    const uint32_t at = raw + (pg << ps_shift) * kQ4RowBytes;
-                    c = ptx::ld_shared_v4(at + slot * 64 + piece * 16);
-                    sc = ptx::f16x2_of_e4m3x2(ptx::ld_shared_u16(at + ps * 64 + slot * 8 + piece * 2));
-                }
-                const uint32_t s0 = __byte_perm(sc, 0u, sel0), s1 = __byte_perm(sc, 0u, sel1);
-                const uint32_t word[4] = {upper ? c.z : c.x, upper ? c.w : c.y, upper ? c.x : c.z,
-                                          upper ? c.y : c.w};
-                const uint32_t row = dst + r * 128;
-                const uint32_t col =
-                    static_cast<uint32_t>(((piece & 1) * 4) ^ (upper ? 2 : 0) ^ (r & 7)) << 4;
+                const uint32_t s = ptx::f16x2_of_e4m3x2(sc[i]);
+                const uint32_t s0 = __byte_perm(s, 0u, sel0), s1 = __byte_perm(s, 0u, sel1);
+                const uint32_t word[4] = {upper ? c[i].z : c[i].x, upper ? c[i].w : c[i].y,
+                                          upper ? c[i].x : c[i].z, upper ? c[i].y : c[i].w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint32_t o[4];
                     widen_word(word[k], k < 2 ? s0 : s1, o);
-                    ptx::st_shared_v4(row + (col ^ (k << 4)), o[0], o[1], o[2], o[3]);
+                    ptx::st_shared_v4(dst + i * 1024 + (col ^ (k << 4)), o[0], o[1], o[2], o[3]);
                 }
             }
             ptx::fence_proxy_async_smem();  // the MMAs read the tile
             __syncwarp();
-            if (lane == 0) {
-                ptx::mbar_arrive(sm.bar(C::BAR_FULL + stage));
-                ptx::mbar_arrive(sm.bar(C::BAR_REMPTY + rs));
-            }
+            if (lane == 0) ptx::mbar_arrive(sm.bar(C::BAR_FULL + stage));
         }
     }
 }
@@ -624,11 +649,12 @@ __device__ __forceinline__ void exp32(const uint32_t (&s)[32], uint32_t taddr, u
 
 // 32 columns of a finished row, put back into their order (each 8 hold values 0 2
 // 4 6 1 3 5 7): to out (direct) or to its partial block.
-__device__ __forceinline__ void store32(const SplitParams& p, const uint32_t (&r)[32], bool direct,
-                                        int64_t orow, int64_t prow, int c0) {
+__device__ __forceinline__ void store32(void* out, float* part_o, int out_bf16,
+                                        const uint32_t (&r)[32], bool direct, int64_t orow,
+                                        int64_t prow, int c0) {
     auto at = [](int d) { return (d & ~7) + (d & 1) * 4 + ((d & 7) >> 1); };
-    if (direct && p.out_bf16) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * kHD + c0);
+    if (direct && out_bf16) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + orow * kHD + c0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t v[4];
@@ -639,13 +665,13 @@ __device__ __forceinline__ void store32(const SplitParams& p, const uint32_t (&r
             dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
         }
     } else if (direct) {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow * kHD + c0);
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + orow * kHD + c0);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             dst[i] = make_float4(__uint_as_float(r[at(4 * i)]), __uint_as_float(r[at(4 * i + 1)]),
                                  __uint_as_float(r[at(4 * i + 2)]), __uint_as_float(r[at(4 * i + 3)]));
     } else {
-        float* dst = p.part_o + prow * kHD + c0;
+        float* dst = part_o + prow * kHD + c0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t v[8];
@@ -669,33 +695,33 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
     uint32_t jt = 0, jt_other = 0;  // tiles this group and the other got
     int nx = 0;
     int kj = 0;  // joined (one-query-tile) units so far
-    const int ui_end = p.cta_first[blockIdx.x + 1];
-    for (int ui = p.cta_first[blockIdx.x]; ui < ui_end; ++ui) {
-        const Unit u = p.units[ui];
+    // Before the first unit each group makes a dry run of that unit's epilogue (no
+    // tiles, no waits, one thread's stores into a scratch sink) while it waits for
+    // its first tile anyway: fetched cold, from behind the other CTAs' reads, that
+    // code took 2 us of a decode step.
+    const int ui_first = p.cta_first[blockIdx.x], ui_end = p.cta_first[blockIdx.x + 1];
+    for (int ui = ui_first < ui_end ? ui_first - 1 : ui_first; ui < ui_end; ++ui) {
+        const bool dry = ui < ui_first;
+        const Unit u = p.units[dry ? ui_first : ui];
         const Tiles tl(p, u);
         const bool pair = unit_nq<NQ>(u, p.tpt) == 2;
         const int tile_tok = pair ? x * p.tpt : 0;
-        const bool row_valid = row < min(p.tpt, u.n_tok - tile_tok) * p.G;
-        const bool active = __any_sync(0xffffffffu, row_valid);
+        const bool row_valid = dry ? row == 0 : row < min(p.tpt, u.n_tok - tile_tok) * p.G;
+        const bool active = dry || __any_sync(0xffffffffu, row_valid);
         const int tok = u.tok_begin + tile_tok + row / p.G;
         const int row_end = row_valid ? p.tok_pos[tok] + 1 : 0;
+        const int n_tiles = dry ? 0 : tl.n;
         const int j0 = pair ? 0 : (x - nx) & 1, dj = pair ? 1 : 2;
         float m_ref = -INFINITY, l_run = 0.f;
         // the softmax scale, with the power of two that the row of Q carries
         const int xq = pair ? x : 0;
         const uint32_t load = xq == 0 ? n_load[0] : n_load[1];
-        ++n_load[0];
-        if (pair) ++n_load[1];
-        float sl2 = p.scale_log2;
-        if (j0 < tl.n) {
-            if (!warp_wait<NQ>(p, sm, sm.bar(C::BAR_QREADY + xq * (NQ - 1)), load & 1u, 25)) return;
-            if (row_valid) {
-                const int k = static_cast<int>(*sm.fac(load, xq, row)) - 127;
-                sl2 *= __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-            }
+        if (!dry) {
+            ++n_load[0];
+            if (pair) ++n_load[1];
         }
-        const uint64_t sl2p = ptx::f32x2(sl2, sl2);
-        for (int j = j0; j < tl.n; j += dj, ++jt) {
+        float sl2 = p.scale_log2;
+        for (int j = j0; j < n_tiles; j += dj, ++jt) {
             int kt, last, front;
             tl.tile(j, kt, last, front);
             const bool f = j < tl.n_first;
@@ -705,6 +731,14 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
             const bool full = __all_sync(0xffffffffu, lim >= kBN && (lo <= 0 || sink >= kBN));
             if (!warp_wait<NQ>(p, sm, sm.gbar(x, SFULL), jt & 1u, 20)) return;
             ptx::tc_fence_after();
+            // The factor was written before the S product was issued. (Waiting for
+            // QREADY here would be wrong: a group without a tile in a unit may find
+            // that barrier two phases on.)
+            if (j == j0 && row_valid) {
+                const int k = static_cast<int>(*sm.fac(load, xq, row)) - 127;
+                sl2 *= __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+            }
+            const uint64_t sl2p = ptx::f32x2(sl2, sl2);
             float corr = 1.f;
             if (active) {
                 uint32_t s0[32], s1[32];
@@ -750,12 +784,16 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
         }
         l_run *= 0.0078125f;  // 2^-7: the lift of P
         const bool direct = u.part < 0;
-        const int64_t orow = static_cast<int64_t>(tok) * p.H_q + u.kv_head * p.G + row % p.G;
-        const int64_t prow = static_cast<int64_t>(u.part) * (kBM * NQ) + (pair ? kBM * x : 0) + row;
+        const int64_t orow =
+            dry ? 0 : static_cast<int64_t>(tok) * p.H_q + u.kv_head * p.G + row % p.G;
+        const int64_t prow =
+            dry ? 0 : static_cast<int64_t>(u.part) * (kBM * NQ) + (pair ? kBM * x : 0) + row;
+        void* const out = dry ? static_cast<void*>(p.sink) : p.out;
+        float* const part_o = dry ? p.sink : p.part_o;
         float m_out = m_ref, l_out = l_run;
         if (pair) {
-            jt_other += tl.n;
-            if (!warp_wait<NQ>(p, sm, sm.gbar(x, ODONE), (jt - 1) & 1u, 22)) return;
+            jt_other += n_tiles;
+            if (!dry && !warp_wait<NQ>(p, sm, sm.gbar(x, ODONE), (jt - 1) & 1u, 22)) return;
             ptx::tc_fence_after();
             if (active) {
                 const float w = p.o_scale * 0.0078125f * (direct ? (l_run > 0.f ? 1.f / l_run : 0.f) : 1.f);
@@ -767,25 +805,29 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
                     ptx::tmem_ld_wait(r);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * w);
-                    if (row_valid) store32(p, r, direct, orow, prow, 32 * c);
+                    if (row_valid) store32(out, part_o, p.out_bf16, r, direct, orow, prow, 32 * c);
                 }
             }
         } else {
             // Join the groups: exchange (m, l), then each combines 64 columns.
             float2* join = reinterpret_cast<float2*>(sm.ptr + C::kSmemJoin) + (kj & 1) * 2 * kBM;
-            join[x * kBM + row] = make_float2(m_ref, l_run);
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(sm.gbar(x, JOIN));
-            const int n_other = (tl.n + j0) >> 1;  // tiles of the other parity
-            const int n_mine = tl.n - n_other;
-            jt_other += n_other;
-            if (!warp_wait<NQ>(p, sm, sm.gbar(x ^ 1, JOIN), kj & 1, 23)) return;
-            ++kj;
+            const int n_other = (n_tiles + j0) >> 1;  // tiles of the other parity
+            const int n_mine = n_tiles - n_other;
+            if (!dry) {
+                join[x * kBM + row] = make_float2(m_ref, l_run);
+                __syncwarp();
+                // two barriers in turn: a group without a tile in the next unit may
+                // arrive there before this one has waited here
+                if (lane == 0) ptx::mbar_arrive(sm.gbar(x, JOIN + (kj & 1)));
+                jt_other += n_other;
+                if (!warp_wait<NQ>(p, sm, sm.gbar(x ^ 1, JOIN + (kj & 1)), (kj >> 1) & 1, 23)) return;
+                ++kj;
+            }
             if (n_mine > 0 && !warp_wait<NQ>(p, sm, sm.gbar(x, ODONE), (jt - 1) & 1u, 22)) return;
             if (n_other > 0 && !warp_wait<NQ>(p, sm, sm.gbar(x ^ 1, ODONE), (jt_other - 1) & 1u, 24))
                 return;
             ptx::tc_fence_after();
-            nx = (nx + tl.n) & 1;
+            nx = (nx + n_tiles) & 1;
             if (active) {
                 const float2 other = join[(x ^ 1) * kBM + row];
                 const float m_a = l_run > 0.f ? m_ref : -INFINITY;
@@ -812,17 +854,19 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
                     for (int i = 0; i < 32; ++i)
                         a[i] = __float_as_uint((wa != 0.f ? wa * __uint_as_float(a[i]) : 0.f) +
                                                (wb != 0.f ? wb * __uint_as_float(b[i]) : 0.f));
-                    if (row_valid) store32(p, a, direct, orow, prow, 64 * x + 32 * c);
+                    if (row_valid) store32(out, part_o, p.out_bf16, a, direct, orow, prow, 64 * x + 32 * c);
                 }
             }
         }
         if (row_valid && (pair || x == 0)) {
-            if (!direct) p.part_ml[prow] = make_float2(m_out, l_out);
-            else if (p.lse) p.lse[orow] = (m_out + __log2f(l_out)) * 0.69314718055994531f;
+            float2* const ml = dry ? reinterpret_cast<float2*>(p.sink) : p.part_ml;
+            float* const lse = dry ? p.sink : p.lse;
+            if (!direct) ml[prow] = make_float2(m_out, l_out);
+            else if (lse) lse[orow] = (m_out + __log2f(l_out)) * 0.69314718055994531f;
         }
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(sm.bar(C::BAR_OFREE));
+        if (lane == 0 && !dry) ptx::mbar_arrive(sm.bar(C::BAR_OFREE));
     }
 }
 
@@ -861,6 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(sm.gbar(x, PFULL), kGroupWarps);
             ptx::mbar_init(sm.gbar(x, ODONE), 1);
             ptx::mbar_init(sm.gbar(x, JOIN), kGroupWarps);
+            ptx::mbar_init(sm.gbar(x, JOIN + 1), kGroupWarps);
         }
         *sm.abort_flag() = 0;
         ptx::fence_barrier_init();
@@ -884,9 +929,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < kWarpSoftmax) {
         q_warp<NQ>(p, sm, warp - kWarpQ);
     } else if (warp < kWarpWiden) {
+        ptx::regs_inc<kRegsSoftmax>();
         softmax_group<NQ>(p, sm, tmem, (warp - kWarpSoftmax) / kGroupWarps);
     } else {
-        widen_warp<NQ>(p, sm, warp - kWarpWiden);
+        ptx::regs_dec<kRegsWiden>();
+        widen_warp<NQ>(p, sm, (warp - kWarpWiden) & 3, warp >= kWarpWiden + kGroupWarps);
     }
 
     ptx::tc_fence_before();
