@@ -29,7 +29,9 @@
 // GB300 mapping, one persistent CTA per SM, 20 warps:
 //   warp 0      producer: page blocks by cp.async.bulk into a ring of raw tiles
 //               (9 KB: 128 rows of 72 bytes), Q by TMA when its buffer is free;
-//   warp 1      TMEM owner and single-thread tcgen05 issuer;
+//   warp 1      TMEM owner and tcgen05 issuer: the whole warp runs the issue loop, so
+//               that descriptors stay in uniform registers, and one elected lane
+//               issues (a single-lane loop took twice as long per product);
 //   warps 2-3   turn Q tiles into scaled f16, in place;
 //   warps 4-11  two softmax groups of 4 warps, thread = row;
 //   warps 12-19 widen raw tiles into the swizzled f16 ring (4 warps the K tiles, 4
@@ -471,30 +473,32 @@ struct Issuer {
     const SplitParams& p;
     const Smem<NQ>& sm;
     uint32_t tmem;
+    uint32_t leader;  // 1 in the lane that issues
     bool issued_any = false;
 
-    __device__ bool wait(uint32_t bar, uint32_t parity, int site) {
-        if (ptx::mbar_wait(bar, parity, p.wait_limit_ns, sm.abort_flag())) return true;
-        record_timeout(p, sm.abort_flag(), site);
-        return false;
+    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, int site) {
+        return warp_wait<NQ>(p, sm, bar, parity, site);
     }
-    __device__ bool wait_full(uint32_t pos, int site) {
+    __device__ __forceinline__ bool wait_full(uint32_t pos, int site) {
         return wait(sm.bar(C::BAR_FULL + pos % C::kStages), (pos / C::kStages) & 1u, site);
     }
-    __device__ void release(uint32_t pos) { ptx::mma_commit(sm.bar(C::BAR_EMPTY + pos % C::kStages)); }
+    __device__ __forceinline__ void commit(uint32_t bar) { ptx::mma_commit_if(bar, leader); }
+    __device__ __forceinline__ void release(uint32_t pos) {
+        commit(sm.bar(C::BAR_EMPTY + pos % C::kStages));
+    }
     // S of group x = Q tile qx times the K tile at pos.
-    __device__ void issue_s(int x, int qx, uint32_t pos) {
+    __device__ __forceinline__ void issue_s(int x, int qx, uint32_t pos) {
         ptx::tc_fence_after();
         const uint64_t dq = ptx::sdesc_sw128(sm.base + C::kSmemQ + qx * kQBytes, 16, 1024);
         const uint64_t dk = ptx::sdesc_sw128(sm.tile(pos), 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < kHD / 16; ++kk)
-            ptx::mma_bf16_ss(tmem + 128u * x, dq + kmajor_step(kk), dk + kmajor_step(kk), kIdescQK,
-                             kk > 0);
-        ptx::mma_commit(sm.gbar(x, SFULL));
+            ptx::mma_f16_ss_if(tmem + 128u * x, dq + kmajor_step(kk), dk + kmajor_step(kk), kIdescQK,
+                               kk > 0, leader);
+        commit(sm.gbar(x, SFULL));
         issued_any = true;
     }
-    __device__ bool issue_pv(const PvOp& op) {
+    __device__ __forceinline__ bool issue_pv(const PvOp& op) {
         if (!wait(sm.gbar(op.x, PFULL), op.t & 1u, 14)) return false;
         if (op.first && op.k > 0 && !wait(sm.bar(C::BAR_OFREE), (op.k - 1) & 1, 15)) return false;
         ptx::tc_fence_after();
@@ -503,12 +507,13 @@ struct Issuer {
         const uint64_t dv = ptx::sdesc_sw128(sm.tile(op.pos), kHalfBytes, 1024);
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk)
-            ptx::mma_bf16_ts(d, a + 8u * kk, dv + 128u * kk, kIdescPV, (!op.first || kk > 0) ? 1u : 0u);
-        ptx::mma_commit(sm.gbar(op.x, ODONE));
+            ptx::mma_f16_ts_if(d, a + 8u * kk, dv + 128u * kk, kIdescPV,
+                               (!op.first || kk > 0) ? 1u : 0u, leader);
+        commit(sm.gbar(op.x, ODONE));
         return true;
     }
     // The held P.V of a unit of one query tile, if any.
-    __device__ bool issue_held(const PvOp& op, bool& held) {
+    __device__ __forceinline__ bool issue_held(const PvOp& op, bool& held) {
         if (!held) return true;
         held = false;
         if (!wait_full(op.pos, 13) || !issue_pv(op)) return false;
@@ -522,9 +527,10 @@ struct Issuer {
 // last P.V is held until the next such unit's first S is issued. An S that
 // reuses the TMEM of an earlier P is always issued after that P's product.
 template <int NQ>
-__device__ void mma_thread(const SplitParams& p, const Smem<NQ>& sm, uint32_t tmem) {
+__device__ void mma_warp(const SplitParams& p, const Smem<NQ>& sm, uint32_t tmem) {
     using C = Cfg<NQ>;
-    Issuer<NQ> is{p, sm, tmem};
+    // broadcasts: the values are warp-uniform, and known to be
+    Issuer<NQ> is{p, sm, __shfl_sync(0xffffffffu, tmem, 0), ptx::elect_one()};
     bool ok = true;
     uint32_t pos = 0;           // ring position of the unit's K_0 (K_j at pos + 2j, V_j behind it)
     uint32_t jt[2] = {0, 0};    // tiles each softmax group got before
@@ -536,8 +542,8 @@ __device__ void mma_thread(const SplitParams& p, const Smem<NQ>& sm, uint32_t tm
     const int ui_end = p.cta_first[blockIdx.x + 1];
     for (int ui = p.cta_first[blockIdx.x]; ui < ui_end && ok; ++ui, ++k) {
         const Unit u = p.units[ui];
-        const int n = Tiles(p, u).n;
-        if (unit_nq<NQ>(u, p.tpt) == 2) {
+        const int n = __shfl_sync(0xffffffffu, Tiles(p, u).n, 0);
+        if (__shfl_sync(0xffffffffu, unit_nq<NQ>(u, p.tpt), 0) == 2) {
             if (!(ok = is.issue_held(pend, held))) break;
             if (!(ok = is.wait(sm.bar(C::BAR_QREADY), qu[0] & 1u, 10) &&
                        is.wait(sm.bar(C::BAR_QREADY + NQ - 1), qu[1] & 1u, 10)))
@@ -547,7 +553,7 @@ __device__ void mma_thread(const SplitParams& p, const Smem<NQ>& sm, uint32_t tm
                 if (j < n) {
                     if (!(ok = is.wait_full(posK, 11))) break;
                     is.issue_s(0, 0, posK);
-                    if (j == n - 1) ptx::mma_commit(sm.bar(C::BAR_QFREE));
+                    if (j == n - 1) is.commit(sm.bar(C::BAR_QFREE));
                 }
                 if (j > 0) {
                     if (!(ok = is.issue_pv(PvOp{1, jt[1] + j - 1, j == 1, k, posVp}))) break;
@@ -556,7 +562,7 @@ __device__ void mma_thread(const SplitParams& p, const Smem<NQ>& sm, uint32_t tm
                 if (j < n) {
                     is.issue_s(1, NQ - 1, posK);
                     is.release(posK);
-                    if (j == n - 1) ptx::mma_commit(sm.bar(C::BAR_QFREE + NQ - 1));
+                    if (j == n - 1) is.commit(sm.bar(C::BAR_QFREE + NQ - 1));
                     if (!(ok = is.wait_full(posV, 13))) break;
                     if (!(ok = is.issue_pv(PvOp{0, jt[0] + j, j == 0, k, posV}))) break;
                 }
@@ -567,7 +573,7 @@ __device__ void mma_thread(const SplitParams& p, const Smem<NQ>& sm, uint32_t tm
             ++qu[0];
             ++qu[1];
         } else {
-            if (held && !ptx::mbar_test_wait(sm.bar(C::BAR_QREADY), qu[0] & 1u) &&
+            if (held && !__all_sync(0xffffffffu, ptx::mbar_test_wait(sm.bar(C::BAR_QREADY), qu[0] & 1u)) &&
                 !(ok = is.issue_held(pend, held)))
                 break;
             for (int j = 0; j < n && ok; ++j) {
@@ -577,7 +583,7 @@ __device__ void mma_thread(const SplitParams& p, const Smem<NQ>& sm, uint32_t tm
                 if (j == 0 && !(ok = is.wait(sm.bar(C::BAR_QREADY), qu[0] & 1u, 10))) break;
                 is.issue_s(x, 0, posK);
                 is.release(posK);
-                if (j == n - 1) ptx::mma_commit(sm.bar(C::BAR_QFREE));
+                if (j == n - 1) is.commit(sm.bar(C::BAR_QFREE));
                 if (!(ok = is.issue_held(pend, held))) break;
                 const uint32_t t = x == 0 ? jt[0]++ : jt[1]++;
                 pend = PvOp{x, t, j < 2, k, posK + 1u};
@@ -591,7 +597,7 @@ __device__ void mma_thread(const SplitParams& p, const Smem<NQ>& sm, uint32_t tm
     }
     if (ok) ok = is.issue_held(pend, held);
     if (!ok && is.issued_any) {
-        ptx::mma_commit(sm.bar(C::BAR_DRAIN));
+        is.commit(sm.bar(C::BAR_DRAIN));
         ptx::mbar_wait(sm.bar(C::BAR_DRAIN), 0, p.wait_limit_ns, nullptr);
     }
 }
@@ -924,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         producer_warp<NQ>(p, sm, &tm_q);
     } else if (warp == 1) {
-        if (lane == 0) mma_thread<NQ>(p, sm, tmem);
+        mma_warp<NQ>(p, sm, tmem);
         __syncwarp();
     } else if (warp < kWarpSoftmax) {
         q_warp<NQ>(p, sm, warp - kWarpQ);
