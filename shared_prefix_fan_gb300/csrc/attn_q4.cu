@@ -37,11 +37,16 @@
 //   warps 12-19 widen raw tiles into the swizzled f16 ring (4 warps the K tiles, 4
 //               the V tiles), rows that no row of the unit sees as zeros. With 4
 //               warps for both, a decode step waited for them: 35 us, not 15.
-// Registers (launched with 96 a thread): softmax warps 136, widening 56.
+// Registers (launched with 96 a thread): softmax warps 144, the others 64.
 // A unit of two query tiles gives each group one of them. A unit of one query
 // tile (decode) is split over the groups by keys instead: tile t goes to group
 // t mod 2, each with its own S, (m, l) and O in TMEM, and the two are joined at
 // the unit's end (64 columns of O each), so that two tiles' softmaxes overlap.
+// Of such a unit that has at most 64 (32) rows and writes a partial, the rows are
+// copied to all 128 lanes 2 (4) times, and each copy takes its part of a tile's
+// keys: a thread then exponentiates 64 (32) scores of a tile, not 128, and stores
+// zeros for the other keys' P; each copy ends as a partial row of its own. The
+// softmax of one tile was the longest step of a decode CTA's loop.
 // TMEM: S_0 = 0, S_1 = 128, O_0 = 256, O_1 = 384 (512 columns).
 // Every wait is bounded, as in attn_fwd.cu.
 #include <cuda_bf16.h>
@@ -69,9 +74,10 @@ constexpr int kQWarps = 2;
 constexpr int kWarpSoftmax = 4;  // first softmax warp
 constexpr int kWarpWiden = 12;   // first widening warp
 constexpr int kThreads = 32 * 20;
-// 96 * 640 = 61440 registers at launch >= 136 * 256 + 56 * 256 + 96 * 128
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 136, kRegsWiden = 56;
-static_assert(kRegsSoftmax * 256 + kRegsWiden * 256 + kRegsLaunch * 128 <= kRegsLaunch * kThreads,
+// Registers per thread: at launch, and after the warpgroups' split (the sum must
+// not exceed what the block was launched with).
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsWiden = 64, kRegsOther = 64;
+static_assert(kRegsSoftmax * 256 + kRegsWiden * 256 + kRegsOther * 128 <= kRegsLaunch * kThreads,
               "register split");
 constexpr int kFacBufs = 4;      // units whose row factors are held
 
@@ -310,8 +316,8 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ>& sm, const CU
 // ------------------------------------------------------------------ Q to f16
 // Two warps turn the rows of a loaded Q tile into f16 in place: a thread finds its
 // row's largest exponent, scales by a power of two and stores the 8 values of each
-// 16-byte piece in the order the widened K tiles have. Rows behind the unit's last
-// are left as they are (their scores are never used).
+// 16-byte piece in the order the widened K tiles have, in every copy of the row.
+// Rows behind the unit's last are left as they are (their scores are never used).
 template <int NQ>
 __device__ void q_warp(const SplitParams& p, const Smem<NQ>& sm, int w) {
     using C = Cfg<NQ>;
@@ -325,20 +331,24 @@ __device__ void q_warp(const SplitParams& p, const Smem<NQ>& sm, int w) {
             const uint32_t n = x == 0 ? loads[0]++ : loads[1]++;
             if (!warp_wait<NQ>(p, sm, sm.bar(C::BAR_QFULL + x), n & 1u, 50)) return;
             const int rows = min(p.tpt, u.n_tok - x * p.tpt) * p.G;
+            const int split = nq == 1 ? key_split(u, p.G) : 1;
             for (int row = w * 32 + lane; row < rows; row += 32 * kQWarps) {
                 const uint32_t at = sm.base + C::kSmemQ + x * kQBytes + row * 128;
                 const uint32_t swz = static_cast<uint32_t>(row & 7) << 4;
-                uint4 v[16];
-#pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    v[c] = ptx::ld_shared_v4(at + (c >> 3) * kHalfBytes + (((c & 7) << 4) ^ swz));
+                auto piece = [&](int c) { return at + (c >> 3) * kHalfBytes + (((c & 7) << 4) ^ swz); };
                 uint32_t top[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    top[0] = ptx::max_abs_bf16x2(top[0], v[c].x);
-                    top[1] = ptx::max_abs_bf16x2(top[1], v[c].y);
-                    top[2] = ptx::max_abs_bf16x2(top[2], v[c].z);
-                    top[3] = ptx::max_abs_bf16x2(top[3], v[c].w);
+                for (int half = 0; half < 2; ++half) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) v[c] = ptx::ld_shared_v4(piece(8 * half + c));
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        top[0] = ptx::max_abs_bf16x2(top[0], v[c].x);
+                        top[1] = ptx::max_abs_bf16x2(top[1], v[c].y);
+                        top[2] = ptx::max_abs_bf16x2(top[2], v[c].z);
+                        top[3] = ptx::max_abs_bf16x2(top[3], v[c].w);
+                    }
                 }
                 const uint32_t t = ptx::max_abs_bf16x2(ptx::max_abs_bf16x2(top[0], top[1]),
                                                        ptx::max_abs_bf16x2(top[2], top[3]));
@@ -349,13 +359,24 @@ __device__ void q_warp(const SplitParams& p, const Smem<NQ>& sm, int w) {
                 auto lo = [f](uint32_t b) { return __uint_as_float(b << 16) * f; };
                 auto hi = [f](uint32_t b) { return __uint_as_float(b & 0xffff0000u) * f; };
 #pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    ptx::st_shared_v4(at + (c >> 3) * kHalfBytes + (((c & 7) << 4) ^ swz),
-                                      ptx::pack_f16x2(lo(v[c].x), lo(v[c].y)),
-                                      ptx::pack_f16x2(lo(v[c].z), lo(v[c].w)),
-                                      ptx::pack_f16x2(hi(v[c].x), hi(v[c].y)),
-                                      ptx::pack_f16x2(hi(v[c].z), hi(v[c].w)));
-                *sm.fac(n, x, row) = static_cast<uint8_t>(k + 127);
+                for (int half = 0; half < 2; ++half) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) v[c] = ptx::ld_shared_v4(piece(8 * half + c));
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        v[c] = make_uint4(ptx::pack_f16x2(lo(v[c].x), lo(v[c].y)),
+                                          ptx::pack_f16x2(lo(v[c].z), lo(v[c].w)),
+                                          ptx::pack_f16x2(hi(v[c].x), hi(v[c].y)),
+                                          ptx::pack_f16x2(hi(v[c].z), hi(v[c].w)));
+                    for (int copy = 0; copy < kBM; copy += kBM / split)
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            ptx::st_shared_v4(piece(8 * half + c) + copy * 128, v[c].x, v[c].y,
+                                              v[c].z, v[c].w);
+                }
+                for (int copy = 0; copy < kBM; copy += kBM / split)
+                    *sm.fac(n, x, row + copy) = static_cast<uint8_t>(k + 127);
             }
             ptx::fence_proxy_async_smem();  // the MMAs read the tile
             __syncwarp();
@@ -611,12 +632,12 @@ __device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&a)[32], uint32
 }
 
 // Scores a row does not see become -inf in TMEM (tiles at a mask's border only,
-// so that the common path carries no masks): it sees columns below lim, and not
-// [sink, lo).
-__device__ __forceinline__ void mask_tile(uint32_t taddr, int lim, int lo, int sink) {
+// so that the common path carries no masks): of columns [c0, c1) it sees those
+// below lim, and not [sink, lo).
+__device__ __forceinline__ void mask_tile(uint32_t taddr, int c0, int c1, int lim, int lo, int sink) {
     uint32_t s[32];
 #pragma unroll 1
-    for (int c0 = 0; c0 < kBN; c0 += 32) {
+    for (; c0 < c1; c0 += 32) {
         __syncwarp();
         ptx::tmem_ld32(taddr + c0, s);
         ptx::tmem_ld_wait(s);
@@ -641,16 +662,84 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32], float m) {
 // P of 32 columns to TMEM (16 columns of f16 pairs), their sum added to l.
 __device__ __forceinline__ void exp32(const uint32_t (&s)[32], uint32_t taddr, uint64_t sl2,
                                       uint64_t negm, uint64_t (&l)[2]) {
-    uint32_t packed[16];
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-        const uint64_t t = ptx::fma_f32x2(
-            ptx::f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sl2, negm);
-        const float e0 = ptx::ex2(ptx::lo_f32(t)), e1 = ptx::ex2(ptx::hi_f32(t));
-        l[(c >> 1) & 1] = ptx::add_f32x2(l[(c >> 1) & 1], ptx::f32x2(e0, e1));
-        packed[c >> 1] = ptx::pack_f16x2(e0, e1);
+    for (int h = 0; h < 2; ++h) {
+        uint32_t packed[8];
+#pragma unroll
+        for (int c = 0; c < 16; c += 2) {
+            const uint64_t t = ptx::fma_f32x2(ptx::f32x2(__uint_as_float(s[16 * h + c]),
+                                                         __uint_as_float(s[16 * h + c + 1])),
+                                              sl2, negm);
+            const float e0 = ptx::ex2(ptx::lo_f32(t)), e1 = ptx::ex2(ptx::hi_f32(t));
+            l[(c >> 1) & 1] = ptx::add_f32x2(l[(c >> 1) & 1], ptx::f32x2(e0, e1));
+            packed[c >> 1] = ptx::pack_f16x2(e0, e1);
+        }
+        ptx::tmem_st8(taddr + 8 * h, packed);
     }
-    ptx::tmem_st16(taddr, packed);
+}
+__device__ __forceinline__ void zero16(uint32_t taddr) {
+    const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    ptx::tmem_st8(taddr, z);
+    ptx::tmem_st8(taddr + 8, z);
+}
+
+// The running reference and sum of a row (of one copy's keys).
+struct Running {
+    float m = -INFINITY, l = 0.f;
+    // A tile's maximum: the factor that O and l take, and the exponent's addend.
+    __device__ __forceinline__ float raise(float mx, float& neg) {
+        float corr = 1.f;
+        if (mx > m + kRescaleLog2) {
+            corr = (m == -INFINITY) ? 0.f : ptx::ex2(m - mx);
+            m = mx;
+        }
+        neg = kLiftLog2 - ((m == -INFINITY) ? 0.f : m);
+        return corr;
+    }
+};
+
+// One tile's softmax of this thread's row, over the keys of its copy `seg` of F: P
+// over the first 64 columns of S. Returns the rescale factor.
+template <int F>
+__device__ __forceinline__ float softmax_tile(uint32_t colS, int seg, float sl2, Running& run) {
+    const uint64_t sl2p = ptx::f32x2(sl2, sl2);
+    uint64_t l[2] = {0ull, 0ull};
+    uint32_t s0[32];
+    float neg, corr;
+    if (F == 4) {
+        ptx::tmem_ld32(colS + 32 * seg, s0);
+        ptx::tmem_ld_wait(s0);
+        corr = run.raise(max32(s0, -INFINITY) * sl2, neg);  // scale > 0: max commutes
+        const uint64_t negm = ptx::f32x2(neg, neg);
+        exp32(s0, colS + 16 * seg, sl2p, negm, l);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) zero16(colS + 16 * (seg ^ i));
+    } else if (F == 2) {
+        uint32_t s1[32];
+        load64(colS + 64 * seg, s0, s1);
+        corr = run.raise(max32(s1, max32(s0, -INFINITY)) * sl2, neg);
+        const uint64_t negm = ptx::f32x2(neg, neg);
+        exp32(s0, colS + 32 * seg, sl2p, negm, l);
+        exp32(s1, colS + 32 * seg + 16, sl2p, negm, l);
+        zero16(colS + 32 * (seg ^ 1));
+        zero16(colS + 32 * (seg ^ 1) + 16);
+    } else {
+        // columns 64.. first for the maximum; 0.. stay in registers
+        uint32_t s1[32];
+        load64(colS + 64, s0, s1);
+        const float mx = max32(s1, max32(s0, -INFINITY));
+        load64(colS, s0, s1);
+        corr = run.raise(max32(s1, max32(s0, mx)) * sl2, neg);
+        const uint64_t negm = ptx::f32x2(neg, neg);
+        exp32(s0, colS, sl2p, negm, l);
+        exp32(s1, colS + 16, sl2p, negm, l);
+        load64(colS + 64, s0, s1);
+        exp32(s0, colS + 32, sl2p, negm, l);
+        exp32(s1, colS + 48, sl2p, negm, l);
+    }
+    const uint64_t sum = ptx::add_f32x2(l[0], l[1]);
+    run.l = run.l * corr + (ptx::lo_f32(sum) + ptx::hi_f32(sum));
+    return corr;
 }
 
 // 32 columns of a finished row, put back into their order (each 8 hold values 0 2
@@ -712,13 +801,15 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
         const Tiles tl(p, u);
         const bool pair = unit_nq<NQ>(u, p.tpt) == 2;
         const int tile_tok = pair ? x * p.tpt : 0;
-        const bool row_valid = dry ? row == 0 : row < min(p.tpt, u.n_tok - tile_tok) * p.G;
+        const int split = pair ? 1 : key_split(u, p.G);
+        const int urow = row & (kBM / split - 1), seg = row / (kBM / split);  // row, copy of it
+        const bool row_valid = dry ? row == 0 : urow < min(p.tpt, u.n_tok - tile_tok) * p.G;
         const bool active = dry || __any_sync(0xffffffffu, row_valid);
-        const int tok = u.tok_begin + tile_tok + row / p.G;
+        const int tok = u.tok_begin + tile_tok + urow / p.G;
         const int row_end = row_valid ? p.tok_pos[tok] + 1 : 0;
         const int n_tiles = dry ? 0 : tl.n;
         const int j0 = pair ? 0 : (x - nx) & 1, dj = pair ? 1 : 2;
-        float m_ref = -INFINITY, l_run = 0.f;
+        Running run;
         // the softmax scale, with the power of two that the row of Q carries
         const int xq = pair ? x : 0;
         const uint32_t load = xq == 0 ? n_load[0] : n_load[1];
@@ -744,30 +835,13 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
                 const int k = static_cast<int>(*sm.fac(load, xq, row)) - 127;
                 sl2 *= __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
             }
-            const uint64_t sl2p = ptx::f32x2(sl2, sl2);
             float corr = 1.f;
             if (active) {
-                uint32_t s0[32], s1[32];
-                // the row's maximum: columns 64.. first, 0.. stay in registers
-                if (!full) mask_tile(colS, lim, lo, sink);
-                load64(colS + 64, s0, s1);
-                float mx = max32(s1, max32(s0, -INFINITY));
-                load64(colS, s0, s1);
-                mx = max32(s1, max32(s0, mx)) * sl2;  // scale > 0: max commutes with scaling
-                if (mx > m_ref + kRescaleLog2) {
-                    corr = (m_ref == -INFINITY) ? 0.f : ptx::ex2(m_ref - mx);
-                    m_ref = mx;
-                }
-                const float neg = kLiftLog2 - ((m_ref == -INFINITY) ? 0.f : m_ref);
-                const uint64_t negm = ptx::f32x2(neg, neg);
-                uint64_t l[2] = {0ull, 0ull};
-                exp32(s0, colS, sl2p, negm, l);
-                exp32(s1, colS + 16, sl2p, negm, l);
-                load64(colS + 64, s0, s1);
-                exp32(s0, colS + 32, sl2p, negm, l);
-                exp32(s1, colS + 48, sl2p, negm, l);
-                const uint64_t sum = ptx::add_f32x2(l[0], l[1]);
-                l_run = l_run * corr + (ptx::lo_f32(sum) + ptx::hi_f32(sum));
+                if (!full)
+                    mask_tile(colS, seg * (kBN / split), (seg + 1) * (kBN / split), lim, lo, sink);
+                corr = split == 4   ? softmax_tile<4>(colS, seg, sl2, run)
+                       : split == 2 ? softmax_tile<2>(colS, seg, sl2, run)
+                                    : softmax_tile<1>(colS, seg, sl2, run);
             }
             // O is rescaled in place: this S was issued after the group's previous
             // product, so that one has completed.
@@ -788,10 +862,10 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(sm.gbar(x, PFULL));
         }
-        l_run *= 0.0078125f;  // 2^-7: the lift of P
+        const float m_ref = run.m, l_run = run.l * 0.0078125f;  // 2^-7: the lift of P
         const bool direct = u.part < 0;
         const int64_t orow =
-            dry ? 0 : static_cast<int64_t>(tok) * p.H_q + u.kv_head * p.G + row % p.G;
+            dry ? 0 : static_cast<int64_t>(tok) * p.H_q + u.kv_head * p.G + urow % p.G;
         const int64_t prow =
             dry ? 0 : static_cast<int64_t>(u.part) * (kBM * NQ) + (pair ? kBM * x : 0) + row;
         void* const out = dry ? static_cast<void*>(p.sink) : p.out;
@@ -927,6 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after();
     const uint32_t tmem = *sm.tmem_slot();
 
+    if (warp < kWarpSoftmax) ptx::regs_dec<kRegsOther>();
     if (warp == 0) {
         producer_warp<NQ>(p, sm, &tm_q);
     } else if (warp == 1) {

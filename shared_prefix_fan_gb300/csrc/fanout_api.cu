@@ -173,7 +173,10 @@ int attn_call(AttnKind kind, const void* q, const void* k_pages, const void* v_p
     in.rows = rows;
     in.window = window;
     in.sinks = sinks;
-    if (q4) in.row_bytes = 2 * kQ4RowBytes;
+    if (q4) {
+        in.row_bytes = 2 * kQ4RowBytes;
+        in.key_split = 1;
+    }
     bool patched = false;
     if (ws->plan_ready && key != ws->key && key.size() == ws->key.size() &&
         std::equal(key.begin(), key.begin() + fixed, ws->key.begin()) &&
