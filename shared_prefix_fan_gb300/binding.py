@@ -45,10 +45,10 @@ ABI = {
                                            _i32, _i32, _f32, _f32, _vp]),
     "fanout_kv_read_q4": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _f32, _f32,
                                          _vp, _vp, _i64, _i64, _vp]),
-    "fanout_attn_window": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32p, _i32p, _i32, _i32,
+    "fanout_attn_window": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32,
                                           _i32, _i32, _i32, _i32, _i32, _f32, _i32, _i32, _vp,
                                           _i32, _vp, _vp]),
-    "fanout_attn_q4": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32p, _i32p, _i32, _i32, _i32,
+    "fanout_attn_q4": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32,
                                       _i32, _i32, _i32, _i32, _f32, _i32, _f32, _f32, _i32, _i32,
                                       _vp, _i32, _vp, _vp]),
     "fanout_lse_merge": (ctypes.c_int, [_vp, _vp, _i32, _i64, _i32, _vp, _i32, _vp, _vp]),
@@ -178,24 +178,34 @@ def kv_append(k_new, v_new, k_pages, v_pages, page_table, prefix_len: int, suffi
         int(k_pages.shape[3]), int(page_size), _stream_handle(stream)), "fanout_kv_append")
 
 
-def _on(dev, stream):
-    """(device guard, stream handle): `dev` current for a call on its tensors, and
-    its own current stream when none is given."""
+def _device_call(name: str, dev, stream, *args) -> None:
+    """Call the library with `dev` current, on `stream` or on dev's current one.
+
+    The serving calls below take a few microseconds of GPU time for a decode step,
+    so their host side is kept short: raw stream handles, a device switch only when
+    another device is current, one conversion for a call's host lengths."""
     import torch
-    handle = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream_handle(stream)
-    return torch.cuda.device(dev), handle
+    idx = dev.index
+    handle = torch._C._cuda_getCurrentRawStream(idx) if stream is None else _stream_handle(stream)
+    fn = getattr(_lib or load(), name)
+    if torch.cuda.current_device() == idx:
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(idx):
+            rc = fn(*args, handle)
+    if rc:
+        raise FanoutError(rc, name)
 
 
-def _dev_tensor(name: str, t, dtype, dev, shape=None, contiguous=True):
-    if not t.is_cuda or t.device != dev or t.dtype != dtype:
-        raise ValueError(f"{name} must be a {dtype} tensor on {dev}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+def _need(name: str, t, dtype, dev, shape=None) -> None:
+    """A contiguous tensor of this type, on this CUDA device (and of this shape)."""
+    if t.dtype is not dtype or t.device != dev or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on one CUDA device ({dev})")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
 
 
-def _opt_ptr(t):
+def _ptr_or_none(t):
     return None if t is None else t.data_ptr()
 
 
@@ -209,29 +219,29 @@ def fork_device(prefix_pages, prefix_len: int, suffix_lens, page_size: int, free
     with its page or want_cow is false. What the lengths get wrong on the device
     is reported by last_error() and leaves `out` as it was."""
     import torch
-    dev, B = suffix_lens.device, int(suffix_lens.numel())
+    i32, dev = torch.int32, suffix_lens.device
+    B = suffix_lens.numel()
     if page_size <= 0:
         raise ValueError("page_size must be positive")
-    _dev_tensor("suffix_lens", suffix_lens, torch.int32, dev, (B,))
-    _dev_tensor("prefix_pages", prefix_pages, torch.int32, dev)
-    _dev_tensor("free_pages", free_pages, torch.int32, dev)
-    if prefix_pages.numel() < -(-int(prefix_len) // page_size):
+    _need("suffix_lens", suffix_lens, i32, dev, (B,))
+    _need("prefix_pages", prefix_pages, i32, dev)
+    _need("free_pages", free_pages, i32, dev)
+    if prefix_pages.numel() < -(-prefix_len // page_size):
         raise ValueError("prefix_pages holds fewer pages than the prefix")
     if used is not None:
-        _dev_tensor("used", used, torch.int32, dev, (1,))
+        _need("used", used, i32, dev, (1,))
     if out is None:
-        out = torch.empty((B, int(max_pages)), dtype=torch.int32, device=dev)
-    _dev_tensor("out", out, torch.int32, dev, (B, int(max_pages)))
+        out = torch.empty((B, max_pages), dtype=i32, device=dev)
+    else:
+        _need("out", out, i32, dev, (B, max_pages))
     cow = None
     if want_cow and prefix_len % page_size:
-        cow = torch.empty((B, 2), dtype=torch.int32, device=dev)
-    after = torch.empty((1,), dtype=torch.int32, device=dev)
-    guard, handle = _on(dev, stream)
-    with guard:
-        _check(load().fanout_fork_device(
-            prefix_pages.data_ptr(), int(prefix_len), B, suffix_lens.data_ptr(), int(page_size),
-            free_pages.data_ptr(), int(free_pages.numel()), _opt_ptr(used), after.data_ptr(),
-            out.data_ptr(), int(max_pages), _opt_ptr(cow), handle), "fanout_fork_device")
+        cow = torch.empty((B, 2), dtype=i32, device=dev)
+    after = torch.empty((1,), dtype=i32, device=dev)
+    _device_call("fanout_fork_device", dev, stream, prefix_pages.data_ptr(), prefix_len, B,
+                 suffix_lens.data_ptr(), page_size, free_pages.data_ptr(), free_pages.numel(),
+                 _ptr_or_none(used), after.data_ptr(), out.data_ptr(), max_pages,
+                 _ptr_or_none(cow))
     return out, cow, after
 
 
@@ -242,25 +252,23 @@ def extend_device(page_table, prefix_len: int, suffix_lens, add_lens, page_size:
     slots (int64 [n_slots]) maps the new tokens' rows for kv_append_q4; rows
     behind the last one get -1. `used` as in fork_device."""
     import torch
-    dev = page_table.device
-    B, width = (int(x) for x in page_table.shape)
-    _dev_tensor("page_table", page_table, torch.int32, dev)
-    _dev_tensor("suffix_lens", suffix_lens, torch.int32, dev, (B,))
-    _dev_tensor("add_lens", add_lens, torch.int32, dev, (B,))
-    _dev_tensor("free_pages", free_pages, torch.int32, dev)
+    i32, dev = torch.int32, page_table.device
+    B, width = page_table.shape
+    _need("page_table", page_table, i32, dev)
+    _need("suffix_lens", suffix_lens, i32, dev, (B,))
+    _need("add_lens", add_lens, i32, dev, (B,))
+    _need("free_pages", free_pages, i32, dev)
     if used is not None:
-        _dev_tensor("used", used, torch.int32, dev, (1,))
+        _need("used", used, i32, dev, (1,))
     if slots is None:
-        slots = torch.empty((int(n_slots),), dtype=torch.int64, device=dev)
-    _dev_tensor("slots", slots, torch.int64, dev, (int(n_slots),))
-    after = torch.empty((1,), dtype=torch.int32, device=dev)
-    guard, handle = _on(dev, stream)
-    with guard:
-        _check(load().fanout_extend_device(
-            page_table.data_ptr(), B, width, int(prefix_len), suffix_lens.data_ptr(),
-            add_lens.data_ptr(), int(page_size), free_pages.data_ptr(), int(free_pages.numel()),
-            _opt_ptr(used), after.data_ptr(), slots.data_ptr(), int(n_slots), handle),
-            "fanout_extend_device")
+        slots = torch.empty((n_slots,), dtype=torch.int64, device=dev)
+    else:
+        _need("slots", slots, torch.int64, dev, (n_slots,))
+    after = torch.empty((1,), dtype=i32, device=dev)
+    _device_call("fanout_extend_device", dev, stream, page_table.data_ptr(), B, width, prefix_len,
+                 suffix_lens.data_ptr(), add_lens.data_ptr(), page_size, free_pages.data_ptr(),
+                 free_pages.numel(), _ptr_or_none(used), after.data_ptr(), slots.data_ptr(),
+                 n_slots)
     return slots, after
 
 
@@ -276,28 +284,31 @@ def q4_pool(num_pages: int, h_kv: int, page_size: int, device="cuda"):
 
 
 def _q4_pools(k_pages, v_pages, page_size: int, dev):
+    """(num_pages, H_kv) of a pair of 4-bit pools."""
     import torch
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        _dev_tensor(name, t, torch.uint8, dev)
-        if t.dim() != 3 or int(t.shape[2]) != int(page_size) * Q4_ROW_BYTES:
-            raise ValueError(f"{name} must be [num_pages, H_kv, page_size * {Q4_ROW_BYTES}]")
-    if k_pages.shape != v_pages.shape:
-        raise ValueError("k_pages / v_pages differ in shape")
-    return int(k_pages.shape[0]), int(k_pages.shape[1])
+    shape = k_pages.shape
+    _need("k_pages", k_pages, torch.uint8, dev)
+    _need("v_pages", v_pages, torch.uint8, dev, shape)
+    if len(shape) != 3 or shape[2] != page_size * Q4_ROW_BYTES:
+        raise ValueError(f"k_pages / v_pages must be [num_pages, H_kv, page_size * {Q4_ROW_BYTES}]")
+    return shape[0], shape[1]
 
 
 def _rows_of(name: str, t, n: int, h_kv: int, dev) -> int:
     """Elements between the rows of a bf16 [n, H_kv, d] tensor whose heads are packed."""
     import torch
-    _dev_tensor(name, t, torch.bfloat16, dev, contiguous=False)
-    if t.dim() != 3 or int(t.shape[0]) != n or int(t.shape[1]) != h_kv:
+    if t.dtype is not torch.bfloat16 or t.device != dev or not t.is_cuda:
+        raise ValueError(f"{name} must be a bf16 tensor on {dev}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != n or shape[1] != h_kv:
         raise ValueError(f"{name} must be [{n}, {h_kv}, d]")
-    d = int(t.shape[2])
+    row = h_kv * shape[2]
     if n == 0:
-        return h_kv * d
-    if t.stride(2) != 1 or (h_kv > 1 and t.stride(1) != d):
+        return row
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (h_kv > 1 and s1 != shape[2]):
         raise ValueError(f"{name}: a row's heads must be packed")
-    return int(t.stride(0)) if n > 1 else h_kv * d
+    return s0 if n > 1 else row
 
 
 def kv_append_q4(k_new, v_new, k_pages, v_pages, slots, page_size: int, k_scale: float = 1.0,
@@ -305,18 +316,16 @@ def kv_append_q4(k_new, v_new, k_pages, v_pages, slots, page_size: int, k_scale:
     """Write new K/V rows (bf16 [R, H_kv, 128], rows may be strided) into 4-bit
     pools at `slots` (int64 [R]; negative: the row is skipped)."""
     import torch
-    dev, n = k_pages.device, int(slots.numel())
+    dev, n = k_pages.device, slots.numel()
     num_pages, h_kv = _q4_pools(k_pages, v_pages, page_size, dev)
-    _dev_tensor("slots", slots, torch.int64, dev, (n,))
+    _need("slots", slots, torch.int64, dev, (n,))
     ks, vs = _rows_of("k_new", k_new, n, h_kv, dev), _rows_of("v_new", v_new, n, h_kv, dev)
-    if k_new.shape != v_new.shape:
+    d = k_new.shape[2]
+    if v_new.shape[2] != d:
         raise ValueError("k_new / v_new differ in shape")
-    guard, handle = _on(dev, stream)
-    with guard:
-        _check(load().fanout_kv_append_q4(
-            k_new.data_ptr(), v_new.data_ptr(), ks, vs, k_pages.data_ptr(), v_pages.data_ptr(),
-            slots.data_ptr(), n, num_pages, h_kv, int(k_new.shape[2]), int(page_size),
-            float(k_scale), float(v_scale), handle), "fanout_kv_append_q4")
+    _device_call("fanout_kv_append_q4", dev, stream, k_new.data_ptr(), v_new.data_ptr(), ks, vs,
+                 k_pages.data_ptr(), v_pages.data_ptr(), slots.data_ptr(), n, num_pages, h_kv, d,
+                 page_size, k_scale, v_scale)
 
 
 def kv_read_q4(k_pages, v_pages, slots, page_size: int, k_scale: float = 1.0,
@@ -324,22 +333,20 @@ def kv_read_q4(k_pages, v_pages, slots, page_size: int, k_scale: float = 1.0,
     """The bf16 rows [R, H_kv, 128] that `slots` of 4-bit pools stand for: (k, v).
     Rows with a negative slot are left as they were (undefined when allocated here)."""
     import torch
-    dev, n = k_pages.device, int(slots.numel())
+    dev, n = k_pages.device, slots.numel()
     num_pages, h_kv = _q4_pools(k_pages, v_pages, page_size, dev)
-    _dev_tensor("slots", slots, torch.int64, dev, (n,))
+    _need("slots", slots, torch.int64, dev, (n,))
     if k_out is None:
         k_out = torch.empty((n, h_kv, 128), dtype=torch.bfloat16, device=dev)
     if v_out is None:
         v_out = torch.empty((n, h_kv, 128), dtype=torch.bfloat16, device=dev)
     ks, vs = _rows_of("k_out", k_out, n, h_kv, dev), _rows_of("v_out", v_out, n, h_kv, dev)
-    if k_out.shape != v_out.shape:
+    d = k_out.shape[2]
+    if v_out.shape[2] != d:
         raise ValueError("k_out / v_out differ in shape")
-    guard, handle = _on(dev, stream)
-    with guard:
-        _check(load().fanout_kv_read_q4(
-            k_pages.data_ptr(), v_pages.data_ptr(), slots.data_ptr(), n, num_pages, h_kv,
-            int(k_out.shape[2]), int(page_size), float(k_scale), float(v_scale),
-            k_out.data_ptr(), v_out.data_ptr(), ks, vs, handle), "fanout_kv_read_q4")
+    _device_call("fanout_kv_read_q4", dev, stream, k_pages.data_ptr(), v_pages.data_ptr(),
+                 slots.data_ptr(), n, num_pages, h_kv, d, page_size, k_scale, v_scale,
+                 k_out.data_ptr(), v_out.data_ptr(), ks, vs)
     return k_out, v_out
 
 
@@ -349,16 +356,11 @@ def copy_pages_q4(k_pages, v_pages, pairs, page_size: int, stream=None) -> None:
     import torch
     dev = k_pages.device
     num_pages, h_kv = _q4_pools(k_pages, v_pages, page_size, dev)
-    _dev_tensor("pairs", pairs, torch.int32, dev)
-    if pairs.dim() != 2 or int(pairs.shape[1]) != 2:
-        raise ValueError("pairs must be [n, 2]")
+    _need("pairs", pairs, torch.int32, dev, (pairs.shape[0], 2))
     # a block of page_size * 72 bytes as page_size / 2 rows of 72 16-bit values
-    guard, handle = _on(dev, stream)
-    with guard:
-        _check(load().fanout_copy_pages(k_pages.data_ptr(), v_pages.data_ptr(), pairs.data_ptr(),
-                                        int(pairs.shape[0]), int(page_size) // 2, num_pages, h_kv,
-                                        Q4_ROW_BYTES, int(page_size) // 2, handle),
-               "fanout_copy_pages")
+    _device_call("fanout_copy_pages", dev, stream, k_pages.data_ptr(), v_pages.data_ptr(),
+                 pairs.data_ptr(), pairs.shape[0], page_size // 2, num_pages, h_kv, Q4_ROW_BYTES,
+                 page_size // 2)
 
 
 def plan(suffix_lens, q_rows, prefix_len: int, h_q: int, h_kv: int, page_size: int,
@@ -451,32 +453,38 @@ def attn(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens: Sequence
     return out, lse
 
 
-def _attn_tensors(q, k_pages, v_pages, pool_dtype, page_table, suffix_lens, q_rows, h_q: int,
-                  page_size: int, out, lse, out_dtype: str, want_lse: bool):
-    """Checks and outputs the two calls below share: (suffix lens, q rows, d, out
-    dtype code, out, lse, max pages)."""
+def _lens(suffix_lens, q_rows):
+    """Host lengths of a call as one int32 array [2, B]: (array, address, B, rows)."""
+    if len(suffix_lens) != len(q_rows):
+        raise ValueError("suffix_lens and q_rows differ in length")
+    both = np.array((suffix_lens, q_rows), dtype=np.int32)
+    if both.ndim != 2:
+        raise ValueError("suffix_lens and q_rows must be sequences of integers")
+    rows = sum(q_rows) if type(q_rows) is list else int(both[1].sum())
+    return both, both.ctypes.data, both.shape[1], rows
+
+
+def _attn_out(q, page_table, R: int, B: int, h_q: int, out, lse, out_dtype: str, want_lse: bool):
+    """Checks and outputs the two calls below share: (out dtype code, out, lse)."""
     import torch
-    sl, tq = _i32arr(suffix_lens), _i32arr(q_rows)
-    if sl.ndim != 1 or sl.shape != tq.shape:
-        raise ValueError("suffix_lens and q_rows must be sequences of one length")
-    R, d, dev = int(tq.sum()), int(q.shape[-1]), q.device
+    dev, d = q.device, q.shape[-1]
     if out_dtype not in ("f32", "bf16"):
         raise ValueError("out_dtype must be 'f32' or 'bf16'")
     dt, code = (torch.float32, OUT_F32) if out_dtype == "f32" else (torch.bfloat16, OUT_BF16)
-    _dev_tensor("q", q, torch.bfloat16, dev, (R, h_q, d))
-    _dev_tensor("page_table", page_table, torch.int32, dev)
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        _dev_tensor(name, t, pool_dtype, dev)
-    if page_table.dim() != 2 or int(page_table.shape[0]) != int(sl.shape[0]):
+    shape = (R, h_q, d)
+    _need("q", q, torch.bfloat16, dev, shape)
+    _need("page_table", page_table, torch.int32, dev)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [num_branches, max_pages]")
     if out is None:
-        out = torch.empty((R, h_q, d), dtype=dt, device=dev)
-    _dev_tensor("out", out, dt, dev, (R, h_q, d))
-    if lse is None and want_lse:
-        lse = torch.empty((R, h_q), dtype=torch.float32, device=dev)
+        out = torch.empty(shape, dtype=dt, device=dev)
+    else:
+        _need("out", out, dt, dev, shape)
     if lse is not None:
-        _dev_tensor("lse", lse, torch.float32, dev, (R, h_q))
-    return sl, tq, d, code, out, lse, int(page_table.shape[1])
+        _need("lse", lse, torch.float32, dev, (R, h_q))
+    elif want_lse:
+        lse = torch.empty((R, h_q), dtype=torch.float32, device=dev)
+    return code, out, lse
 
 
 def attn_window(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q_rows, h_q: int,
@@ -485,18 +493,17 @@ def attn_window(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q
     """attn(), causal, where a row at pos sees keys j <= pos with j > pos - window
     or j < sinks. Pages that no row sees may have been given back."""
     import torch
-    sl, tq, d, code, out, lse, width = _attn_tensors(
-        q, k_pages, v_pages, torch.bfloat16, page_table, suffix_lens, q_rows, h_q, page_size, out,
-        lse, out_dtype, want_lse)
-    if k_pages.shape != v_pages.shape or tuple(k_pages.shape[1:]) != (h_kv, page_size, d):
-        raise ValueError("k_pages / v_pages must be [num_pages, H_kv, page, d]")
-    guard, handle = _on(q.device, stream)
-    with guard:
-        _check(load().fanout_attn_window(
-            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-            int(prefix_len), _ptr(sl), _ptr(tq), int(sl.shape[0]), width, int(k_pages.shape[0]),
-            int(h_q), int(h_kv), d, int(page_size), float(scale), int(window), int(sinks),
-            out.data_ptr(), code, _opt_ptr(lse), handle), "fanout_attn_window")
+    held, lens, B, R = _lens(suffix_lens, q_rows)
+    code, out, lse = _attn_out(q, page_table, R, B, h_q, out, lse, out_dtype, want_lse)
+    dev, d = q.device, q.shape[-1]
+    num_pages = k_pages.shape[0]
+    pool = (num_pages, h_kv, page_size, d)
+    _need("k_pages", k_pages, torch.bfloat16, dev, pool)
+    _need("v_pages", v_pages, torch.bfloat16, dev, pool)
+    _device_call("fanout_attn_window", dev, stream, q.data_ptr(), k_pages.data_ptr(),
+                 v_pages.data_ptr(), page_table.data_ptr(), prefix_len, lens, lens + 4 * B, B,
+                 page_table.shape[1], num_pages, h_q, h_kv, d, page_size, scale, window, sinks,
+                 out.data_ptr(), code, _ptr_or_none(lse))
     return out, lse
 
 
@@ -506,21 +513,17 @@ def attn_q4(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q_row
             out_dtype: str = "f32", want_lse: bool = True, stream=None):
     """attn() over 4-bit pools (uint8 [num_pages, H_kv, page_size * 72]); window and
     sinks as in attn_window (0, 0: none)."""
-    import torch
-    sl, tq, d, code, out, lse, width = _attn_tensors(
-        q, k_pages, v_pages, torch.uint8, page_table, suffix_lens, q_rows, h_q, page_size, out,
-        lse, out_dtype, want_lse)
-    num_pages, heads = _q4_pools(k_pages, v_pages, page_size, q.device)
+    held, lens, B, R = _lens(suffix_lens, q_rows)
+    code, out, lse = _attn_out(q, page_table, R, B, h_q, out, lse, out_dtype, want_lse)
+    dev = q.device
+    num_pages, heads = _q4_pools(k_pages, v_pages, page_size, dev)
     if heads != h_kv:
         raise ValueError(f"pools hold {heads} KV heads, not {h_kv}")
-    guard, handle = _on(q.device, stream)
-    with guard:
-        _check(load().fanout_attn_q4(
-            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-            int(prefix_len), _ptr(sl), _ptr(tq), int(sl.shape[0]), width, num_pages, int(h_q),
-            int(h_kv), d, int(page_size), float(scale), int(bool(causal)), float(k_scale),
-            float(v_scale), int(window), int(sinks), out.data_ptr(), code, _opt_ptr(lse), handle),
-            "fanout_attn_q4")
+    _device_call("fanout_attn_q4", dev, stream, q.data_ptr(), k_pages.data_ptr(),
+                 v_pages.data_ptr(), page_table.data_ptr(), prefix_len, lens, lens + 4 * B, B,
+                 page_table.shape[1], num_pages, h_q, h_kv, q.shape[-1], page_size, scale,
+                 1 if causal else 0, k_scale, v_scale, window, sinks, out.data_ptr(), code,
+                 _ptr_or_none(lse))
     return out, lse
 
 
