@@ -146,7 +146,8 @@ FANOUT_API int fanout_extend(int32_t *page_table, int32_t num_branches,
  * free list and tables are device memory, ordered on `stream`. "AHBM Agentic
  * Runtime Architecture", section 3.1 "Fan-out context structure".
  *   prefix_pages  dev int32 [ceil(prefix_len / page_size)].
- *   suffix_lens   dev int32 [B], B <= 4096 (FANOUT_EUNSUPPORTED above).
+ *   suffix_lens   dev int32 [B], B <= 4096, max_pages_per_branch <= 2^24
+ *                 (FANOUT_EUNSUPPORTED above).
  *   free_pages    dev int32 [n_free]; the call takes entries from *used_in on,
  *                 branch 0 first.
  *   used_in       dev int32 [1] or NULL (0): entries taken before this call.
@@ -243,6 +244,7 @@ FANOUT_API int fanout_kv_append(const void *k_new, const void *v_new, void *k_pa
  *                 past num_pages * page_size: skipped, and fanout_last_error()
  *                 reports FANOUT_EINVAL. A slot given to two rows holds
  *                 unspecified bytes of them.
+ * n_rows * H_kv < 2^31, else FANOUT_EUNSUPPORTED.
  * Infinities are held as the largest value of their group's scale; a NaN is held
  * as 0 and reported as FANOUT_EINVAL, so no cached row can poison others. Can be
  * captured (first call on a device outside a capture).

@@ -46,10 +46,6 @@
 // brings the next unit's Q into L2 one unit ahead; each softmax warp keeps its
 // unit's output fields in a shared-memory slot, and each group runs its
 // epilogue once dry before the first unit so that code is warm.
-// ROWS instances serve row plans (a sliding window with first keys that stay
-// visible): each row's position comes from a table, so that rows of different
-// branches can share a unit, a unit may sweep its first keys as tiles in front
-// of its own range, and page ids are checked before they are read through.
 // The producer signals the dependent merge launch once it has issued its last
 // copies. Every wait is bounded (mbar_wait); on expiry the CTA records
 // FANOUT_ETIMEOUT, drains its own in-flight copies and MMAs, frees TMEM and
@@ -62,7 +58,6 @@
 #include "fanout_internal.h"
 #include "merge_row.cuh"
 #include "ptx_sm100.cuh"
-#include "row_unit.cuh"
 
 namespace fanout {
 namespace {
@@ -138,10 +133,8 @@ __device__ __forceinline__ void record_timeout(const SplitParams& p, volatile in
     }
 }
 
-template <bool ROWS>
-__device__ __forceinline__ int unit_tiles(const SplitParams& p, const Unit& u) {
-    return ROWS ? first_tiles(u, p.split_at) + range_tiles(u, p.page_size)
-                : (u.key_end - u.key_begin + kBN - 1) / kBN;
+__device__ __forceinline__ int unit_tiles(const Unit& u) {
+    return (u.key_end - u.key_begin + kBN - 1) / kBN;
 }
 
 // Query tiles of a unit that hold at least one row.
@@ -182,7 +175,7 @@ __device__ __forceinline__ bool load_q(const SplitParams& p, const Smem<NQ>& sm,
     return true;
 }
 
-template <int NQ, bool ROWS>
+template <int NQ>
 __device__ void producer_warp(const SplitParams& p, const Smem<NQ>& sm, const CUtensorMap* tm_q,
                               const CUtensorMap* tm_k, const CUtensorMap* tm_v) {
     using C = Cfg<NQ>;
@@ -201,7 +194,8 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ>& sm, const CU
     const int ui_end = p.cta_first[blockIdx.x + 1];
     for (int ui = p.cta_first[blockIdx.x]; ui < ui_end && ok; ++ui) {
         const Unit u = p.units[ui];
-        if (unit_tiles<ROWS>(p, u) <= 0) continue;
+        const int n_tiles = unit_tiles(u);
+        if (n_tiles <= 0) continue;
         const int nq = unit_nq<NQ>(u, p.tpt);
         // The CTA's first unit loads its Q tiles first. A later unit's Q waits
         // for the previous unit's last S MMAs, so its first K/V tile is issued
@@ -215,7 +209,7 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ>& sm, const CU
         if (!ok) break;
         if (lane == 0 && ui + 1 < ui_end) {
             const Unit un = p.units[ui + 1];
-            if (unit_tiles<ROWS>(p, un) > 0) {
+            if (unit_tiles(un) > 0) {
                 for (int x = 0; x < unit_nq<NQ>(un, p.tpt); ++x) {
                     const int y = un.kv_head * p.G, z = un.tok_begin + x * p.tpt;
                     ptx::tma_prefetch_3d(tm_q, 0, y, z);
@@ -225,96 +219,79 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ>& sm, const CU
         }
         // Page ids of the unit, 32 per window (lane l holds page l of the window),
         // loaded one window ahead so no tile waits on the page table.
-        // A unit of a row plan may have a run of first keys before its own range.
-        bool first_tile = true;
-        for (int run = ROWS && u.pos_base > 0 ? 0 : 1; run < 2 && ok; ++run) {
-            const int key_begin = run == 0 ? first_begin(u, p.split_at)
-                                           : ROWS ? range_begin(u, ps) : u.key_begin;
-            const int key_end = run == 0 ? u.pos_base : u.key_end;
-            const int n_front = ROWS && run == 1 ? u.key_begin - key_begin : 0;  // rows to zero
-            const int n_tiles = (key_end - key_begin + kBN - 1) / kBN;
-            const int32_t* prow = p.page_table + static_cast<int64_t>(u.branch) * p.max_pages +
-                                  key_begin / ps;
-            const int n_pages_unit = (key_end - key_begin + ps - 1) / ps;
-            const int ppt = kBN / ps;  // pages per tile: 1, 2, 4 or 8 (divides 32)
-            auto load_window = [&](int w) -> int {
-                const int idx = w * 32 + lane;
-                return idx < n_pages_unit ? __ldg(prow + idx) : 0;
-            };
-            int win = 0;
-            int win_cur = load_window(0);
-            int win_nxt = load_window(1);
-            for (int j = 0; j < n_tiles && ok; ++j) {
-                const int kt = key_begin + j * kBN;
-                const int n_valid = min(kBN, key_end - kt);
-                const int n_pg = (n_valid + ps - 1) / ps;
-                const int rel = j * ppt;  // first page of the tile, relative to the unit
-                if ((rel >> 5) != win) {
-                    win = rel >> 5;
-                    win_cur = win_nxt;
-                    win_nxt = load_window(win + 1);
-                }
-                const int pg_off = rel & 31;
-                for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
-                    const uint32_t stage = it % C::kStages;
-                    const uint32_t par = (it / C::kStages) & 1u;
-                    bool w = true;
-                    if (lane == 0) w = ptx::mbar_wait(sm.bar(C::BAR_EMPTY + stage), par ^ 1u, lim, abort);
-                    if (!__shfl_sync(0xffffffffu, w, 0)) { ok = false; if (lane == 0) record_timeout(p, abort, 2); break; }
-                    const uint32_t dst = sm.base + C::kSmemRing + stage * kTileBytes;
-                    const CUtensorMap* tm = kv == 0 ? tm_k : tm_v;
-                    const bool partial = n_valid < kBN || (ROWS && j == 0 && n_front > 0);
-                    const uint32_t bar = partial ? sm.bar(C::BAR_AUX) : sm.bar(C::BAR_FULL + stage);
-                    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n_pg * ps) * 256u);
-                    {
-                        // one lane per page of the tile: the tile's copies go out in two
-                        // warp instructions (lane pg holds window entry pg_off + pg)
-                        int page = __shfl_sync(0xffffffffu, win_cur, (pg_off + lane) & 31);
-                        if (lane < n_pg) {
-                            if (ROWS) page = checked_page(p, page);
-                            const int row = (page * p.H_kv + u.kv_head) * ps;
-                            const uint32_t off = static_cast<uint32_t>(lane * ps) * 128u;
-                            ptx::tma_load_2d(dst + off, tm, bar, 0, row);
-                            ptx::tma_load_2d(dst + kHalfBytes + off, tm, bar, 64, row);
-                        }
-                    }
-                    if (lane == 0) {
-                        issued_mask |= 1u << stage;
-                        issued_par = (issued_par & ~(1u << stage)) | (par << stage);
-                    }
-                    if (partial) {
-                        // Tail tile: wait for the pages, then zero every row past the
-                        // last valid key so no stale value reaches the MMAs.
-                        aux_pending = true;
-                        bool w2 = true;
-                        if (lane == 0) w2 = ptx::mbar_wait(sm.bar(C::BAR_AUX), aux_phase, lim, abort);
-                        if (!__shfl_sync(0xffffffffu, w2, 0)) { ok = false; if (lane == 0) record_timeout(p, abort, 3); break; }
-                        aux_pending = false;
-                        aux_phase ^= 1u;
-                        const int n_zero = (kBN - n_valid) * 16;  // 16-byte chunks, both halves
-                        for (int idx = lane; idx < n_zero; idx += 32) {
-                            const int r = n_valid + (idx >> 4);
-                            const int ch = idx & 15;
-                            const uint32_t a = dst + (ch >> 3) * kHalfBytes + r * 128 + (ch & 7) * 16;
-                            ptx::st_shared_v4(a, 0u, 0u, 0u, 0u);
-                        }
-                        // and the keys of its first page that no row sees any more
-                        for (int idx = lane; ROWS && j == 0 && idx < n_front * 16; idx += 32) {
-                            const int r = idx >> 4, ch = idx & 15;
-                            const uint32_t a = dst + (ch >> 3) * kHalfBytes + r * 128 + (ch & 7) * 16;
-                            ptx::st_shared_v4(a, 0u, 0u, 0u, 0u);
-                        }
-                        ptx::fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(sm.bar(C::BAR_FULL + stage));
+        const int32_t* prow = p.page_table + static_cast<int64_t>(u.branch) * p.max_pages +
+                              u.key_begin / ps;
+        const int n_pages_unit = (u.key_end - u.key_begin + ps - 1) / ps;
+        const int ppt = kBN / ps;  // pages per tile: 1, 2, 4 or 8 (divides 32)
+        auto load_window = [&](int w) -> int {
+            const int idx = w * 32 + lane;
+            return idx < n_pages_unit ? __ldg(prow + idx) : 0;
+        };
+        int win = 0;
+        int win_cur = load_window(0);
+        int win_nxt = load_window(1);
+        for (int j = 0; j < n_tiles && ok; ++j) {
+            const int kt = u.key_begin + j * kBN;
+            const int n_valid = min(kBN, u.key_end - kt);
+            const int n_pg = (n_valid + ps - 1) / ps;
+            const int rel = j * ppt;  // first page of the tile, relative to the unit
+            if ((rel >> 5) != win) {
+                win = rel >> 5;
+                win_cur = win_nxt;
+                win_nxt = load_window(win + 1);
+            }
+            const int pg_off = rel & 31;
+            for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
+                const uint32_t stage = it % C::kStages;
+                const uint32_t par = (it / C::kStages) & 1u;
+                bool w = true;
+                if (lane == 0) w = ptx::mbar_wait(sm.bar(C::BAR_EMPTY + stage), par ^ 1u, lim, abort);
+                if (!__shfl_sync(0xffffffffu, w, 0)) { ok = false; if (lane == 0) record_timeout(p, abort, 2); break; }
+                const uint32_t dst = sm.base + C::kSmemRing + stage * kTileBytes;
+                const CUtensorMap* tm = kv == 0 ? tm_k : tm_v;
+                const bool partial = n_valid < kBN;
+                const uint32_t bar = partial ? sm.bar(C::BAR_AUX) : sm.bar(C::BAR_FULL + stage);
+                if (lane == 0) ptx::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n_pg * ps) * 256u);
+                {
+                    // one lane per page of the tile: the tile's copies go out in two
+                    // warp instructions (lane pg holds window entry pg_off + pg)
+                    const int page = __shfl_sync(0xffffffffu, win_cur, (pg_off + lane) & 31);
+                    if (lane < n_pg) {
+                        const int row = (page * p.H_kv + u.kv_head) * ps;
+                        const uint32_t off = static_cast<uint32_t>(lane * ps) * 128u;
+                        ptx::tma_load_2d(dst + off, tm, bar, 0, row);
+                        ptx::tma_load_2d(dst + kHalfBytes + off, tm, bar, 64, row);
                     }
                 }
-                if (k > 0 && first_tile) {
+                if (lane == 0) {
+                    issued_mask |= 1u << stage;
+                    issued_par = (issued_par & ~(1u << stage)) | (par << stage);
+                }
+                if (partial) {
+                    // Tail tile: wait for the pages, then zero every row past the
+                    // last valid key so no stale value reaches the MMAs.
+                    aux_pending = true;
+                    bool w2 = true;
+                    if (lane == 0) w2 = ptx::mbar_wait(sm.bar(C::BAR_AUX), aux_phase, lim, abort);
+                    if (!__shfl_sync(0xffffffffu, w2, 0)) { ok = false; if (lane == 0) record_timeout(p, abort, 3); break; }
+                    aux_pending = false;
+                    aux_phase ^= 1u;
+                    const int n_zero = (kBN - n_valid) * 16;  // 16-byte chunks, both halves
+                    for (int idx = lane; idx < n_zero; idx += 32) {
+                        const int r = n_valid + (idx >> 4);
+                        const int ch = idx & 15;
+                        const uint32_t a = dst + (ch >> 3) * kHalfBytes + r * 128 + (ch & 7) * 16;
+                        ptx::st_shared_v4(a, 0u, 0u, 0u, 0u);
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(sm.bar(C::BAR_FULL + stage));
+                }
+            }
+            if (k > 0 && j == 0) {
 #pragma unroll
-                    for (int x = 0; x < NQ; ++x)
-                        if (ok && x < nq) ok = load_q<NQ>(p, sm, tm_q, u, x, q_loads[x]);
-                }
-                first_tile = false;
+                for (int x = 0; x < NQ; ++x)
+                    if (ok && x < nq) ok = load_q<NQ>(p, sm, tm_q, u, x, q_loads[x]);
             }
         }
         ++k;
@@ -430,7 +407,7 @@ __device__ __forceinline__ bool issue_held(const SplitParams& p, const Smem<NQ>&
 // while the tensor core works on the other's products (ping-pong); the unit's
 // last P.V_1 is issued before the next unit starts. Units with one query tile
 // run S_0(j), P.V_0(j).
-template <int NQ, bool ROWS>
+template <int NQ>
 __device__ void mma_thread_pair(const SplitParams& p, const Smem<NQ>& sm, uint32_t tmem) {
     using C = Cfg<NQ>;
     const uint64_t lim = p.wait_limit_ns;
@@ -452,7 +429,7 @@ __device__ void mma_thread_pair(const SplitParams& p, const Smem<NQ>& sm, uint32
     const int ui_end = p.cta_first[blockIdx.x + 1];
     for (int ui = p.cta_first[blockIdx.x]; ui < ui_end && ok; ++ui) {
         const Unit u = p.units[ui];
-        const int n = unit_tiles<ROWS>(p, u);
+        const int n = unit_tiles(u);
         if (n <= 0) continue;
         const bool two = unit_nq<NQ>(u, p.tpt) == 2;
         if (!ptx::mbar_wait(sm.bar(C::BAR_QFULL), qu0 & 1u, lim, abort) ||
@@ -517,7 +494,7 @@ __device__ void mma_thread_pair(const SplitParams& p, const Smem<NQ>& sm, uint32
 // the CTA's tiles). A unit's last P.V is held back and issued after the next
 // unit's first S, so the S double buffer stays full across the boundary; if
 // that unit's Q has not landed yet the held P.V goes first.
-template <int NQ, bool ROWS>
+template <int NQ>
 __device__ void mma_thread_stream(const SplitParams& p, const Smem<NQ>& sm, uint32_t tmem) {
     using C = Cfg<NQ>;
     const uint64_t lim = p.wait_limit_ns;
@@ -533,7 +510,7 @@ __device__ void mma_thread_stream(const SplitParams& p, const Smem<NQ>& sm, uint
     const int ui_end = p.cta_first[blockIdx.x + 1];
     for (int ui = p.cta_first[blockIdx.x]; ui < ui_end && ok; ++ui) {
         const Unit u = p.units[ui];
-        const int n = unit_tiles<ROWS>(p, u);
+        const int n = unit_tiles(u);
         if (n <= 0) continue;
         if (has_pend && !ptx::mbar_test_wait(sm.bar(C::BAR_QFULL), qu & 1u) &&
             !(ok = issue_held<NQ>(p, sm, tmem, pend, has_pend)))
@@ -591,7 +568,7 @@ __device__ __forceinline__ float sum8(const float (&a)[8]) {
 // Group x owns query tile x of every unit (rows 128x .. 128x+127); thread i
 // owns row i of the tile (TMEM lane i). A warp whose 32 rows are all padding
 // follows the barrier protocol but skips the TMEM traffic and the math.
-template <int NQ, bool ROWS>
+template <int NQ>
 __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t tmem, int x) {
     using C = Cfg<NQ>;
     const int warp = threadIdx.x >> 5;
@@ -620,7 +597,7 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
     for (int ui = ui_first < ui_end ? ui_first - 1 : ui_first; ui < ui_end && ok; ++ui) {
         const bool dry = ui < ui_first;
         const Unit u = p.units[dry ? ui_first : ui];
-        const int n_tiles = dry ? 0 : unit_tiles<ROWS>(p, u);
+        const int n_tiles = dry ? 0 : unit_tiles(u);
         if (!dry && (n_tiles <= 0 || x >= unit_nq<NQ>(u, p.tpt))) continue;
         // row within the unit: tile x holds its tokens x * tpt .. (128 / G of them, so
         // a G that does not divide 128 leaves the tile's last rows empty)
@@ -635,16 +612,11 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
         const bool active = dry || __any_sync(0xffffffffu, row_valid);
         // Only the key start and this row's visible end stay live through the
         // tile loop (registers).
-        const int key_begin = ROWS ? range_begin(u, p.page_size) : u.key_begin;
-        const int vis_end = ROWS ? 0 : row_valid ? min(u.key_end, u.pos_base + u.tok_begin + tile_tok + row / p.G + 1) : 0;
-        // a row plan's row sees keys [lo, pos] and keys < sinks, of this tile's run
-        const int n_first = ROWS ? first_tiles(u, p.split_at) : 0;
-        const int run_begin = ROWS ? first_begin(u, p.split_at) : 0;
-        const int row_end = ROWS && row_valid && !dry ? p.tok_pos[u.tok_begin + tile_tok + row / p.G] + 1 : 0;
+        const int key_begin = u.key_begin;
+        const int vis_end = row_valid ? min(u.key_end, u.pos_base + u.tok_begin + tile_tok + row / p.G + 1) : 0;
         float m_ref = -INFINITY, l_run = 0.f;
         for (int j = 0; j < n_tiles; ++j, ++jt) {
-            const int kt = ROWS && j < n_first ? run_begin + j * kBN
-                                               : key_begin + (j - n_first) * kBN;
+            const int kt = key_begin + j * kBN;
             bool w = ptx::mbar_wait(sm.gbar(x, SFULL), jt & 1u, lim, abort);
             if (!__all_sync(0xffffffffu, w)) { ok = false; record_timeout(p, abort, 20); break; }
             ptx::tc_fence_after();
@@ -657,14 +629,8 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
             const uint32_t colS = s_col<NQ>(x, jt);
             float corr = 1.f;
             if (active) {
-                const int lim_c =
-                    ROWS ? min(row_end, j < n_first ? u.pos_base : u.key_end) - kt : vis_end - kt;
-                // columns below lo_c are behind the row's window, unless below sink_c
-                const int lo_c = ROWS ? row_end - p.window - kt : 0;
-                // (a run of first keys before the range leaves none of them to it)
-                const int sink_c = ROWS && (j < n_first || n_first == 0) ? p.sinks - kt : 0;
-                const bool full = __all_sync(
-                    0xffffffffu, lim_c >= kBN && (!ROWS || lo_c <= 0 || sink_c >= kBN));
+                const int lim_c = vis_end - kt;
+                const bool full = __all_sync(0xffffffffu, lim_c >= kBN);
                 uint32_t s[kBN];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -679,8 +645,7 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
                 if (!full) {
 #pragma unroll
                     for (int c = 0; c < kBN; ++c)
-                        if (c >= lim_c || (ROWS && c < lo_c && c >= sink_c))
-                            s[c] = __float_as_uint(-INFINITY);
+                        if (c >= lim_c) s[c] = __float_as_uint(-INFINITY);
                 }
                 float mx[8];
 #pragma unroll
@@ -1055,7 +1020,7 @@ __device__ __noinline__ void merge_tail(const SplitParams& p, const Smem<NQ>& sm
     }
 }
 
-template <int NQ, bool ROWS>
+template <int NQ>
 __global__ void __launch_bounds__(Cfg<NQ>::kThreads, 1) __maxnreg__(NQ == 2 ? 200 : 255)
     attn_fwd_kernel(const __grid_constant__ SplitParams p,
                     const __grid_constant__ CUtensorMap tm_q,
@@ -1111,15 +1076,15 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, 1) __maxnreg__(NQ == 2 ? 20
     const uint32_t tmem = *sm.tmem_slot();
 
     if (warp == 0) {
-        producer_warp<NQ, ROWS>(p, sm, &tm_q, &tm_k, &tm_v);
+        producer_warp<NQ>(p, sm, &tm_q, &tm_k, &tm_v);
     } else if (warp == 1) {
         if (lane == 0) {
-            if (NQ == 2) mma_thread_pair<NQ, ROWS>(p, sm, tmem);
-            else mma_thread_stream<NQ, ROWS>(p, sm, tmem);
+            if (NQ == 2) mma_thread_pair<NQ>(p, sm, tmem);
+            else mma_thread_stream<NQ>(p, sm, tmem);
         }
         __syncwarp();
     } else {
-        softmax_group<NQ, ROWS>(p, sm, tmem, (warp - 2) >> 2);
+        softmax_group<NQ>(p, sm, tmem, (warp - 2) >> 2);
     }
 
     ptx::tc_fence_before();
@@ -1128,10 +1093,10 @@ __global__ void __launch_bounds__(Cfg<NQ>::kThreads, 1) __maxnreg__(NQ == 2 ? 20
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, C::kTmemCols);
     }
-    if (!ROWS && p.fused_merge) merge_tail<NQ>(p, sm);
+    if (p.fused_merge) merge_tail<NQ>(p, sm);
 }
 
-template <int NQ, bool ROWS>
+template <int NQ>
 cudaError_t launch_nq(const SplitParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                       const CUtensorMap& tm_v, int grid, bool cooperative, cudaStream_t stream) {
     // The shared-memory attribute is set once per device (under a lock: calls
@@ -1145,7 +1110,7 @@ cudaError_t launch_nq(const SplitParams& p, const CUtensorMap& tm_q, const CUten
     if (!known || !attr_set[dev].load(std::memory_order_acquire)) {
         std::lock_guard<std::mutex> lk(attr_mu);
         if (!known || !attr_set[dev].load(std::memory_order_relaxed)) {
-            e = cudaFuncSetAttribute(attn_fwd_kernel<NQ, ROWS>,
+            e = cudaFuncSetAttribute(attn_fwd_kernel<NQ>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      Cfg<NQ>::kSmemAlloc);
             if (e != cudaSuccess) return e;
@@ -1162,7 +1127,7 @@ cudaError_t launch_nq(const SplitParams& p, const CUtensorMap& tm_q, const CUten
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cooperative ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, attn_fwd_kernel<NQ, ROWS>, p, tm_q, tm_k, tm_v);
+    return cudaLaunchKernelEx(&cfg, attn_fwd_kernel<NQ>, p, tm_q, tm_k, tm_v);
 }
 
 }  // namespace
@@ -1170,11 +1135,8 @@ cudaError_t launch_nq(const SplitParams& p, const CUtensorMap& tm_q, const CUten
 cudaError_t launch_split_attn(const SplitParams& p, const CUtensorMap& tm_q,
                               const CUtensorMap& tm_k, const CUtensorMap& tm_v, int grid,
                               bool cooperative, cudaStream_t stream) {
-    if (p.tok_pos != nullptr)  // a row plan
-        return p.nq == 2 ? launch_nq<2, true>(p, tm_q, tm_k, tm_v, grid, cooperative, stream)
-                         : launch_nq<1, true>(p, tm_q, tm_k, tm_v, grid, cooperative, stream);
-    return p.nq == 2 ? launch_nq<2, false>(p, tm_q, tm_k, tm_v, grid, cooperative, stream)
-                     : launch_nq<1, false>(p, tm_q, tm_k, tm_v, grid, cooperative, stream);
+    return p.nq == 2 ? launch_nq<2>(p, tm_q, tm_k, tm_v, grid, cooperative, stream)
+                     : launch_nq<1>(p, tm_q, tm_k, tm_v, grid, cooperative, stream);
 }
 
 }  // namespace fanout

@@ -107,6 +107,7 @@ struct AppendParams {
 // Page tables and slot maps built on the device (tables.cu). Every pointer is
 // device memory.
 constexpr int kMaxTableBranches = 4096;  // two int32 offsets per branch in shared memory
+constexpr int kMaxTablePages = 1 << 24;   // entries of a forked row
 struct TableParams {
     const int32_t* prefix_pages;  // fork
     const int32_t* suffix_lens;
@@ -137,7 +138,9 @@ struct Q4RowParams {
     int64_t k_stride, v_stride;  // elements between rows
     int64_t n_slots;             // num_pages * page_size
     int32_t n_rows, H_kv, page_shift;
+    int32_t align32;  // 1: every group of a row starts on 32 bytes
     float k_scale, v_scale;
+    float k_rcp6, v_rcp6;  // 1 / (6 scale), rounded to nearest
 };
 
 // Launchers (defined in the .cu files); return cudaError_t.
@@ -145,9 +148,9 @@ struct Q4RowParams {
 cudaError_t launch_split_attn(const SplitParams& p, const CUtensorMap& tm_q,
                               const CUtensorMap& tm_k, const CUtensorMap& tm_v, int grid,
                               bool cooperative, cudaStream_t stream);
-// Attention over 4-bit pools (row plans; never fused with the merge).
-cudaError_t launch_attn_q4(const SplitParams& p, const CUtensorMap& tm_q, int grid,
-                           cudaStream_t stream);
+// Row plans, over bf16 or 4-bit pools; never fused with the merge.
+cudaError_t launch_attn_rows(const SplitParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                             const CUtensorMap& tm_v, bool q4, int grid, cudaStream_t stream);
 cudaError_t launch_lse_merge(const MergeParams& p, cudaStream_t stream);
 cudaError_t err_word_ptr(int32_t** ptr);
 cudaError_t launch_copy_pages(void* k_pool, void* v_pool, const int32_t* pairs, int32_t n_pairs,

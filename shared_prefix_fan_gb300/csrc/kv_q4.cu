@@ -13,19 +13,27 @@
 // pair of neighbours to the same place of both halves of a register, which is
 // how the attention kernel widens them.
 //
-// One warp per (row, KV head): lanes 0..15 its K row, lanes 16..31 its V row,
-// 8 values (16 bytes of bf16, one code word) a lane; two lanes share a group.
+// A lane owns one group: 16 values (32 bytes of bf16), two code words and a scale;
+// 8 lanes make a K row, 8 its V row, so a warp handles two (row, KV head) pairs in
+// one pass, without exchanges. HBM-bound when there are many rows (656 bytes a pair
+// of K and V rows): 32 bytes a lane keep enough reads in flight (with 16, and a row
+// per warp, 8192 rows of 8 heads took 33 us in and out), and the work per value is
+// kept short: the quotients are products with the reciprocal, corrected (quotient,
+// below), the largest magnitude comes from packed maxima, codes from the e2m1
+// conversions (with fp32 divisions it took 47 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
 #include "fanout_internal.h"
+#include "ptx_sm100.cuh"
 
 namespace fanout {
 namespace {
 
 constexpr int kErrInval = 1;  // FANOUT_EINVAL
+constexpr int kWarps = 8;
 
 // Two fp32 -> e4m3 (low byte: lo), saturating.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -33,12 +41,14 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ float e4m3_f32(uint32_t byte) {
-    uint32_t h2;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(byte)));
+__device__ __forceinline__ float lo_f16_f32(uint32_t h2) {
     float f;
     asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(f) : "r"(h2));
     return f;
+}
+__device__ __forceinline__ float hi_f16_f32(uint32_t h2) { return lo_f16_f32(h2 >> 16); }
+__device__ __forceinline__ float e4m3_f32(uint32_t byte) {
+    return lo_f16_f32(ptx::f16x2_of_e4m3x2(byte));
 }
 // Eight fp32 -> a code word (the order above).
 __device__ __forceinline__ uint32_t e2m1_word(const float (&y)[8]) {
@@ -53,13 +63,13 @@ __device__ __forceinline__ uint32_t e2m1_word(const float (&y)[8]) {
         : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
     return w;
 }
-// e2m1 code (4 bits) -> fp32.
-__device__ __forceinline__ float e2m1_f32(uint32_t code) {
-    const uint32_t m = code & 7u;
-    // magnitudes below 2 are code / 2; from 2 on, exponent and half step as stored
-    const float a = m < 4 ? 0.5f * static_cast<float>(m)
-                          : static_cast<float>((2u + (m & 1u)) << ((m >> 1) - 2u));
-    return (code & 8u) ? -a : a;
+// x / den rounded to nearest, from r = 1 / den rounded to nearest: the quotient's
+// remainder is exact in one fused step, and adding its share rounds correctly
+// (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990). |x| <= 512 den here, and den is in [2e-33, 6e30].
+__device__ __forceinline__ float quotient(float x, float den, float r) {
+    const float q = x * r;
+    return fmaf(fmaf(-q, den, x), r, q);
 }
 
 struct Place {
@@ -72,83 +82,125 @@ __device__ __forceinline__ Place place_of(const Q4RowParams& p, int64_t slot, in
     return {block + off * 64, block + (static_cast<int64_t>(64) << p.page_shift) + off * 8};
 }
 
-__global__ void __launch_bounds__(256) append_q4_kernel(const Q4RowParams p) {
-    const int lane = threadIdx.x & 31, part = lane & 15;
-    const bool is_v = lane >= 16;
-    const int64_t items = static_cast<int64_t>(p.n_rows) * p.H_kv;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-    const float gs = is_v ? p.v_scale : p.k_scale;
-    const float c6 = 6.0f * gs;
-    for (int64_t item = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-         item < items; item += warps) {
-        const int64_t r = item / p.H_kv;
-        const int32_t h = static_cast<int32_t>(item - r * p.H_kv);
-        const int64_t slot = p.slots[r];
-        if (slot < 0) continue;  // a padded row
-        if (slot >= p.n_slots) {
-            if (lane == 0) atomicCAS(p.err, 0, kErrInval);
-            continue;
-        }
-        const __nv_bfloat16* src = is_v ? p.v_rows + r * p.v_stride : p.k_rows + r * p.k_stride;
-        const uint4 raw = *reinterpret_cast<const uint4*>(src + h * kHD + part * 8);
-        float x[8] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u),
-                      __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u),
-                      __uint_as_float(raw.z << 16), __uint_as_float(raw.z & 0xffff0000u),
-                      __uint_as_float(raw.w << 16), __uint_as_float(raw.w & 0xffff0000u)};
-        float top = 0.f;
-        bool nan = false;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (isnan(x[i])) {  // recorded, and held as 0: it must not reach other rows
-                nan = true;
-                x[i] = 0.f;
-            }
-            top = fmaxf(top, fabsf(x[i]));
-        }
-        if (nan) atomicCAS(p.err, 0, kErrInval);
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        const uint32_t sc = e4m3x2(__fdiv_rn(top, c6), 0.f) & 0xffu;
-        const float den = e4m3_f32(sc) * gs;
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = den > 0.f ? __fdiv_rn(x[i], den) : 0.f;
-        const Place at = place_of(p, slot, h);
-        uint8_t* pool = is_v ? p.v_pool : p.k_pool;
-        *reinterpret_cast<uint32_t*>(pool + at.codes + part * 4) = e2m1_word(y);
-        if ((part & 1) == 0) pool[at.scales + (part >> 1)] = static_cast<uint8_t>(sc);
+// The (row, head) pair of this half-warp and its slot; false when there is nothing
+// to do.
+__device__ __forceinline__ bool item_of(const Q4RowParams& p, uint32_t& r, uint32_t& h,
+                                        int64_t& slot) {
+    const uint32_t item = blockIdx.x * (2 * kWarps) + (threadIdx.x >> 4);  // < 2^31 + 16 (host check)
+    r = item / static_cast<uint32_t>(p.H_kv);
+    h = item - r * static_cast<uint32_t>(p.H_kv);
+    if (r >= static_cast<uint32_t>(p.n_rows)) return false;
+    slot = __ldg(p.slots + r);
+    if (slot < 0) return false;  // a padded row
+    if (slot >= p.n_slots) {
+        if ((threadIdx.x & 15) == 0) atomicCAS(p.err, 0, kErrInval);
+        return false;
     }
+    return true;
 }
 
-__global__ void __launch_bounds__(256) read_q4_kernel(const Q4RowParams p) {
-    const int lane = threadIdx.x & 31, part = lane & 15;
-    const bool is_v = lane >= 16;
-    const int64_t items = static_cast<int64_t>(p.n_rows) * p.H_kv;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-    const float gs = is_v ? p.v_scale : p.k_scale;
-    for (int64_t item = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-         item < items; item += warps) {
-        const int64_t r = item / p.H_kv;
-        const int32_t h = static_cast<int32_t>(item - r * p.H_kv);
-        const int64_t slot = p.slots[r];
-        if (slot < 0) continue;
-        if (slot >= p.n_slots) {
-            if (lane == 0) atomicCAS(p.err, 0, kErrInval);
-            continue;
-        }
-        const Place at = place_of(p, slot, h);
-        const uint8_t* pool = is_v ? p.v_pool : p.k_pool;
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(pool + at.codes + part * 4);
-        const float den = e4m3_f32(pool[at.scales + (part >> 1)]) * gs;
-        uint32_t out[4];
+__global__ void __launch_bounds__(32 * kWarps) append_q4_kernel(const Q4RowParams p) {
+    const int group = threadIdx.x & 7;
+    const bool is_v = threadIdx.x & 8;
+    uint32_t r, h;
+    int64_t slot;
+    if (!item_of(p, r, h, slot)) return;
+    const __nv_bfloat16* src = is_v ? p.v_rows + static_cast<int64_t>(r) * p.v_stride
+                                    : p.k_rows + static_cast<int64_t>(r) * p.k_stride;
+    uint32_t raw[8];
+    src += h * kHD + group * 16;
+    if (p.align32) {  // one load of a whole sector
+        ptx::ld_global_v8(src, raw);
+    } else {
+        const uint4* from = reinterpret_cast<const uint4*>(src);
+        const uint4 a = __ldg(from), b = __ldg(from + 1);
+        raw[0] = a.x, raw[1] = a.y, raw[2] = a.z, raw[3] = a.w;
+        raw[4] = b.x, raw[5] = b.y, raw[6] = b.z, raw[7] = b.w;
+    }
+    // largest magnitude; a NaN among the values shows in it
+    uint32_t top2 = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = e2m1_f32((w >> (4 * i)) & 15u) * den;
-            const float b = e2m1_f32((w >> (16 + 4 * i)) & 15u) * den;
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out[i]) : "f"(b), "f"(a));
+    for (int i = 0; i < 8; ++i) top2 = ptx::max_nan_bf16x2(top2, raw[i] & 0x7fff7fffu);
+    if ((top2 & 0x7fffu) > 0x7f80u || (top2 >> 16) > 0x7f80u) {
+        // recorded, and held as 0: it must not reach other rows
+        atomicCAS(p.err, 0, kErrInval);
+        top2 = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if ((raw[i] & 0x7fffu) > 0x7f80u) raw[i] &= 0xffff0000u;
+            if ((raw[i] & 0x7fff0000u) > 0x7f800000u) raw[i] &= 0xffffu;
+            top2 = ptx::max_nan_bf16x2(top2, raw[i] & 0x7fff7fffu);
         }
-        __nv_bfloat16* dst = is_v ? p.v_out + r * p.v_stride : p.k_out + r * p.k_stride;
-        *reinterpret_cast<uint4*>(dst + h * kHD + part * 8) =
-            make_uint4(out[0], out[1], out[2], out[3]);
+    }
+    const float top = fmaxf(__uint_as_float(top2 << 16), __uint_as_float(top2 & 0xffff0000u));
+    const float gs = is_v ? p.v_scale : p.k_scale;
+    // (from 448 on the scale saturates, so 512 stands for whatever is larger)
+    const float c6 = 6.0f * gs;
+    const float most = quotient(fminf(top, 512.f * c6), c6, is_v ? p.v_rcp6 : p.k_rcp6);
+    const uint32_t sc = e4m3x2(most, 0.f) & 0xffu;
+    const float den = e4m3_f32(sc) * gs;
+    uint32_t w[2] = {0u, 0u};
+    if (sc > 0) {
+        const float rcp = __frcp_rn(den);
+        if (sc >= 0x7e) {
+            // saturated: whatever is above 8 den (infinity too) has code 6, as 8 den has
+            const float most = 8.f * den;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float lo = fminf(fmaxf(__uint_as_float(raw[i] << 16), -most), most);
+                const float hi = fminf(fmaxf(__uint_as_float(raw[i] & 0xffff0000u), -most), most);
+                raw[i] = (__float_as_uint(lo) >> 16) | (__float_as_uint(hi) & 0xffff0000u);
+            }
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t v = raw[4 * half + (i >> 1)];
+                const float x = __uint_as_float(i & 1 ? v & 0xffff0000u : v << 16);
+                y[i] = quotient(x, den, rcp);
+            }
+            w[half] = e2m1_word(y);
+        }
+    }
+    const Place at = place_of(p, slot, h);
+    uint8_t* pool = is_v ? p.v_pool : p.k_pool;
+    *reinterpret_cast<uint2*>(pool + at.codes + group * 8) = make_uint2(w[0], w[1]);
+    pool[at.scales + group] = static_cast<uint8_t>(sc);
+}
+
+__global__ void __launch_bounds__(32 * kWarps) read_q4_kernel(const Q4RowParams p) {
+    const int group = threadIdx.x & 7;
+    const bool is_v = threadIdx.x & 8;
+    uint32_t r, h;
+    int64_t slot;
+    if (!item_of(p, r, h, slot)) return;
+    const Place at = place_of(p, slot, h);
+    const uint8_t* pool = is_v ? p.v_pool : p.k_pool;
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(pool + at.codes + group * 8));
+    const float den = e4m3_f32(__ldg(pool + at.scales + group)) * (is_v ? p.v_scale : p.k_scale);
+    __nv_bfloat16* dst = is_v ? p.v_out + static_cast<int64_t>(r) * p.v_stride
+                              : p.k_out + static_cast<int64_t>(r) * p.k_stride;
+    dst += h * kHD + group * 16;
+    uint32_t out[8];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        uint32_t v[4];  // values 0 2, 4 6, 1 3, 5 7
+        ptx::f16x2_of_e2m1x8(half ? w.y : w.x, v);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            out[4 * half + 2 * i] =
+                ptx::pack_bf16x2(lo_f16_f32(v[i]) * den, lo_f16_f32(v[2 + i]) * den);
+            out[4 * half + 2 * i + 1] =
+                ptx::pack_bf16x2(hi_f16_f32(v[i]) * den, hi_f16_f32(v[2 + i]) * den);
+        }
+    }
+    if (p.align32) {
+        ptx::st_global_v8(dst, out);
+    } else {
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(out[0], out[1], out[2], out[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(out[4], out[5], out[6], out[7]);
     }
 }
 
@@ -157,13 +209,9 @@ __global__ void __launch_bounds__(256) read_q4_kernel(const Q4RowParams p) {
 cudaError_t launch_q4_rows(const Q4RowParams& p, bool read, cudaStream_t stream) {
     const int64_t items = static_cast<int64_t>(p.n_rows) * p.H_kv;
     if (items <= 0) return cudaSuccess;
-    int dev = 0, sms = 152;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int64_t blocks = (items + 7) / 8;
-    const int grid = static_cast<int>(blocks < 8LL * sms ? blocks : 8LL * sms);
-    if (read) read_q4_kernel<<<grid, 256, 0, stream>>>(p);
-    else append_q4_kernel<<<grid, 256, 0, stream>>>(p);
+    const unsigned grid = static_cast<unsigned>((items + 2 * kWarps - 1) / (2 * kWarps));
+    if (read) read_q4_kernel<<<grid, 32 * kWarps, 0, stream>>>(p);
+    else append_q4_kernel<<<grid, 32 * kWarps, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

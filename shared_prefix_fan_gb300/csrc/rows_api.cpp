@@ -32,6 +32,7 @@ int check_rows(const void* k_rows, const void* v_rows, const void* k_pages, cons
     if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
         return FANOUT_EUNSUPPORTED;
     if (!q4_scale_ok(k_scale) || !q4_scale_ok(v_scale)) return FANOUT_EINVAL;
+    if (static_cast<int64_t>(n_rows) * H_kv >= (1LL << 31)) return FANOUT_EUNSUPPORTED;
     if (n_rows == 0) return FANOUT_OK;
     const int64_t row = static_cast<int64_t>(H_kv) * d;
     if (k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0)
@@ -44,6 +45,11 @@ int check_rows(const void* k_rows, const void* v_rows, const void* k_pages, cons
 }
 
 int run_rows(Q4RowParams& p, bool read, int32_t page_size, fanout_stream_t stream) {
+    const void* k = read ? static_cast<const void*>(p.k_out) : p.k_rows;
+    const void* v = read ? static_cast<const void*>(p.v_out) : p.v_rows;
+    p.align32 = aligned(k, 32) && aligned(v, 32) && p.k_stride % 16 == 0 && p.v_stride % 16 == 0;
+    p.k_rcp6 = 1.0f / (6.0f * p.k_scale);
+    p.v_rcp6 = 1.0f / (6.0f * p.v_scale);
     p.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
     const cudaError_t ce = err_word_ptr(&p.err);
     if (ce != cudaSuccess) return status_from_cuda(ce);
@@ -68,7 +74,8 @@ int fanout_fork_device(const int32_t* prefix_pages, int32_t prefix_len, int32_t 
     if (prefix_len < 0 || num_branches < 0 || page_size <= 0 || n_free < 0 ||
         max_pages_per_branch < 0)
         return FANOUT_EINVAL;
-    if (num_branches > kMaxTableBranches) return FANOUT_EUNSUPPORTED;
+    if (num_branches > kMaxTableBranches || max_pages_per_branch > kMaxTablePages)
+        return FANOUT_EUNSUPPORTED;
     const int64_t n_prefix = (static_cast<int64_t>(prefix_len) + page_size - 1) / page_size;
     if (num_branches > 0 && n_prefix > max_pages_per_branch) return FANOUT_EINVAL;
     if (num_branches > 0 && (!suffix_lens || (n_prefix > 0 && !prefix_pages) ||

@@ -161,7 +161,7 @@ int launch_plan(const CallArgs& a, const Plan& pl, const Layout& L, uint8_t* bas
                 cudaStream_t stream, cudaEvent_t ev_before, cudaEvent_t ev_after) {
     if (!encode_fn()) return FANOUT_ECUDA;
     const int32_t G = a.H_q / a.H_kv;
-    CUtensorMap tm_q, tm_k, tm_v;
+    CUtensorMap tm_q, tm_k{}, tm_v{};
     const int64_t pool_rows = static_cast<int64_t>(a.num_pages) * a.H_kv * a.page_size;
     int st;
     if ((st = map_q(&tm_q, a.q, a.R, a.H_q, G, pl.tpt)) != FANOUT_OK) return st;
@@ -231,8 +231,8 @@ int launch_plan(const CallArgs& a, const Plan& pl, const Layout& L, uint8_t* bas
 
     if (ev_before) cudaEventRecord(ev_before, stream);
     p.fused_merge = fuse ? 1 : 0;
-    ce = a.q4 ? launch_attn_q4(p, tm_q, pl.n_cta(), stream)
-              : launch_split_attn(p, tm_q, tm_k, tm_v, pl.n_cta(), fuse, stream);
+    ce = p.tok_pos ? launch_attn_rows(p, tm_q, tm_k, tm_v, a.q4 != 0, pl.n_cta(), stream)
+                   : launch_split_attn(p, tm_q, tm_k, tm_v, pl.n_cta(), fuse, stream);
     if (ce != cudaSuccess && fuse) {
         (void)cudaGetLastError();  // refused as a cooperative launch: merge separately
         p.fused_merge = 0;

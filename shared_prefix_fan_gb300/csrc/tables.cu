@@ -57,33 +57,42 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int64_t&
     return before + incl - v;
 }
 
+// Pages of up to kMaxTokens tokens, in 32 bits: with 64-bit divisions the scan over
+// 1024 branches took three quarters of a fork's time.
 __device__ __forceinline__ int32_t pages_of(int64_t tokens, int32_t ps) {
-    return static_cast<int32_t>((tokens + ps - 1) / ps);
+    return static_cast<int32_t>(
+        (static_cast<uint32_t>(tokens) + static_cast<uint32_t>(ps) - 1u) / static_cast<uint32_t>(ps));
 }
 
-// Pages held and needed by a branch, and its new rows; false when its lengths
-// are not valid. Tokens are counted in 64 bits.
+// Pages that forked branch b needs (at least the prefix's n_prefix); false when its
+// lengths are not valid. Tokens are counted in 64 bits.
+__device__ __forceinline__ bool fork_pages(const TableParams& p, int32_t b, int32_t n_prefix,
+                                           int32_t& need) {
+    const int32_t S = __ldg(p.suffix_lens + b);
+    const int64_t end = static_cast<int64_t>(p.prefix_len) + S;
+    need = n_prefix;
+    if (S < 0 || end > kMaxTokens) return false;
+    need = max(need, pages_of(end, p.page_size));
+    return need <= p.max_pages;
+}
+
+// Pages that branch b holds and needs after its growth, and its new rows.
 __device__ __forceinline__ bool branch_pages(const TableParams& p, int32_t b, int32_t& held,
                                              int32_t& need, int32_t& rows) {
-    const int32_t S = p.suffix_lens[b];
-    const int32_t A = p.extend ? p.add_lens[b] : 0;
+    const int32_t S = __ldg(p.suffix_lens + b), A = __ldg(p.add_lens + b);
     const int64_t end = static_cast<int64_t>(p.prefix_len) + S + A;
     if (S < 0 || A < 0 || end > kMaxTokens) {
         held = need = rows = 0;
         return false;
     }
     rows = A;
-    if (p.extend) {
-        held = pages_of(end - A, p.page_size);
-        need = pages_of(end, p.page_size);
-    } else {
-        held = p.prefix_len / p.page_size;
-        need = max(pages_of(end, p.page_size), pages_of(p.prefix_len, p.page_size));
-    }
+    held = pages_of(end - A, p.page_size);
+    need = pages_of(end, p.page_size);
     return need <= p.max_pages;
 }
 
-// The scan over all branches into sm (each thread a contiguous run of them).
+// The scan over all branches into sm, for an extension (each thread a contiguous run
+// of them).
 // Returns whether the call is valid; `used` is the free list's first entry.
 __device__ bool scan_branches(const TableParams& p, Scan& sm, int32_t& used, int64_t& pages,
                               int64_t& rows) {
@@ -134,39 +143,99 @@ __device__ __forceinline__ int32_t branch_of(const int32_t* off, int32_t n, int3
     return lo;
 }
 
-// CTAs take (branch, run of kRun table entries) items; one row's entries come
-// from the prefix list, then from the branch's run of the free list, then -1.
-constexpr int kRun = 4 * kThreads;
+// A CTA takes a run of consecutive (branch, kRun table entries) items. Of the scan
+// it needs the pages taken before its first branch and the total (for the verdict),
+// so it only adds up the lengths; the later branches' starts follow one by one.
+// A row's entries come from the prefix list, the branch's run of the free list, -1.
+constexpr int kQuads = 2;  // runs of 4 entries a thread takes of an item
+constexpr int kRun = 4 * kQuads * kThreads;
 
 __global__ void __launch_bounds__(kThreads) fork_kernel(const TableParams p) {
-    __shared__ Scan sm;
-    int32_t used;
-    int64_t pages, rows;
-    const bool ok = scan_branches(p, sm, used, pages, rows);
+    __shared__ int64_t part[2][kThreads / 32];
+    __shared__ int32_t bad;
+    if (threadIdx.x == 0) bad = 0;
+    __syncthreads();
+    const int32_t used = p.used_in ? *p.used_in : 0;
+    const int32_t n_full = p.prefix_len / p.page_size;
+    const bool partial = p.prefix_len % p.page_size != 0;
+    const int32_t n_prefix = n_full + (partial ? 1 : 0);
+    const int32_t runs = max(1, (p.max_pages + kRun - 1) / kRun);
+    const int32_t items = p.num_branches * runs;  // <= 2^12 * 2^13 (host check)
+    const int32_t per = (items + gridDim.x - 1) / gridDim.x;
+    const int32_t it0 = min(items, static_cast<int32_t>(blockIdx.x) * per);
+    const int32_t it1 = min(items, it0 + per);
+    int32_t b = it0 / runs, run = it0 - b * runs;
+    int64_t mine = 0, all = 0;
+    bool ok = true;
+    for (int i = threadIdx.x; i < p.num_branches; i += kThreads) {
+        int32_t need;
+        ok &= fork_pages(p, i, n_prefix, need);
+        all += need - n_full;
+        if (i < b) mine += need - n_full;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, d);
+        mine += __shfl_xor_sync(0xffffffffu, mine, d);
+    }
+    if ((threadIdx.x & 31) == 0) {
+        part[0][threadIdx.x >> 5] = all;
+        part[1][threadIdx.x >> 5] = mine;
+    }
+    if (!ok) bad = 1;
+    __syncthreads();
+    all = mine = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        all += part[0][w];
+        mine += part[1][w];
+    }
+    ok = !bad && used >= 0 && (all == 0 || used + all <= p.n_free);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-        if (p.used_out) *p.used_out = used + (ok ? static_cast<int32_t>(pages) : 0);
+        if (p.used_out) *p.used_out = used + (ok ? static_cast<int32_t>(all) : 0);
         if (!ok) atomicCAS(p.err, 0, kErrInval);
     }
     if (!ok) return;
-    const int32_t n_full = p.prefix_len / p.page_size;
-    const bool partial = p.prefix_len % p.page_size != 0;
-    const int32_t runs = (p.max_pages + kRun - 1) / kRun;
-    const int64_t items = static_cast<int64_t>(p.num_branches) * runs;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const int32_t b = static_cast<int32_t>(it / runs);
-        const int32_t i0 = static_cast<int32_t>(it % runs) * kRun;
-        const int32_t n_own = sm.page_off[b + 1] - sm.page_off[b];
-        const int32_t* list = p.free_pages + used + sm.page_off[b] - n_full;
+    const int32_t* list = p.free_pages + used + mine - n_full;  // of branch b, by table entry
+    // 16-byte copies where every row and the prefix list start on 16 bytes
+    const bool quads = p.max_pages % 4 == 0 &&
+                       ((reinterpret_cast<uintptr_t>(p.page_table) |
+                         reinterpret_cast<uintptr_t>(p.prefix_pages)) & 15u) == 0;
+    for (int32_t it = it0; it < it1; ++it) {
+        int32_t need;
+        fork_pages(p, b, n_prefix, need);
         int32_t* row = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+        int4 v[kQuads];
 #pragma unroll
-        for (int u = 0; u < kRun / kThreads; ++u) {
-            const int32_t i = i0 + u * kThreads + threadIdx.x;
-            if (i < p.max_pages)
-                row[i] = i < n_full ? p.prefix_pages[i] : i < n_full + n_own ? list[i] : -1;
+        for (int u = 0; u < kQuads; ++u) {
+            const int32_t i = run * kRun + 4 * (u * kThreads + static_cast<int>(threadIdx.x));
+            auto entry = [&](int32_t e) {
+                return e < n_full ? __ldg(p.prefix_pages + e) : e < need ? __ldg(list + e) : -1;
+            };
+            if (i + 3 < n_full && quads) v[u] = __ldg(reinterpret_cast<const int4*>(p.prefix_pages + i));
+            else if (i < p.max_pages) v[u] = make_int4(entry(i), entry(i + 1), entry(i + 2), entry(i + 3));
         }
-        if (partial && p.cow_pairs && i0 == 0 && threadIdx.x == 0) {
+#pragma unroll
+        for (int u = 0; u < kQuads; ++u) {
+            const int32_t i = run * kRun + 4 * (u * kThreads + static_cast<int>(threadIdx.x));
+            if (i >= p.max_pages) continue;
+            if (quads) {
+                *reinterpret_cast<int4*>(row + i) = v[u];
+            } else {
+                row[i] = v[u].x;
+                if (i + 1 < p.max_pages) row[i + 1] = v[u].y;
+                if (i + 2 < p.max_pages) row[i + 2] = v[u].z;
+                if (i + 3 < p.max_pages) row[i + 3] = v[u].w;
+            }
+        }
+        if (partial && p.cow_pairs && run == 0 && threadIdx.x == 0) {
             p.cow_pairs[2 * b] = p.prefix_pages[n_full];
             p.cow_pairs[2 * b + 1] = list[n_full];
+        }
+        if (++run == runs) {
+            run = 0;
+            ++b;
+            list += need - n_full;
         }
     }
 }
@@ -201,13 +270,15 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const TableParams p) {
             const int32_t b = branch_of(sm.row_off, p.num_branches, static_cast<int32_t>(r));
             const int32_t before = p.prefix_len + p.suffix_lens[b];  // <= kMaxTokens (scan)
             const int32_t pos = before + (static_cast<int32_t>(r) - sm.row_off[b]);
-            const int32_t held = pages_of(before, p.page_size), i = pos / p.page_size;
+            const int32_t held = pages_of(before, p.page_size);
+            const int32_t i = static_cast<int32_t>(static_cast<uint32_t>(pos) /
+                                                   static_cast<uint32_t>(p.page_size));
             // a page taken by this call comes from the list: the table entry may
             // be another CTA's store
             const int32_t page = i >= held
                                      ? p.free_pages[used + sm.page_off[b] + (i - held)]
                                      : p.page_table[static_cast<int64_t>(b) * p.max_pages + i];
-            if (page >= 0) slot = static_cast<int64_t>(page) * p.page_size + pos % p.page_size;
+            if (page >= 0) slot = static_cast<int64_t>(page) * p.page_size + (pos - i * p.page_size);
             else atomicCAS(p.err, 0, kErrInval);
         }
         p.slots[r] = slot;
@@ -227,7 +298,7 @@ cudaError_t launch_tables(const TableParams& p, cudaStream_t stream) {
         extend_kernel<<<grid, kThreads, 0, stream>>>(p);
     } else {
         const int64_t items =
-            static_cast<int64_t>(p.num_branches) * ((p.max_pages + kRun - 1) / kRun);
+            static_cast<int64_t>(p.num_branches) * std::max(1, (p.max_pages + kRun - 1) / kRun);
         const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(items, 4 * sms)));
         fork_kernel<<<grid, kThreads, 0, stream>>>(p);
     }

@@ -35,7 +35,8 @@ READ = dict(kp=1024, vp=1024, slots=1024, n=4, pages=8, hkv=2, d=128, ps=16, kg=
 
 @pytest.mark.parametrize("kw,rc", [
     (dict(P=-1), E), (dict(B=-1), E), (dict(ps=0), E), (dict(n_free=-1), E), (dict(width=-1), E),
-    (dict(B=4097), U), (dict(width=2), E), (dict(S=None), E), (dict(prefix=None), E),
+    (dict(B=4097), U), (dict(width=(1 << 24) + 1), U), (dict(width=2), E), (dict(S=None), E),
+    (dict(prefix=None), E),
     (dict(table=None), E), (dict(free=None), E), (dict(used=2048), E), (dict(table=1026), E),
     (dict(cow=1025), E), (dict(after=2046 + 1), E)])
 def test_fork_device_refuses(lib, kw, rc):
@@ -58,7 +59,7 @@ def test_extend_device_refuses(lib, kw, rc):
     (dict(kg=0.0), E), (dict(vg=float("nan")), E), (dict(vg=float("inf")), E), (dict(kg=-1.0), E),
     (dict(ks=255), E), (dict(vs=260), E), (dict(ks=128), E), (dict(k=None), E), (dict(v=1032), E),
     (dict(kp=None), E), (dict(vp=1028), E), (dict(slots=None), E), (dict(slots=1028), E),
-    (dict(n=0, k=None, slots=None), OK)])
+    (dict(n=1 << 30, hkv=2), U), (dict(n=0, k=None, slots=None), OK)])
 def test_rows_refuse(lib, name, base, kw, rc):
     assert call(getattr(lib, name), base, **kw) == rc
 
