@@ -401,13 +401,13 @@ __device__ void q_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, int w) {
                     continue;
                 }
                 uint32_t top[4] = {0, 0, 0, 0};
+#pragma unroll 1
+                for (int q = 0; q < 16; q += 4) {
+                    uint4 v[4];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint4 v[8];
+                    for (int c = 0; c < 4; ++c) v[c] = ptx::ld_shared_v4(piece(q + c));
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) v[c] = ptx::ld_shared_v4(piece(8 * half + c));
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
+                    for (int c = 0; c < 4; ++c) {
                         top[0] = ptx::max_abs_bf16x2(top[0], v[c].x);
                         top[1] = ptx::max_abs_bf16x2(top[1], v[c].y);
                         top[2] = ptx::max_abs_bf16x2(top[2], v[c].z);
@@ -422,22 +422,22 @@ __device__ void q_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, int w) {
                 const float f = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
                 auto lo = [f](uint32_t b) { return __uint_as_float(b << 16) * f; };
                 auto hi = [f](uint32_t b) { return __uint_as_float(b & 0xffff0000u) * f; };
+#pragma unroll 1
+                for (int q = 0; q < 16; q += 4) {
+                    uint4 v[4];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint4 v[8];
+                    for (int c = 0; c < 4; ++c) v[c] = ptx::ld_shared_v4(piece(q + c));
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) v[c] = ptx::ld_shared_v4(piece(8 * half + c));
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
+                    for (int c = 0; c < 4; ++c)
                         v[c] = make_uint4(ptx::pack_f16x2(lo(v[c].x), lo(v[c].y)),
                                           ptx::pack_f16x2(lo(v[c].z), lo(v[c].w)),
                                           ptx::pack_f16x2(hi(v[c].x), hi(v[c].y)),
                                           ptx::pack_f16x2(hi(v[c].z), hi(v[c].w)));
                     for (int copy = 0; copy < kBM; copy += kBM / split)
 #pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            ptx::st_shared_v4(piece(8 * half + c) + copy * 128, v[c].x, v[c].y,
-                                              v[c].z, v[c].w);
+                        for (int c = 0; c < 4; ++c)
+                            ptx::st_shared_v4(piece(q + c) + copy * 128, v[c].x, v[c].y, v[c].z,
+                                              v[c].w);
                 }
                 for (int copy = 0; copy < kBM; copy += kBM / split)
                     *sm.fac(n, x, row + copy) = static_cast<uint8_t>(k + 127);
@@ -721,25 +721,20 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32], float m) {
 template <bool Q4>
 __device__ __forceinline__ void exp32(const uint32_t (&s)[32], uint32_t taddr, uint64_t sl2,
                                       uint64_t negm, uint64_t (&l)[2]) {
+    uint32_t packed[16];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t packed[8];
-#pragma unroll
-        for (int c = 0; c < 16; c += 2) {
-            const uint64_t t = ptx::fma_f32x2(ptx::f32x2(__uint_as_float(s[16 * h + c]),
-                                                         __uint_as_float(s[16 * h + c + 1])),
-                                              sl2, negm);
-            const float e0 = ptx::ex2(ptx::lo_f32(t)), e1 = ptx::ex2(ptx::hi_f32(t));
-            l[(c >> 1) & 1] = ptx::add_f32x2(l[(c >> 1) & 1], ptx::f32x2(e0, e1));
-            packed[c >> 1] = Q4 ? ptx::pack_f16x2(e0, e1) : ptx::pack_bf16x2(e0, e1);
-        }
-        ptx::tmem_st8(taddr + 8 * h, packed);
+    for (int c = 0; c < 32; c += 2) {
+        const uint64_t t = ptx::fma_f32x2(
+            ptx::f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sl2, negm);
+        const float e0 = ptx::ex2(ptx::lo_f32(t)), e1 = ptx::ex2(ptx::hi_f32(t));
+        l[(c >> 1) & 1] = ptx::add_f32x2(l[(c >> 1) & 1], ptx::f32x2(e0, e1));
+        packed[c >> 1] = Q4 ? ptx::pack_f16x2(e0, e1) : ptx::pack_bf16x2(e0, e1);
     }
+    ptx::tmem_st16(taddr, packed);
 }
 __device__ __forceinline__ void zero16(uint32_t taddr) {
-    const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-    ptx::tmem_st8(taddr, z);
-    ptx::tmem_st8(taddr + 8, z);
+    const uint32_t z[16] = {};
+    ptx::tmem_st16(taddr, z);
 }
 
 // The running reference and sum of a row (of one copy's keys).
@@ -784,17 +779,32 @@ __device__ __forceinline__ float softmax_tile(uint32_t colS, int seg, float sl2,
         zero16(colS + 32 * (seg ^ 1));
         zero16(colS + 32 * (seg ^ 1) + 16);
     } else {
-        // columns 64.. first for the maximum; 0.. stay in registers
+        // 32 columns at a time, the next ones on their way from TMEM while these are
+        // worked on: the maximum from the last columns down, P from the first up
         uint32_t s1[32];
-        load64(colS + 64, s0, s1);
-        const float mx = max32(s1, max32(s0, -INFINITY));
-        load64(colS, s0, s1);
-        corr = run.raise(max32(s1, max32(s0, mx)) * sl2, kLift, neg);
+        ptx::tmem_ld32(colS + 96, s1);
+        ptx::tmem_ld_wait(s1);
+        ptx::tmem_ld32(colS + 64, s0);
+        float mx = max32(s1, -INFINITY);
+        ptx::tmem_ld_wait(s0);
+        ptx::tmem_ld32(colS + 32, s1);
+        mx = max32(s0, mx);
+        ptx::tmem_ld_wait(s1);
+        ptx::tmem_ld32(colS, s0);
+        mx = max32(s1, mx);
+        ptx::tmem_ld_wait(s0);
+        ptx::tmem_ld32(colS + 32, s1);
+        mx = max32(s0, mx);
+        corr = run.raise(mx * sl2, kLift, neg);
         const uint64_t negm = ptx::f32x2(neg, neg);
         exp32<Q4>(s0, colS, sl2p, negm, l);
+        ptx::tmem_ld_wait(s1);
+        ptx::tmem_ld32(colS + 64, s0);
         exp32<Q4>(s1, colS + 16, sl2p, negm, l);
-        load64(colS + 64, s0, s1);
+        ptx::tmem_ld_wait(s0);
+        ptx::tmem_ld32(colS + 96, s1);
         exp32<Q4>(s0, colS + 32, sl2p, negm, l);
+        ptx::tmem_ld_wait(s1);
         exp32<Q4>(s1, colS + 48, sl2p, negm, l);
     }
     const uint64_t sum = ptx::add_f32x2(l[0], l[1]);

@@ -1,43 +1,29 @@
-// attn_q4.cu -- fan-out attention over a cache held in 4 bits, for sm_103a.
+// attn_rows.cu -- fan-out attention of row plans, for sm_103a: over bf16 pools with a
+// sliding window and first keys that stay visible, and over pools held in 4 bits
+// (with or without a window).
 //
-// The rows of a cache (kv_q4.cu) are e2m1 codes with one e4m3 scale per 16
-// values; out = softmax(scale q K^T) V over the values they stand for. Units,
-// tiles and the online softmax are those of attn_fwd.cu (128 query rows x 128
-// keys, base 2, the reference maximum m raised only when a row's maximum passes
-// it by 2^8); positions, windows and first keys are those of its row plans.
+// Units, tiles and the online softmax are those of attn_fwd.cu (128 query rows x
+// 128 keys, base 2, the reference maximum m raised only when a row's maximum passes
+// it by 2^8). A row plan gives every token's position in a table, so that rows of
+// different branches share a unit whatever their windows; a unit may sweep its first
+// keys as tiles in front of its own range; its range may begin inside a page.
 //
-// The tensor core gets f16 tiles that hold the cached values exactly: a code has 2
-// significant bits and a group scale 4, their product 6, and it lies between 2^-10
-// and 2688.
-//   S = Q K^T from shared memory, Q as f16 too: its rows are scaled by the power
-//   of two that brings their largest element into [2^14, 2^15) (undone in the
-//   row's softmax scale), so bf16's 8 bits fit f16's 11, and only elements below
-//   2^-28 of the row's largest lose bits;
-//   O += P V with P from TMEM, P = 2^(x - m + 7): at most 2^15, and its rounding is
-//   f16's half step of 2^-11 (bf16's, as for bf16 pools, would be 2^-8); a P below
-//   2^-21 of the row's reference has a step of 2^-31 of it. The 2^7 is taken out
-//   of l and of the output, where V's pool scale goes too (K's: softmax scale).
-//
-// Widening is one conversion (a byte of two codes to an f16 pair) and one packed
-// product per two values: both run at 64 lanes a cycle and SM (measured), so a K
-// and a V tile take 256 cycles of either pipe, under the 1024 their four (two for
-// a single query tile) products take on the tensor core. Bit tricks on bf16 tiles
-// instead took 2.5 times the instructions: a prefill step was 2.1 times slower.
-// The codes of a word come out as values 0 2 4 6 1 3 5 7 of its 8; K and Q keep
-// that order (it is summed over), V's columns are put back when O is stored.
-//
-// GB300 mapping, one persistent CTA per SM, 20 warps:
-//   warp 0      producer: page blocks by cp.async.bulk into a ring of raw tiles
-//               (9 KB: 128 rows of 72 bytes), Q by TMA when its buffer is free;
+// GB300 mapping, one persistent CTA per SM:
+//   warp 0      producer. bf16 pools: TMA boxes, a page of a KV head each, into a
+//               ring of 32 KB tiles. 4-bit pools: page blocks by cp.async.bulk into
+//               a ring of raw tiles (9 KB: 128 rows of 72 bytes). Q by TMA as soon as
+//               its buffer is free. Page ids are checked before they are read through;
 //   warp 1      TMEM owner and tcgen05 issuer: the whole warp runs the issue loop, so
 //               that descriptors stay in uniform registers, and one elected lane
 //               issues (a single-lane loop took twice as long per product);
-//   warps 2-3   turn Q tiles into scaled f16, in place;
+//   warps 2-3   prepare loaded Q tiles in place (copies, and f16 for 4-bit pools);
 //   warps 4-11  two softmax groups of 4 warps, thread = row;
-//   warps 12-19 widen raw tiles into the swizzled f16 ring (4 warps the K tiles, 4
-//               the V tiles), rows that no row of the unit sees as zeros. With 4
-//               warps for both, a decode step waited for them: 35 us, not 15.
-// Registers (launched with 96 a thread): softmax warps 144, the others 64.
+//   warps 12-19 4-bit pools only: widen raw tiles into the swizzled 16-bit ring (4
+//               warps the K tiles, 4 the V tiles). With 4 warps for both, a decode
+//               step waited for them: 35 us, not 31.
+// Keys of a tile that no row of the unit sees are zeros in shared memory, whatever
+// the pool holds there.
+//
 // A unit of two query tiles gives each group one of them. A unit of one query
 // tile (decode) is split over the groups by keys instead: tile t goes to group
 // t mod 2, each with its own S, (m, l) and O in TMEM, and the two are joined at
@@ -48,6 +34,26 @@
 // zeros for the other keys' P; each copy ends as a partial row of its own. The
 // softmax of one tile was the longest step of a decode CTA's loop.
 // TMEM: S_0 = 0, S_1 = 128, O_0 = 256, O_1 = 384 (512 columns).
+//
+// 4-bit pools. The rows of a cache (kv_q4.cu) are e2m1 codes with one e4m3 scale per
+// 16 values; the tensor core gets f16 tiles that hold the cached values exactly: a
+// code has 2 significant bits and a group scale 4, their product 6, and it lies
+// between 2^-10 and 2688.
+//   S = Q K^T from shared memory, Q as f16 too: its rows are scaled by the power
+//   of two that brings their largest element into [2^14, 2^15) (undone in the
+//   row's softmax scale), so bf16's 8 bits fit f16's 11, and only elements below
+//   2^-28 of the row's largest lose bits;
+//   O += P V with P from TMEM, P = 2^(x - m + 7): at most 2^15, and its rounding is
+//   f16's half step of 2^-11 (bf16's, as for bf16 pools, would be 2^-8); a P below
+//   2^-21 of the row's reference has a step of 2^-31 of it. The 2^7 is taken out
+//   of l and of the output, where V's pool scale goes too (K's: softmax scale).
+// Widening is one conversion (a byte of two codes to an f16 pair) and one packed
+// product per two values: both run at 64 lanes a cycle and SM (measured), so a K
+// and a V tile take 256 cycles of either pipe, under the 1024 their four (two for
+// a single query tile) products take on the tensor core. Bit tricks on bf16 tiles
+// instead took 2.5 times the instructions: a prefill step was 2.1 times slower.
+// The codes of a word come out as values 0 2 4 6 1 3 5 7 of its 8; K and Q keep
+// that order (it is summed over), V's columns are put back when O is stored.
 // Every wait is bounded, as in attn_fwd.cu.
 #include <cuda_bf16.h>
 
@@ -66,29 +72,34 @@ constexpr int kHalfBytes = kTileBytes / 2;  // 128 rows x 64 columns (128 B rows
 constexpr int kQBytes = kBM * kHD * 2;
 constexpr int kRawBytes = kBN * kQ4RowBytes;
 constexpr float kRescaleLog2 = 8.0f;  // lazy rescale threshold (base-2 units)
-constexpr float kLiftLog2 = 7.0f;     // P is 2^7 times the probability's numerator
 constexpr int kErrTimeout = 5;        // FANOUT_ETIMEOUT
 constexpr int kGroupWarps = 4;
 constexpr int kWarpQ = 2;        // first warp of the Q conversion
 constexpr int kQWarps = 2;
 constexpr int kWarpSoftmax = 4;  // first softmax warp
 constexpr int kWarpWiden = 12;   // first widening warp
-constexpr int kThreads = 32 * 20;
-// Registers per thread: at launch, and after the warpgroups' split (the sum must
-// not exceed what the block was launched with).
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsWiden = 64, kRegsOther = 64;
-static_assert(kRegsSoftmax * 256 + kRegsWiden * 256 + kRegsOther * 128 <= kRegsLaunch * kThreads,
+// Registers per thread of the 4-bit instances: at launch, and after the warpgroups'
+// split (the sum must not exceed what the block was launched with).
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 152, kRegsWiden = 60, kRegsOther = 56;
+static_assert(kRegsSoftmax * 256 + kRegsWiden * 256 + kRegsOther * 128 <= kRegsLaunch * 640,
               "register split");
 constexpr int kFacBufs = 4;      // units whose row factors are held
 
-template <int NQ>
+template <int NQ, bool Q4>
 struct Cfg {
-    static constexpr int kStages = 4;            // widened tiles
-    static constexpr int kRaw = NQ == 1 ? 6 : 2;  // raw tiles
+    static constexpr int kThreads = 32 * (Q4 ? 20 : 12);
+    static constexpr int kStages = !Q4 && NQ == 1 ? 5 : 4;   // 16-bit tiles
+    static constexpr int kRaw = !Q4 ? 0 : NQ == 1 ? 6 : 2;  // raw tiles
+    // P is 2^lift times the probability's numerator
+    static constexpr float kLiftLog2 = Q4 ? 7.0f : 0.0f, kUnlift = Q4 ? 0.0078125f : 1.0f;
+    static constexpr uint32_t kIdescQK = Q4 ? ptx::idesc_f16_f32(kBM, kBN, false, false)
+                                            : ptx::idesc_bf16_f32(kBM, kBN, false, false);
+    static constexpr uint32_t kIdescPV = Q4 ? ptx::idesc_f16_f32(kBM, kHD, false, true)
+                                            : ptx::idesc_bf16_f32(kBM, kHD, false, true);
     // K tiles take the even and V tiles the odd ring positions, and the warps that
     // widen one kind wait for its stages only: with an odd ring a stage would change
     // kind, and a warp could take the phase before last of its barrier for the last.
-    static_assert(kStages % 2 == 0 && kRaw % 2 == 0, "rings of K/V pairs");
+    static_assert(!Q4 || (kStages % 2 == 0 && kRaw % 2 == 0), "rings of K/V pairs");
     static constexpr int kSmemQ = 0;
     static constexpr int kSmemRing = NQ * kQBytes;
     static constexpr int kSmemRaw = kSmemRing + kStages * kTileBytes;
@@ -101,13 +112,14 @@ struct Cfg {
     static constexpr int BAR_QFREE = BAR_QFULL + NQ;     // + x
     static constexpr int BAR_QREADY = BAR_QFREE + NQ;    // + x
     static constexpr int BAR_OFREE = BAR_QREADY + NQ;
-    static constexpr int BAR_DRAIN = BAR_OFREE + 1;
+    static constexpr int BAR_AUX = BAR_OFREE + 1;
+    static constexpr int BAR_DRAIN = BAR_AUX + 1;
     static constexpr int BAR_GROUP = BAR_DRAIN + 1;  // + 5 x + {SFULL, PFULL, ODONE, JOIN, JOIN + 1}
     static constexpr int kNumBars = BAR_GROUP + 10;
     static constexpr int kSmemMisc = kSmemBar + kNumBars * 8;
     static constexpr int kSmemJoin = (kSmemMisc + 16 + 15) & ~15;  // float2 [2][2][128]
     static constexpr int kSmemFac = kSmemJoin + 2 * 2 * kBM * 8;  // uint8 [kFacBufs][NQ][128]
-    static constexpr int kSmemTotal = kSmemFac + kFacBufs * NQ * kBM;
+    static constexpr int kSmemTotal = kSmemFac + (Q4 ? kFacBufs * NQ * kBM : 0);
     static constexpr int kSmemAlloc = kSmemTotal + 1024;  // base aligned up to 1024 B
     static_assert(kSmemAlloc <= 232448, "shared memory per CTA");
     static_assert(kSmemBar % 16 == 0 && kSmemRaw % 128 == 0, "shared-memory alignment");
@@ -116,12 +128,9 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;
 enum { SFULL = 0, PFULL = 1, ODONE = 2, JOIN = 3 };
 
-constexpr uint32_t kIdescQK = ptx::idesc_f16_f32(kBM, kBN, false, false);
-constexpr uint32_t kIdescPV = ptx::idesc_f16_f32(kBM, kHD, false, true);
-
-template <int NQ>
+template <int NQ, bool Q4>
 struct Smem {
-    using C = Cfg<NQ>;
+    using C = Cfg<NQ, Q4>;
     uint32_t base;  // shared-window address of the 1024-aligned base
     uint8_t* ptr;   // generic pointer to the same place
     __device__ uint32_t bar(int i) const { return base + C::kSmemBar + 8u * i; }
@@ -150,8 +159,8 @@ __device__ __forceinline__ void record_timeout(const SplitParams& p, volatile in
 }
 
 // Wait of a whole warp (every lane returns the same).
-template <int NQ>
-__device__ __forceinline__ bool warp_wait(const SplitParams& p, const Smem<NQ>& sm, uint32_t bar,
+template <int NQ, bool Q4>
+__device__ __forceinline__ bool warp_wait(const SplitParams& p, const Smem<NQ, Q4>& sm, uint32_t bar,
                                           uint32_t parity, int site) {
     const bool w = ptx::mbar_wait(bar, parity, p.wait_limit_ns, sm.abort_flag());
     if (__all_sync(0xffffffffu, w)) return true;
@@ -186,14 +195,20 @@ struct Tiles {
 };
 
 // ------------------------------------------------------------------ producer
-template <int NQ>
-__device__ void producer_warp(const SplitParams& p, const Smem<NQ>& sm, const CUtensorMap* tm_q) {
-    using C = Cfg<NQ>;
+template <int NQ, bool Q4>
+__device__ void producer_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, const CUtensorMap* tm_q,
+                              const CUtensorMap* tm_k, const CUtensorMap* tm_v) {
+    using C = Cfg<NQ, Q4>;
     const int lane = threadIdx.x & 31;
     volatile int* abort = sm.abort_flag();
     const int ps = p.page_size;
     const int64_t block = static_cast<int64_t>(ps) * kQ4RowBytes;
-    uint32_t it = 0;                // raw tiles issued
+    // the ring this warp fills: raw tiles, or the 16-bit tiles themselves
+    constexpr uint32_t kRing = Q4 ? C::kRaw : C::kStages;
+    constexpr int kFull = Q4 ? C::BAR_RFULL : C::BAR_FULL, kEmpty = Q4 ? C::BAR_REMPTY : C::BAR_EMPTY;
+    uint32_t it = 0;                // tiles issued
+    uint32_t n_aux = 0;             // partial tiles issued
+    bool aux_pending = false;
     uint32_t q_loads[NQ] = {};      // loads of each Q buffer so far
     bool ok = true;
 
@@ -275,23 +290,60 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ>& sm, const CU
                     win_nxt = load_window(win + 1);
                 }
                 const int page = __shfl_sync(0xffffffffu, win_cur, ((j * ppt) & 31) + (lane & 7));
-                int64_t src = 0;
-                if (lane < n_pg)
-                    src = (static_cast<int64_t>(checked_page(p, page)) * p.H_kv + u.kv_head) * block;
+                const int page_ok = lane < n_pg ? checked_page(p, page) : 0;
+                const int64_t head = static_cast<int64_t>(page_ok) * p.H_kv + u.kv_head;
+                // rows of the tile that no row of the unit sees: before front, from n_valid
+                const int front = run == 1 && j == 0 ? tl.key_begin - tl.begin : 0;
+                const int n_valid = min(kBN, end - (begin + j * kBN));
                 for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
-                    const uint32_t s = it % C::kRaw, par = (it / C::kRaw) & 1u;
-                    const uint32_t empty = sm.bar(C::BAR_REMPTY + s), full = sm.bar(C::BAR_RFULL + s);
+                    const uint32_t s = it % kRing, par = (it / kRing) & 1u;
+                    const uint32_t empty = sm.bar(kEmpty + s);
                     ok = wait_for([&] { return ptx::mbar_test_wait(empty, par ^ 1u); }, 2);
                     if (!ok) break;
-                    if (lane == 0)
-                        ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(n_pg) *
-                                                             static_cast<uint32_t>(block));
-                    __syncwarp();
-                    if (lane < n_pg)
-                        ptx::bulk_load(sm.base + C::kSmemRaw + s * kRawBytes +
-                                           lane * static_cast<uint32_t>(block),
-                                       (kv == 0 ? p.k_pool : p.v_pool) + src,
-                                       static_cast<uint32_t>(block), full);
+                    if (Q4) {
+                        const uint32_t full = sm.bar(kFull + s);
+                        if (lane == 0)
+                            ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(n_pg) *
+                                                                 static_cast<uint32_t>(block));
+                        __syncwarp();
+                        if (lane < n_pg)
+                            ptx::bulk_load(sm.base + C::kSmemRaw + s * kRawBytes +
+                                               lane * static_cast<uint32_t>(block),
+                                           (kv == 0 ? p.k_pool : p.v_pool) + head * block,
+                                           static_cast<uint32_t>(block), full);
+                    } else {
+                        const bool partial = n_valid < kBN || front > 0;
+                        const uint32_t bar = partial ? sm.bar(C::BAR_AUX) : sm.bar(kFull + s);
+                        const uint32_t dst = sm.tile(it);
+                        if (lane == 0)
+                            ptx::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n_pg * ps) * 256u);
+                        __syncwarp();
+                        if (lane < n_pg) {
+                            const CUtensorMap* tm = kv == 0 ? tm_k : tm_v;
+                            const int row = static_cast<int>(head * ps);
+                            const uint32_t off = static_cast<uint32_t>(lane * ps) * 128u;
+                            ptx::tma_load_2d(dst + off, tm, bar, 0, row);
+                            ptx::tma_load_2d(dst + kHalfBytes + off, tm, bar, 64, row);
+                        }
+                        if (partial) {
+                            // wait for the pages, then zero the rows nobody sees
+                            const uint32_t aux = sm.bar(C::BAR_AUX), aux_par = n_aux & 1u;
+                            aux_pending = true;
+                            ok = wait_for([&] { return ptx::mbar_test_wait(aux, aux_par); }, 3);
+                            if (!ok) break;
+                            aux_pending = false;
+                            ++n_aux;
+                            for (int i = lane; i < (kBN - n_valid + front) * 16; i += 32) {
+                                const int r = (i >> 4) < front ? i >> 4 : n_valid + (i >> 4) - front;
+                                const uint32_t ch = i & 15;
+                                ptx::st_shared_v4(dst + (ch >> 3) * kHalfBytes + r * 128 + (ch & 7) * 16,
+                                                  0u, 0u, 0u, 0u);
+                            }
+                            ptx::fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(sm.bar(kFull + s));
+                        }
+                    }
                 }
             }
         }
@@ -301,10 +353,12 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ>& sm, const CU
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (!ok && lane == 0) {
         // Drain: every copy this warp started must land before the CTA exits.
-        const uint32_t n = it < C::kRaw ? it : C::kRaw;
+        // (A tile of the 16-bit ring that still waits for its partial pages is covered
+        // by the AUX barrier alone: its full barrier never completes.)
+        const uint32_t n = it < kRing ? it : kRing;
         for (uint32_t i = it - n; i != it; ++i)
-            ptx::mbar_wait(sm.bar(C::BAR_RFULL + i % C::kRaw), (i / C::kRaw) & 1u, p.wait_limit_ns,
-                           nullptr);
+            ptx::mbar_wait(sm.bar(kFull + i % kRing), (i / kRing) & 1u, p.wait_limit_ns, nullptr);
+        if (aux_pending) ptx::mbar_wait(sm.bar(C::BAR_AUX), n_aux & 1u, p.wait_limit_ns, nullptr);
 #pragma unroll
         for (int x = 0; x < NQ; ++x)
             if (q_loads[x] > 0)
@@ -313,14 +367,15 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ>& sm, const CU
     }
 }
 
-// ------------------------------------------------------------------ Q to f16
-// Two warps turn the rows of a loaded Q tile into f16 in place: a thread finds its
+// ------------------------------------------------------------------ Q tiles
+// Two warps prepare a loaded Q tile in place. For bf16 pools they only write the
+// copies of its rows, if any. For 4-bit pools rows become f16: a thread finds its
 // row's largest exponent, scales by a power of two and stores the 8 values of each
 // 16-byte piece in the order the widened K tiles have, in every copy of the row.
 // Rows behind the unit's last are left as they are (their scores are never used).
-template <int NQ>
-__device__ void q_warp(const SplitParams& p, const Smem<NQ>& sm, int w) {
-    using C = Cfg<NQ>;
+template <int NQ, bool Q4>
+__device__ void q_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, int w) {
+    using C = Cfg<NQ, Q4>;
     const int lane = threadIdx.x & 31;
     uint32_t loads[2] = {0, 0};
     const int ui_end = p.cta_first[blockIdx.x + 1];
@@ -329,21 +384,30 @@ __device__ void q_warp(const SplitParams& p, const Smem<NQ>& sm, int w) {
         const int nq = unit_nq<NQ>(u, p.tpt);
         for (int x = 0; x < nq; ++x) {
             const uint32_t n = x == 0 ? loads[0]++ : loads[1]++;
-            if (!warp_wait<NQ>(p, sm, sm.bar(C::BAR_QFULL + x), n & 1u, 50)) return;
+            if (!warp_wait<NQ, Q4>(p, sm, sm.bar(C::BAR_QFULL + x), n & 1u, 50)) return;
             const int rows = min(p.tpt, u.n_tok - x * p.tpt) * p.G;
             const int split = nq == 1 ? key_split(u, p.G) : 1;
-            for (int row = w * 32 + lane; row < rows; row += 32 * kQWarps) {
+            for (int row = w * 32 + lane; row < rows && (Q4 || split > 1); row += 32 * kQWarps) {
                 const uint32_t at = sm.base + C::kSmemQ + x * kQBytes + row * 128;
                 const uint32_t swz = static_cast<uint32_t>(row & 7) << 4;
                 auto piece = [&](int c) { return at + (c >> 3) * kHalfBytes + (((c & 7) << 4) ^ swz); };
+                if (!Q4) {
+#pragma unroll 4
+                    for (int c = 0; c < 16; ++c) {
+                        const uint4 v = ptx::ld_shared_v4(piece(c));
+                        for (int copy = kBM / split; copy < kBM; copy += kBM / split)
+                            ptx::st_shared_v4(piece(c) + copy * 128, v.x, v.y, v.z, v.w);
+                    }
+                    continue;
+                }
                 uint32_t top[4] = {0, 0, 0, 0};
+#pragma unroll 1
+                for (int q = 0; q < 16; q += 4) {
+                    uint4 v[4];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint4 v[8];
+                    for (int c = 0; c < 4; ++c) v[c] = ptx::ld_shared_v4(piece(q + c));
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) v[c] = ptx::ld_shared_v4(piece(8 * half + c));
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
+                    for (int c = 0; c < 4; ++c) {
                         top[0] = ptx::max_abs_bf16x2(top[0], v[c].x);
                         top[1] = ptx::max_abs_bf16x2(top[1], v[c].y);
                         top[2] = ptx::max_abs_bf16x2(top[2], v[c].z);
@@ -358,22 +422,22 @@ __device__ void q_warp(const SplitParams& p, const Smem<NQ>& sm, int w) {
                 const float f = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
                 auto lo = [f](uint32_t b) { return __uint_as_float(b << 16) * f; };
                 auto hi = [f](uint32_t b) { return __uint_as_float(b & 0xffff0000u) * f; };
+#pragma unroll 1
+                for (int q = 0; q < 16; q += 4) {
+                    uint4 v[4];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint4 v[8];
+                    for (int c = 0; c < 4; ++c) v[c] = ptx::ld_shared_v4(piece(q + c));
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) v[c] = ptx::ld_shared_v4(piece(8 * half + c));
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
+                    for (int c = 0; c < 4; ++c)
                         v[c] = make_uint4(ptx::pack_f16x2(lo(v[c].x), lo(v[c].y)),
                                           ptx::pack_f16x2(lo(v[c].z), lo(v[c].w)),
                                           ptx::pack_f16x2(hi(v[c].x), hi(v[c].y)),
                                           ptx::pack_f16x2(hi(v[c].z), hi(v[c].w)));
                     for (int copy = 0; copy < kBM; copy += kBM / split)
 #pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            ptx::st_shared_v4(piece(8 * half + c) + copy * 128, v[c].x, v[c].y,
-                                              v[c].z, v[c].w);
+                        for (int c = 0; c < 4; ++c)
+                            ptx::st_shared_v4(piece(q + c) + copy * 128, v[c].x, v[c].y, v[c].z,
+                                              v[c].w);
                 }
                 for (int copy = 0; copy < kBM; copy += kBM / split)
                     *sm.fac(n, x, row + copy) = static_cast<uint8_t>(k + 127);
@@ -388,14 +452,7 @@ __device__ void q_warp(const SplitParams& p, const Smem<NQ>& sm, int w) {
 // ------------------------------------------------------------------ widening
 // Eight codes to eight f16 values (0 2 4 6 1 3 5 7) times their group's scale.
 __device__ __forceinline__ void widen_word(uint32_t w, uint32_t scale, uint32_t (&o)[4]) {
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
-        : "r"(w));
+    ptx::f16x2_of_e2m1x8(w, o);
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = ptx::mul_f16x2(o[i], scale);
 }
@@ -407,8 +464,8 @@ __device__ __forceinline__ void widen_word(uint32_t w, uint32_t scale, uint32_t 
 // sixteen-byte columns. A row that no row of the unit sees gets scale 0 (codes are
 // finite whatever they are).
 template <int NQ>
-__device__ void widen_warp(const SplitParams& p, const Smem<NQ>& sm, int w, bool is_v) {
-    using C = Cfg<NQ>;
+__device__ void widen_warp(const SplitParams& p, const Smem<NQ, true>& sm, int w, bool is_v) {
+    using C = Cfg<NQ, true>;
     const int lane = threadIdx.x & 31;
     const int ps = p.page_size, ps_shift = 31 - __clz(ps), piece = lane & 3;
     const bool upper = piece >= 2;
@@ -435,7 +492,7 @@ __device__ void widen_warp(const SplitParams& p, const Smem<NQ>& sm, int w, bool
             int kt, last, front;
             tl.tile(j, kt, last, front);
             const uint32_t rs = it % C::kRaw, stage = it % C::kStages;
-            if (!warp_wait<NQ>(p, sm, sm.bar(C::BAR_RFULL + rs), (it / C::kRaw) & 1u, 40)) return;
+            if (!warp_wait<NQ, true>(p, sm, sm.bar(C::BAR_RFULL + rs), (it / C::kRaw) & 1u, 40)) return;
             const uint32_t raw = sm.base + C::kSmemRaw + rs * kRawBytes;
             uint4 c[4];
             uint32_t sc[4];
@@ -448,7 +505,7 @@ __device__ void widen_warp(const SplitParams& p, const Smem<NQ>& sm, int w, bool
             }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(sm.bar(C::BAR_REMPTY + rs));  // in registers now
-            if (!warp_wait<NQ>(p, sm, sm.bar(C::BAR_EMPTY + stage), ((it / C::kStages) & 1u) ^ 1u, 41))
+            if (!warp_wait<NQ, true>(p, sm, sm.bar(C::BAR_EMPTY + stage), ((it / C::kStages) & 1u) ^ 1u, 41))
                 return;
             const uint32_t dst = sm.tile(it) + row_at;
 #pragma unroll
@@ -488,17 +545,17 @@ struct PvOp {
     uint32_t pos;
 };
 
-template <int NQ>
+template <int NQ, bool Q4>
 struct Issuer {
-    using C = Cfg<NQ>;
+    using C = Cfg<NQ, Q4>;
     const SplitParams& p;
-    const Smem<NQ>& sm;
+    const Smem<NQ, Q4>& sm;
     uint32_t tmem;
     uint32_t leader;  // 1 in the lane that issues
     bool issued_any = false;
 
     __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, int site) {
-        return warp_wait<NQ>(p, sm, bar, parity, site);
+        return warp_wait<NQ, Q4>(p, sm, bar, parity, site);
     }
     __device__ __forceinline__ bool wait_full(uint32_t pos, int site) {
         return wait(sm.bar(C::BAR_FULL + pos % C::kStages), (pos / C::kStages) & 1u, site);
@@ -514,7 +571,7 @@ struct Issuer {
         const uint64_t dk = ptx::sdesc_sw128(sm.tile(pos), 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < kHD / 16; ++kk)
-            ptx::mma_f16_ss_if(tmem + 128u * x, dq + kmajor_step(kk), dk + kmajor_step(kk), kIdescQK,
+            ptx::mma_f16_ss_if(tmem + 128u * x, dq + kmajor_step(kk), dk + kmajor_step(kk), C::kIdescQK,
                                kk > 0, leader);
         commit(sm.gbar(x, SFULL));
         issued_any = true;
@@ -528,7 +585,7 @@ struct Issuer {
         const uint64_t dv = ptx::sdesc_sw128(sm.tile(op.pos), kHalfBytes, 1024);
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk)
-            ptx::mma_f16_ts_if(d, a + 8u * kk, dv + 128u * kk, kIdescPV,
+            ptx::mma_f16_ts_if(d, a + 8u * kk, dv + 128u * kk, C::kIdescPV,
                                (!op.first || kk > 0) ? 1u : 0u, leader);
         commit(sm.gbar(op.x, ODONE));
         return true;
@@ -547,11 +604,11 @@ struct Issuer {
 // S(t) into group t mod 2's buffer, then P.V(t-1) of the other group; a unit's
 // last P.V is held until the next such unit's first S is issued. An S that
 // reuses the TMEM of an earlier P is always issued after that P's product.
-template <int NQ>
-__device__ void mma_warp(const SplitParams& p, const Smem<NQ>& sm, uint32_t tmem) {
-    using C = Cfg<NQ>;
+template <int NQ, bool Q4>
+__device__ void mma_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, uint32_t tmem) {
+    using C = Cfg<NQ, Q4>;
     // broadcasts: the values are warp-uniform, and known to be
-    Issuer<NQ> is{p, sm, __shfl_sync(0xffffffffu, tmem, 0), ptx::elect_one()};
+    Issuer<NQ, Q4> is{p, sm, __shfl_sync(0xffffffffu, tmem, 0), ptx::elect_one()};
     bool ok = true;
     uint32_t pos = 0;           // ring position of the unit's K_0 (K_j at pos + 2j, V_j behind it)
     uint32_t jt[2] = {0, 0};    // tiles each softmax group got before
@@ -659,49 +716,47 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32], float m) {
     return fmaxf(a, b);
 }
 
-// P of 32 columns to TMEM (16 columns of f16 pairs), their sum added to l.
+// P of 32 columns to TMEM (16 columns of 16-bit pairs; bf16 as V for bf16 pools: half
+// a step is 2^-8 of each p), their sum, of the unrounded values, added to l.
+template <bool Q4>
 __device__ __forceinline__ void exp32(const uint32_t (&s)[32], uint32_t taddr, uint64_t sl2,
                                       uint64_t negm, uint64_t (&l)[2]) {
+    uint32_t packed[16];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t packed[8];
-#pragma unroll
-        for (int c = 0; c < 16; c += 2) {
-            const uint64_t t = ptx::fma_f32x2(ptx::f32x2(__uint_as_float(s[16 * h + c]),
-                                                         __uint_as_float(s[16 * h + c + 1])),
-                                              sl2, negm);
-            const float e0 = ptx::ex2(ptx::lo_f32(t)), e1 = ptx::ex2(ptx::hi_f32(t));
-            l[(c >> 1) & 1] = ptx::add_f32x2(l[(c >> 1) & 1], ptx::f32x2(e0, e1));
-            packed[c >> 1] = ptx::pack_f16x2(e0, e1);
-        }
-        ptx::tmem_st8(taddr + 8 * h, packed);
+    for (int c = 0; c < 32; c += 2) {
+        const uint64_t t = ptx::fma_f32x2(
+            ptx::f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sl2, negm);
+        const float e0 = ptx::ex2(ptx::lo_f32(t)), e1 = ptx::ex2(ptx::hi_f32(t));
+        l[(c >> 1) & 1] = ptx::add_f32x2(l[(c >> 1) & 1], ptx::f32x2(e0, e1));
+        packed[c >> 1] = Q4 ? ptx::pack_f16x2(e0, e1) : ptx::pack_bf16x2(e0, e1);
     }
+    ptx::tmem_st16(taddr, packed);
 }
 __device__ __forceinline__ void zero16(uint32_t taddr) {
-    const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-    ptx::tmem_st8(taddr, z);
-    ptx::tmem_st8(taddr + 8, z);
+    const uint32_t z[16] = {};
+    ptx::tmem_st16(taddr, z);
 }
 
 // The running reference and sum of a row (of one copy's keys).
 struct Running {
     float m = -INFINITY, l = 0.f;
     // A tile's maximum: the factor that O and l take, and the exponent's addend.
-    __device__ __forceinline__ float raise(float mx, float& neg) {
+    __device__ __forceinline__ float raise(float mx, float lift, float& neg) {
         float corr = 1.f;
         if (mx > m + kRescaleLog2) {
             corr = (m == -INFINITY) ? 0.f : ptx::ex2(m - mx);
             m = mx;
         }
-        neg = kLiftLog2 - ((m == -INFINITY) ? 0.f : m);
+        neg = lift - ((m == -INFINITY) ? 0.f : m);
         return corr;
     }
 };
 
 // One tile's softmax of this thread's row, over the keys of its copy `seg` of F: P
 // over the first 64 columns of S. Returns the rescale factor.
-template <int F>
+template <int F, bool Q4>
 __device__ __forceinline__ float softmax_tile(uint32_t colS, int seg, float sl2, Running& run) {
+    constexpr float kLift = Cfg<1, Q4>::kLiftLog2;
     const uint64_t sl2p = ptx::f32x2(sl2, sl2);
     uint64_t l[2] = {0ull, 0ull};
     uint32_t s0[32];
@@ -709,45 +764,61 @@ __device__ __forceinline__ float softmax_tile(uint32_t colS, int seg, float sl2,
     if (F == 4) {
         ptx::tmem_ld32(colS + 32 * seg, s0);
         ptx::tmem_ld_wait(s0);
-        corr = run.raise(max32(s0, -INFINITY) * sl2, neg);  // scale > 0: max commutes
+        corr = run.raise(max32(s0, -INFINITY) * sl2, kLift, neg);  // scale > 0: max commutes
         const uint64_t negm = ptx::f32x2(neg, neg);
-        exp32(s0, colS + 16 * seg, sl2p, negm, l);
+        exp32<Q4>(s0, colS + 16 * seg, sl2p, negm, l);
 #pragma unroll
         for (int i = 1; i < 4; ++i) zero16(colS + 16 * (seg ^ i));
     } else if (F == 2) {
         uint32_t s1[32];
         load64(colS + 64 * seg, s0, s1);
-        corr = run.raise(max32(s1, max32(s0, -INFINITY)) * sl2, neg);
+        corr = run.raise(max32(s1, max32(s0, -INFINITY)) * sl2, kLift, neg);
         const uint64_t negm = ptx::f32x2(neg, neg);
-        exp32(s0, colS + 32 * seg, sl2p, negm, l);
-        exp32(s1, colS + 32 * seg + 16, sl2p, negm, l);
+        exp32<Q4>(s0, colS + 32 * seg, sl2p, negm, l);
+        exp32<Q4>(s1, colS + 32 * seg + 16, sl2p, negm, l);
         zero16(colS + 32 * (seg ^ 1));
         zero16(colS + 32 * (seg ^ 1) + 16);
     } else {
-        // columns 64.. first for the maximum; 0.. stay in registers
+        // 32 columns at a time, the next ones on their way from TMEM while these are
+        // worked on: the maximum from the last columns down, P from the first up
         uint32_t s1[32];
-        load64(colS + 64, s0, s1);
-        const float mx = max32(s1, max32(s0, -INFINITY));
-        load64(colS, s0, s1);
-        corr = run.raise(max32(s1, max32(s0, mx)) * sl2, neg);
+        ptx::tmem_ld32(colS + 96, s1);
+        ptx::tmem_ld_wait(s1);
+        ptx::tmem_ld32(colS + 64, s0);
+        float mx = max32(s1, -INFINITY);
+        ptx::tmem_ld_wait(s0);
+        ptx::tmem_ld32(colS + 32, s1);
+        mx = max32(s0, mx);
+        ptx::tmem_ld_wait(s1);
+        ptx::tmem_ld32(colS, s0);
+        mx = max32(s1, mx);
+        ptx::tmem_ld_wait(s0);
+        ptx::tmem_ld32(colS + 32, s1);
+        mx = max32(s0, mx);
+        corr = run.raise(mx * sl2, kLift, neg);
         const uint64_t negm = ptx::f32x2(neg, neg);
-        exp32(s0, colS, sl2p, negm, l);
-        exp32(s1, colS + 16, sl2p, negm, l);
-        load64(colS + 64, s0, s1);
-        exp32(s0, colS + 32, sl2p, negm, l);
-        exp32(s1, colS + 48, sl2p, negm, l);
+        exp32<Q4>(s0, colS, sl2p, negm, l);
+        ptx::tmem_ld_wait(s1);
+        ptx::tmem_ld32(colS + 64, s0);
+        exp32<Q4>(s1, colS + 16, sl2p, negm, l);
+        ptx::tmem_ld_wait(s0);
+        ptx::tmem_ld32(colS + 96, s1);
+        exp32<Q4>(s0, colS + 32, sl2p, negm, l);
+        ptx::tmem_ld_wait(s1);
+        exp32<Q4>(s1, colS + 48, sl2p, negm, l);
     }
     const uint64_t sum = ptx::add_f32x2(l[0], l[1]);
     run.l = run.l * corr + (ptx::lo_f32(sum) + ptx::hi_f32(sum));
     return corr;
 }
 
-// 32 columns of a finished row, put back into their order (each 8 hold values 0 2
-// 4 6 1 3 5 7): to out (direct) or to its partial block.
+// 32 columns of a finished row to out (direct) or to its partial block; from 4-bit
+// pools put back into their order first (each 8 hold values 0 2 4 6 1 3 5 7).
+template <bool Q4>
 __device__ __forceinline__ void store32(void* out, float* part_o, int out_bf16,
                                         const uint32_t (&r)[32], bool direct, int64_t orow,
                                         int64_t prow, int c0) {
-    auto at = [](int d) { return (d & ~7) + (d & 1) * 4 + ((d & 7) >> 1); };
+    auto at = [](int d) { return Q4 ? (d & ~7) + (d & 1) * 4 + ((d & 7) >> 1) : d; };
     if (direct && out_bf16) {
         uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + orow * kHD + c0);
 #pragma unroll
@@ -778,9 +849,9 @@ __device__ __forceinline__ void store32(void* out, float* part_o, int out_bf16,
 }
 
 // Group x: thread i owns row i of the group's query tile (TMEM lane i).
-template <int NQ>
-__device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t tmem, int x) {
-    using C = Cfg<NQ>;
+template <int NQ, bool Q4>
+__device__ void softmax_group(const SplitParams& p, const Smem<NQ, Q4>& sm, uint32_t tmem, int x) {
+    using C = Cfg<NQ, Q4>;
     const int lane = threadIdx.x & 31;
     const int quarter = (threadIdx.x >> 5) & 3;  // TMEM lane quarter this warp may access
     const int row = quarter * 32 + lane;
@@ -826,12 +897,12 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
             const int lim = min(row_end, last) - kt, lo = row_end - p.window - kt;
             const int sink = f || tl.n_first == 0 ? p.sinks - kt : 0;
             const bool full = __all_sync(0xffffffffu, lim >= kBN && (lo <= 0 || sink >= kBN));
-            if (!warp_wait<NQ>(p, sm, sm.gbar(x, SFULL), jt & 1u, 20)) return;
+            if (!warp_wait<NQ, Q4>(p, sm, sm.gbar(x, SFULL), jt & 1u, 20)) return;
             ptx::tc_fence_after();
             // The factor was written before the S product was issued. (Waiting for
             // QREADY here would be wrong: a group without a tile in a unit may find
             // that barrier two phases on.)
-            if (j == j0 && row_valid) {
+            if (Q4 && j == j0 && row_valid) {
                 const int k = static_cast<int>(*sm.fac(load, xq, row)) - 127;
                 sl2 *= __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
             }
@@ -839,9 +910,9 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
             if (active) {
                 if (!full)
                     mask_tile(colS, seg * (kBN / split), (seg + 1) * (kBN / split), lim, lo, sink);
-                corr = split == 4   ? softmax_tile<4>(colS, seg, sl2, run)
-                       : split == 2 ? softmax_tile<2>(colS, seg, sl2, run)
-                                    : softmax_tile<1>(colS, seg, sl2, run);
+                corr = split == 4   ? softmax_tile<4, Q4>(colS, seg, sl2, run)
+                       : split == 2 ? softmax_tile<2, Q4>(colS, seg, sl2, run)
+                                    : softmax_tile<1, Q4>(colS, seg, sl2, run);
             }
             // O is rescaled in place: this S was issued after the group's previous
             // product, so that one has completed.
@@ -862,7 +933,7 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(sm.gbar(x, PFULL));
         }
-        const float m_ref = run.m, l_run = run.l * 0.0078125f;  // 2^-7: the lift of P
+        const float m_ref = run.m, l_run = run.l * C::kUnlift;  // without P's lift
         const bool direct = u.part < 0;
         const int64_t orow =
             dry ? 0 : static_cast<int64_t>(tok) * p.H_q + u.kv_head * p.G + urow % p.G;
@@ -873,10 +944,10 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
         float m_out = m_ref, l_out = l_run;
         if (pair) {
             jt_other += n_tiles;
-            if (!dry && !warp_wait<NQ>(p, sm, sm.gbar(x, ODONE), (jt - 1) & 1u, 22)) return;
+            if (!dry && !warp_wait<NQ, Q4>(p, sm, sm.gbar(x, ODONE), (jt - 1) & 1u, 22)) return;
             ptx::tc_fence_after();
             if (active) {
-                const float w = p.o_scale * 0.0078125f * (direct ? (l_run > 0.f ? 1.f / l_run : 0.f) : 1.f);
+                const float w = p.o_scale * C::kUnlift * (direct ? (l_run > 0.f ? 1.f / l_run : 0.f) : 1.f);
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t r[32];
@@ -885,7 +956,7 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
                     ptx::tmem_ld_wait(r);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * w);
-                    if (row_valid) store32(out, part_o, p.out_bf16, r, direct, orow, prow, 32 * c);
+                    if (row_valid) store32<Q4>(out, part_o, p.out_bf16, r, direct, orow, prow, 32 * c);
                 }
             }
         } else {
@@ -900,11 +971,11 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
                 // arrive there before this one has waited here
                 if (lane == 0) ptx::mbar_arrive(sm.gbar(x, JOIN + (kj & 1)));
                 jt_other += n_other;
-                if (!warp_wait<NQ>(p, sm, sm.gbar(x ^ 1, JOIN + (kj & 1)), (kj >> 1) & 1, 23)) return;
+                if (!warp_wait<NQ, Q4>(p, sm, sm.gbar(x ^ 1, JOIN + (kj & 1)), (kj >> 1) & 1, 23)) return;
                 ++kj;
             }
-            if (n_mine > 0 && !warp_wait<NQ>(p, sm, sm.gbar(x, ODONE), (jt - 1) & 1u, 22)) return;
-            if (n_other > 0 && !warp_wait<NQ>(p, sm, sm.gbar(x ^ 1, ODONE), (jt_other - 1) & 1u, 24))
+            if (n_mine > 0 && !warp_wait<NQ, Q4>(p, sm, sm.gbar(x, ODONE), (jt - 1) & 1u, 22)) return;
+            if (n_other > 0 && !warp_wait<NQ, Q4>(p, sm, sm.gbar(x ^ 1, ODONE), (jt_other - 1) & 1u, 24))
                 return;
             ptx::tc_fence_after();
             nx = (nx + n_tiles) & 1;
@@ -916,7 +987,7 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
                 float wa = m_a == -INFINITY ? 0.f : ptx::ex2(m_a - m_out);
                 float wb = m_b == -INFINITY ? 0.f : ptx::ex2(m_b - m_out);
                 l_out = wa * l_run + wb * other.y;
-                const float w = p.o_scale * 0.0078125f * (direct ? (l_out > 0.f ? 1.f / l_out : 0.f) : 1.f);
+                const float w = p.o_scale * C::kUnlift * (direct ? (l_out > 0.f ? 1.f / l_out : 0.f) : 1.f);
                 wa *= w;
                 wb *= w;
                 const uint32_t oa = lane_addr + kColO + 128u * x + 64u * x;
@@ -934,7 +1005,7 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
                     for (int i = 0; i < 32; ++i)
                         a[i] = __float_as_uint((wa != 0.f ? wa * __uint_as_float(a[i]) : 0.f) +
                                                (wb != 0.f ? wb * __uint_as_float(b[i]) : 0.f));
-                    if (row_valid) store32(out, part_o, p.out_bf16, a, direct, orow, prow, 64 * x + 32 * c);
+                    if (row_valid) store32<Q4>(out, part_o, p.out_bf16, a, direct, orow, prow, 64 * x + 32 * c);
                 }
             }
         }
@@ -950,12 +1021,14 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
     }
 }
 
-template <int NQ>
-__global__ void __launch_bounds__(kThreads, 1)
-    attn_q4_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ CUtensorMap tm_q) {
-    using C = Cfg<NQ>;
+template <int NQ, bool Q4>
+__global__ void __launch_bounds__(Cfg<NQ, Q4>::kThreads, 1)
+    attn_rows_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ CUtensorMap tm_q,
+                     const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v) {
+    using C = Cfg<NQ, Q4>;
     extern __shared__ uint8_t smem_raw[];
-    Smem<NQ> sm;
+    Smem<NQ, Q4> sm;
     {
         const uint32_t raw = ptx::smem_u32(smem_raw);
         const uint32_t aligned = (raw + 1023u) & ~1023u;
@@ -966,7 +1039,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            ptx::mbar_init(sm.bar(C::BAR_FULL + s), kGroupWarps);
+            ptx::mbar_init(sm.bar(C::BAR_FULL + s), Q4 ? kGroupWarps : 1);
             ptx::mbar_init(sm.bar(C::BAR_EMPTY + s), 1);
         }
         for (int s = 0; s < C::kRaw; ++s) {
@@ -979,6 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(sm.bar(C::BAR_QREADY + x), kQWarps);
         }
         ptx::mbar_init(sm.bar(C::BAR_OFREE), 2 * kGroupWarps);
+        ptx::mbar_init(sm.bar(C::BAR_AUX), 1);
         ptx::mbar_init(sm.bar(C::BAR_DRAIN), 1);
         for (int x = 0; x < 2; ++x) {
             ptx::mbar_init(sm.gbar(x, SFULL), 1);
@@ -991,7 +1065,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::fence_barrier_init();
         ptx::fence_proxy_async_smem();
     }
-    if (warp == 0 && lane == 0) ptx::prefetch_tmap(&tm_q);
+    if (warp == 0 && lane == 0) {
+        ptx::prefetch_tmap(&tm_q);
+        if (!Q4) {
+            ptx::prefetch_tmap(&tm_k);
+            ptx::prefetch_tmap(&tm_v);
+        }
+    }
     if (warp == 1) {
         ptx::tmem_alloc(ptx::smem_u32(sm.tmem_slot()), kTmemCols);
         ptx::tmem_relinquish();
@@ -1001,20 +1081,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after();
     const uint32_t tmem = *sm.tmem_slot();
 
-    if (warp < kWarpSoftmax) ptx::regs_dec<kRegsOther>();
+    if (Q4 && warp < kWarpSoftmax) ptx::regs_dec<kRegsOther>();
     if (warp == 0) {
-        ;
+        producer_warp<NQ, Q4>(p, sm, &tm_q, &tm_k, &tm_v);
     } else if (warp == 1) {
-        mma_warp<NQ>(p, sm, tmem);
+        ;
         __syncwarp();
     } else if (warp < kWarpSoftmax) {
-        q_warp<NQ>(p, sm, warp - kWarpQ);
+        q_warp<NQ, Q4>(p, sm, warp - kWarpQ);
     } else if (warp < kWarpWiden) {
-        ptx::regs_inc<kRegsSoftmax>();
-        softmax_group<NQ>(p, sm, tmem, (warp - kWarpSoftmax) / kGroupWarps);
+        if (Q4) ptx::regs_inc<kRegsSoftmax>();
+        softmax_group<NQ, Q4>(p, sm, tmem, (warp - kWarpSoftmax) / kGroupWarps);
     } else {
-        ptx::regs_dec<kRegsWiden>();
-        widen_warp<NQ>(p, sm, (warp - kWarpWiden) & 3, warp >= kWarpWiden + kGroupWarps);
+        if constexpr (Q4) {
+            ptx::regs_dec<kRegsWiden>();
+            widen_warp<NQ>(p, sm, (warp - kWarpWiden) & 3, warp >= kWarpWiden + kGroupWarps);
+        }
     }
 
     ptx::tc_fence_before();
@@ -1025,8 +1107,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int NQ>
-cudaError_t launch_nq(const SplitParams& p, const CUtensorMap& tm_q, int grid, cudaStream_t stream) {
+template <int NQ, bool Q4>
+cudaError_t launch_nq(const SplitParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                      const CUtensorMap& tm_v, int grid, cudaStream_t stream) {
     // The shared-memory attribute is set once per device (see attn_fwd.cu).
     static std::atomic<bool> attr_set[64];
     static std::mutex attr_mu;
@@ -1037,21 +1120,27 @@ cudaError_t launch_nq(const SplitParams& p, const CUtensorMap& tm_q, int grid, c
     if (!known || !attr_set[dev].load(std::memory_order_acquire)) {
         std::lock_guard<std::mutex> lk(attr_mu);
         if (!known || !attr_set[dev].load(std::memory_order_relaxed)) {
-            e = cudaFuncSetAttribute(attn_q4_kernel<NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     Cfg<NQ>::kSmemAlloc);
+            e = cudaFuncSetAttribute(attn_rows_kernel<NQ, Q4>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     Cfg<NQ, Q4>::kSmemAlloc);
             if (e != cudaSuccess) return e;
             if (known) attr_set[dev].store(true, std::memory_order_release);
         }
     }
-    attn_q4_kernel<NQ><<<grid, kThreads, Cfg<NQ>::kSmemAlloc, stream>>>(p, tm_q);
+    attn_rows_kernel<NQ, Q4><<<grid, Cfg<NQ, Q4>::kThreads, Cfg<NQ, Q4>::kSmemAlloc, stream>>>(
+        p, tm_q, tm_k, tm_v);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attn_q4(const SplitParams& p, const CUtensorMap& tm_q, int grid,
-                           cudaStream_t stream) {
-    return p.nq == 2 ? launch_nq<2>(p, tm_q, grid, stream) : launch_nq<1>(p, tm_q, grid, stream);
+cudaError_t launch_attn_rows(const SplitParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                             const CUtensorMap& tm_v, bool q4, int grid, cudaStream_t stream) {
+    if (q4)
+        return p.nq == 2 ? launch_nq<2, true>(p, tm_q, tm_k, tm_v, grid, stream)
+                         : launch_nq<1, true>(p, tm_q, tm_k, tm_v, grid, stream);
+    return p.nq == 2 ? launch_nq<2, false>(p, tm_q, tm_k, tm_v, grid, stream)
+                     : launch_nq<1, false>(p, tm_q, tm_k, tm_v, grid, stream);
 }
 
 }  // namespace fanout
