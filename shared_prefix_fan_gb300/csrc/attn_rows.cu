@@ -14,9 +14,9 @@
 //               a ring of raw tiles (9 KB: 128 rows of 72 bytes). Q by TMA as soon as
 //               its buffer is free. Page ids are checked before they are read through;
 //   warp 1      TMEM owner and tcgen05 issuer: the whole warp runs the issue loop, so
-//               that descriptors stay in uniform registers, and one elected lane
-//               issues (a single-lane loop took twice as long per product);
-//   warps 2-3   prepare loaded Q tiles in place (copies, and f16 for 4-bit pools);
+//               that descriptors stay in uniform registers (they are constants: a
+//               branch per ring stage), and one elected lane issues;
+//   warps 2-3   4-bit pools only: turn loaded Q tiles into f16 in place;
 //   warps 4-11  two softmax groups of 4 warps, thread = row;
 //   warps 12-19 4-bit pools only: widen raw tiles into the swizzled 16-bit ring (4
 //               warps the K tiles, 4 the V tiles). With 4 warps for both, a decode
@@ -25,14 +25,11 @@
 // the pool holds there.
 //
 // A unit of two query tiles gives each group one of them. A unit of one query
-// tile (decode) is split over the groups by keys instead: tile t goes to group
-// t mod 2, each with its own S, (m, l) and O in TMEM, and the two are joined at
-// the unit's end (64 columns of O each), so that two tiles' softmaxes overlap.
-// Of such a unit that has at most 64 (32) rows and writes a partial, the rows are
-// copied to all 128 lanes 2 (4) times, and each copy takes its part of a tile's
-// keys: a thread then exponentiates 64 (32) scores of a tile, not 128, and stores
-// zeros for the other keys' P; each copy ends as a partial row of its own. The
-// softmax of one tile was the longest step of a decode CTA's loop.
+// tile (decode) is split over the groups by keys instead: even tiles (counted over
+// the CTA) go to group 0, odd ones to group 1, each with its own S, (m, l) and O in
+// TMEM, and the two are joined at the unit's end (64 columns of O each), so that two
+// tiles' softmaxes overlap. (All eight softmax warps on every tile, two to a row,
+// was slower: their phases coincide, and the exponentials' pipe idles between.)
 // TMEM: S_0 = 0, S_1 = 128, O_0 = 256, O_1 = 384 (512 columns).
 //
 // 4-bit pools. The rows of a cache (kv_q4.cu) are e2m1 codes with one e4m3 scale per
@@ -73,6 +70,7 @@ constexpr int kQBytes = kBM * kHD * 2;
 constexpr int kRawBytes = kBN * kQ4RowBytes;
 constexpr float kRescaleLog2 = 8.0f;  // lazy rescale threshold (base-2 units)
 constexpr int kErrTimeout = 5;        // FANOUT_ETIMEOUT
+constexpr int kErrCuda = 3;           // FANOUT_ECUDA
 constexpr int kGroupWarps = 4;
 constexpr int kWarpQ = 2;        // first warp of the Q conversion
 constexpr int kQWarps = 2;
@@ -88,7 +86,7 @@ constexpr int kFacBufs = 4;      // units whose row factors are held
 template <int NQ, bool Q4>
 struct Cfg {
     static constexpr int kThreads = 32 * (Q4 ? 20 : 12);
-    static constexpr int kStages = !Q4 && NQ == 1 ? 5 : 4;   // 16-bit tiles
+    static constexpr int kStages = 4;                        // 16-bit tiles
     static constexpr int kRaw = !Q4 ? 0 : NQ == 1 ? 6 : 2;  // raw tiles
     // P is 2^lift times the probability's numerator
     static constexpr float kLiftLog2 = Q4 ? 7.0f : 0.0f, kUnlift = Q4 ? 0.0078125f : 1.0f;
@@ -99,7 +97,7 @@ struct Cfg {
     // K tiles take the even and V tiles the odd ring positions, and the warps that
     // widen one kind wait for its stages only: with an odd ring a stage would change
     // kind, and a warp could take the phase before last of its barrier for the last.
-    static_assert(!Q4 || (kStages % 2 == 0 && kRaw % 2 == 0), "rings of K/V pairs");
+    static_assert(kStages == 4 && kRaw % 2 == 0, "rings of K/V pairs");
     static constexpr int kSmemQ = 0;
     static constexpr int kSmemRing = NQ * kQBytes;
     static constexpr int kSmemRaw = kSmemRing + kStages * kTileBytes;
@@ -120,7 +118,7 @@ struct Cfg {
     static constexpr int kSmemJoin = (kSmemMisc + 16 + 15) & ~15;  // float2 [2][2][128]
     static constexpr int kSmemFac = kSmemJoin + 2 * 2 * kBM * 8;  // uint8 [kFacBufs][NQ][128]
     static constexpr int kSmemTotal = kSmemFac + (Q4 ? kFacBufs * NQ * kBM : 0);
-    static constexpr int kSmemAlloc = kSmemTotal + 1024;  // base aligned up to 1024 B
+    static constexpr int kSmemAlloc = kSmemTotal;
     static_assert(kSmemAlloc <= 232448, "shared memory per CTA");
     static_assert(kSmemBar % 16 == 0 && kSmemRaw % 128 == 0, "shared-memory alignment");
 };
@@ -149,23 +147,26 @@ struct Smem {
     }
 };
 
-__device__ __forceinline__ void record_timeout(const SplitParams& p, volatile int* abort_flag,
-                                               int site) {
-    *abort_flag = 1;
-    if (atomicCAS(p.err, 0, kErrTimeout) == 0) {
-        p.err[1] = site;
-        p.err[2] = static_cast<int32_t>(blockIdx.x);
-    }
-}
-
-// Wait of a whole warp (every lane returns the same).
+// Wait of a whole warp (every lane returns the same). Bounded: false once another
+// wait of the CTA has given up, or after p.wait_limit_ns; the site goes into the
+// CTA's abort word, which the kernel reports at its end. Every role's waits are
+// inlined, and the roles share an instruction cache that their code overflows, so
+// this is kept short (the kernel was 105 KB of code and is 60 KB; a prefill gained a
+// sixth).
 template <int NQ, bool Q4>
 __device__ __forceinline__ bool warp_wait(const SplitParams& p, const Smem<NQ, Q4>& sm, uint32_t bar,
                                           uint32_t parity, int site) {
-    const bool w = ptx::mbar_wait(bar, parity, p.wait_limit_ns, sm.abort_flag());
-    if (__all_sync(0xffffffffu, w)) return true;
-    record_timeout(p, sm.abort_flag(), site);
-    return false;
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity)); ++i) {
+        if ((i & 63u) != 0) continue;
+        const uint64_t now = ptx::globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (__any_sync(0xffffffffu, *sm.abort_flag() != 0 || now - t0 > p.wait_limit_ns)) {
+            if (*sm.abort_flag() == 0) *sm.abort_flag() = site;
+            return false;
+        }
+    }
+    return true;
 }
 
 // Query tiles of a unit.
@@ -252,18 +253,18 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, cons
                 ++q_next;
             }
         };
-        // Waits for a condition of this warp, sending Q when it can.
-        auto wait_for = [&](auto cond, int site) {
+        // Waits for a barrier of this warp, sending Q when it can.
+        auto wait_for = [&](uint32_t bar, uint32_t parity, int site) {
             uint64_t t0 = 0;
             for (uint32_t i = 0;; ++i) {
                 try_q();
-                if (__shfl_sync(0xffffffffu, cond(), 0)) return true;
-                if ((i & 15u) == 15u) {
+                if (q_next == nq) return warp_wait<NQ, Q4>(p, sm, bar, parity, site);
+                if (__all_sync(0xffffffffu, ptx::mbar_test_wait(bar, parity))) return true;
+                if ((i & 63u) == 63u) {
                     const uint64_t now = ptx::globaltimer_ns();
                     if (t0 == 0) t0 = now;
-                    const bool over = *abort || now - t0 > p.wait_limit_ns;
-                    if (__shfl_sync(0xffffffffu, over, 0)) {
-                        if (lane == 0) record_timeout(p, abort, site);
+                    if (__any_sync(0xffffffffu, *abort != 0 || now - t0 > p.wait_limit_ns)) {
+                        if (*abort == 0) *abort = site;
                         return false;
                     }
                 }
@@ -298,7 +299,7 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, cons
                 for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
                     const uint32_t s = it % kRing, par = (it / kRing) & 1u;
                     const uint32_t empty = sm.bar(kEmpty + s);
-                    ok = wait_for([&] { return ptx::mbar_test_wait(empty, par ^ 1u); }, 2);
+                    ok = wait_for(empty, par ^ 1u, 2);
                     if (!ok) break;
                     if (Q4) {
                         const uint32_t full = sm.bar(kFull + s);
@@ -329,7 +330,7 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, cons
                             // wait for the pages, then zero the rows nobody sees
                             const uint32_t aux = sm.bar(C::BAR_AUX), aux_par = n_aux & 1u;
                             aux_pending = true;
-                            ok = wait_for([&] { return ptx::mbar_test_wait(aux, aux_par); }, 3);
+                            ok = wait_for(aux, aux_par, 3);
                             if (!ok) break;
                             aux_pending = false;
                             ++n_aux;
@@ -347,7 +348,11 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, cons
                 }
             }
         }
-        if (ok && q_next < nq) ok = wait_for([&] { return q_next == nq; }, 1);
+        // Q buffers not seen free so far
+        for (; ok && q_next < nq; try_q())
+            if (q_loads[q_next] > 0)
+                ok = warp_wait<NQ, Q4>(p, sm, sm.bar(C::BAR_QFREE + q_next),
+                                       (q_loads[q_next] - 1) & 1u, 1);
     }
     // (see attn_fwd.cu: the merge grid may start once every copy is issued)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -368,14 +373,13 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, cons
 }
 
 // ------------------------------------------------------------------ Q tiles
-// Two warps prepare a loaded Q tile in place. For bf16 pools they only write the
-// copies of its rows, if any. For 4-bit pools rows become f16: a thread finds its
+// Two warps turn the rows of a loaded Q tile into f16 in place: a thread finds its
 // row's largest exponent, scales by a power of two and stores the 8 values of each
-// 16-byte piece in the order the widened K tiles have, in every copy of the row.
-// Rows behind the unit's last are left as they are (their scores are never used).
-template <int NQ, bool Q4>
-__device__ void q_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, int w) {
-    using C = Cfg<NQ, Q4>;
+// 16-byte piece in the order the widened K tiles have. Rows behind the unit's last
+// are left as they are (their scores are never used).
+template <int NQ>
+__device__ void q_warp(const SplitParams& p, const Smem<NQ, true>& sm, int w) {
+    using C = Cfg<NQ, true>;
     const int lane = threadIdx.x & 31;
     uint32_t loads[2] = {0, 0};
     const int ui_end = p.cta_first[blockIdx.x + 1];
@@ -384,22 +388,12 @@ __device__ void q_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, int w) {
         const int nq = unit_nq<NQ>(u, p.tpt);
         for (int x = 0; x < nq; ++x) {
             const uint32_t n = x == 0 ? loads[0]++ : loads[1]++;
-            if (!warp_wait<NQ, Q4>(p, sm, sm.bar(C::BAR_QFULL + x), n & 1u, 50)) return;
+            if (!warp_wait<NQ, true>(p, sm, sm.bar(C::BAR_QFULL + x), n & 1u, 50)) return;
             const int rows = min(p.tpt, u.n_tok - x * p.tpt) * p.G;
-            const int split = nq == 1 ? key_split(u, p.G) : 1;
-            for (int row = w * 32 + lane; row < rows && (Q4 || split > 1); row += 32 * kQWarps) {
+            for (int row = w * 32 + lane; row < rows; row += 32 * kQWarps) {
                 const uint32_t at = sm.base + C::kSmemQ + x * kQBytes + row * 128;
                 const uint32_t swz = static_cast<uint32_t>(row & 7) << 4;
                 auto piece = [&](int c) { return at + (c >> 3) * kHalfBytes + (((c & 7) << 4) ^ swz); };
-                if (!Q4) {
-#pragma unroll 4
-                    for (int c = 0; c < 16; ++c) {
-                        const uint4 v = ptx::ld_shared_v4(piece(c));
-                        for (int copy = kBM / split; copy < kBM; copy += kBM / split)
-                            ptx::st_shared_v4(piece(c) + copy * 128, v.x, v.y, v.z, v.w);
-                    }
-                    continue;
-                }
                 uint32_t top[4] = {0, 0, 0, 0};
 #pragma unroll 1
                 for (int q = 0; q < 16; q += 4) {
@@ -433,14 +427,11 @@ __device__ void q_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, int w) {
                                           ptx::pack_f16x2(lo(v[c].z), lo(v[c].w)),
                                           ptx::pack_f16x2(hi(v[c].x), hi(v[c].y)),
                                           ptx::pack_f16x2(hi(v[c].z), hi(v[c].w)));
-                    for (int copy = 0; copy < kBM; copy += kBM / split)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            ptx::st_shared_v4(piece(q + c) + copy * 128, v[c].x, v[c].y, v[c].z,
-                                              v[c].w);
+                    for (int c = 0; c < 4; ++c)
+                        ptx::st_shared_v4(piece(q + c), v[c].x, v[c].y, v[c].z, v[c].w);
                 }
-                for (int copy = 0; copy < kBM; copy += kBM / split)
-                    *sm.fac(n, x, row + copy) = static_cast<uint8_t>(k + 127);
+                *sm.fac(n, x, row) = static_cast<uint8_t>(k + 127);
             }
             ptx::fence_proxy_async_smem();  // the MMAs read the tile
             __syncwarp();
@@ -550,19 +541,25 @@ struct Issuer {
     using C = Cfg<NQ, Q4>;
     const SplitParams& p;
     const Smem<NQ, Q4>& sm;
-    uint32_t tmem;
     uint32_t leader;  // 1 in the lane that issues
     bool issued_any = false;
 
-    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, int site) {
-        return warp_wait<NQ, Q4>(p, sm, bar, parity, site);
+    __device__ __forceinline__ uint32_t full(uint32_t pos) const {
+        return sm.bar(C::BAR_FULL + pos % C::kStages);
     }
-    __device__ __forceinline__ bool wait_full(uint32_t pos, int site) {
-        return wait(sm.bar(C::BAR_FULL + pos % C::kStages), (pos / C::kStages) & 1u, site);
-    }
+    __device__ __forceinline__ uint32_t full_par(uint32_t pos) const { return (pos / C::kStages) & 1u; }
     __device__ __forceinline__ void commit(uint32_t bar) { ptx::mma_commit_if(bar, leader); }
     __device__ __forceinline__ void release(uint32_t pos) {
         commit(sm.bar(C::BAR_EMPTY + pos % C::kStages));
+    }
+    // Waits for up to three barriers at once, a lane each: a probe is a trip through a
+    // busy shared-memory pipe (200 cycles and more), and this warp's trips are what the
+    // tensor core waits for.
+    __device__ __forceinline__ bool wait(uint32_t bar0, uint32_t par0, uint32_t bar1, uint32_t par1,
+                                         uint32_t bar2, uint32_t par2, int site) {
+        const uint32_t l = threadIdx.x & 31;
+        return warp_wait<NQ, Q4>(p, sm, l == 1 ? bar1 : l == 2 ? bar2 : bar0,
+                                 l == 1 ? par1 : l == 2 ? par2 : par0, site);
     }
     // S of group x = Q tile qx times the K tile at pos.
     __device__ __forceinline__ void issue_s(int x, int qx, uint32_t pos) {
@@ -571,17 +568,21 @@ struct Issuer {
         const uint64_t dk = ptx::sdesc_sw128(sm.tile(pos), 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < kHD / 16; ++kk)
-            ptx::mma_f16_ss_if(tmem + 128u * x, dq + kmajor_step(kk), dk + kmajor_step(kk), C::kIdescQK,
+            ptx::mma_f16_ss_if(128u * x, dq + kmajor_step(kk), dk + kmajor_step(kk), C::kIdescQK,
                                kk > 0, leader);
         commit(sm.gbar(x, SFULL));
         issued_any = true;
     }
+    // P written (and O rescaled), V widened or loaded, and O free.
     __device__ __forceinline__ bool issue_pv(const PvOp& op) {
-        if (!wait(sm.gbar(op.x, PFULL), op.t & 1u, 14)) return false;
-        if (op.first && op.k > 0 && !wait(sm.bar(C::BAR_OFREE), (op.k - 1) & 1, 15)) return false;
+        const uint32_t pf = sm.gbar(op.x, PFULL);
+        const bool of = op.first && op.k > 0;
+        if (!wait(pf, op.t & 1u, full(op.pos), full_par(op.pos), of ? sm.bar(C::BAR_OFREE) : pf,
+                  of ? (op.k - 1) & 1u : op.t & 1u, 14))
+            return false;
         ptx::tc_fence_after();
-        const uint32_t a = tmem + 128u * op.x;  // P: 64 columns of f16 pairs
-        const uint32_t d = tmem + kColO + 128u * op.x;
+        const uint32_t a = 128u * op.x;  // P: 64 columns of 16-bit pairs
+        const uint32_t d = kColO + 128u * op.x;
         const uint64_t dv = ptx::sdesc_sw128(sm.tile(op.pos), kHalfBytes, 1024);
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk)
@@ -594,26 +595,27 @@ struct Issuer {
     __device__ __forceinline__ bool issue_held(const PvOp& op, bool& held) {
         if (!held) return true;
         held = false;
-        if (!wait_full(op.pos, 13) || !issue_pv(op)) return false;
+        if (!issue_pv(op)) return false;
         release(op.pos);
         return true;
     }
 };
 
 // Two query tiles per unit: S_0(j), P.V_1(j-1), S_1(j), P.V_0(j). One query tile:
-// S(t) into group t mod 2's buffer, then P.V(t-1) of the other group; a unit's
-// last P.V is held until the next such unit's first S is issued. An S that
-// reuses the TMEM of an earlier P is always issued after that P's product.
+// S(t) into the buffer of group t mod 2, then P.V(t-1) of the other group; a unit's
+// last P.V is held until the next such unit's first S is issued. An S that reuses the
+// TMEM of an earlier P is always issued after that P's product. TMEM starts at column
+// 0 (the CTA has all of it).
 template <int NQ, bool Q4>
-__device__ void mma_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, uint32_t tmem) {
+__device__ void mma_warp(const SplitParams& p, const Smem<NQ, Q4>& sm) {
     using C = Cfg<NQ, Q4>;
-    // broadcasts: the values are warp-uniform, and known to be
-    Issuer<NQ, Q4> is{p, sm, __shfl_sync(0xffffffffu, tmem, 0), ptx::elect_one()};
+    Issuer<NQ, Q4> is{p, sm, ptx::elect_one()};
+    // a Q tile is usable when converted (4-bit pools) or loaded
+    constexpr int kQBar = Q4 ? C::BAR_QREADY : C::BAR_QFULL;
     bool ok = true;
     uint32_t pos = 0;           // ring position of the unit's K_0 (K_j at pos + 2j, V_j behind it)
-    uint32_t jt[2] = {0, 0};    // tiles each softmax group got before
-    uint32_t qu[2] = {0, 0};    // loads of each Q buffer consumed
-    int nx = 0;                 // group of the next one-query-tile unit's first tile
+    uint32_t jt0 = 0, jt1 = 0;  // tiles each softmax group got before
+    uint32_t qu0 = 0, qu1 = 0;  // loads of each Q buffer consumed
     PvOp pend{0, 0, false, 0, 0};
     bool held = false;
     int k = 0;
@@ -621,55 +623,55 @@ __device__ void mma_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, uint32_t 
     for (int ui = p.cta_first[blockIdx.x]; ui < ui_end && ok; ++ui, ++k) {
         const Unit u = p.units[ui];
         const int n = __shfl_sync(0xffffffffu, Tiles(p, u).n, 0);
+        const uint32_t qb0 = sm.bar(kQBar), qb1 = sm.bar(kQBar + NQ - 1);
         if (__shfl_sync(0xffffffffu, unit_nq<NQ>(u, p.tpt), 0) == 2) {
             if (!(ok = is.issue_held(pend, held))) break;
-            if (!(ok = is.wait(sm.bar(C::BAR_QREADY), qu[0] & 1u, 10) &&
-                       is.wait(sm.bar(C::BAR_QREADY + NQ - 1), qu[1] & 1u, 10)))
-                break;
             for (int j = 0; j <= n && ok; ++j) {
                 const uint32_t posK = pos + 2u * j, posV = posK + 1u, posVp = posK - 1u;
                 if (j < n) {
-                    if (!(ok = is.wait_full(posK, 11))) break;
+                    const uint32_t fk = is.full(posK), fp = is.full_par(posK);
+                    if (!(ok = is.wait(fk, fp, j == 0 ? qb0 : fk, j == 0 ? qu0 & 1u : fp,
+                                       j == 0 ? qb1 : fk, j == 0 ? qu1 & 1u : fp, 11)))
+                        break;
                     is.issue_s(0, 0, posK);
                     if (j == n - 1) is.commit(sm.bar(C::BAR_QFREE));
                 }
                 if (j > 0) {
-                    if (!(ok = is.issue_pv(PvOp{1, jt[1] + j - 1, j == 1, k, posVp}))) break;
+                    if (!(ok = is.issue_pv(PvOp{1, jt1 + j - 1, j == 1, k, posVp}))) break;
                     is.release(posVp);
                 }
                 if (j < n) {
                     is.issue_s(1, NQ - 1, posK);
                     is.release(posK);
                     if (j == n - 1) is.commit(sm.bar(C::BAR_QFREE + NQ - 1));
-                    if (!(ok = is.wait_full(posV, 13))) break;
-                    if (!(ok = is.issue_pv(PvOp{0, jt[0] + j, j == 0, k, posV}))) break;
+                    if (!(ok = is.issue_pv(PvOp{0, jt0 + j, j == 0, k, posV}))) break;
                 }
             }
             if (!ok) break;
-            jt[0] += n;
-            jt[1] += n;
-            ++qu[0];
-            ++qu[1];
+            jt0 += n;
+            jt1 += n;
+            ++qu0;
+            ++qu1;
         } else {
-            if (held && !__all_sync(0xffffffffu, ptx::mbar_test_wait(sm.bar(C::BAR_QREADY), qu[0] & 1u)) &&
+            if (held && !__all_sync(0xffffffffu, ptx::mbar_test_wait(qb0, qu0 & 1u)) &&
                 !(ok = is.issue_held(pend, held)))
                 break;
             for (int j = 0; j < n && ok; ++j) {
                 const uint32_t posK = pos + 2u * j;
-                const int x = (nx + j) & 1;
-                if (!(ok = is.wait_full(posK, 11))) break;
-                if (j == 0 && !(ok = is.wait(sm.bar(C::BAR_QREADY), qu[0] & 1u, 10))) break;
+                const int x = (posK >> 1) & 1u;
+                const uint32_t fk = is.full(posK), fp = is.full_par(posK);
+                if (!(ok = is.wait(fk, fp, j == 0 ? qb0 : fk, j == 0 ? qu0 & 1u : fp, fk, fp, 11)))
+                    break;
                 is.issue_s(x, 0, posK);
                 is.release(posK);
                 if (j == n - 1) is.commit(sm.bar(C::BAR_QFREE));
                 if (!(ok = is.issue_held(pend, held))) break;
-                const uint32_t t = x == 0 ? jt[0]++ : jt[1]++;
+                const uint32_t t = x == 0 ? jt0++ : jt1++;
                 pend = PvOp{x, t, j < 2, k, posK + 1u};
                 held = true;
             }
             if (!ok) break;
-            nx = (nx + n) & 1;
-            ++qu[0];
+            ++qu0;
         }
         pos += 2u * n;
     }
@@ -689,12 +691,12 @@ __device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&a)[32], uint32
 }
 
 // Scores a row does not see become -inf in TMEM (tiles at a mask's border only,
-// so that the common path carries no masks): of columns [c0, c1) it sees those
-// below lim, and not [sink, lo).
-__device__ __forceinline__ void mask_tile(uint32_t taddr, int c0, int c1, int lim, int lo, int sink) {
+// so that the common path carries no masks): it sees columns below lim, and not
+// [sink, lo).
+__device__ __forceinline__ void mask_tile(uint32_t taddr, int lim, int lo, int sink) {
     uint32_t s[32];
 #pragma unroll 1
-    for (; c0 < c1; c0 += 32) {
+    for (int c0 = 0; c0 < kBN; c0 += 32) {
         __syncwarp();
         ptx::tmem_ld32(taddr + c0, s);
         ptx::tmem_ld_wait(s);
@@ -707,13 +709,11 @@ __device__ __forceinline__ void mask_tile(uint32_t taddr, int c0, int c1, int li
 }
 
 __device__ __forceinline__ float max32(const uint32_t (&s)[32], float m) {
-    float a = m, b = __uint_as_float(s[1]);
+    float a[4] = {m, __uint_as_float(s[1]), __uint_as_float(s[2]), __uint_as_float(s[3])};
 #pragma unroll
-    for (int c = 0; c < 32; c += 4) {
-        a = ptx::fmax3(a, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-        b = ptx::fmax3(b, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-    }
-    return fmaxf(a, b);
+    for (int c = 0; c < 32; c += 2)
+        a[(c >> 1) & 3] = ptx::fmax3(a[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+    return fmaxf(ptx::fmax3(a[0], a[1], a[2]), a[3]);
 }
 
 // P of 32 columns to TMEM (16 columns of 16-bit pairs; bf16 as V for bf16 pools: half
@@ -732,12 +732,7 @@ __device__ __forceinline__ void exp32(const uint32_t (&s)[32], uint32_t taddr, u
     }
     ptx::tmem_st16(taddr, packed);
 }
-__device__ __forceinline__ void zero16(uint32_t taddr) {
-    const uint32_t z[16] = {};
-    ptx::tmem_st16(taddr, z);
-}
-
-// The running reference and sum of a row (of one copy's keys).
+// The running reference and sum of a row.
 struct Running {
     float m = -INFINITY, l = 0.f;
     // A tile's maximum: the factor that O and l take, and the exponent's addend.
@@ -752,61 +747,42 @@ struct Running {
     }
 };
 
-// One tile's softmax of this thread's row, over the keys of its copy `seg` of F: P
-// over the first 64 columns of S. Returns the rescale factor.
-template <int F, bool Q4>
-__device__ __forceinline__ float softmax_tile(uint32_t colS, int seg, float sl2, Running& run) {
+// One tile's softmax of this thread's row: P over the first 64 columns of S. Returns
+// the rescale factor.
+template <bool Q4>
+__device__ __forceinline__ float softmax_tile(uint32_t colS, float sl2, Running& run) {
     constexpr float kLift = Cfg<1, Q4>::kLiftLog2;
     const uint64_t sl2p = ptx::f32x2(sl2, sl2);
     uint64_t l[2] = {0ull, 0ull};
     uint32_t s0[32];
-    float neg, corr;
-    if (F == 4) {
-        ptx::tmem_ld32(colS + 32 * seg, s0);
-        ptx::tmem_ld_wait(s0);
-        corr = run.raise(max32(s0, -INFINITY) * sl2, kLift, neg);  // scale > 0: max commutes
-        const uint64_t negm = ptx::f32x2(neg, neg);
-        exp32<Q4>(s0, colS + 16 * seg, sl2p, negm, l);
-#pragma unroll
-        for (int i = 1; i < 4; ++i) zero16(colS + 16 * (seg ^ i));
-    } else if (F == 2) {
-        uint32_t s1[32];
-        load64(colS + 64 * seg, s0, s1);
-        corr = run.raise(max32(s1, max32(s0, -INFINITY)) * sl2, kLift, neg);
-        const uint64_t negm = ptx::f32x2(neg, neg);
-        exp32<Q4>(s0, colS + 32 * seg, sl2p, negm, l);
-        exp32<Q4>(s1, colS + 32 * seg + 16, sl2p, negm, l);
-        zero16(colS + 32 * (seg ^ 1));
-        zero16(colS + 32 * (seg ^ 1) + 16);
-    } else {
-        // 32 columns at a time, the next ones on their way from TMEM while these are
-        // worked on: the maximum from the last columns down, P from the first up
-        uint32_t s1[32];
-        ptx::tmem_ld32(colS + 96, s1);
-        ptx::tmem_ld_wait(s1);
-        ptx::tmem_ld32(colS + 64, s0);
-        float mx = max32(s1, -INFINITY);
-        ptx::tmem_ld_wait(s0);
-        ptx::tmem_ld32(colS + 32, s1);
-        mx = max32(s0, mx);
-        ptx::tmem_ld_wait(s1);
-        ptx::tmem_ld32(colS, s0);
-        mx = max32(s1, mx);
-        ptx::tmem_ld_wait(s0);
-        ptx::tmem_ld32(colS + 32, s1);
-        mx = max32(s0, mx);
-        corr = run.raise(mx * sl2, kLift, neg);
-        const uint64_t negm = ptx::f32x2(neg, neg);
-        exp32<Q4>(s0, colS, sl2p, negm, l);
-        ptx::tmem_ld_wait(s1);
-        ptx::tmem_ld32(colS + 64, s0);
-        exp32<Q4>(s1, colS + 16, sl2p, negm, l);
-        ptx::tmem_ld_wait(s0);
-        ptx::tmem_ld32(colS + 96, s1);
-        exp32<Q4>(s0, colS + 32, sl2p, negm, l);
-        ptx::tmem_ld_wait(s1);
-        exp32<Q4>(s1, colS + 48, sl2p, negm, l);
-    }
+    float neg;
+    // 32 columns at a time, the next ones on their way from TMEM while these are
+    // worked on: the maximum from the last columns down, P from the first up
+    uint32_t s1[32];
+    ptx::tmem_ld32(colS + 96, s1);
+    ptx::tmem_ld_wait(s1);
+    ptx::tmem_ld32(colS + 64, s0);
+    float mx = max32(s1, -INFINITY);
+    ptx::tmem_ld_wait(s0);
+    ptx::tmem_ld32(colS + 32, s1);
+    mx = max32(s0, mx);
+    ptx::tmem_ld_wait(s1);
+    ptx::tmem_ld32(colS, s0);
+    mx = max32(s1, mx);
+    ptx::tmem_ld_wait(s0);
+    ptx::tmem_ld32(colS + 32, s1);
+    mx = max32(s0, mx);
+    const float corr = run.raise(mx * sl2, kLift, neg);
+    const uint64_t negm = ptx::f32x2(neg, neg);
+    exp32<Q4>(s0, colS, sl2p, negm, l);
+    ptx::tmem_ld_wait(s1);
+    ptx::tmem_ld32(colS + 64, s0);
+    exp32<Q4>(s1, colS + 16, sl2p, negm, l);
+    ptx::tmem_ld_wait(s0);
+    ptx::tmem_ld32(colS + 96, s1);
+    exp32<Q4>(s0, colS + 32, sl2p, negm, l);
+    ptx::tmem_ld_wait(s1);
+    exp32<Q4>(s1, colS + 48, sl2p, negm, l);
     const uint64_t sum = ptx::add_f32x2(l[0], l[1]);
     run.l = run.l * corr + (ptx::lo_f32(sum) + ptx::hi_f32(sum));
     return corr;
@@ -859,7 +835,7 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ, Q4>& sm, uint
     const uint32_t colS = lane_addr + 128u * x, colO = lane_addr + kColO + 128u * x;
     uint32_t n_load[2] = {0, 0};  // loads of each Q buffer before this unit
     uint32_t jt = 0, jt_other = 0;  // tiles this group and the other got
-    int nx = 0;
+    uint32_t tile0 = 0;  // K/V tiles before this unit
     int kj = 0;  // joined (one-query-tile) units so far
     // Before the first unit each group makes a dry run of that unit's epilogue (no
     // tiles, no waits, one thread's stores into a scratch sink) while it waits for
@@ -872,14 +848,12 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ, Q4>& sm, uint
         const Tiles tl(p, u);
         const bool pair = unit_nq<NQ>(u, p.tpt) == 2;
         const int tile_tok = pair ? x * p.tpt : 0;
-        const int split = pair ? 1 : key_split(u, p.G);
-        const int urow = row & (kBM / split - 1), seg = row / (kBM / split);  // row, copy of it
-        const bool row_valid = dry ? row == 0 : urow < min(p.tpt, u.n_tok - tile_tok) * p.G;
+        const bool row_valid = dry ? row == 0 : row < min(p.tpt, u.n_tok - tile_tok) * p.G;
         const bool active = dry || __any_sync(0xffffffffu, row_valid);
-        const int tok = u.tok_begin + tile_tok + urow / p.G;
+        const int tok = u.tok_begin + tile_tok + row / p.G;
         const int row_end = row_valid ? p.tok_pos[tok] + 1 : 0;
         const int n_tiles = dry ? 0 : tl.n;
-        const int j0 = pair ? 0 : (x - nx) & 1, dj = pair ? 1 : 2;
+        const int j0 = pair ? 0 : (x ^ tile0) & 1, dj = pair ? 1 : 2;
         Running run;
         // the softmax scale, with the power of two that the row of Q carries
         const int xq = pair ? x : 0;
@@ -896,7 +870,9 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ, Q4>& sm, uint
             // (a run of first keys before the range leaves none of them to it)
             const int lim = min(row_end, last) - kt, lo = row_end - p.window - kt;
             const int sink = f || tl.n_first == 0 ? p.sinks - kt : 0;
-            const bool full = __all_sync(0xffffffffu, lim >= kBN && (lo <= 0 || sink >= kBN));
+            // (a lane without a row needs no mask: what it computes stays in its lane)
+            const bool full = __all_sync(
+                0xffffffffu, !row_valid || (lim >= kBN && (lo <= 0 || sink >= kBN)));
             if (!warp_wait<NQ, Q4>(p, sm, sm.gbar(x, SFULL), jt & 1u, 20)) return;
             ptx::tc_fence_after();
             // The factor was written before the S product was issued. (Waiting for
@@ -908,11 +884,9 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ, Q4>& sm, uint
             }
             float corr = 1.f;
             if (active) {
-                if (!full)
-                    mask_tile(colS, seg * (kBN / split), (seg + 1) * (kBN / split), lim, lo, sink);
-                corr = split == 4   ? softmax_tile<4, Q4>(colS, seg, sl2, run)
-                       : split == 2 ? softmax_tile<2, Q4>(colS, seg, sl2, run)
-                                    : softmax_tile<1, Q4>(colS, seg, sl2, run);
+                if (!full) mask_tile(colS, lim, lo, sink);
+                corr = softmax_tile<Q4>(colS, sl2, run);
+                if (!row_valid) corr = 1.f;  // nothing of this lane is used
             }
             // O is rescaled in place: this S was issued after the group's previous
             // product, so that one has completed.
@@ -936,77 +910,60 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ, Q4>& sm, uint
         const float m_ref = run.m, l_run = run.l * C::kUnlift;  // without P's lift
         const bool direct = u.part < 0;
         const int64_t orow =
-            dry ? 0 : static_cast<int64_t>(tok) * p.H_q + u.kv_head * p.G + urow % p.G;
+            dry ? 0 : static_cast<int64_t>(tok) * p.H_q + u.kv_head * p.G + row % p.G;
         const int64_t prow =
             dry ? 0 : static_cast<int64_t>(u.part) * (kBM * NQ) + (pair ? kBM * x : 0) + row;
         void* const out = dry ? static_cast<void*>(p.sink) : p.out;
         float* const part_o = dry ? p.sink : p.part_o;
-        float m_out = m_ref, l_out = l_run;
+        float m_out = m_ref, l_out = l_run, wa = 1.f, wb = 0.f;
+        float2* const join = reinterpret_cast<float2*>(sm.ptr + C::kSmemJoin) + (kj & 1) * 2 * kBM;
+        const int n_other = pair ? 0 : (n_tiles + j0) >> 1;  // tiles of the other parity
         if (pair) {
             jt_other += n_tiles;
-            if (!dry && !warp_wait<NQ, Q4>(p, sm, sm.gbar(x, ODONE), (jt - 1) & 1u, 22)) return;
-            ptx::tc_fence_after();
-            if (active) {
-                const float w = p.o_scale * C::kUnlift * (direct ? (l_run > 0.f ? 1.f / l_run : 0.f) : 1.f);
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t r[32];
-                    __syncwarp();
-                    ptx::tmem_ld32(colO + 32 * c, r);
-                    ptx::tmem_ld_wait(r);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * w);
-                    if (row_valid) store32<Q4>(out, part_o, p.out_bf16, r, direct, orow, prow, 32 * c);
-                }
-            }
-        } else {
+        } else if (!dry) {
             // Join the groups: exchange (m, l), then each combines 64 columns.
-            float2* join = reinterpret_cast<float2*>(sm.ptr + C::kSmemJoin) + (kj & 1) * 2 * kBM;
-            const int n_other = (n_tiles + j0) >> 1;  // tiles of the other parity
-            const int n_mine = n_tiles - n_other;
-            if (!dry) {
-                join[x * kBM + row] = make_float2(m_ref, l_run);
-                __syncwarp();
-                // two barriers in turn: a group without a tile in the next unit may
-                // arrive there before this one has waited here
-                if (lane == 0) ptx::mbar_arrive(sm.gbar(x, JOIN + (kj & 1)));
-                jt_other += n_other;
-                if (!warp_wait<NQ, Q4>(p, sm, sm.gbar(x ^ 1, JOIN + (kj & 1)), (kj >> 1) & 1, 23)) return;
-                ++kj;
-            }
-            if (n_mine > 0 && !warp_wait<NQ, Q4>(p, sm, sm.gbar(x, ODONE), (jt - 1) & 1u, 22)) return;
-            if (n_other > 0 && !warp_wait<NQ, Q4>(p, sm, sm.gbar(x ^ 1, ODONE), (jt_other - 1) & 1u, 24))
-                return;
-            ptx::tc_fence_after();
-            nx = (nx + n_tiles) & 1;
-            if (active) {
+            join[x * kBM + row] = make_float2(m_ref, l_run);
+            __syncwarp();
+            // two barriers in turn: a group without a tile in the next unit may
+            // arrive there before this one has waited here
+            if (lane == 0) ptx::mbar_arrive(sm.gbar(x, JOIN + (kj & 1)));
+            jt_other += n_other;
+            if (!warp_wait<NQ, Q4>(p, sm, sm.gbar(x ^ 1, JOIN + (kj & 1)), (kj >> 1) & 1, 23)) return;
+            ++kj;
+        }
+        if (n_tiles > n_other && !warp_wait<NQ, Q4>(p, sm, sm.gbar(x, ODONE), (jt - 1) & 1u, 22)) return;
+        if (n_other > 0 && !warp_wait<NQ, Q4>(p, sm, sm.gbar(x ^ 1, ODONE), (jt_other - 1) & 1u, 24))
+            return;
+        ptx::tc_fence_after();
+        if (active) {
+            if (!pair) {
                 const float2 other = join[(x ^ 1) * kBM + row];
                 const float m_a = l_run > 0.f ? m_ref : -INFINITY;
                 const float m_b = other.y > 0.f ? other.x : -INFINITY;
                 m_out = fmaxf(m_a, m_b);
-                float wa = m_a == -INFINITY ? 0.f : ptx::ex2(m_a - m_out);
-                float wb = m_b == -INFINITY ? 0.f : ptx::ex2(m_b - m_out);
+                wa = m_a == -INFINITY ? 0.f : ptx::ex2(m_a - m_out);
+                wb = m_b == -INFINITY ? 0.f : ptx::ex2(m_b - m_out);
                 l_out = wa * l_run + wb * other.y;
-                const float w = p.o_scale * C::kUnlift * (direct ? (l_out > 0.f ? 1.f / l_out : 0.f) : 1.f);
-                wa *= w;
-                wb *= w;
-                const uint32_t oa = lane_addr + kColO + 128u * x + 64u * x;
-                const uint32_t ob = lane_addr + kColO + 128u * (x ^ 1) + 64u * x;
+            }
+            const float w = p.o_scale * C::kUnlift * (direct ? (l_out > 0.f ? 1.f / l_out : 0.f) : 1.f);
+            wa *= w;
+            wb *= w;
+            const uint32_t oa = lane_addr + kColO + 128u * x, ob = lane_addr + kColO + 128u * (x ^ 1);
+            const int c_end = pair ? kHD : 64 * x + 64;
 #pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t a[32], b[32];
-                    __syncwarp();
-                    ptx::tmem_ld32(oa + 32 * c, a);
-                    ptx::tmem_ld32(ob + 32 * c, b);
-                    ptx::tmem_ld_wait(a);
-                    ptx::reg_touch(b);
-                    // a group without a visible key may never have written its O
+            for (int c = pair ? 0 : 64 * x; c < c_end; c += 32) {
+                uint32_t r[32], b[32];
+                __syncwarp();
+                ptx::tmem_ld32(oa + c, r);
+                if (!pair) ptx::tmem_ld32(ob + c, b);
+                ptx::tmem_ld_wait(r);
+                ptx::reg_touch(b);
+                // a group without a visible key may never have written its O
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        a[i] = __float_as_uint((wa != 0.f ? wa * __uint_as_float(a[i]) : 0.f) +
-                                               (wb != 0.f ? wb * __uint_as_float(b[i]) : 0.f));
-                    if (row_valid) store32<Q4>(out, part_o, p.out_bf16, a, direct, orow, prow, 64 * x + 32 * c);
-                }
+                for (int i = 0; i < 32; ++i)
+                    r[i] = __float_as_uint((wa != 0.f ? wa * __uint_as_float(r[i]) : 0.f) +
+                                           (wb != 0.f ? wb * __uint_as_float(b[i]) : 0.f));
+                if (row_valid) store32<Q4>(out, part_o, p.out_bf16, r, direct, orow, prow, c);
             }
         }
         if (row_valid && (pair || x == 0)) {
@@ -1017,6 +974,7 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ, Q4>& sm, uint
         }
         ptx::tc_fence_before();
         __syncwarp();
+        tile0 += n_tiles;
         if (lane == 0 && !dry) ptx::mbar_arrive(sm.bar(C::BAR_OFREE));
     }
 }
@@ -1027,14 +985,12 @@ __global__ void __launch_bounds__(Cfg<NQ, Q4>::kThreads, 1)
                      const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v) {
     using C = Cfg<NQ, Q4>;
-    extern __shared__ uint8_t smem_raw[];
+    // 1024-byte aligned as declared, so that every shared-memory address is a constant
+    // (checked below).
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     Smem<NQ, Q4> sm;
-    {
-        const uint32_t raw = ptx::smem_u32(smem_raw);
-        const uint32_t aligned = (raw + 1023u) & ~1023u;
-        sm.base = aligned;
-        sm.ptr = smem_raw + (aligned - raw);
-    }
+    sm.base = ptx::smem_u32(smem_raw);
+    sm.ptr = smem_raw;
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -1082,13 +1038,16 @@ __global__ void __launch_bounds__(Cfg<NQ, Q4>::kThreads, 1)
     const uint32_t tmem = *sm.tmem_slot();
 
     if (Q4 && warp < kWarpSoftmax) ptx::regs_dec<kRegsOther>();
-    if (warp == 0) {
+    if (tmem != 0 || (sm.base & 1023u) != 0) {
+        // the issuer counts on both; a CTA that gets all TMEM columns gets them from 0
+        if (threadIdx.x == 0) atomicCAS(p.err, 0, kErrCuda);
+    } else if (warp == 0) {
         producer_warp<NQ, Q4>(p, sm, &tm_q, &tm_k, &tm_v);
     } else if (warp == 1) {
-        mma_warp<NQ, Q4>(p, sm, tmem);
+        mma_warp<NQ, Q4>(p, sm);
         __syncwarp();
     } else if (warp < kWarpSoftmax) {
-        q_warp<NQ, Q4>(p, sm, warp - kWarpQ);
+        if constexpr (Q4) q_warp<NQ>(p, sm, warp - kWarpQ);
     } else if (warp < kWarpWiden) {
         if (Q4) ptx::regs_inc<kRegsSoftmax>();
         softmax_group<NQ, Q4>(p, sm, tmem, (warp - kWarpSoftmax) / kGroupWarps);
@@ -1104,6 +1063,10 @@ __global__ void __launch_bounds__(Cfg<NQ, Q4>::kThreads, 1)
     if (warp == 1) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, kTmemCols);
+    }
+    if (threadIdx.x == 0 && *sm.abort_flag() != 0 && atomicCAS(p.err, 0, kErrTimeout) == 0) {
+        p.err[1] = *sm.abort_flag();
+        p.err[2] = static_cast<int32_t>(blockIdx.x);
     }
 }
 

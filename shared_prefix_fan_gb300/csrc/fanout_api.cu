@@ -173,7 +173,6 @@ int attn_call(AttnKind kind, const void* q, const void* k_pages, const void* v_p
     in.rows = rows;
     in.window = window;
     in.sinks = sinks;
-    in.key_split = rows;
     if (q4) in.row_bytes = 2 * kQ4RowBytes;
     bool patched = false;
     if (ws->plan_ready && key != ws->key && key.size() == ws->key.size() &&

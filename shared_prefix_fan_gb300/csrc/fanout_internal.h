@@ -36,11 +36,6 @@ struct Unit {
 };
 static_assert(sizeof(Unit) == 32, "Unit is 8 int32");
 
-// Copies of `rows` query rows that fit one 128-row tile in whole warps.
-__host__ __device__ constexpr int rows_key_split(int rows) {
-    return rows <= kBM / 4 ? 4 : rows <= kBM / 2 ? 2 : 1;
-}
-
 struct MergeParams {
     const float* part_o;
     const float2* part_ml;

@@ -527,14 +527,10 @@ int build_plan(const PlanInput& in, Plan& plan) {
     if (n_parts > 0) {
         const size_t n_keys = static_cast<size_t>(R) * in.H_kv;
         plan.merge_cnt.assign(n_keys, 0);
-        // partial rows a unit writes for each of its rows
-        auto copies = [&](const Unit& u) {
-            return in.key_split && u.n_tok <= plan.tpt ? rows_key_split(u.n_tok * G) : 1;
-        };
         for (const Unit& u : plan.units)
             if (u.part >= 0)
                 for (int32_t t = u.tok_begin; t < u.tok_begin + u.n_tok; ++t)
-                    plan.merge_cnt[static_cast<size_t>(t) * in.H_kv + u.kv_head] += copies(u);
+                    ++plan.merge_cnt[static_cast<size_t>(t) * in.H_kv + u.kv_head];
         int32_t stride = 1;
         for (int32_t c : plan.merge_cnt) stride = std::max(stride, c);
         plan.merge_stride = stride;
@@ -544,14 +540,10 @@ int build_plan(const PlanInput& in, Plan& plan) {
             if (u.part >= 0)
                 for (int32_t t = u.tok_begin; t < u.tok_begin + u.n_tok; ++t) {
                     const size_t key = static_cast<size_t>(t) * in.H_kv + u.kv_head;
-                    const int32_t i = t - u.tok_begin, n = copies(u);
-                    for (int32_t c = 0; c < n; ++c) {
-                        const size_t e = key * stride + fill_e[key]++;
-                        plan.merge_ent[2 * e] = u.part;
-                        // first row of its i-th token (of copy c of its rows)
-                        plan.merge_ent[2 * e + 1] =
-                            i / plan.tpt * kBM + i % plan.tpt * G + c * (kBM / n);
-                    }
+                    const size_t e = key * stride + fill_e[key]++;
+                    plan.merge_ent[2 * e] = u.part;
+                    const int32_t i = t - u.tok_begin;  // first row of its i-th token
+                    plan.merge_ent[2 * e + 1] = i / plan.tpt * kBM + i % plan.tpt * G;
                 }
         // a (token, head) covered by a single direct unit has count 0; when
         // some are, the merge visits only the keys listed here

@@ -25,7 +25,6 @@ struct PlanInput {
     int32_t window = 0;    // > 0: a row at pos sees keys > pos - window ...
     int32_t sinks = 0;     // ... and keys < sinks
     int32_t row_bytes = 2 * 2 * kHD;  // K and V of one token and KV head
-    int32_t key_split = 0;  // 1: one-tile partial units write a row per copy (rows_key_split)
 };
 
 // A key range of the plan: the rows of n_tok tokens from tok_begin (one KV

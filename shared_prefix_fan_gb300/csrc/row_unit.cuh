@@ -25,13 +25,6 @@ __device__ __forceinline__ int first_tiles(const Unit& u, int split_at) {
     return u.pos_base > 0 ? (u.pos_base - first_begin(u, split_at) + kBN - 1) / kBN : 0;
 }
 
-// Copies of a one-query-tile unit's rows in 4-bit attention, each of which takes
-// its part of every tile's keys and writes a partial row of its own (the merge
-// index of such a plan has an entry per copy: build_plan).
-__device__ __forceinline__ int key_split(const Unit& u, int G) {
-    return u.part < 0 ? 1 : rows_key_split(u.n_tok * G);
-}
-
 // A page id outside the pool is recorded and page 0 read in its place: the
 // call's result is then unspecified, but nothing outside the pool is touched.
 __device__ __forceinline__ int32_t checked_page(const SplitParams& p, int32_t page) {
