@@ -494,8 +494,15 @@ __device__ void widen_warp(const SplitParams& p, const Smem<NQ, true>& sm, int w
                 sc[i] = ptx::ld_shared_u16(raw + scale_at[i]);
                 if (r < front || kt + r >= last) sc[i] = 0;
             }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(sm.bar(C::BAR_REMPTY + rs));  // in registers now
+            // The raw stage is free once its words are in registers, which a loaded
+            // value's use shows and the loads' issue does not (an arrival right behind
+            // them let the next copy overwrite words still to be read): a vote over all
+            // of them. Should the vote come out true, the stage is freed further down.
+            uint32_t seen = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) seen ^= c[i].x ^ c[i].y ^ c[i].z ^ c[i].w ^ sc[i];
+            const bool late = __all_sync(0xffffffffu, seen == 0x9e3779b9u);
+            if (lane == 0 && !late) ptx::mbar_arrive(sm.bar(C::BAR_REMPTY + rs));
             if (!warp_wait<NQ, true>(p, sm, sm.bar(C::BAR_EMPTY + stage), ((it / C::kStages) & 1u) ^ 1u, 41))
                 return;
             const uint32_t dst = sm.tile(it) + row_at;
@@ -514,7 +521,10 @@ __device__ void widen_warp(const SplitParams& p, const Smem<NQ, true>& sm, int w
             }
             ptx::fence_proxy_async_smem();  // the MMAs read the tile
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(sm.bar(C::BAR_FULL + stage));
+            if (lane == 0) {
+                ptx::mbar_arrive(sm.bar(C::BAR_FULL + stage));
+                if (late) ptx::mbar_arrive(sm.bar(C::BAR_REMPTY + rs));
+            }
         }
     }
 }

@@ -195,3 +195,44 @@ def test_decode_loop_on_the_4_bit_cache():
         r = ref.attention(q.double().numpy(), k64, v64, table.cpu().numpy(), P, S, A, page,
                           128 ** -0.5, True, window, sinks if window else 0)
         ref.check_attention(out, lse, r, P_STEP[True], f"step {step}")
+
+
+def device_reference(prob):
+    """`prob.reference()` of a problem with one branch, computed on the device (64
+    bits): for lengths at which the host form takes minutes."""
+    P, S, T, page, G = prob.P, prob.S[0], prob.T[0], prob.page, prob.hq // prob.hkv
+    n = P + S
+    j = torch.arange(n, device="cuda")
+    pos = torch.arange(n - T, n, device="cuda")[:, None]
+    see = (j <= pos) if prob.causal else torch.ones((T, n), dtype=torch.bool, device="cuda")
+    if prob.window:
+        see = see & ((j > pos - prob.window) | (j < prob.sinks))
+    at = torch.from_numpy(prob.table[0].astype(np.int64)).cuda()[j // page], j % page
+    q = prob.q.double().cuda()
+    parts = []
+    for h in range(prob.hkv):
+        k, v = (torch.from_numpy(np.ascontiguousarray(x[:, h])).cuda()[at]
+                for x in (prob.k64, prob.v64))
+        for g in range(h * G, (h + 1) * G):
+            x = (q[:, g] @ k.T * prob.scale).masked_fill(~see, -torch.inf)
+            p = torch.softmax(x, -1)
+            e = (q[:, g].abs() @ k.abs().T * prob.scale).masked_fill(~see, 0.0)
+            parts.append((p @ v, torch.logsumexp(x, -1), p @ v.abs(), e.amax(-1),
+                          see.double() @ v.abs()))
+    return tuple(torch.stack([p[i] for p in parts], 1).cpu().numpy() for i in range(5))
+
+
+@pytest.mark.parametrize("hq,hkv,page,P,T,window,sinks,gs", [
+    (40, 8, 16, 4588, 1011, 2714, 100, 0.25), (64, 8, 16, 4500, 700, 0, 0, 1.0),
+    (8, 8, 64, 3900, 515, 0, 0, 0.5), (16, 1, 32, 8000, 40, 5000, 7, 1.0)])
+def test_long_sweeps_of_the_4_bit_cache(hq, hkv, page, P, T, window, sinks, gs):
+    """Many key tiles through one ring: a stage that is refilled while a warp still
+    reads its words gives wrong rows here, and other ones from run to run."""
+    prob = ref.Problem([T], [T], P, hq, hkv, page, window=window, sinks=sinks, q4=True, gs=gs)
+    want, first = device_reference(prob), None
+    for _ in range(4):
+        out, lse = prob.run()
+        assert binding.last_error_detail()[0] == binding.OK
+        ref.check_attention(out, lse, want, P_STEP[True])
+        first = first or (out, lse)
+        assert torch.equal(first[0], out) and torch.equal(first[1], lse)
