@@ -562,14 +562,15 @@ struct Issuer {
     __device__ __forceinline__ void release(uint32_t pos) {
         commit(sm.bar(C::BAR_EMPTY + pos % C::kStages));
     }
-    // Waits for up to three barriers at once, a lane each: a probe is a trip through a
+    // Waits for up to four barriers at once, a lane each: a probe is a trip through a
     // busy shared-memory pipe (200 cycles and more), and this warp's trips are what the
     // tensor core waits for.
     __device__ __forceinline__ bool wait(uint32_t bar0, uint32_t par0, uint32_t bar1, uint32_t par1,
-                                         uint32_t bar2, uint32_t par2, int site) {
+                                         uint32_t bar2, uint32_t par2, uint32_t bar3, uint32_t par3,
+                                         int site) {
         const uint32_t l = threadIdx.x & 31;
-        return warp_wait<NQ, Q4>(p, sm, l == 1 ? bar1 : l == 2 ? bar2 : bar0,
-                                 l == 1 ? par1 : l == 2 ? par2 : par0, site);
+        return warp_wait<NQ, Q4>(p, sm, l == 1 ? bar1 : l == 2 ? bar2 : l == 3 ? bar3 : bar0,
+                                 l == 1 ? par1 : l == 2 ? par2 : l == 3 ? par3 : par0, site);
     }
     // S of group x = Q tile qx times the K tile at pos.
     __device__ __forceinline__ void issue_s(int x, int qx, uint32_t pos) {
@@ -583,12 +584,14 @@ struct Issuer {
         commit(sm.gbar(x, SFULL));
         issued_any = true;
     }
-    // P written (and O rescaled), V widened or loaded, and O free.
-    __device__ __forceinline__ bool issue_pv(const PvOp& op) {
+    // P written (and O rescaled), V widened or loaded, O free; and the tile at `next`,
+    // which the S product that follows reads (any tile of the ring that is there, if
+    // none does).
+    __device__ __forceinline__ bool issue_pv(const PvOp& op, uint32_t next) {
         const uint32_t pf = sm.gbar(op.x, PFULL);
         const bool of = op.first && op.k > 0;
         if (!wait(pf, op.t & 1u, full(op.pos), full_par(op.pos), of ? sm.bar(C::BAR_OFREE) : pf,
-                  of ? (op.k - 1) & 1u : op.t & 1u, 14))
+                  of ? (op.k - 1) & 1u : op.t & 1u, full(next), full_par(next), 14))
             return false;
         ptx::tc_fence_after();
         const uint32_t a = 128u * op.x;  // P: 64 columns of 16-bit pairs
@@ -605,7 +608,7 @@ struct Issuer {
     __device__ __forceinline__ bool issue_held(const PvOp& op, bool& held) {
         if (!held) return true;
         held = false;
-        if (!issue_pv(op)) return false;
+        if (!issue_pv(op, op.pos)) return false;
         release(op.pos);
         return true;
     }
@@ -639,22 +642,24 @@ __device__ void mma_warp(const SplitParams& p, const Smem<NQ, Q4>& sm) {
             for (int j = 0; j <= n && ok; ++j) {
                 const uint32_t posK = pos + 2u * j, posV = posK + 1u, posVp = posK - 1u;
                 if (j < n) {
-                    const uint32_t fk = is.full(posK), fp = is.full_par(posK);
-                    if (!(ok = is.wait(fk, fp, j == 0 ? qb0 : fk, j == 0 ? qu0 & 1u : fp,
-                                       j == 0 ? qb1 : fk, j == 0 ? qu1 & 1u : fp, 11)))
+                    if (j == 0 && !(ok = is.wait(is.full(posK), is.full_par(posK), qb0, qu0 & 1u,
+                                                 qb1, qu1 & 1u, qb0, qu0 & 1u, 11)))
                         break;
                     is.issue_s(0, 0, posK);
                     if (j == n - 1) is.commit(sm.bar(C::BAR_QFREE));
                 }
                 if (j > 0) {
-                    if (!(ok = is.issue_pv(PvOp{1, jt1 + j - 1, j == 1, k, posVp}))) break;
+                    if (!(ok = is.issue_pv(PvOp{1, jt1 + j - 1, j == 1, k, posVp}, posVp))) break;
                     is.release(posVp);
                 }
                 if (j < n) {
                     is.issue_s(1, NQ - 1, posK);
                     is.release(posK);
                     if (j == n - 1) is.commit(sm.bar(C::BAR_QFREE + NQ - 1));
-                    if (!(ok = is.issue_pv(PvOp{0, jt0 + j, j == 0, k, posV}))) break;
+                    // the next tile's S_0 follows at once
+                    if (!(ok = is.issue_pv(PvOp{0, jt0 + j, j == 0, k, posV},
+                                           j + 1 < n ? posV + 1u : posV)))
+                        break;
                 }
             }
             if (!ok) break;
@@ -670,7 +675,7 @@ __device__ void mma_warp(const SplitParams& p, const Smem<NQ, Q4>& sm) {
                 const uint32_t posK = pos + 2u * j;
                 const int x = (posK >> 1) & 1u;
                 const uint32_t fk = is.full(posK), fp = is.full_par(posK);
-                if (!(ok = is.wait(fk, fp, j == 0 ? qb0 : fk, j == 0 ? qu0 & 1u : fp, fk, fp, 11)))
+                if (!(ok = is.wait(fk, fp, j == 0 ? qb0 : fk, j == 0 ? qu0 & 1u : fp, fk, fp, fk, fp, 11)))
                     break;
                 is.issue_s(x, 0, posK);
                 is.release(posK);
