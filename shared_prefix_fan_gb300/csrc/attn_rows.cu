@@ -208,8 +208,14 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, cons
     constexpr uint32_t kRing = Q4 ? C::kRaw : C::kStages;
     constexpr int kFull = Q4 ? C::BAR_RFULL : C::BAR_FULL, kEmpty = Q4 ? C::BAR_REMPTY : C::BAR_EMPTY;
     uint32_t it = 0;                // tiles issued
-    uint32_t n_aux = 0;             // partial tiles issued
+    // bf16 pools: a V tile that holds rows no row of the unit sees (in front of
+    // tail_front, from tail_valid) is zeroed there when its pages have landed, which
+    // the warp waits for only after the next K tile is on its way. (K's such rows stay:
+    // their scores are masked, whatever they are.)
+    uint32_t n_aux = 0;             // such tiles finished
     bool aux_pending = false;
+    uint32_t tail_pos = 0;
+    int tail_front = 0, tail_valid = 0;
     uint32_t q_loads[NQ] = {};      // loads of each Q buffer so far
     bool ok = true;
 
@@ -228,6 +234,20 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, cons
     auto q_free = [&](int x) {
         return q_loads[x] == 0 ||
                ptx::mbar_test_wait(sm.bar(C::BAR_QFREE + x), (q_loads[x] - 1) & 1u);
+    };
+
+    auto zero_tail = [&]() {
+        const uint32_t dst = sm.tile(tail_pos);
+        for (int i = lane; i < (kBN - tail_valid + tail_front) * 16; i += 32) {
+            const int r = (i >> 4) < tail_front ? i >> 4 : tail_valid + (i >> 4) - tail_front;
+            const uint32_t ch = i & 15;
+            ptx::st_shared_v4(dst + (ch >> 3) * kHalfBytes + r * 128 + (ch & 7) * 16, 0u, 0u, 0u, 0u);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(sm.bar(kFull + tail_pos % kRing));
+        aux_pending = false;
+        ++n_aux;
     };
 
     const int ui_end = p.cta_first[blockIdx.x + 1];
@@ -270,6 +290,11 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, cons
                 }
             }
         };
+        auto finish_tail = [&]() {
+            if (!wait_for(sm.bar(C::BAR_AUX), n_aux & 1u, 3)) return false;
+            zero_tail();
+            return true;
+        };
         const int32_t* table = p.page_table + static_cast<int64_t>(u.branch) * p.max_pages;
         for (int run = tl.n_first > 0 ? 0 : 1; run < 2 && ok; ++run) {
             const int begin = run == 0 ? tl.first_begin : tl.begin;
@@ -297,6 +322,7 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, cons
                 const int front = run == 1 && j == 0 ? tl.key_begin - tl.begin : 0;
                 const int n_valid = min(kBN, end - (begin + j * kBN));
                 for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
+                    if (!Q4 && kv == 1 && aux_pending && !(ok = finish_tail())) break;
                     const uint32_t s = it % kRing, par = (it / kRing) & 1u;
                     const uint32_t empty = sm.bar(kEmpty + s);
                     ok = wait_for(empty, par ^ 1u, 2);
@@ -313,7 +339,7 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, cons
                                            (kv == 0 ? p.k_pool : p.v_pool) + head * block,
                                            static_cast<uint32_t>(block), full);
                     } else {
-                        const bool partial = n_valid < kBN || front > 0;
+                        const bool partial = kv == 1 && (n_valid < kBN || front > 0);
                         const uint32_t bar = partial ? sm.bar(C::BAR_AUX) : sm.bar(kFull + s);
                         const uint32_t dst = sm.tile(it);
                         if (lane == 0)
@@ -327,22 +353,10 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, cons
                             ptx::tma_load_2d(dst + kHalfBytes + off, tm, bar, 64, row);
                         }
                         if (partial) {
-                            // wait for the pages, then zero the rows nobody sees
-                            const uint32_t aux = sm.bar(C::BAR_AUX), aux_par = n_aux & 1u;
                             aux_pending = true;
-                            ok = wait_for(aux, aux_par, 3);
-                            if (!ok) break;
-                            aux_pending = false;
-                            ++n_aux;
-                            for (int i = lane; i < (kBN - n_valid + front) * 16; i += 32) {
-                                const int r = (i >> 4) < front ? i >> 4 : n_valid + (i >> 4) - front;
-                                const uint32_t ch = i & 15;
-                                ptx::st_shared_v4(dst + (ch >> 3) * kHalfBytes + r * 128 + (ch & 7) * 16,
-                                                  0u, 0u, 0u, 0u);
-                            }
-                            ptx::fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) ptx::mbar_arrive(sm.bar(kFull + s));
+                            tail_pos = it;
+                            tail_front = front;
+                            tail_valid = n_valid;
                         }
                     }
                 }
@@ -354,15 +368,21 @@ __device__ void producer_warp(const SplitParams& p, const Smem<NQ, Q4>& sm, cons
                 ok = warp_wait<NQ, Q4>(p, sm, sm.bar(C::BAR_QFREE + q_next),
                                        (q_loads[q_next] - 1) & 1u, 1);
     }
+    if (!Q4 && ok && aux_pending) {
+        ok = warp_wait<NQ, Q4>(p, sm, sm.bar(C::BAR_AUX), n_aux & 1u, 3);
+        if (ok) zero_tail();
+    }
     // (see attn_fwd.cu: the merge grid may start once every copy is issued)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (!ok && lane == 0) {
         // Drain: every copy this warp started must land before the CTA exits.
-        // (A tile of the 16-bit ring that still waits for its partial pages is covered
-        // by the AUX barrier alone: its full barrier never completes.)
+        // (A V tile that still waits for its pages is covered by the AUX barrier: its
+        // full barrier never completes.)
         const uint32_t n = it < kRing ? it : kRing;
         for (uint32_t i = it - n; i != it; ++i)
-            ptx::mbar_wait(sm.bar(kFull + i % kRing), (i / kRing) & 1u, p.wait_limit_ns, nullptr);
+            if (!aux_pending || i != tail_pos)
+                ptx::mbar_wait(sm.bar(kFull + i % kRing), (i / kRing) & 1u, p.wait_limit_ns,
+                               nullptr);
         if (aux_pending) ptx::mbar_wait(sm.bar(C::BAR_AUX), n_aux & 1u, p.wait_limit_ns, nullptr);
 #pragma unroll
         for (int x = 0; x < NQ; ++x)
@@ -804,37 +824,40 @@ __device__ __forceinline__ float softmax_tile(uint32_t colS, float sl2, Running&
 }
 
 // 32 columns of a finished row to out (direct) or to its partial block; from 4-bit
-// pools put back into their order first (each 8 hold values 0 2 4 6 1 3 5 7).
+// pools put back into their order first (each 8 hold values 0 2 4 6 1 3 5 7). A
+// store is a line of its own for every lane, so 32 bytes at once take half as long
+// as 16 (an output that is aligned to 16 bytes only gets those).
 template <bool Q4>
 __device__ __forceinline__ void store32(void* out, float* part_o, int out_bf16,
                                         const uint32_t (&r)[32], bool direct, int64_t orow,
                                         int64_t prow, int c0) {
     auto at = [](int d) { return Q4 ? (d & ~7) + (d & 1) * 4 + ((d & 7) >> 1) : d; };
-    if (direct && out_bf16) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + orow * kHD + c0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t v[4];
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-                v[h] = ptx::pack_bf16x2(__uint_as_float(r[at(8 * i + 2 * h)]),
-                                        __uint_as_float(r[at(8 * i + 2 * h + 1)]));
-            dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
+    auto put = [direct](void* dst, const uint32_t* v) {
+        if (!direct || (reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
+            ptx::st_global_v8(dst, v);
+        } else {
+            static_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+            static_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
         }
-    } else if (direct) {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + orow * kHD + c0);
+    };
+    uint32_t v[8];
+    if (direct && out_bf16) {
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out) + orow * kHD + c0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(__uint_as_float(r[at(4 * i)]), __uint_as_float(r[at(4 * i + 1)]),
-                                 __uint_as_float(r[at(4 * i + 2)]), __uint_as_float(r[at(4 * i + 3)]));
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int h = 0; h < 8; ++h)
+                v[h] = ptx::pack_bf16x2(__uint_as_float(r[at(16 * i + 2 * h)]),
+                                        __uint_as_float(r[at(16 * i + 2 * h + 1)]));
+            put(dst + 16 * i, v);
+        }
     } else {
-        float* dst = part_o + prow * kHD + c0;
+        float* dst = (direct ? static_cast<float*>(out) + orow * kHD : part_o + prow * kHD) + c0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint32_t v[8];
 #pragma unroll
             for (int h = 0; h < 8; ++h) v[h] = r[at(8 * i + h)];
-            ptx::st_global_v8(dst + 8 * i, v);
+            put(dst + 8 * i, v);
         }
     }
 }

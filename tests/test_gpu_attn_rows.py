@@ -236,3 +236,17 @@ def test_long_sweeps_of_the_4_bit_cache(hq, hkv, page, P, T, window, sinks, gs):
         ref.check_attention(out, lse, want, P_STEP[True])
         first = first or (out, lse)
         assert torch.equal(first[0], out) and torch.equal(first[1], lse)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+def test_output_aligned_to_16_bytes_only(q4, out_dtype):
+    prob = ref.Problem([40, 300], [40, 3], 128, 8, 1, 16, window=200, sinks=3, q4=q4)
+    dt = torch.float32 if out_dtype == "f32" else torch.bfloat16
+    n, lead = 43 * 8 * 128, 16 // dt.itemsize
+    buf = torch.full((n + 2 * lead,), 7.0, dtype=dt, device="cuda")
+    out = buf[lead:lead + n].view(43, 8, 128)
+    assert out.data_ptr() % 32 == 16
+    _, lse = prob.run(out_dtype, out=out)
+    ref.check_attention(out, lse, prob.reference(), P_STEP[q4])
+    assert (buf[:lead] == 7).all() and (buf[lead + n:] == 7).all()
