@@ -53,6 +53,10 @@ inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // unit boundaries measured 3-5 us).
 constexpr double kUnitOverhead2 = 2.0;
 constexpr double kUnitOverhead1 = 3.0;
+// The row kernel's boundary of two-tile units: 10000 cycles against 3300 a tile (3 or
+// more: a windowed prefill of 4096 tokens is no longer cut, 166 us, not 186, and a
+// 4-bit prefill takes 1456, not 1466; 32 ragged 4-bit branches take 840, not 831).
+constexpr double kUnitOverheadRows2 = 3.0;
 constexpr double kMergePerPart = 2.0;  // write + read of one 128-row partial, in tile times
 constexpr double kMergeLaunch = 4.0;   // the extra merge launch, in tile times
 
@@ -446,7 +450,7 @@ int build_plan(const PlanInput& in, Plan& plan) {
 
     // Chunk size from the cost model (or the forced split count).
     const int32_t max_cta = std::max(1, in.num_sms);
-    const double ovh = plan.nq == 2 ? kUnitOverhead2 : kUnitOverhead1;
+    const double ovh = plan.nq == 1 ? kUnitOverhead1 : in.rows ? kUnitOverheadRows2 : kUnitOverhead2;
     Cand best, cand;
     if (in.force_splits > 0) {
         make_candidate(ranges, 0, in.force_splits, max_cta, ovh, best);
