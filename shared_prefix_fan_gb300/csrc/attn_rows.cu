@@ -557,11 +557,11 @@ __device__ __forceinline__ uint64_t kmajor_step(int kk) {
 
 // One P.V product: group x's P of its t-th tile times the V tile at ring position
 // pos. first: the group's first product of unit k (O is overwritten; both groups
-// must have read the previous unit's O).
+// must have read the previous unit's O); last: its last one there.
 struct PvOp {
     int x;
     uint32_t t;
-    bool first;
+    bool first, last;
     int k;
     uint32_t pos;
 };
@@ -621,7 +621,7 @@ struct Issuer {
         for (int kk = 0; kk < kBN / 16; ++kk)
             ptx::mma_f16_ts_if(d, a + 8u * kk, dv + 128u * kk, C::kIdescPV,
                                (!op.first || kk > 0) ? 1u : 0u, leader);
-        commit(sm.gbar(op.x, ODONE));
+        if (op.last) commit(sm.gbar(op.x, ODONE));
         return true;
     }
     // The held P.V of a unit of one query tile, if any.
@@ -649,7 +649,7 @@ __device__ void mma_warp(const SplitParams& p, const Smem<NQ, Q4>& sm) {
     uint32_t pos = 0;           // ring position of the unit's K_0 (K_j at pos + 2j, V_j behind it)
     uint32_t jt0 = 0, jt1 = 0;  // tiles each softmax group got before
     uint32_t qu0 = 0, qu1 = 0;  // loads of each Q buffer consumed
-    PvOp pend{0, 0, false, 0, 0};
+    PvOp pend{0, 0, false, false, 0, 0};
     bool held = false;
     int k = 0;
     const int ui_end = p.cta_first[blockIdx.x + 1];
@@ -669,7 +669,7 @@ __device__ void mma_warp(const SplitParams& p, const Smem<NQ, Q4>& sm) {
                     if (j == n - 1) is.commit(sm.bar(C::BAR_QFREE));
                 }
                 if (j > 0) {
-                    if (!(ok = is.issue_pv(PvOp{1, jt1 + j - 1, j == 1, k, posVp}, posVp))) break;
+                    if (!(ok = is.issue_pv(PvOp{1, jt1 + j - 1, j == 1, j == n, k, posVp}, posVp))) break;
                     is.release(posVp);
                 }
                 if (j < n) {
@@ -677,7 +677,7 @@ __device__ void mma_warp(const SplitParams& p, const Smem<NQ, Q4>& sm) {
                     is.release(posK);
                     if (j == n - 1) is.commit(sm.bar(C::BAR_QFREE + NQ - 1));
                     // the next tile's S_0 follows at once
-                    if (!(ok = is.issue_pv(PvOp{0, jt0 + j, j == 0, k, posV},
+                    if (!(ok = is.issue_pv(PvOp{0, jt0 + j, j == 0, j == n - 1, k, posV},
                                            j + 1 < n ? posV + 1u : posV)))
                         break;
                 }
@@ -702,7 +702,7 @@ __device__ void mma_warp(const SplitParams& p, const Smem<NQ, Q4>& sm) {
                 if (j == n - 1) is.commit(sm.bar(C::BAR_QFREE));
                 if (!(ok = is.issue_held(pend, held))) break;
                 const uint32_t t = x == 0 ? jt0++ : jt1++;
-                pend = PvOp{x, t, j < 2, k, posK + 1u};
+                pend = PvOp{x, t, j < 2, j >= n - 2, k, posK + 1u};
                 held = true;
             }
             if (!ok) break;
@@ -879,7 +879,8 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ, Q4>& sm, uint
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t colS = lane_addr + 128u * x, colO = lane_addr + kColO + 128u * x;
     uint32_t n_load[2] = {0, 0};  // loads of each Q buffer before this unit
-    uint32_t jt = 0, jt_other = 0;  // tiles this group and the other got
+    uint32_t jt = 0;                // tiles this group got
+    uint32_t ku = 0, ku_other = 0;  // units in which this group and the other got tiles
     uint32_t tile0 = 0;  // K/V tiles before this unit
     int kj = 0;  // joined (one-query-tile) units so far
     // Before the first unit each group makes a dry run of that unit's epilogue (no
@@ -964,7 +965,7 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ, Q4>& sm, uint
         float2* const join = reinterpret_cast<float2*>(sm.ptr + C::kSmemJoin) + (kj & 1) * 2 * kBM;
         const int n_other = pair ? 0 : (n_tiles + j0) >> 1;  // tiles of the other parity
         if (pair) {
-            jt_other += n_tiles;
+            if (!dry) ++ku_other;
         } else if (!dry) {
             // Join the groups: exchange (m, l), then each combines 64 columns.
             join[x * kBM + row] = make_float2(m_ref, l_run);
@@ -972,12 +973,12 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ, Q4>& sm, uint
             // two barriers in turn: a group without a tile in the next unit may
             // arrive there before this one has waited here
             if (lane == 0) ptx::mbar_arrive(sm.gbar(x, JOIN + (kj & 1)));
-            jt_other += n_other;
+            if (n_other > 0) ++ku_other;
             if (!warp_wait<NQ, Q4>(p, sm, sm.gbar(x ^ 1, JOIN + (kj & 1)), (kj >> 1) & 1, 23)) return;
             ++kj;
         }
-        if (n_tiles > n_other && !warp_wait<NQ, Q4>(p, sm, sm.gbar(x, ODONE), (jt - 1) & 1u, 22)) return;
-        if (n_other > 0 && !warp_wait<NQ, Q4>(p, sm, sm.gbar(x ^ 1, ODONE), (jt_other - 1) & 1u, 24))
+        if (n_tiles > n_other && !warp_wait<NQ, Q4>(p, sm, sm.gbar(x, ODONE), ku++ & 1u, 22)) return;
+        if (n_other > 0 && !warp_wait<NQ, Q4>(p, sm, sm.gbar(x ^ 1, ODONE), (ku_other - 1) & 1u, 24))
             return;
         ptx::tc_fence_after();
         if (active) {
