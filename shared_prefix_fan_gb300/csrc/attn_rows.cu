@@ -14,13 +14,12 @@
 //               a ring of raw tiles (9 KB: 128 rows of 72 bytes). Q by TMA as soon as
 //               its buffer is free. Page ids are checked before they are read through;
 //   warp 1      TMEM owner and tcgen05 issuer: the whole warp runs the issue loop, so
-//               that descriptors stay in uniform registers (they are constants: a
-//               branch per ring stage), and one elected lane issues;
+//               that its addresses stay warp-uniform, and one elected lane issues;
 //   warps 2-3   4-bit pools only: turn loaded Q tiles into f16 in place;
 //   warps 4-11  two softmax groups of 4 warps, thread = row;
 //   warps 12-19 4-bit pools only: widen raw tiles into the swizzled 16-bit ring (4
-//               warps the K tiles, 4 the V tiles). With 4 warps for both, a decode
-//               step waited for them: 35 us, not 31.
+//               warps the K tiles, 4 the V tiles): with 4 warps for both, a decode
+//               step waited for them (35 us against 31 with 8).
 // Keys of a tile that no row of the unit sees are zeros in shared memory, whatever
 // the pool holds there.
 //
@@ -46,11 +45,26 @@
 //   of l and of the output, where V's pool scale goes too (K's: softmax scale).
 // Widening is one conversion (a byte of two codes to an f16 pair) and one packed
 // product per two values: both run at 64 lanes a cycle and SM (measured), so a K
-// and a V tile take 256 cycles of either pipe, under the 1024 their four (two for
-// a single query tile) products take on the tensor core. Bit tricks on bf16 tiles
-// instead took 2.5 times the instructions: a prefill step was 2.1 times slower.
+// and a V tile take 256 cycles of either pipe, under the 2048 that the four products
+// of two query tiles (1024: the two of one) take on the tensor core. Bit tricks on
+// bf16 tiles took 2.5 times the instructions: a prefill step was 2.1 times slower.
 // The codes of a word come out as values 0 2 4 6 1 3 5 7 of its 8; K and Q keep
 // that order (it is summed over), V's columns are put back when O is stored.
+//
+// What bounds it (GB300, L2 flushed, whole calls). Two query tiles: the chain of a
+// group, S product (512 cycles), softmax (1650: its maximum 500, exponentials 850,
+// P's store 300), hand-off (400), P.V product (512); P lies over S, and two S and
+// two O are all of TMEM, so S cannot be doubled, and a key tile takes about 3250
+// cycles a pair where its products are 2048. A boundary between units costs about
+// 10000 cycles (epilogue, next Q, masked tiles).
+//   4-bit prefill, 2048 rows x 64 heads over 32768 keys: 1436 us, 1484 TFLOP/s
+//   4-bit, 32 branches of 1..32 tokens over 65536 shared keys: 830 us, 1202 TFLOP/s
+//   bf16, the same over 16384 keys, window 2048: 102 us, 2060 GB/s, 356 TFLOP/s
+//   bf16 prefill, 4096 rows x 64 heads, window 1024: 166 us, 832 TFLOP/s
+// One query tile (decode), 8 rows x 64 heads over 32768 keys: 33 us for 42.5 MB in 4
+// bits (bf16 pools through attn_fwd.cu: 45 us for 151 MB): 15 tiles a CTA of 1900
+// cycles each, half a group's chain, and 6600 cycles until the first S. Window 4096:
+// 20.5 us, four tiles a CTA and nearly all start and epilogue.
 // Every wait is bounded, as in attn_fwd.cu.
 #include <cuda_bf16.h>
 
@@ -151,8 +165,7 @@ struct Smem {
 // wait of the CTA has given up, or after p.wait_limit_ns; the site goes into the
 // CTA's abort word, which the kernel reports at its end. Every role's waits are
 // inlined, and the roles share an instruction cache that their code overflows, so
-// this is kept short (the kernel was 105 KB of code and is 60 KB; a prefill gained a
-// sixth).
+// this is kept short.
 template <int NQ, bool Q4>
 __device__ __forceinline__ bool warp_wait(const SplitParams& p, const Smem<NQ, Q4>& sm, uint32_t bar,
                                           uint32_t parity, int site) {
@@ -638,7 +651,9 @@ struct Issuer {
 // S(t) into the buffer of group t mod 2, then P.V(t-1) of the other group; a unit's
 // last P.V is held until the next such unit's first S is issued. An S that reuses the
 // TMEM of an earlier P is always issued after that P's product. TMEM starts at column
-// 0 (the CTA has all of it).
+// 0 (the CTA has all of it). One loop with few branches: a state machine over both
+// groups' next steps, and loops specialised by ring stage, had longer code paths and
+// were slower (a prefill 2237 and 1687 us when this one took 1558).
 template <int NQ, bool Q4>
 __device__ void mma_warp(const SplitParams& p, const Smem<NQ, Q4>& sm) {
     using C = Cfg<NQ, Q4>;
@@ -790,7 +805,8 @@ struct Running {
 };
 
 // One tile's softmax of this thread's row: P over the first 64 columns of S. Returns
-// the rescale factor.
+// the rescale factor. (One pass with the reference of the tiles before, starting over
+// when it must be raised, was slower: a prefill 1661 us against 1583.)
 template <bool Q4>
 __device__ __forceinline__ float softmax_tile(uint32_t colS, float sl2, Running& run) {
     constexpr float kLift = Cfg<1, Q4>::kLiftLog2;

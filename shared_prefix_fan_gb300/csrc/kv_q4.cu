@@ -20,7 +20,9 @@
 // per warp, 8192 rows of 8 heads took 33 us in and out), and the work per value is
 // kept short: the quotients are products with the reciprocal, corrected (quotient,
 // below), the largest magnitude comes from packed maxima, codes from the e2m1
-// conversions (with fp32 divisions it took 47 us).
+// conversions (with fp32 divisions it took 47 us). Measured: 8192 rows of 8 heads in
+// and out 26.6 us (86 MB: 3.2 TB/s, the rows just written read from L2), 8 rows 10 us
+// (two launches).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -16,6 +16,9 @@
 // loads and a few shuffles per branch, from L2), so no CTA waits for another
 // and all of them come to the same verdict on the lengths: a negative length, a
 // row too narrow, a list too short or too few slots leaves the table untouched.
+// Measured: extend of 8 branches 8.2 us (a launch and three dependent reads), fork of
+// 1024 branches over 4096 prefix pages 12.3 us for 18.4 MB (2.7 us at the copy rate:
+// the scan in front of the copies and one wave of blocks are the rest).
 #include <cuda_runtime.h>
 
 #include <algorithm>
