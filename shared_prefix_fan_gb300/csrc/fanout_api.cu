@@ -151,8 +151,19 @@ int attn_call(AttnKind kind, const void* q, const void* k_pages, const void* v_p
         if (ce != cudaSuccess) return status_from_cuda(ce);
         const int32_t n_pre = prefix_len / page_size;
         for (int32_t b = 0; b < num_branches; ++b) {
-            const int64_t n = (static_cast<int64_t>(prefix_len) + suffix_lens[b] + page_size - 1) / page_size;
+            const int64_t keys = static_cast<int64_t>(prefix_len) + suffix_lens[b];
+            const int64_t n = (keys + page_size - 1) / page_size;
+            // with a window, pages [n_first, hidden_end) hold no key of the branch's rows
+            int64_t n_first = 0, hidden_end = 0;
+            if (window > 0) {
+                n_first = (std::min<int64_t>(sinks, keys) + page_size - 1) / page_size;
+                hidden_end = q_rows_per_branch[b] == 0
+                                 ? n
+                                 : std::max<int64_t>(0, keys - q_rows_per_branch[b] + 1 - window) / page_size;
+                if (q_rows_per_branch[b] == 0) n_first = 0;
+            }
             for (int64_t i = 0; i < n; ++i) {
+                if (i >= n_first && i < hidden_end) continue;
                 const int32_t v = tab[static_cast<size_t>(b) * max_pages_per_branch + i];
                 if (v < 0 || v >= num_pages) return FANOUT_EINVAL;
                 if (i < n_pre && v != tab[i]) return FANOUT_EINVAL;  // prefix must be shared

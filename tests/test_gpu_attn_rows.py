@@ -250,3 +250,34 @@ def test_output_aligned_to_16_bytes_only(q4, out_dtype):
     _, lse = prob.run(out_dtype, out=out)
     ref.check_attention(out, lse, prob.reference(), P_STEP[q4])
     assert (buf[:lead] == 7).all() and (buf[lead + n:] == 7).all()
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_table_validation_leaves_hidden_pages_alone(q4):
+    """With the host-side check on: entries that the window hides may be anything,
+    a bad one that it shows is refused."""
+    prob = ref.Problem([40, 30, 9], [3, 2, 0], 300, 8, 2, 16, window=50, sinks=20, q4=q4)
+    bad = prob.table.copy()
+    bad[:, 2:] = -1  # hidden, except from the oldest key a row sees on
+    for b, (s, t) in enumerate(((40, 3), (30, 2))):
+        first = (300 + s - t - 50 + 1) // 16
+        bad[b, first:] = prob.table[b, first:]
+    low = min((300 + s - t - 50 + 1) // 16 for s, t in ((40, 3), (30, 2)))
+    bad[0, low:18] = prob.table[0, low:18]  # row 0 stands for the shared pages
+    bad[2] = -1                             # no rows: nothing of it is read
+    binding.set_option(binding.OPT_VALIDATE_TABLE, 1)
+    try:
+        prob.call_table = bad
+        out, lse = prob.run()
+        ref.check_attention(out, lse, prob.reference(), P_STEP[q4])
+        for b, i in ((0, 1), (1, bad.shape[1] - 3)):
+            if bad[b, i] < 0:
+                continue
+            worse = bad.copy()
+            worse[b, i] = prob.num_pages
+            prob.dev[3] = torch.from_numpy(worse).cuda()
+            with pytest.raises(binding.FanoutError) as e:
+                prob.run()
+            assert e.value.code == binding.EINVAL
+    finally:
+        binding.set_option(binding.OPT_VALIDATE_TABLE, 0)
