@@ -346,7 +346,8 @@ FANOUT_API int fanout_attn_window(const void *q, const void *k_pages, const void
 /*
  * fanout_attn_q4 -- fanout_attn over 4-bit pools: out = softmax(scale q K^T) V
  * and lse over the values that the pools' bytes stand for (uint8 [num_pages][H_kv]
- * [page_size * 72], 16-byte aligned, scales k_scale and v_scale).
+ * [page_size * 72], 16-byte aligned, scales k_scale and v_scale; scale * k_scale
+ * within 1e-37 .. 1e37, else FANOUT_EINVAL).
  *   window, sinks  0, 0: every key (up to pos with causal != 0); window >= 1
  *                  needs causal and means what it does in fanout_attn_window.
  *                  sinks without a window is FANOUT_EINVAL.

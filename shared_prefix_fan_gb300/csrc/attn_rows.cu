@@ -942,7 +942,8 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ, Q4>& sm, uint
             // that barrier two phases on.)
             if (Q4 && j == j0 && row_valid) {
                 const int k = static_cast<int>(*sm.fac(load, xq, row)) - 127;
-                sl2 *= __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+                // (finite, so that a key of zeros scores 0 with the largest Q too)
+                sl2 = fminf(sl2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23), 3e38f);
             }
             float corr = 1.f;
             if (active) {

@@ -281,3 +281,24 @@ def test_table_validation_leaves_hidden_pages_alone(q4):
             assert e.value.code == binding.EINVAL
     finally:
         binding.set_option(binding.OPT_VALIDATE_TABLE, 0)
+
+
+@pytest.mark.parametrize("T", [1, 20])
+def test_largest_queries_on_keys_of_zeros(T):
+    """Scores are 0 whatever the scales: the output is the mean of V."""
+    n, page, hkv, hq, ks = 200, 16, 2, 16, 1e6
+    pools = [binding.q4_pool(13, hkv, page) for _ in range(2)]
+    v = torch.from_numpy(np.random.default_rng(3).standard_normal((n, hkv, 128)).astype(np.float32))
+    slots = torch.arange(n, device="cuda")
+    binding.kv_append_q4(torch.zeros((n, hkv, 128), dtype=torch.bfloat16, device="cuda"),
+                         v.bfloat16().cuda(), *pools, slots, page, ks, 1.0)
+    q = torch.full((T, hq, 128), 3e38, dtype=torch.bfloat16, device="cuda")
+    table = torch.arange(13, dtype=torch.int32, device="cuda")[None]
+    out, lse = binding.attn_q4(q, *pools, table, 0, [n], [T], hq, hkv, page, 1.0, False, ks, 1.0)
+    held = ref.decode(*ref.parts_of(pools[1].cpu().numpy(), page), 1.0)
+    held = held.transpose(0, 2, 1, 3).reshape(-1, hkv, 128)[:n]
+    want = np.repeat(held.mean(0), hq // hkv, 0)
+    # P is 1 for every key: exact in f16; the sums are of fp32 (see check_attention)
+    tol = np.repeat(np.abs(held).mean(0), hq // hkv, 0) * 2.0 ** -16 + 1e-30
+    assert (np.abs(out.double().cpu().numpy() - want) <= tol).all()
+    assert (lse.double().cpu() - np.log(n)).abs().max() <= 2.0 ** -16 + 2.0 ** -22 * np.log(n)

@@ -96,6 +96,11 @@ def test_window_rules(lib):
     assert lib.fanout_attn_q4(*attn_args(True, kg=0.0)[1]) == E
 
 
+@pytest.mark.parametrize("scale,kg", [(1e-20, 1e-18), (1e30, 1e8), (3e38, 1.0), (1e-38, 1.0)])
+def test_softmax_scale_of_the_held_values(lib, scale, kg):
+    assert lib.fanout_attn_q4(*attn_args(True, scale=scale, kg=kg)[1]) == E
+
+
 def test_binding_refuses_host_tensors():
     i, pool = torch.zeros(2, dtype=torch.int32), torch.zeros((2, 1, 16 * 72), dtype=torch.uint8)
     x = torch.zeros((2, 1, 128), dtype=torch.bfloat16)
