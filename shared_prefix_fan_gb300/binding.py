@@ -453,6 +453,9 @@ def attn(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens: Sequence
     return out, lse
 
 
+_I32_MAX = 2 ** 31 - 1  # ctypes would take the low 32 bits of more
+
+
 def _lens(suffix_lens, q_rows):
     """Host lengths of a call as one int32 array [2, B]: (array, address, B, rows)."""
     if len(suffix_lens) != len(q_rows):
@@ -493,6 +496,7 @@ def attn_window(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q
     """attn(), causal, where a row at pos sees keys j <= pos with j > pos - window
     or j < sinks. Pages that no row sees may have been given back."""
     import torch
+    window, sinks = min(window, _I32_MAX), min(sinks, _I32_MAX)
     held, lens, B, R = _lens(suffix_lens, q_rows)
     code, out, lse = _attn_out(q, page_table, R, B, h_q, out, lse, out_dtype, want_lse)
     dev, d = q.device, q.shape[-1]
@@ -513,6 +517,7 @@ def attn_q4(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q_row
             out_dtype: str = "f32", want_lse: bool = True, stream=None):
     """attn() over 4-bit pools (uint8 [num_pages, H_kv, page_size * 72]); window and
     sinks as in attn_window (0, 0: none)."""
+    window, sinks = min(window, _I32_MAX), min(sinks, _I32_MAX)
     held, lens, B, R = _lens(suffix_lens, q_rows)
     code, out, lse = _attn_out(q, page_table, R, B, h_q, out, lse, out_dtype, want_lse)
     dev = q.device

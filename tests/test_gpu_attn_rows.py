@@ -302,3 +302,39 @@ def test_largest_queries_on_keys_of_zeros(T):
     tol = np.repeat(np.abs(held).mean(0), hq // hkv, 0) * 2.0 ** -16 + 1e-30
     assert (np.abs(out.double().cpu().numpy() - want) <= tol).all()
     assert (lse.double().cpu() - np.log(n)).abs().max() <= 2.0 ** -16 + 2.0 ** -22 * np.log(n)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_windows_wider_than_32_bits(q4):
+    a = ref.Problem([40, 30], [3, 2], 64, 8, 2, 16, window=2 ** 31 - 1, sinks=0, q4=q4)
+    x = a.run()
+    a.window, a.sinks = 2 ** 32 + 5, 2 ** 40
+    y = a.run()
+    assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_pools_past_32_bit_offsets(q4):
+    """The same pages at both ends of pools of more than 4 GB."""
+    prob = ref.Problem([200, 70], [3, 1], 128, 8, 8, 64, window=150, sinks=10, q4=q4)
+    near = prob.run()
+    block = prob.k_pool[0].numel() * prob.k_pool.element_size()
+    far = 2 ** 32 // block + 7
+    pools = [torch.zeros((far + prob.num_pages, *prob.k_pool.shape[1:]), dtype=prob.k_pool.dtype,
+                         device="cuda") for _ in range(2)]
+    for pool, x in zip(pools, (prob.k_pool, prob.v_pool)):
+        pool[far:] = x.cuda()
+    table = prob.table + np.where(prob.table >= 0, far, 0).astype(np.int32)
+    prob.dev = [prob.dev[0], *pools, torch.from_numpy(table).cuda()]
+    out, lse = prob.run()
+    assert torch.equal(out, near[0]) and torch.equal(lse, near[1])
+    if q4:  # and the rows of the last page
+        slots = (torch.arange(64, device="cuda") + (far + prob.num_pages - 1) * 64)
+        new = torch.randn((64, 8, 128), device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+        binding.kv_append_q4(new.bfloat16(), -new.bfloat16(), *pools, slots, 64)
+        small = [binding.q4_pool(1, 8, 64) for _ in range(2)]
+        binding.kv_append_q4(new.bfloat16(), -new.bfloat16(), *small, slots % 64, 64)
+        assert torch.equal(pools[0][-1], small[0][0]) and torch.equal(pools[1][-1], small[1][0])
+        k, v = binding.kv_read_q4(*pools, slots, 64)
+        ks, vs = binding.kv_read_q4(*small, slots % 64, 64)
+        assert torch.equal(k, ks) and torch.equal(v, vs)
