@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from typing import Optional, Sequence, Tuple
 
 import numpy as np
@@ -460,11 +461,13 @@ def _lens(suffix_lens, q_rows):
     """Host lengths of a call as one int32 array [2, B]: (array, address, B, rows)."""
     if len(suffix_lens) != len(q_rows):
         raise ValueError("suffix_lens and q_rows differ in length")
+    if type(suffix_lens) is list and type(q_rows) is list:
+        ints = array("i", suffix_lens + q_rows)
+        return ints, ints.buffer_info()[0], len(q_rows), sum(q_rows)
     both = np.array((suffix_lens, q_rows), dtype=np.int32)
     if both.ndim != 2:
         raise ValueError("suffix_lens and q_rows must be sequences of integers")
-    rows = sum(q_rows) if type(q_rows) is list else int(both[1].sum())
-    return both, both.ctypes.data, both.shape[1], rows
+    return both, both.ctypes.data, both.shape[1], int(both[1].sum())
 
 
 def _attn_out(q, page_table, R: int, B: int, h_q: int, out, lse, out_dtype: str, want_lse: bool):
