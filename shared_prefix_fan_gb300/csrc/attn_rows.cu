@@ -63,8 +63,11 @@
 //   bf16 prefill, 4096 rows x 64 heads, window 1024: 166 us, 832 TFLOP/s
 // One query tile (decode), 8 rows x 64 heads over 32768 keys: 33 us for 42.5 MB in 4
 // bits (bf16 pools through attn_fwd.cu: 45 us for 151 MB): 15 tiles a CTA of 1900
-// cycles each, half a group's chain, and 6600 cycles until the first S. Window 4096:
-// 20.5 us, four tiles a CTA and nearly all start and epilogue.
+// cycles each, and 6600 cycles until the first S. A tile moves 200 KB through shared
+// memory (raw rows in and out 36, widened 64, the products' operands K, V and Q 96),
+// 1570 cycles at 128 bytes a cycle, so shorter chains gain little there
+// (rows copied into a tile's idle half, so that a row's keys were split over two warps,
+// gained nothing). Window 4096: 20.5 us, four tiles a CTA, start and epilogue.
 // Every wait is bounded, as in attn_fwd.cu.
 #include <cuda_bf16.h>
 
