@@ -137,3 +137,17 @@ def test_window_that_stays_private_is_one_unit(shim):
     units, info = check(shim, [500, 600], [1, 1], 4096, 8, 1, 64, 1, 256, 4, splits=1)
     assert int(info[0]) == 0 and int(info[3]) == 0 and len(units) == 2
     assert (units[:, 6] == 4).all()
+
+
+def test_short_contexts_need_no_merge(shim):
+    """A few tiles of keys: every branch sweeps its own; a long prefix stays shared.
+    Steps carry either plan over."""
+    for prev in (None, [20, 30, 10]):
+        S = [21, 31, 11]
+        units, info = check(shim, S, [1, 1, 1], 256, 16, 2, 16, prev=prev, row_bytes=144)
+        assert int(info[0]) == 0 and int(info[3]) == 0 and len(units) == 6
+        assert prev is None or int(info[4]) == 1
+        units, info = check(shim, S, [1, 1, 1], 2048, 16, 2, 16, prev=prev, row_bytes=144)
+        assert int(info[0]) == 2048 and int(info[3]) > 0
+    units, info = check(shim, [500, 20], [40, 3], 200, 8, 1, 16, window=90, sinks=5)
+    assert int(info[0]) in (0, 192)
