@@ -599,12 +599,12 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
         const Unit u = p.units[dry ? ui_first : ui];
         const int n_tiles = dry ? 0 : unit_tiles(u);
         if (!dry && (n_tiles <= 0 || x >= unit_nq<NQ>(u, p.tpt))) continue;
-        // row within the unit: tile x holds its tokens x * tpt .. (128 / G of them, so
-        // a G that does not divide 128 leaves the tile's last rows empty)
-        const int urow = kBM * x + row;
-        const int tile_tok = x * p.tpt;
-        const bool row_valid =
-            dry ? (lane == 0 && quarter == 0) : row < min(p.tpt, u.n_tok - tile_tok) * p.G;
+        // The row's number among the unit's rows: a tile holds p.tpt tokens, so a G that
+        // does not divide 128 leaves the tile's last rows empty.
+        const int tile_rows = p.tpt * p.G;
+        const int urow = tile_rows * x + row;
+        const bool row_valid = dry ? (lane == 0 && quarter == 0)
+                                   : row < tile_rows && urow < u.n_tok * p.G;
         if (lane == 0)
             ptx::st_shared_v4(slot, static_cast<uint32_t>(u.tok_begin), static_cast<uint32_t>(u.kv_head),
                               static_cast<uint32_t>(u.part), 0u);
@@ -613,7 +613,7 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
         // Only the key start and this row's visible end stay live through the
         // tile loop (registers).
         const int key_begin = u.key_begin;
-        const int vis_end = row_valid ? min(u.key_end, u.pos_base + u.tok_begin + tile_tok + row / p.G + 1) : 0;
+        const int vis_end = row_valid ? min(u.key_end, u.pos_base + u.tok_begin + urow / p.G + 1) : 0;
         float m_ref = -INFINITY, l_run = 0.f;
         for (int j = 0; j < n_tiles; ++j, ++jt) {
             const int kt = key_begin + j * kBN;
@@ -729,10 +729,10 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ>& sm, uint32_t
         if (active) {
             const uint4 f = ptx::ld_shared_v4(slot);
             const int e_part = static_cast<int>(f.z);
-            const int tok = static_cast<int>(f.x) + x * p.tpt + row / p.G;
-            const int hq = static_cast<int>(f.y) * p.G + row % p.G;
+            const int tok = static_cast<int>(f.x) + urow / p.G;
+            const int hq = static_cast<int>(f.y) * p.G + urow % p.G;
             const int64_t orow = dry ? 0 : static_cast<int64_t>(tok) * p.H_q + hq;
-            const int64_t prow = dry ? 0 : static_cast<int64_t>(e_part) * rows_per_part + urow;
+            const int64_t prow = dry ? 0 : static_cast<int64_t>(e_part) * rows_per_part + (kBM * x + row);
             void* const out_base = dry ? static_cast<void*>(p.sink) : p.out;
             float* const po_base = dry ? p.sink : p.part_o;
             float* const lse_base = dry ? p.sink : p.lse;
