@@ -945,8 +945,11 @@ __device__ void softmax_group(const SplitParams& p, const Smem<NQ, Q4>& sm, uint
             // that barrier two phases on.)
             if (Q4 && j == j0 && row_valid) {
                 const int k = static_cast<int>(*sm.fac(load, xq, row)) - 127;
-                // (finite, so that a key of zeros scores 0 with the largest Q too)
-                sl2 = fminf(sl2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23), 3e38f);
+                // Finite, so that a key of zeros scores 0 with the largest Q too, and
+                // not 0, so that a hidden key's -inf stays one (0 * -inf is a NaN) with the
+                // smallest: a score is at most 2^34, so 1.2e-38 gives what less would, 0.
+                sl2 = fmaxf(fminf(sl2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23), 3e38f),
+                            1.2e-38f);
             }
             float corr = 1.f;
             if (active) {

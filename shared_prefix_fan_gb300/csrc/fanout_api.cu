@@ -556,7 +556,8 @@ int fanout_attn_q4(const void* q, const void* k_pages, const void* v_pages,
     if (window < 0 || sinks < 0 || (window > 0 && !causal) || (window == 0 && sinks > 0))
         return FANOUT_EINVAL;
     if (!q4_scale_ok(k_scale) || !q4_scale_ok(v_scale)) return FANOUT_EINVAL;
-    // their product is the softmax scale of the held values: it and its inverse normal
+    // their product is the softmax scale of the held values: it and its inverse normal (the
+    // kernel keeps it so when a row's own power of two comes in)
     if (!(scale * k_scale >= 1e-37f && scale * k_scale <= 1e37f)) return FANOUT_EINVAL;
     try {
         return attn_call(window > 0 ? kQ4Window : kQ4, q, k_pages, v_pages, page_table,
