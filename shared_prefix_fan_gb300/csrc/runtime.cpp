@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <limits>
 #include <mutex>
 
 #include "../../include/fanout.h"
@@ -193,7 +194,13 @@ int launch_plan(const CallArgs& a, const Plan& pl, const Layout& L, uint8_t* bas
     p.tpt = pl.tpt;
     p.nq = pl.nq;
     p.out_bf16 = a.out_bf16;
-    p.scale_log2 = a.scale * 1.4426950408889634f;
+    // Formed in 64 bits, where neither a scale at the end of fp32's range nor k_scale moves
+    // it out of range before their product is there; without k_scale the bits of one fp32
+    // product.
+    const double scale_log2 = static_cast<double>(a.scale) * (a.q4 ? a.k_scale : 1.0f) *
+                              static_cast<double>(1.4426950408889634f);
+    p.scale_log2 = static_cast<float>(
+        std::min(scale_log2, static_cast<double>(std::numeric_limits<float>::max())));
     p.tok_pos = pl.tok_pos.empty() ? nullptr : reinterpret_cast<const int32_t*>(base + L.pos);
     p.window = a.window > 0 ? a.window : kNoWindow;
     p.sinks = a.sinks;
@@ -201,7 +208,6 @@ int launch_plan(const CallArgs& a, const Plan& pl, const Layout& L, uint8_t* bas
     p.k_pool = static_cast<const uint8_t*>(a.k);
     p.v_pool = static_cast<const uint8_t*>(a.v);
     p.o_scale = a.v_scale;
-    if (a.q4) p.scale_log2 *= a.k_scale;
     p.wait_limit_ns = a.wait_limit_ns;
     MergeParams& m = p.merge;
     m.part_o = p.part_o;
