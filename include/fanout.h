@@ -160,12 +160,23 @@ FANOUT_API int fanout_extend(int32_t *page_table, int32_t num_branches,
  *   cow_pairs     dev int32 [B][2] or NULL: as fanout_fork_cow, written when
  *                 prefix_len is not a multiple of page_size.
  * What only the device can see -- a negative suffix, more than 2^31 - 1 tokens,
- * a row too narrow, a free list too short, *used_in < 0 -- leaves the table and
- * cow_pairs as they were, copies *used_in to *used_out and is reported by
- * fanout_last_error() as FANOUT_EINVAL. No workspace, no host copy: the call can
- * be captured (make the first call on a device outside a capture).
+ * a row too narrow, a free list too short, *used_in < 0 -- leaves the table as it
+ * was, writes -1 to cow_pairs (pairs that fanout_copy_pages does not copy), copies
+ * *used_in to *used_out and is reported by fanout_last_error() as FANOUT_EINVAL.
+ * No workspace, no host copy: the call can be captured (make the first call on a
+ * device outside a capture).
  */
 FANOUT_API int fanout_fork_device(const int32_t *prefix_pages, int32_t prefix_len,
+                int32_t num_branches, const int32_t *suffix_lens, int32_t page_size,
+                const int32_t *free_pages, int32_t n_free, const int32_t *used_in,
+                int32_t *used_out, int32_t *page_table, int32_t max_pages_per_branch,
+                int32_t *cow_pairs, fanout_stream_t stream);
+
+/*
+ * fanout_fork_device_new -- fanout_fork_device into memory that holds no table yet:
+ * a refused call writes -1 to every entry, so that no stale word is taken for a page.
+ */
+FANOUT_API int fanout_fork_device_new(const int32_t *prefix_pages, int32_t prefix_len,
                 int32_t num_branches, const int32_t *suffix_lens, int32_t page_size,
                 const int32_t *free_pages, int32_t n_free, const int32_t *used_in,
                 int32_t *used_out, int32_t *page_table, int32_t max_pages_per_branch,

@@ -40,6 +40,8 @@ ABI = {
                                            _vp, _vp]),
     "fanout_fork_device": (ctypes.c_int, [_vp, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp,
                                           _i32, _vp, _vp]),
+    "fanout_fork_device_new": (ctypes.c_int, [_vp, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp,
+                                              _vp, _i32, _vp, _vp]),
     "fanout_extend_device": (ctypes.c_int, [_vp, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _i32, _vp,
                                             _vp, _vp, _i64, _vp]),
     "fanout_kv_append_q4": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _i32, _i32, _i32,
@@ -218,7 +220,8 @@ def fork_device(prefix_pages, prefix_len: int, suffix_lens, page_size: int, free
     None: 0) counts the free-list entries already taken, the returned one those
     taken after this call. cow_pairs (int32 [B, 2]) is None when the prefix ends
     with its page or want_cow is false. What the lengths get wrong on the device
-    is reported by last_error() and leaves `out` as it was."""
+    is reported by last_error(); the call then hands out no page: cow_pairs and a
+    table allocated here are -1 throughout, a given `out` is left as it was."""
     import torch
     i32, dev = torch.int32, suffix_lens.device
     B = suffix_lens.numel()
@@ -231,7 +234,9 @@ def fork_device(prefix_pages, prefix_len: int, suffix_lens, page_size: int, free
         raise ValueError("prefix_pages holds fewer pages than the prefix")
     if used is not None:
         _need("used", used, i32, dev, (1,))
+    name = "fanout_fork_device"
     if out is None:
+        name = "fanout_fork_device_new"
         out = torch.empty((B, max_pages), dtype=i32, device=dev)
     else:
         _need("out", out, i32, dev, (B, max_pages))
@@ -239,7 +244,7 @@ def fork_device(prefix_pages, prefix_len: int, suffix_lens, page_size: int, free
     if want_cow and prefix_len % page_size:
         cow = torch.empty((B, 2), dtype=i32, device=dev)
     after = torch.empty((1,), dtype=i32, device=dev)
-    _device_call("fanout_fork_device", dev, stream, prefix_pages.data_ptr(), prefix_len, B,
+    _device_call(name, dev, stream, prefix_pages.data_ptr(), prefix_len, B,
                  suffix_lens.data_ptr(), page_size, free_pages.data_ptr(), free_pages.numel(),
                  _ptr_or_none(used), after.data_ptr(), out.data_ptr(), max_pages,
                  _ptr_or_none(cow))

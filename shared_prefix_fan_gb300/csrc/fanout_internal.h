@@ -117,6 +117,7 @@ struct TableParams {
     int64_t n_slots;
     int32_t num_branches, prefix_len, page_size, n_free, max_pages;
     int32_t extend;  // 0: a fork
+    int32_t clear;   // fork: 1: a refused call fills the table with -1, 0: leaves it
 };
 
 // Rows into the 4-bit pools and back (kv_q4.cu).

@@ -22,6 +22,48 @@ int launch_checked_tables(TableParams& p, fanout_stream_t stream) {
     return status_from_cuda(launch_tables(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// What the two fork calls share (clear: see TableParams).
+int fork_device(const int32_t* prefix_pages, int32_t prefix_len, int32_t num_branches,
+                const int32_t* suffix_lens, int32_t page_size, const int32_t* free_pages,
+                int32_t n_free, const int32_t* used_in, int32_t* used_out, int32_t* page_table,
+                int32_t max_pages_per_branch, int32_t* cow_pairs, int32_t clear,
+                fanout_stream_t stream) {
+    if (prefix_len < 0 || num_branches < 0 || page_size <= 0 || n_free < 0 ||
+        max_pages_per_branch < 0)
+        return FANOUT_EINVAL;
+    if (num_branches > kMaxTableBranches || max_pages_per_branch > kMaxTablePages)
+        return FANOUT_EUNSUPPORTED;
+    const int64_t n_prefix = (static_cast<int64_t>(prefix_len) + page_size - 1) / page_size;
+    if (num_branches > 0 && n_prefix > max_pages_per_branch) return FANOUT_EINVAL;
+    if (num_branches > 0 && (!suffix_lens || (n_prefix > 0 && !prefix_pages) ||
+                             (max_pages_per_branch > 0 && !page_table)))
+        return FANOUT_EINVAL;
+    if (n_free > 0 && !free_pages) return FANOUT_EINVAL;
+    if (used_out && used_out == used_in) return FANOUT_EINVAL;
+    for (const void* ptr : {static_cast<const void*>(prefix_pages),
+                            static_cast<const void*>(suffix_lens),
+                            static_cast<const void*>(free_pages),
+                            static_cast<const void*>(used_in), static_cast<const void*>(used_out),
+                            static_cast<const void*>(page_table),
+                            static_cast<const void*>(cow_pairs)})
+        if (!aligned(ptr, 4)) return FANOUT_EINVAL;
+    TableParams p{};
+    p.prefix_pages = prefix_pages;
+    p.suffix_lens = suffix_lens;
+    p.free_pages = free_pages;
+    p.used_in = used_in;
+    p.used_out = used_out;
+    p.page_table = page_table;
+    p.cow_pairs = cow_pairs;
+    p.num_branches = num_branches;
+    p.prefix_len = prefix_len;
+    p.page_size = page_size;
+    p.n_free = n_free;
+    p.max_pages = max_pages_per_branch;
+    p.clear = clear;
+    return launch_checked_tables(p, stream);
+}
+
 // What the two row calls check alike.
 int check_rows(const void* k_rows, const void* v_rows, const void* k_pages, const void* v_pages,
                const int64_t* slots, int32_t n_rows, int64_t k_stride, int64_t v_stride,
@@ -71,39 +113,19 @@ int fanout_fork_device(const int32_t* prefix_pages, int32_t prefix_len, int32_t 
                        int32_t n_free, const int32_t* used_in, int32_t* used_out,
                        int32_t* page_table, int32_t max_pages_per_branch, int32_t* cow_pairs,
                        fanout_stream_t stream) {
-    if (prefix_len < 0 || num_branches < 0 || page_size <= 0 || n_free < 0 ||
-        max_pages_per_branch < 0)
-        return FANOUT_EINVAL;
-    if (num_branches > kMaxTableBranches || max_pages_per_branch > kMaxTablePages)
-        return FANOUT_EUNSUPPORTED;
-    const int64_t n_prefix = (static_cast<int64_t>(prefix_len) + page_size - 1) / page_size;
-    if (num_branches > 0 && n_prefix > max_pages_per_branch) return FANOUT_EINVAL;
-    if (num_branches > 0 && (!suffix_lens || (n_prefix > 0 && !prefix_pages) ||
-                             (max_pages_per_branch > 0 && !page_table)))
-        return FANOUT_EINVAL;
-    if (n_free > 0 && !free_pages) return FANOUT_EINVAL;
-    if (used_out && used_out == used_in) return FANOUT_EINVAL;
-    for (const void* ptr : {static_cast<const void*>(prefix_pages),
-                            static_cast<const void*>(suffix_lens),
-                            static_cast<const void*>(free_pages),
-                            static_cast<const void*>(used_in), static_cast<const void*>(used_out),
-                            static_cast<const void*>(page_table),
-                            static_cast<const void*>(cow_pairs)})
-        if (!aligned(ptr, 4)) return FANOUT_EINVAL;
-    TableParams p{};
-    p.prefix_pages = prefix_pages;
-    p.suffix_lens = suffix_lens;
-    p.free_pages = free_pages;
-    p.used_in = used_in;
-    p.used_out = used_out;
-    p.page_table = page_table;
-    p.cow_pairs = cow_pairs;
-    p.num_branches = num_branches;
-    p.prefix_len = prefix_len;
-    p.page_size = page_size;
-    p.n_free = n_free;
-    p.max_pages = max_pages_per_branch;
-    return launch_checked_tables(p, stream);
+    return fork_device(prefix_pages, prefix_len, num_branches, suffix_lens, page_size, free_pages,
+                       n_free, used_in, used_out, page_table, max_pages_per_branch, cow_pairs, 0,
+                       stream);
+}
+
+int fanout_fork_device_new(const int32_t* prefix_pages, int32_t prefix_len, int32_t num_branches,
+                           const int32_t* suffix_lens, int32_t page_size,
+                           const int32_t* free_pages, int32_t n_free, const int32_t* used_in,
+                           int32_t* used_out, int32_t* page_table, int32_t max_pages_per_branch,
+                           int32_t* cow_pairs, fanout_stream_t stream) {
+    return fork_device(prefix_pages, prefix_len, num_branches, suffix_lens, page_size, free_pages,
+                       n_free, used_in, used_out, page_table, max_pages_per_branch, cow_pairs, 1,
+                       stream);
 }
 
 int fanout_extend_device(int32_t* page_table, int32_t num_branches, int32_t max_pages_per_branch,
