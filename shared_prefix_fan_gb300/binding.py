@@ -200,6 +200,27 @@ def _device_call(name: str, dev, stream, *args) -> None:
         raise FanoutError(rc, name)
 
 
+def _empty(shape, dtype, dev, stream):
+    """A call's result, for the work of its `stream` (None: dev's current one).
+
+    From another stream's pool than the one the call runs on, its block could still be
+    read or written there by work queued before it was freed, and a result that is
+    dropped early would be lent out again while the call has yet to write it. The
+    caller may use and drop it on the current stream: its reuse waits for that."""
+    import torch
+    if stream is not None:
+        handle, here = _stream_handle(stream), torch.cuda.current_stream(dev)
+        if handle != here.cuda_stream:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = (torch.cuda.ExternalStream(handle, device=dev) if handle > 1 else
+                          torch.cuda.default_stream(dev))  # 0 and 1 name the default stream
+            with torch.cuda.stream(stream):
+                t = torch.empty(shape, dtype=dtype, device=dev)
+            t.record_stream(here)
+            return t
+    return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _need(name: str, t, dtype, dev, shape=None) -> None:
     """A contiguous tensor of this type, on this CUDA device (and of this shape)."""
     if t.dtype is not dtype or t.device != dev or not t.is_cuda or not t.is_contiguous():
@@ -237,13 +258,13 @@ def fork_device(prefix_pages, prefix_len: int, suffix_lens, page_size: int, free
     name = "fanout_fork_device"
     if out is None:
         name = "fanout_fork_device_new"
-        out = torch.empty((B, max_pages), dtype=i32, device=dev)
+        out = _empty((B, max_pages), i32, dev, stream)
     else:
         _need("out", out, i32, dev, (B, max_pages))
     cow = None
     if want_cow and prefix_len % page_size:
-        cow = torch.empty((B, 2), dtype=i32, device=dev)
-    after = torch.empty((1,), dtype=i32, device=dev)
+        cow = _empty((B, 2), i32, dev, stream)
+    after = _empty((1,), i32, dev, stream)
     _device_call(name, dev, stream, prefix_pages.data_ptr(), prefix_len, B,
                  suffix_lens.data_ptr(), page_size, free_pages.data_ptr(), free_pages.numel(),
                  _ptr_or_none(used), after.data_ptr(), out.data_ptr(), max_pages,
@@ -267,10 +288,10 @@ def extend_device(page_table, prefix_len: int, suffix_lens, add_lens, page_size:
     if used is not None:
         _need("used", used, i32, dev, (1,))
     if slots is None:
-        slots = torch.empty((n_slots,), dtype=torch.int64, device=dev)
+        slots = _empty((n_slots,), torch.int64, dev, stream)
     else:
         _need("slots", slots, torch.int64, dev, (n_slots,))
-    after = torch.empty((1,), dtype=i32, device=dev)
+    after = _empty((1,), i32, dev, stream)
     _device_call("fanout_extend_device", dev, stream, page_table.data_ptr(), B, width, prefix_len,
                  suffix_lens.data_ptr(), add_lens.data_ptr(), page_size, free_pages.data_ptr(),
                  free_pages.numel(), _ptr_or_none(used), after.data_ptr(), slots.data_ptr(),
@@ -343,9 +364,9 @@ def kv_read_q4(k_pages, v_pages, slots, page_size: int, k_scale: float = 1.0,
     num_pages, h_kv = _q4_pools(k_pages, v_pages, page_size, dev)
     _need("slots", slots, torch.int64, dev, (n,))
     if k_out is None:
-        k_out = torch.empty((n, h_kv, 128), dtype=torch.bfloat16, device=dev)
+        k_out = _empty((n, h_kv, 128), torch.bfloat16, dev, stream)
     if v_out is None:
-        v_out = torch.empty((n, h_kv, 128), dtype=torch.bfloat16, device=dev)
+        v_out = _empty((n, h_kv, 128), torch.bfloat16, dev, stream)
     ks, vs = _rows_of("k_out", k_out, n, h_kv, dev), _rows_of("v_out", v_out, n, h_kv, dev)
     d = k_out.shape[2]
     if v_out.shape[2] != d:
@@ -444,9 +465,9 @@ def attn(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens: Sequence
         raise ValueError("k_pages / v_pages must be [num_pages, H_kv, page, d]")
     odt = {"f32": (torch.float32, OUT_F32), "bf16": (torch.bfloat16, OUT_BF16)}[out_dtype]
     if out is None:
-        out = torch.empty((R, h_q, d), dtype=odt[0], device=dev)
+        out = _empty((R, h_q, d), odt[0], dev, stream)
     if lse is None and want_lse:
-        lse = torch.empty((R, h_q), dtype=torch.float32, device=dev)
+        lse = _empty((R, h_q), torch.float32, dev, stream)
     if out.dtype != odt[0] or not out.is_contiguous():
         raise ValueError("out dtype/layout mismatch")
     rc = lib.fanout_attn(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
@@ -475,7 +496,8 @@ def _lens(suffix_lens, q_rows):
     return both, both.ctypes.data, both.shape[1], int(both[1].sum())
 
 
-def _attn_out(q, page_table, R: int, B: int, h_q: int, out, lse, out_dtype: str, want_lse: bool):
+def _attn_out(q, page_table, R: int, B: int, h_q: int, out, lse, out_dtype: str, want_lse: bool,
+              stream):
     """Checks and outputs the two calls below share: (out dtype code, out, lse)."""
     import torch
     dev, d = q.device, q.shape[-1]
@@ -488,13 +510,13 @@ def _attn_out(q, page_table, R: int, B: int, h_q: int, out, lse, out_dtype: str,
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [num_branches, max_pages]")
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
+        out = _empty(shape, dt, dev, stream)
     else:
         _need("out", out, dt, dev, shape)
     if lse is not None:
         _need("lse", lse, torch.float32, dev, (R, h_q))
     elif want_lse:
-        lse = torch.empty((R, h_q), dtype=torch.float32, device=dev)
+        lse = _empty((R, h_q), torch.float32, dev, stream)
     return code, out, lse
 
 
@@ -506,7 +528,8 @@ def attn_window(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q
     import torch
     window, sinks = min(window, _I32_MAX), min(sinks, _I32_MAX)
     held, lens, B, R = _lens(suffix_lens, q_rows)
-    code, out, lse = _attn_out(q, page_table, R, B, h_q, out, lse, out_dtype, want_lse)
+    code, out, lse = _attn_out(q, page_table, R, B, h_q, out, lse, out_dtype, want_lse,
+                               stream)
     dev, d = q.device, q.shape[-1]
     num_pages = k_pages.shape[0]
     pool = (num_pages, h_kv, page_size, d)
@@ -527,7 +550,8 @@ def attn_q4(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q_row
     sinks as in attn_window (0, 0: none)."""
     window, sinks = min(window, _I32_MAX), min(sinks, _I32_MAX)
     held, lens, B, R = _lens(suffix_lens, q_rows)
-    code, out, lse = _attn_out(q, page_table, R, B, h_q, out, lse, out_dtype, want_lse)
+    code, out, lse = _attn_out(q, page_table, R, B, h_q, out, lse, out_dtype, want_lse,
+                               stream)
     dev = q.device
     num_pages, heads = _q4_pools(k_pages, v_pages, page_size, dev)
     if heads != h_kv:
@@ -568,9 +592,9 @@ def lse_merge(part_o, part_ml, out=None, lse=None, out_dtype: str = "f32", strea
     n_parts, n_out, d = (int(x) for x in part_o.shape)
     odt = {"f32": (torch.float32, OUT_F32), "bf16": (torch.bfloat16, OUT_BF16)}[out_dtype]
     if out is None:
-        out = torch.empty((n_out, d), dtype=odt[0], device=part_o.device)
+        out = _empty((n_out, d), odt[0], part_o.device, stream)
     if lse is None:
-        lse = torch.empty((n_out,), dtype=torch.float32, device=part_o.device)
+        lse = _empty((n_out,), torch.float32, part_o.device, stream)
     _check(load().fanout_lse_merge(part_o.data_ptr(), part_ml.data_ptr(), n_parts, n_out, d,
                                    out.data_ptr(), odt[1], lse.data_ptr(), _stream_handle(stream)),
            "fanout_lse_merge")
