@@ -65,6 +65,10 @@ constexpr double kMergeLaunch = 4.0;   // the extra merge launch, in tile times
 inline int32_t piece_pos(const Range& r, bool first) { return r.rows && !first ? 0 : r.pos_base; }
 inline int32_t piece_begin(const Range& r, int32_t k_lo) { return k_lo == r.lo ? k_lo + r.front : k_lo; }
 
+// Tiles of a range's first keys, which go with the piece at its tile t_lo = 0: every
+// candidate counts them as that piece's work.
+inline int64_t lead_tiles(const Range& r, int64_t t_lo) { return t_lo == 0 ? r.first_tiles : 0; }
+
 struct Cand {
     std::vector<Unit> units;   // in assignment order
     std::vector<int64_t> work;
@@ -93,7 +97,7 @@ void make_candidate(const std::vector<Range>& ranges, int64_t chunk, int32_t for
             const int64_t t_lo = ch * nkt / nch, t_hi = (ch + 1) * nkt / nch;
             const int32_t k_lo = r.lo + static_cast<int32_t>(t_lo) * kBN;
             const int32_t k_hi = std::min<int32_t>(r.hi, r.lo + static_cast<int32_t>(t_hi) * kBN);
-            all.push_back({t_hi - t_lo + (ch == 0 ? r.first_tiles : 0),
+            all.push_back({t_hi - t_lo + lead_tiles(r, t_lo),
                            Unit{r.kv_head, r.branch, r.tok_begin, r.n_tok, piece_begin(r, k_lo), k_hi,
                                 piece_pos(r, ch == 0), 0},
                            r.complete && nch == 1, static_cast<int32_t>(ri)});
@@ -142,7 +146,7 @@ double candidate_cost_bound(const std::vector<Range>& ranges, int64_t chunk, int
         int64_t nch = chunk > 0 ? cdiv(nkt, chunk) : 1;
         nch = std::max<int64_t>(1, std::min(nch, nkt));
         for (int64_t ch = 0; ch < nch; ++ch)
-            max_w = std::max(max_w, (ch + 1) * nkt / nch - ch * nkt / nch);
+            max_w = std::max(max_w, (ch + 1) * nkt / nch - ch * nkt / nch + lead_tiles(r, ch));
         total += nkt + r.first_tiles;
         n += nch;
         if (!(r.complete && nch == 1)) n_parts += nch;
@@ -159,7 +163,7 @@ double candidate_cost_bound(const std::vector<Range>& ranges, int64_t chunk, int
 // range and the next CTA continues it.
 void make_streamk(const std::vector<Range>& ranges, int32_t max_cta, double unit_ovh, Cand& c) {
     int64_t total = 0;
-    for (const Range& r : ranges) total += cdiv(r.hi - r.lo, kBN);
+    for (const Range& r : ranges) total += cdiv(r.hi - r.lo, kBN) + r.first_tiles;
     const int32_t n_cta = static_cast<int32_t>(std::min<int64_t>(max_cta, total));
     // per-CTA quota in tile times, counting one unit overhead per range and per
     // cut (about one cut per CTA)
@@ -177,7 +181,8 @@ void make_streamk(const std::vector<Range>& ranges, int32_t max_cta, double unit
         const int64_t nkt = cdiv(r.hi - r.lo, kBN);
         int64_t t = 0;
         while (t < nkt) {
-            const double room = quota - load[cta] - unit_ovh;
+            const int64_t lead = lead_tiles(r, t);
+            const double room = quota - load[cta] - unit_ovh - static_cast<double>(lead);
             if (room < 0.5 && load[cta] > 0 && cta + 1 < n_cta) {
                 ++cta;
                 continue;
@@ -191,10 +196,10 @@ void make_streamk(const std::vector<Range>& ranges, int32_t max_cta, double unit
             c.units.push_back(Unit{r.kv_head, r.branch, r.tok_begin, r.n_tok, piece_begin(r, k_lo), k_hi,
                                    piece_pos(r, t == 0), whole ? -1 : 0});
             if (!whole) ++n_parts;
-            c.work.push_back(take);
+            c.work.push_back(take + lead);
             c.cta_of.push_back(cta);
             c.range_of.push_back(static_cast<int32_t>(ri));
-            load[cta] += static_cast<double>(take) + unit_ovh;
+            load[cta] += static_cast<double>(take + lead) + unit_ovh;
             t += take;
         }
     }
@@ -212,7 +217,7 @@ void make_streamk(const std::vector<Range>& ranges, int32_t max_cta, double unit
 // only the cut pieces become partials.
 void make_lpt_cut(const std::vector<Range>& ranges, int32_t max_cta, double unit_ovh, Cand& c) {
     struct Piece {
-        int64_t work;
+        int64_t work;  // its tiles, those of the range's first keys among them
         int32_t range;
         int64_t t_lo;  // first tile of the piece within its range
         // the queue's order after the size: first key, KV head, branch, token
@@ -222,7 +227,7 @@ void make_lpt_cut(const std::vector<Range>& ranges, int32_t max_cta, double unit
     std::vector<int64_t> nkt(ranges.size());
     for (size_t i = 0; i < ranges.size(); ++i) {
         nkt[i] = cdiv(ranges[i].hi - ranges[i].lo, kBN);
-        total += nkt[i];
+        total += nkt[i] + ranges[i].first_tiles;
     }
     const int32_t n_cta = static_cast<int32_t>(std::min<int64_t>(max_cta, total));
     const double target = (static_cast<double>(total) +
@@ -231,9 +236,9 @@ void make_lpt_cut(const std::vector<Range>& ranges, int32_t max_cta, double unit
         return std::make_tuple(-b.work, b.k_lo, b.kv_head, b.branch, b.tok_begin) <
                std::make_tuple(-a.work, a.k_lo, a.kv_head, a.branch, a.tok_begin);
     };
-    auto piece = [&](int64_t work, int32_t ri, int64_t t_lo) {
+    auto piece = [&](int64_t tiles, int32_t ri, int64_t t_lo) {
         const Range& r = ranges[ri];
-        return Piece{work, ri, t_lo, r.lo + static_cast<int32_t>(t_lo) * kBN, r.kv_head, r.branch,
+        return Piece{tiles + lead_tiles(r, t_lo), ri, t_lo, r.lo + static_cast<int32_t>(t_lo) * kBN, r.kv_head, r.branch,
                      r.tok_begin};
     };
     std::priority_queue<Piece, std::vector<Piece>, decltype(later)> queue(later);
@@ -254,23 +259,24 @@ void make_lpt_cut(const std::vector<Range>& ranges, int32_t max_cta, double unit
         queue.pop();
         Slot s = heap.top();
         heap.pop();
-        int64_t take = pc.work;
-        const double room = target - s.first - unit_ovh;
+        const Range& r = ranges[pc.range];
+        const int64_t lead = lead_tiles(r, pc.t_lo), tiles = pc.work - lead;
+        int64_t take = tiles;
+        const double room = target - s.first - unit_ovh - static_cast<double>(lead);
         if (s.first + unit_ovh + static_cast<double>(pc.work) > target + 0.5 && room >= 1.0 &&
-            pc.work >= 2) {
-            take = std::min<int64_t>(pc.work - 1, static_cast<int64_t>(room));
-            queue.push(piece(pc.work - take, pc.range, pc.t_lo + take));
+            tiles >= 2) {
+            take = std::min<int64_t>(tiles - 1, static_cast<int64_t>(room));
+            queue.push(piece(tiles - take, pc.range, pc.t_lo + take));
             cut[pc.range] = true;
         }
-        const Range& r = ranges[pc.range];
         const int32_t k_lo = r.lo + static_cast<int32_t>(pc.t_lo) * kBN;
         const int32_t k_hi = std::min<int32_t>(r.hi, r.lo + static_cast<int32_t>(pc.t_lo + take) * kBN);
         c.units.push_back(Unit{r.kv_head, r.branch, r.tok_begin, r.n_tok, piece_begin(r, k_lo), k_hi,
                                piece_pos(r, pc.t_lo == 0), 0});
-        c.work.push_back(take);
+        c.work.push_back(take + lead);
         c.cta_of.push_back(s.second);
         range_of.push_back(pc.range);
-        s.first += static_cast<double>(take) + unit_ovh;
+        s.first += static_cast<double>(take + lead) + unit_ovh;
         makespan = std::max(makespan, s.first);
         heap.push(s);
     }
@@ -498,7 +504,7 @@ int build_plan(const PlanInput& in, Plan& plan) {
         if (in.rows) {  // no more than what the ranges read
             int64_t read = 0;
             for (const Range& r : ranges)
-                if (r.kv_head == 0) read += r.hi - r.lo;
+                if (r.kv_head == 0) read += r.hi - r.lo + r.first_tiles * kBN;
             kv_tokens = std::min(kv_tokens, read);
         }
         const int64_t kv_bytes = kv_tokens * in.H_kv * in.row_bytes;
