@@ -201,7 +201,7 @@ struct Tiles {
           begin(range_begin(u, p.page_size)),
           end(u.key_end),
           key_begin(u.key_begin),
-          n(n_first + (end - begin + kBN - 1) / kBN) {}
+          n(n_first + range_tiles(u, p.page_size)) {}
     // first key, one past the last key, first key that some row sees
     __device__ __forceinline__ void tile(int j, int& kt, int& last, int& front) const {
         const bool f = j < n_first;

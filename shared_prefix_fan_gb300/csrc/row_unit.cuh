@@ -1,6 +1,6 @@
-// row_unit.cuh -- what the attention kernels share about units of a row plan
-// (windowed or 4-bit attention): the first keys a unit sweeps in front of its
-// own range, and the check of a page id before it is read through.
+// row_unit.cuh -- a unit of a row plan (windowed or 4-bit attention) as attn_rows.cu
+// reads it: the first keys it sweeps in front of its own range, where that range's
+// tiles begin, and the check of a page id before it is read through.
 #pragma once
 
 #include "fanout_internal.h"
