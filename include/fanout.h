@@ -408,7 +408,8 @@ enum fanout_option {
     FANOUT_OPT_SPLITS = 1,          /* >0: cut every key range into this many chunks; 0 = cost model */
     FANOUT_OPT_VALIDATE_TABLE = 2,  /* 1: check page-table entries on the host each call (with a
                                        window: those of pages that a row of the call sees) */
-    FANOUT_OPT_WAIT_LIMIT_NS = 3,   /* bound of every device-side wait (default 1e9 ns) */
+    FANOUT_OPT_WAIT_LIMIT_NS = 3,   /* bound of every device-side wait (default 1e9 ns; less than
+                                       1e6 counts as that) */
     FANOUT_OPT_NUM_SMS = 4,         /* >0: plan for this many SMs instead of the device's */
     FANOUT_OPT_FUSED_MERGE = 5      /* 0 (default): the log-sum-exp merge is a separate kernel,
                                        a programmatic dependent of the attention kernel; 1: it

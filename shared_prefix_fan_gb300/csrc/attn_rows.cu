@@ -88,6 +88,7 @@ constexpr int kRawBytes = kBN * kQ4RowBytes;
 constexpr float kRescaleLog2 = 8.0f;  // lazy rescale threshold (base-2 units)
 constexpr int kErrTimeout = 5;        // FANOUT_ETIMEOUT
 constexpr int kErrCuda = 3;           // FANOUT_ECUDA
+constexpr uint64_t kLingerNs = 1000000;  // a CTA's stay after a wait has given up
 constexpr int kGroupWarps = 4;
 constexpr int kWarpQ = 2;        // first warp of the Q conversion
 constexpr int kQWarps = 2;
@@ -1129,6 +1130,10 @@ __global__ void __launch_bounds__(Cfg<NQ, Q4>::kThreads, 1)
 
     ptx::tc_fence_before();
     __syncthreads();
+    // A role that gave up drained what it had in flight itself, as far as it could; one that
+    // had ended before it could not. Copies and products take microseconds to land.
+    if (*sm.abort_flag() != 0)
+        for (const uint64_t t0 = ptx::globaltimer_ns(); ptx::globaltimer_ns() - t0 < kLingerNs;) {}
     if (warp == 1) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, kTmemCols);

@@ -208,7 +208,8 @@ int launch_plan(const CallArgs& a, const Plan& pl, const Layout& L, uint8_t* bas
     p.k_pool = static_cast<const uint8_t*>(a.k);
     p.v_pool = static_cast<const uint8_t*>(a.v);
     p.o_scale = a.v_scale;
-    p.wait_limit_ns = a.wait_limit_ns;
+    // No shorter than copies in flight may take to land: attn_fwd.cu bounds its drain by it too.
+    p.wait_limit_ns = std::max(a.wait_limit_ns, 1000000ull);
     MergeParams& m = p.merge;
     m.part_o = p.part_o;
     m.part_ml = p.part_ml;
