@@ -1161,6 +1161,14 @@ cudaError_t launch_nq(const SplitParams& p, const CUtensorMap& tm_q, const CUten
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      Cfg<NQ, Q4>::kSmemAlloc);
             if (e != cudaSuccess) return e;
+            if (Q4) {
+                // The split asks for what the block was launched with: with fewer registers
+                // than it counts on, the softmax warps would wait for more without an end.
+                cudaFuncAttributes fa;
+                e = cudaFuncGetAttributes(&fa, attn_rows_kernel<NQ, Q4>);
+                if (e != cudaSuccess) return e;
+                if (fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+            }
             if (known) attr_set[dev].store(true, std::memory_order_release);
         }
     }
