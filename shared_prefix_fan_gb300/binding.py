@@ -381,6 +381,8 @@ def copy_pages_q4(k_pages, v_pages, pairs, page_size: int, stream=None) -> None:
     """Copy whole pages of 4-bit pools for page pairs (int32 [n, 2] on the device):
     the copy-on-write step of a fork whose prefix ends inside a page."""
     import torch
+    if page_size % 2:
+        raise ValueError("page_size of a 4-bit pool is 16, 32, 64 or 128")
     dev = k_pages.device
     num_pages, h_kv = _q4_pools(k_pages, v_pages, page_size, dev)
     _need("pairs", pairs, torch.int32, dev, (pairs.shape[0], 2))
