@@ -200,6 +200,15 @@ def _device_call(name: str, dev, stream, *args) -> None:
         raise FanoutError(rc, name)
 
 
+_I32_MAX = 2 ** 31 - 1  # ctypes would take the low 32 bits of more
+
+
+def _fit32(name: str, *values: int) -> None:
+    for v in values:
+        if not -_I32_MAX - 1 <= v <= _I32_MAX:
+            raise ValueError(f"{name}: {v} does not fit 32 bits")
+
+
 def _empty(shape, dtype, dev, stream):
     """A call's result, for the work of its `stream` (None: dev's current one).
 
@@ -248,6 +257,7 @@ def fork_device(prefix_pages, prefix_len: int, suffix_lens, page_size: int, free
     B = suffix_lens.numel()
     if page_size <= 0:
         raise ValueError("page_size must be positive")
+    _fit32("fork_device", prefix_len, page_size, max_pages)
     _need("suffix_lens", suffix_lens, i32, dev, (B,))
     _need("prefix_pages", prefix_pages, i32, dev)
     _need("free_pages", free_pages, i32, dev)
@@ -281,6 +291,7 @@ def extend_device(page_table, prefix_len: int, suffix_lens, add_lens, page_size:
     import torch
     i32, dev = torch.int32, page_table.device
     B, width = page_table.shape
+    _fit32("extend_device", prefix_len, page_size)
     _need("page_table", page_table, i32, dev)
     _need("suffix_lens", suffix_lens, i32, dev, (B,))
     _need("add_lens", add_lens, i32, dev, (B,))
@@ -482,9 +493,6 @@ def attn(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens: Sequence
     return out, lse
 
 
-_I32_MAX = 2 ** 31 - 1  # ctypes would take the low 32 bits of more
-
-
 def _lens(suffix_lens, q_rows):
     """Host lengths of a call as one int32 array [2, B]: (array, address, B, rows)."""
     if len(suffix_lens) != len(q_rows):
@@ -492,9 +500,12 @@ def _lens(suffix_lens, q_rows):
     if type(suffix_lens) is list and type(q_rows) is list:
         ints = array("i", suffix_lens + q_rows)
         return ints, ints.buffer_info()[0], len(q_rows), sum(q_rows)
-    both = np.array((suffix_lens, q_rows), dtype=np.int32)
-    if both.ndim != 2:
+    wide = np.array((suffix_lens, q_rows), dtype=np.int64)
+    if wide.ndim != 2:
         raise ValueError("suffix_lens and q_rows must be sequences of integers")
+    both = wide.astype(np.int32)
+    if (both != wide).any():
+        raise ValueError("suffix_lens / q_rows: a length does not fit 32 bits")
     return both, both.ctypes.data, both.shape[1], int(both[1].sum())
 
 
@@ -528,7 +539,8 @@ def attn_window(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q
     """attn(), causal, where a row at pos sees keys j <= pos with j > pos - window
     or j < sinks. Pages that no row sees may have been given back."""
     import torch
-    window, sinks = min(window, _I32_MAX), min(sinks, _I32_MAX)
+    window, sinks = max(-1, min(window, _I32_MAX)), max(-1, min(sinks, _I32_MAX))
+    _fit32("prefix_len", prefix_len)
     held, lens, B, R = _lens(suffix_lens, q_rows)
     code, out, lse = _attn_out(q, page_table, R, B, h_q, out, lse, out_dtype, want_lse,
                                stream)
@@ -550,7 +562,8 @@ def attn_q4(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q_row
             out_dtype: str = "f32", want_lse: bool = True, stream=None):
     """attn() over 4-bit pools (uint8 [num_pages, H_kv, page_size * 72]); window and
     sinks as in attn_window (0, 0: none)."""
-    window, sinks = min(window, _I32_MAX), min(sinks, _I32_MAX)
+    window, sinks = max(-1, min(window, _I32_MAX)), max(-1, min(sinks, _I32_MAX))
+    _fit32("prefix_len", prefix_len)
     held, lens, B, R = _lens(suffix_lens, q_rows)
     code, out, lse = _attn_out(q, page_table, R, B, h_q, out, lse, out_dtype, want_lse,
                                stream)

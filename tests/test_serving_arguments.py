@@ -13,3 +13,63 @@ def test_copy_pages_q4_refuses_pages_it_would_copy_in_part(page):
     pool = torch.zeros((2, 1, page * 72), dtype=torch.uint8)
     with pytest.raises(ValueError, match="page_size"):
         binding.copy_pages_q4(pool, pool, torch.zeros((1, 2), dtype=torch.int32), page)
+
+
+class Pointer:
+    """What a call would have handed to the library."""
+
+    def __init__(self, monkeypatch):
+        self.calls = []
+        monkeypatch.setattr(binding, "_device_call", lambda *a: self.calls.append(a))
+        monkeypatch.setattr(binding, "_need", lambda *a, **k: None)
+        monkeypatch.setattr(binding, "_q4_pools", lambda k, v, page, dev: (4, 1))
+
+
+BIG = (2 ** 31, 2 ** 32 + 16, -2 ** 31 - 1)
+
+
+@pytest.mark.parametrize("big", BIG)
+def test_integers_past_32_bits_are_refused(monkeypatch, big):
+    """ctypes hands their low 32 bits over: 2^32 + 16 would be 16 tokens."""
+    p = Pointer(monkeypatch)
+    i = torch.zeros(2, dtype=torch.int32)
+    q = torch.zeros((2, 1, 128), dtype=torch.bfloat16)
+    pool = torch.zeros((4, 1, 16, 128), dtype=torch.bfloat16)
+    table = torch.zeros((1, 4), dtype=torch.int32)
+    long = torch.zeros(1, dtype=torch.int32).expand(2 ** 33)  # a prefix list of any length
+    for f in (lambda: binding.fork_device(long, big, i, 16, i, 4),
+              lambda: binding.fork_device(long, 16, i, big if big > 0 else 2 ** 31, i, 4),
+              lambda: binding.fork_device(long, 0, i[:0], 16, i, abs(big), out=table),
+              lambda: binding.extend_device(table, big, i[:1], i[:1], 16, i, 2),
+              lambda: binding.extend_device(table, 16, i[:1], i[:1], big, i, 2),
+              lambda: binding.attn_window(q, pool, pool, table, big, [4], [2], 1, 1, 16, 1.0, 4),
+              lambda: binding.attn_q4(q, pool, pool, table, big, [4], [2], 1, 1, 16, 1.0, True)):
+        with pytest.raises((ValueError, OverflowError), match="32 bits"):
+            f()
+    assert not p.calls
+
+
+@pytest.mark.parametrize("kind", ["numpy", "tensor", "list"])
+def test_lengths_past_32_bits_are_refused(kind):
+    import numpy as np
+    wrap = {"numpy": lambda x: np.array(x, dtype=np.int64), "tensor": torch.tensor,
+            "list": list}[kind]
+    for S, T in (([2 ** 32 + 5], [1]), ([5], [2 ** 32 + 1]), ([-2 ** 31 - 1], [1])):
+        with pytest.raises((ValueError, OverflowError)):
+            binding._lens(wrap(S), wrap(T))
+    held, at, B, R = binding._lens(wrap([5, 6]), wrap([1, 2]))
+    assert (B, R) == (2, 3) and list(np.frombuffer(held, np.int32)) == [5, 6, 1, 2] and at
+
+
+@pytest.mark.parametrize("window,sinks", [(-2 ** 32 + 5, 0), (-1, 0), (4, -2 ** 32 + 1)])
+def test_negative_windows_stay_negative(monkeypatch, window, sinks):
+    """The library refuses them: they must reach it as what they are."""
+    p = Pointer(monkeypatch)
+    q = torch.zeros((2, 1, 128), dtype=torch.bfloat16)
+    pool = torch.zeros((4, 1, 16, 128), dtype=torch.bfloat16)
+    table = torch.zeros((1, 4), dtype=torch.int32)
+    binding.attn_window(q, pool, pool, table, 16, [4], [2], 1, 1, 16, 1.0, window, sinks)
+    binding.attn_q4(q, pool, pool, table, 16, [4], [2], 1, 1, 16, 1.0, True, 1.0, 1.0, window, sinks)
+    for args in p.calls:
+        ints = [a for a in args if isinstance(a, int) and a < 0]
+        assert len(ints) == (window < 0) + (sinks < 0) and all(a >= -2 ** 31 for a in ints)
