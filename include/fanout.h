@@ -156,7 +156,9 @@ FANOUT_API int fanout_extend(int32_t *page_table, int32_t num_branches,
  *                 call does the same again.
  *   page_table    dev int32 [B][max_pages_per_branch], every entry written: the
  *                 whole prefix pages, the branch's own pages (the copy of a
- *                 partial prefix page first), then -1.
+ *                 partial prefix page first), then -1. No array that is read may
+ *                 share a byte with one that is written (FANOUT_EINVAL), but for a
+ *                 row of page_table whose whole prefix pages are the prefix.
  *   cow_pairs     dev int32 [B][2] or NULL: as fanout_fork_cow, written when
  *                 prefix_len is not a multiple of page_size.
  * What only the device can see -- a negative suffix, more than 2^31 - 1 tokens,
@@ -190,7 +192,7 @@ FANOUT_API int fanout_fork_device_new(const int32_t *prefix_pages, int32_t prefi
  * for row r = token t of branch b (rows grouped by branch) at pos = prefix_len +
  * suffix_lens[b] + t: where fanout_kv_append_q4 puts the row.
  *   page_table    dev int32 [B][max_pages_per_branch], updated in place: only
- *                 the new entries are written.
+ *                 the new entries are written. Arrays apart as in fanout_fork_device.
  *   suffix_lens, add_lens  dev int32 [B], B <= 4096; suffix_lens BEFORE the growth.
  *   slots         dev int64 [n_slots], 8-byte aligned; NULL with n_slots == 0:
  *                 no map wanted. Rows behind the last token get -1 (a padded

@@ -2,7 +2,7 @@
 // 4-bit rows: argument checks and launches (kernels in tables.cu, kv_q4.cu).
 #include <cuda_runtime.h>
 
-#include <cmath>
+#include <cstddef>
 #include <cstdint>
 
 #include "../../include/fanout.h"
@@ -15,6 +15,25 @@ namespace {
 int status_from_cuda(cudaError_t e) { return e == cudaSuccess ? FANOUT_OK : FANOUT_ECUDA; }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Whether two arrays share a byte. What a table call reads must not be what it writes:
+// its blocks do not wait for one another.
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && a_bytes > 0 && b_bytes > 0 && x < y + static_cast<uint64_t>(b_bytes) &&
+           y < x + static_cast<uint64_t>(a_bytes);
+}
+struct Array {
+    const void* at;
+    int64_t bytes;
+};
+template <size_t N, size_t M>
+bool any_overlap(const Array (&read)[N], const Array (&written)[M]) {
+    for (const Array& r : read)
+        for (const Array& w : written)
+            if (overlap(r.at, r.bytes, w.at, w.bytes)) return true;
+    return false;
+}
 
 int launch_checked_tables(TableParams& p, fanout_stream_t stream) {
     const cudaError_t ce = err_word_ptr(&p.err);
@@ -47,6 +66,20 @@ int fork_device(const int32_t* prefix_pages, int32_t prefix_len, int32_t num_bra
                             static_cast<const void*>(page_table),
                             static_cast<const void*>(cow_pairs)})
         if (!aligned(ptr, 4)) return FANOUT_EINVAL;
+    const int64_t table_bytes = 4LL * num_branches * max_pages_per_branch;
+    const int64_t n_full = prefix_len / page_size;
+    // The whole prefix pages may be those of a row of the table itself: it is given its
+    // own entries.
+    const int64_t into = reinterpret_cast<intptr_t>(prefix_pages) - reinterpret_cast<intptr_t>(page_table);
+    const bool own_row = max_pages_per_branch > 0 && into >= 0 && into < table_bytes &&
+                         into % (4LL * max_pages_per_branch) == 0;
+    const Array read[] = {{prefix_pages, own_row ? 0 : 4 * n_full},
+                          {n_full < n_prefix && cow_pairs ? prefix_pages + n_full : nullptr, 4},
+                          {suffix_lens, 4LL * num_branches},
+                          {free_pages, 4LL * n_free},
+                          {used_in, 4}};
+    const Array written[] = {{page_table, table_bytes}, {cow_pairs, 8LL * num_branches}, {used_out, 4}};
+    if (any_overlap(read, written)) return FANOUT_EINVAL;
     TableParams p{};
     p.prefix_pages = prefix_pages;
     p.suffix_lens = suffix_lens;
@@ -151,6 +184,14 @@ int fanout_extend_device(int32_t* page_table, int32_t num_branches, int32_t max_
                             static_cast<const void*>(used_out)})
         if (!aligned(ptr, 4)) return FANOUT_EINVAL;
     if (!aligned(slots, 8)) return FANOUT_EINVAL;
+    const int64_t table_bytes = 4LL * num_branches * max_pages_per_branch;
+    const Array read[] = {{suffix_lens, 4LL * num_branches},
+                          {add_lens, 4LL * num_branches},
+                          {free_pages, 4LL * n_free},
+                          {used_in, 4}};
+    const Array written[] = {{page_table, table_bytes}, {slots, 8 * n_slots}, {used_out, 4}};
+    if (any_overlap(read, written) || overlap(slots, 8 * n_slots, page_table, table_bytes))
+        return FANOUT_EINVAL;
     TableParams p{};
     p.extend = 1;
     p.suffix_lens = suffix_lens;

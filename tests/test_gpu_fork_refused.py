@@ -67,3 +67,19 @@ def test_refused_fork_without_pairs():
                                             dev(list(range(10, 20))), 8, want_cow=want)
         assert cow is None and (table == -1).all()
         assert binding.last_error() == binding.EINVAL
+
+
+def test_prefix_from_a_row_of_the_table():
+    """The whole prefix pages of a branch as the prefix of a new fork into the same table;
+    a page that the fork replaces in that row is not taken from it."""
+    table = torch.full((3, 9), 5, dtype=torch.int32, device="cuda")
+    table[1, :2] = dev([8, 9])
+    S, free = dev([20, 0, 33]), dev(list(range(20, 40)))
+    want, _, used = binding.fork_device(dev([8, 9]), 32, S, 16, free, 9)
+    out, cow, after = binding.fork_device(table[1, :2], 32, S, 16, free, 9, out=table)
+    assert cow is None and torch.equal(out, want) and int(after) == int(used)
+    before = table.clone()
+    with pytest.raises(binding.FanoutError) as e:
+        binding.fork_device(table[1, :3], 40, S, 16, free, 9, out=table)
+    assert e.value.code == binding.EINVAL and torch.equal(table, before)
+    assert binding.last_error() == binding.OK

@@ -73,3 +73,66 @@ def test_negative_windows_stay_negative(monkeypatch, window, sinks):
     for args in p.calls:
         ints = [a for a in args if isinstance(a, int) and a < 0]
         assert len(ints) == (window < 0) + (sinks < 0) and all(a >= -2 ** 31 for a in ints)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from shared_prefix_fan_gb300 import build
+    build.build()
+    return binding.load()
+
+
+# made-up addresses, every array apart from the others
+FORK = dict(prefix=0x10000, P=40, B=2, S=0x20000, ps=16, free=0x30000, n_free=9, used=0x40000,
+            after=0x50000, table=0x60000, width=8, cow=0x70000, stream=None)
+EXTEND = dict(table=0x10000, B=2, width=8, P=40, S=0x20000, A=0x30000, ps=16, free=0x40000, n_free=9,
+              used=0x50000, after=0x60000, slots=0x70000, n_slots=4, stream=None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(prefix=0x60000 + 4), dict(prefix=0x60000 + 24),  # into a row, and over its last entries
+    dict(prefix=0x60000), dict(prefix=0x60000 + 32),      # a row, whose partial page is replaced
+    dict(S=0x60000 + 60), dict(S=0x70000 + 12), dict(S=0x50000 - 4), dict(free=0x60000 - 32),
+    dict(free=0x70000), dict(used=0x60000 + 8), dict(prefix=0x70000 - 8), dict(prefix=0x50000 - 8)])
+@pytest.mark.parametrize("name", ["fanout_fork_device", "fanout_fork_device_new"])
+def test_fork_refuses_arrays_that_share_memory(lib, name, kw):
+    assert getattr(lib, name)(*{**FORK, **kw}.values()) == binding.EINVAL
+
+
+@pytest.mark.parametrize("kw", [
+    dict(S=0x10000), dict(A=0x10000 + 60), dict(free=0x10000 - 32), dict(used=0x10000 + 4),
+    dict(slots=0x10000 + 56), dict(slots=0x10000 - 24), dict(S=0x70000 + 28), dict(A=0x60000),
+    dict(free=0x60000 - 32), dict(S=0x60000 - 4)])
+def test_extend_refuses_arrays_that_share_memory(lib, kw):
+    assert lib.fanout_extend_device(*{**EXTEND, **kw}.values()) == binding.EINVAL
+
+
+E_, U_ = binding.EINVAL, binding.EUNSUPPORTED
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(P=-1), E_), (dict(B=-1), E_), (dict(ps=0), E_), (dict(n_free=-1), E_), (dict(width=-1), E_),
+    (dict(B=4097), U_), (dict(width=(1 << 24) + 1), U_), (dict(width=2), E_), (dict(S=None), E_),
+    (dict(prefix=None), E_), (dict(table=None), E_), (dict(free=None), E_), (dict(used=0x50000), E_),
+    (dict(table=0x60002), E_), (dict(cow=0x70001), E_), (dict(after=0x50003), E_)])
+def test_fork_refusals_with_arrays_apart(lib, kw, rc):
+    assert lib.fanout_fork_device(*{**FORK, **kw}.values()) == rc
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(P=-1), E_), (dict(B=-1), E_), (dict(ps=0), E_), (dict(n_free=-1), E_), (dict(width=-1), E_),
+    (dict(B=4097), U_), (dict(S=None), E_), (dict(A=None), E_), (dict(table=None), E_),
+    (dict(free=None), E_), (dict(slots=None), E_), (dict(n_slots=-1), E_), (dict(n_slots=1 << 31), E_),
+    (dict(used=0x60000), E_), (dict(slots=0x70004), E_), (dict(A=0x30002), E_)])
+def test_extend_refusals_with_arrays_apart(lib, kw, rc):
+    assert lib.fanout_extend_device(*{**EXTEND, **kw}.values()) == rc
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are made up")
+@pytest.mark.parametrize("kw", [
+    {}, dict(prefix=0x60000 + 32, P=48), dict(prefix=0x60000, P=48, cow=None),
+    dict(prefix=0x60000, cow=None), dict(S=0x50000 + 4), dict(used=None), dict(n_free=0, free=None),
+    dict(table=0x70000 - 64)])
+def test_arrays_apart_are_not_refused(lib, kw):
+    """(They fail later, for want of a device.)"""
+    assert lib.fanout_fork_device(*{**FORK, **kw}.values()) == binding.ECUDA
