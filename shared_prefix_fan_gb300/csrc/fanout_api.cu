@@ -107,6 +107,7 @@ int attn_call(AttnKind kind, const void* q, const void* k_pages, const void* v_p
     st = validate_call(q, k_pages, v_pages, page_table, suffix_lens, num_branches, prefix_len,
                        max_pages_per_branch, num_pages, page_size, scale, out_dtype, out);
     if (st != FANOUT_OK) return st;
+    if (reinterpret_cast<uintptr_t>(lse) & 3u) return FANOUT_EINVAL;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     if (rows) {
         // A captured call would replay a plan that later calls on the stream move.
@@ -410,7 +411,8 @@ int fanout_kv_append(const void* k_new, const void* v_new, void* k_pages, void* 
     p.row_off[num_branches] = static_cast<int32_t>(R);
     p.R = static_cast<int32_t>(R);
     if (!k_new || !v_new || !k_pages || !v_pages || !page_table) return FANOUT_EINVAL;
-    if (!ok_align16(k_new) || !ok_align16(v_new) || !ok_align16(k_pages) || !ok_align16(v_pages))
+    if (!ok_align16(k_new) || !ok_align16(v_new) || !ok_align16(k_pages) || !ok_align16(v_pages) ||
+        (reinterpret_cast<uintptr_t>(page_table) & 3u))
         return FANOUT_EINVAL;
     int32_t* err = nullptr;
     cudaError_t ce = err_word_ptr(&err);

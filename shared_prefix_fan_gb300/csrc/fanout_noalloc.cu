@@ -93,6 +93,7 @@ extern "C" FANOUT_API int fanout_attn_noalloc(
     st = validate_call(q, k_pages, v_pages, page_table, suffix_lens, num_branches, prefix_len,
                        max_pages_per_branch, num_pages, page_size, scale, out_dtype, out);
     if (st != FANOUT_OK) return st;
+    if (reinterpret_cast<uintptr_t>(lse) & 3u) return FANOUT_EINVAL;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     // The plan is copied to the array from host memory that lives only for this
     // call; a captured copy would read it after it is gone. Refused, nothing done.

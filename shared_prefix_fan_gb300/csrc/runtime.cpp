@@ -101,6 +101,7 @@ int validate_call(const void* q, const void* k, const void* v, const int32_t* pa
     if (!(scale > 0.0f) || scale > 3.0e38f) return FANOUT_EINVAL;  // positive, finite
     if (!q || !k || !v || !page_table || !out) return FANOUT_EINVAL;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return FANOUT_EINVAL;
+    if (reinterpret_cast<uintptr_t>(page_table) & 3u) return FANOUT_EINVAL;
     int64_t need_pages = 0;
     for (int32_t b = 0; b < B; ++b)
         need_pages = std::max<int64_t>(

@@ -136,3 +136,33 @@ def test_extend_refusals_with_arrays_apart(lib, kw, rc):
 def test_arrays_apart_are_not_refused(lib, kw):
     """(They fail later, for want of a device.)"""
     assert lib.fanout_fork_device(*{**FORK, **kw}.values()) == binding.ECUDA
+
+
+@pytest.mark.parametrize("name", ["fanout_attn", "fanout_attn_noalloc", "fanout_attn_window",
+                                  "fanout_attn_q4"])
+@pytest.mark.parametrize("kw", [dict(pt=1026), dict(pt=1025), dict(lse=4098), dict(lse=4097)])
+def test_attention_refuses_words_off_their_boundary(lib, name, kw):
+    """Read or written as 32-bit words on the device, where that would be a fault."""
+    import ctypes
+
+    import numpy as np
+    a = dict(q=1024, k=1024, v=1024, pt=1024, P=64, S=[32, 32], T=[2, 2], B=2, maxp=8, npages=16,
+             hq=8, hkv=2, d=128, ps=16, scale=0.088, causal=1, kg=1.0, vg=1.0, window=9, sinks=0,
+             out=1024, od=0, lse=None, stream=None)
+    a.update(kw)
+    held = [np.asarray(a[n], np.int32) for n in "ST"]
+    a["S"], a["T"] = (h.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)) for h in held)
+    drop = {"fanout_attn_q4": (), "fanout_attn_window": ("causal", "kg", "vg")}.get(
+        name, ("kg", "vg", "window", "sinks"))
+    args = [v for n, v in a.items() if n not in drop]
+    assert getattr(lib, name)(*args) == binding.EINVAL
+
+
+def test_append_refuses_a_table_off_its_boundary(lib):
+    import ctypes
+
+    import numpy as np
+    n = np.array([3, 2], np.int32)
+    at = n.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
+    assert lib.fanout_kv_append(1024, 1024, 1024, 1024, 1026, 0, at, at, 2, 4, 8, 2, 128, 16,
+                                None) == binding.EINVAL
