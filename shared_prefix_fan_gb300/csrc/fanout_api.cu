@@ -191,6 +191,9 @@ int attn_call(AttnKind kind, const void* q, const void* k_pages, const void* v_p
         std::equal(key.begin(), key.begin() + fixed, ws->key.begin()) &&
         std::equal(key.begin() + fixed + num_branches, key.end(),
                    ws->key.begin() + fixed + num_branches)) {
+        // (not ready while it moves: an allocation that fails half way must not leave a plan
+        // whose host and device sides differ)
+        ws->plan_ready = false;
         if (patch_plan(in, ws->plan)) {
             ce = cudaMemcpyAsync(static_cast<uint8_t*>(ws->buf) + ws->layout.units,
                                  ws->plan.units.data(), ws->plan.units.size() * sizeof(Unit),
@@ -200,12 +203,9 @@ int attn_call(AttnKind kind, const void* q, const void* k_pages, const void* v_p
                                      ws->plan.tok_pos.data(),
                                      ws->plan.tok_pos.size() * sizeof(int32_t),
                                      cudaMemcpyHostToDevice, stream);
-            if (ce != cudaSuccess) {
-                ws->plan_ready = false;
-                return status_from_cuda(ce);
-            }
+            if (ce != cudaSuccess) return status_from_cuda(ce);
             ws->key = key;
-            patched = true;
+            ws->plan_ready = patched = true;
         }
     }
     if (!patched && (!ws->plan_ready || key != ws->key)) {
