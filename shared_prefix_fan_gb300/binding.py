@@ -203,31 +203,34 @@ def _device_call(name: str, dev, stream, *args) -> None:
 _I32_MAX = 2 ** 31 - 1  # ctypes would take the low 32 bits of more
 
 
-def _fit32(name: str, *values: int) -> None:
-    for v in values:
-        if not -_I32_MAX - 1 <= v <= _I32_MAX:
-            raise ValueError(f"{name}: {v} does not fit 32 bits")
+def _fit32(name: str, v: int) -> None:
+    """For integers with bits past the 31st: negative ones are the library's to refuse."""
+    if not -_I32_MAX - 1 <= v <= _I32_MAX:
+        raise ValueError(f"{name}: {v} does not fit 32 bits")
 
 
-def _empty(shape, dtype, dev, stream):
-    """A call's result, for the work of its `stream` (None: dev's current one).
+def _empty_on(dev, stream):
+    """torch.empty for the results of a call on `stream` (calls without one use
+    torch.empty itself: dev's current stream).
 
-    From another stream's pool than the one the call runs on, its block could still be
-    read or written there by work queued before it was freed, and a result that is
-    dropped early would be lent out again while the call has yet to write it. The
-    caller may use and drop it on the current stream: its reuse waits for that."""
+    From another stream's pool than the one the call runs on, a result's block could
+    still be read or written there by work queued before it was freed, and a result
+    that is dropped early would be lent out again while the call has yet to write it.
+    The caller may use and drop it on the current stream: its reuse waits for that."""
     import torch
-    if stream is not None:
-        handle, here = _stream_handle(stream), torch.cuda.current_stream(dev)
-        if handle != here.cuda_stream:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = (torch.cuda.ExternalStream(handle, device=dev) if handle > 1 else
-                          torch.cuda.default_stream(dev))  # 0 and 1 name the default stream
-            with torch.cuda.stream(stream):
-                t = torch.empty(shape, dtype=dtype, device=dev)
-            t.record_stream(here)
-            return t
-    return torch.empty(shape, dtype=dtype, device=dev)
+    handle, here = _stream_handle(stream), torch.cuda.current_stream(dev)
+    if handle == here.cuda_stream:
+        return torch.empty
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(handle, device=dev) if handle > 1 else
+                  torch.cuda.default_stream(dev))  # 0 and 1 name the default stream
+
+    def empty(shape, dtype, device):
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=device)
+        t.record_stream(here)
+        return t
+    return empty
 
 
 def _need(name: str, t, dtype, dev, shape=None) -> None:
@@ -257,7 +260,10 @@ def fork_device(prefix_pages, prefix_len: int, suffix_lens, page_size: int, free
     B = suffix_lens.numel()
     if page_size <= 0:
         raise ValueError("page_size must be positive")
-    _fit32("fork_device", prefix_len, page_size, max_pages)
+    if prefix_len >> 31 or page_size >> 31 or max_pages >> 31:
+        _fit32("prefix_len", prefix_len)
+        _fit32("page_size", page_size)
+        _fit32("max_pages", max_pages)
     _need("suffix_lens", suffix_lens, i32, dev, (B,))
     _need("prefix_pages", prefix_pages, i32, dev)
     _need("free_pages", free_pages, i32, dev)
@@ -265,16 +271,17 @@ def fork_device(prefix_pages, prefix_len: int, suffix_lens, page_size: int, free
         raise ValueError("prefix_pages holds fewer pages than the prefix")
     if used is not None:
         _need("used", used, i32, dev, (1,))
+    empty = torch.empty if stream is None else _empty_on(dev, stream)
     name = "fanout_fork_device"
     if out is None:
         name = "fanout_fork_device_new"
-        out = _empty((B, max_pages), i32, dev, stream)
+        out = empty((B, max_pages), dtype=i32, device=dev)
     else:
         _need("out", out, i32, dev, (B, max_pages))
     cow = None
     if want_cow and prefix_len % page_size:
-        cow = _empty((B, 2), i32, dev, stream)
-    after = _empty((1,), i32, dev, stream)
+        cow = empty((B, 2), dtype=i32, device=dev)
+    after = empty((1,), dtype=i32, device=dev)
     _device_call(name, dev, stream, prefix_pages.data_ptr(), prefix_len, B,
                  suffix_lens.data_ptr(), page_size, free_pages.data_ptr(), free_pages.numel(),
                  _ptr_or_none(used), after.data_ptr(), out.data_ptr(), max_pages,
@@ -291,18 +298,21 @@ def extend_device(page_table, prefix_len: int, suffix_lens, add_lens, page_size:
     import torch
     i32, dev = torch.int32, page_table.device
     B, width = page_table.shape
-    _fit32("extend_device", prefix_len, page_size)
+    if prefix_len >> 31 or page_size >> 31:
+        _fit32("prefix_len", prefix_len)
+        _fit32("page_size", page_size)
     _need("page_table", page_table, i32, dev)
     _need("suffix_lens", suffix_lens, i32, dev, (B,))
     _need("add_lens", add_lens, i32, dev, (B,))
     _need("free_pages", free_pages, i32, dev)
     if used is not None:
         _need("used", used, i32, dev, (1,))
+    empty = torch.empty if stream is None else _empty_on(dev, stream)
     if slots is None:
-        slots = _empty((n_slots,), torch.int64, dev, stream)
+        slots = empty((n_slots,), dtype=torch.int64, device=dev)
     else:
         _need("slots", slots, torch.int64, dev, (n_slots,))
-    after = _empty((1,), i32, dev, stream)
+    after = empty((1,), dtype=i32, device=dev)
     _device_call("fanout_extend_device", dev, stream, page_table.data_ptr(), B, width, prefix_len,
                  suffix_lens.data_ptr(), add_lens.data_ptr(), page_size, free_pages.data_ptr(),
                  free_pages.numel(), _ptr_or_none(used), after.data_ptr(), slots.data_ptr(),
@@ -374,10 +384,11 @@ def kv_read_q4(k_pages, v_pages, slots, page_size: int, k_scale: float = 1.0,
     dev, n = k_pages.device, slots.numel()
     num_pages, h_kv = _q4_pools(k_pages, v_pages, page_size, dev)
     _need("slots", slots, torch.int64, dev, (n,))
+    empty = torch.empty if stream is None else _empty_on(dev, stream)
     if k_out is None:
-        k_out = _empty((n, h_kv, 128), torch.bfloat16, dev, stream)
+        k_out = empty((n, h_kv, 128), dtype=torch.bfloat16, device=dev)
     if v_out is None:
-        v_out = _empty((n, h_kv, 128), torch.bfloat16, dev, stream)
+        v_out = empty((n, h_kv, 128), dtype=torch.bfloat16, device=dev)
     ks, vs = _rows_of("k_out", k_out, n, h_kv, dev), _rows_of("v_out", v_out, n, h_kv, dev)
     d = k_out.shape[2]
     if v_out.shape[2] != d:
@@ -477,10 +488,11 @@ def attn(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens: Sequence
     if k_pages.shape != v_pages.shape or k_pages.dim() != 4:
         raise ValueError("k_pages / v_pages must be [num_pages, H_kv, page, d]")
     odt = {"f32": (torch.float32, OUT_F32), "bf16": (torch.bfloat16, OUT_BF16)}[out_dtype]
+    empty = torch.empty if stream is None else _empty_on(dev, stream)
     if out is None:
-        out = _empty((R, h_q, d), odt[0], dev, stream)
+        out = empty((R, h_q, d), dtype=odt[0], device=dev)
     if lse is None and want_lse:
-        lse = _empty((R, h_q), torch.float32, dev, stream)
+        lse = empty((R, h_q), dtype=torch.float32, device=dev)
     if out.dtype != odt[0] or not out.is_contiguous():
         raise ValueError("out dtype/layout mismatch")
     rc = lib.fanout_attn(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
@@ -522,14 +534,15 @@ def _attn_out(q, page_table, R: int, B: int, h_q: int, out, lse, out_dtype: str,
     _need("page_table", page_table, torch.int32, dev)
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [num_branches, max_pages]")
+    empty = torch.empty if stream is None else _empty_on(dev, stream)
     if out is None:
-        out = _empty(shape, dt, dev, stream)
+        out = empty(shape, dtype=dt, device=dev)
     else:
         _need("out", out, dt, dev, shape)
     if lse is not None:
         _need("lse", lse, torch.float32, dev, (R, h_q))
     elif want_lse:
-        lse = _empty((R, h_q), torch.float32, dev, stream)
+        lse = empty((R, h_q), dtype=torch.float32, device=dev)
     return code, out, lse
 
 
@@ -539,8 +552,10 @@ def attn_window(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q
     """attn(), causal, where a row at pos sees keys j <= pos with j > pos - window
     or j < sinks. Pages that no row sees may have been given back."""
     import torch
-    window, sinks = max(-1, min(window, _I32_MAX)), max(-1, min(sinks, _I32_MAX))
-    _fit32("prefix_len", prefix_len)
+    if window >> 31 or sinks >> 31:
+        window, sinks = max(-1, min(window, _I32_MAX)), max(-1, min(sinks, _I32_MAX))
+    if prefix_len >> 31:
+        _fit32("prefix_len", prefix_len)
     held, lens, B, R = _lens(suffix_lens, q_rows)
     code, out, lse = _attn_out(q, page_table, R, B, h_q, out, lse, out_dtype, want_lse,
                                stream)
@@ -562,8 +577,10 @@ def attn_q4(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q_row
             out_dtype: str = "f32", want_lse: bool = True, stream=None):
     """attn() over 4-bit pools (uint8 [num_pages, H_kv, page_size * 72]); window and
     sinks as in attn_window (0, 0: none)."""
-    window, sinks = max(-1, min(window, _I32_MAX)), max(-1, min(sinks, _I32_MAX))
-    _fit32("prefix_len", prefix_len)
+    if window >> 31 or sinks >> 31:
+        window, sinks = max(-1, min(window, _I32_MAX)), max(-1, min(sinks, _I32_MAX))
+    if prefix_len >> 31:
+        _fit32("prefix_len", prefix_len)
     held, lens, B, R = _lens(suffix_lens, q_rows)
     code, out, lse = _attn_out(q, page_table, R, B, h_q, out, lse, out_dtype, want_lse,
                                stream)
@@ -606,10 +623,11 @@ def lse_merge(part_o, part_ml, out=None, lse=None, out_dtype: str = "f32", strea
     import torch
     n_parts, n_out, d = (int(x) for x in part_o.shape)
     odt = {"f32": (torch.float32, OUT_F32), "bf16": (torch.bfloat16, OUT_BF16)}[out_dtype]
+    empty = torch.empty if stream is None else _empty_on(part_o.device, stream)
     if out is None:
-        out = _empty((n_out, d), odt[0], part_o.device, stream)
+        out = empty((n_out, d), dtype=odt[0], device=part_o.device)
     if lse is None:
-        lse = _empty((n_out,), torch.float32, part_o.device, stream)
+        lse = empty((n_out,), dtype=torch.float32, device=part_o.device)
     _check(load().fanout_lse_merge(part_o.data_ptr(), part_ml.data_ptr(), n_parts, n_out, d,
                                    out.data_ptr(), odt[1], lse.data_ptr(), _stream_handle(stream)),
            "fanout_lse_merge")
