@@ -57,15 +57,16 @@
 // two O are all of TMEM, so S cannot be doubled, and a key tile takes about 3250
 // cycles a pair where its products are 2048. A boundary between units costs about
 // 10000 cycles (epilogue, next Q, masked tiles).
-//   4-bit prefill, 2048 rows x 64 heads over 32768 keys: 1436 us, 1484 TFLOP/s
-//   4-bit, 32 branches of 1..32 tokens over 65536 shared keys: 830 us, 1202 TFLOP/s
+//   4-bit prefill, 2048 rows x 64 heads over 32768 keys: 1442 us, 1478 TFLOP/s
+//   4-bit, 32 branches of 1..32 tokens over 65536 shared keys: 836 us, 1194 TFLOP/s
 //   bf16, the same over 16384 keys, window 2048: 102 us, 2060 GB/s, 356 TFLOP/s
 //   bf16 prefill, 4096 rows x 64 heads, window 1024: 166 us, 832 TFLOP/s
 // One query tile (decode), 8 rows x 64 heads over 32768 keys: 33 us for 42.5 MB in 4
 // bits (bf16 pools through attn_fwd.cu: 45 us for 151 MB): 15 tiles a CTA of 1900
-// cycles each, and 6600 cycles until the first S. A tile moves 200 KB through shared
-// memory (raw rows in and out 36, widened 64, the products' operands K, V and Q 96),
-// 1570 cycles at 128 bytes a cycle, so shorter chains gain little there
+// cycles each, and 6600 cycles until the first S (35100 of the 44300 cycles counted; the
+// rest is not accounted for). A tile moves 200 KB through shared memory (raw rows in
+// and out 36, widened 64, the products' operands K, V and Q 96), 1570 cycles at 128 bytes
+// a cycle by reckoning; shorter chains gained little there
 // (rows copied into a tile's idle half, so that a row's keys were split over two warps,
 // gained nothing). Window 4096: 20.5 us, four tiles a CTA, start and epilogue.
 // Every wait is bounded, as in attn_fwd.cu.

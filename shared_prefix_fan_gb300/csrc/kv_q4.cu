@@ -15,14 +15,14 @@
 //
 // A lane owns one group: 16 values (32 bytes of bf16), two code words and a scale;
 // 8 lanes make a K row, 8 its V row, so a warp handles two (row, KV head) pairs in
-// one pass, without exchanges. HBM-bound when there are many rows (656 bytes a pair
-// of K and V rows): 32 bytes a lane keep enough reads in flight (with 16, and a row
+// one pass, without exchanges. The floor of many rows is HBM's (656 bytes a pair of K and
+// V rows): 32 bytes a lane keep enough reads in flight (with 16, and a row
 // per warp, 8192 rows of 8 heads took 33 us in and out), and the work per value is
 // kept short: the quotients are products with the reciprocal, corrected (quotient,
 // below), the largest magnitude comes from packed maxima, codes from the e2m1
 // conversions (with fp32 divisions it took 47 us). Measured: 8192 rows of 8 heads in
-// and out 26.6 us (86 MB: 3.2 TB/s, the rows just written read from L2), 8 rows 10 us
-// (two launches).
+// and out 26.6 us (86 MB: 3.2 TB/s, the rows just written read from L2; what its warps
+// wait for is loads, one dependent chain a lane), 8 rows 10 us (two launches).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
