@@ -63,7 +63,7 @@
 //   bf16 prefill, 4096 rows x 64 heads, window 1024: 166 us, 832 TFLOP/s
 // One query tile (decode), 8 rows x 64 heads over 32768 keys: 33 us for 42.5 MB in 4
 // bits (bf16 pools through attn_fwd.cu: 45 us for 151 MB): 15 tiles a CTA of 1900
-// cycles each, and 6600 cycles until the first S (35100 of the 44300 cycles counted; the
+// cycles each, and 6600 cycles until the first S (35100 of the 44400 cycles counted; the
 // rest is not accounted for). A tile moves 200 KB through shared memory (raw rows in
 // and out 36, widened 64, the products' operands K, V and Q 96), 1570 cycles at 128 bytes
 // a cycle by reckoning; shorter chains gained little there
