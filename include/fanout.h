@@ -278,6 +278,106 @@ FANOUT_API int fanout_kv_read_q4(const void *k_pages, const void *v_pages, const
                 int64_t v_stride, fanout_stream_t stream);
 
 /*
+ * The 8-bit cache. With the pool's scale gs (host float, 1e-30 .. 1e30)
+ *   code = e4m3(x / gs), value = code * gs,
+ * the quotient in fp32, rounded to nearest, ties to even, saturating at 448. A pool is
+ * one e4m3 byte a value, [num_pages][H_kv][page_size][d], 16-byte aligned; page_size is
+ * 16, 32, 64 or 128. (fanout_copy_pages copies it as bf16 rows of d / 2.)
+ *
+ * fanout_kv_append_q8, fanout_kv_read_q8 -- as fanout_kv_append_q4 and
+ * fanout_kv_read_q4, into and from 8-bit pools: infinities are held as 448 gs, a NaN as
+ * 0 (reported). A byte 0x7f or 0xff, which an append never writes, reads as NaN. Both can
+ * be captured.
+ */
+FANOUT_API int fanout_kv_append_q8(const void *k_new, const void *v_new, int64_t k_stride,
+                int64_t v_stride, void *k_pages, void *v_pages, const int64_t *slots,
+                int32_t n_rows, int32_t num_pages, int32_t H_kv, int32_t d, int32_t page_size,
+                float k_scale, float v_scale, fanout_stream_t stream);
+FANOUT_API int fanout_kv_read_q8(const void *k_pages, const void *v_pages, const int64_t *slots,
+                int32_t n_rows, int32_t num_pages, int32_t H_kv, int32_t d, int32_t page_size,
+                float k_scale, float v_scale, void *k_out, void *v_out, int64_t k_stride,
+                int64_t v_stride, fanout_stream_t stream);
+
+/*
+ * Drafted trees. A branch may draft several continuations of its context at once, have
+ * the model look at all of them in one pass, and keep the path that it agrees with. The
+ * T_b drafted tokens of branch b are a forest: token t has a parent below t, or -1 (it
+ * follows the context itself). Their K/V rows lie in the branch's private pages behind
+ * its n_b = prefix_len + suffix_lens[b] cached tokens, token t at key n_b + t. A step is
+ *   fanout_extend_device (pages), fanout_tree_rows (masks, positions, slots),
+ *   fanout_kv_append_q8 / _q4 at the slots (or fanout_kv_append), fanout_attn_tree,
+ *   fanout_tree_accept, fanout_kv_keep,
+ * after which suffix_lens[b] grows by counts[b] and the other drafted rows are free to be
+ * overwritten. (The pages they took stay with the branch: a caller who extends by the
+ * tokens that have no page yet takes each page once.) T_b <= 1024, num_branches <= 4096.
+ *
+ * fanout_tree_rows -- what the drafted rows need (device), rows grouped by branch:
+ *   parents      dev int32 [n_rows]. A value below -1 or not below the token's own index
+ *                counts as -1 and is reported as FANOUT_EINVAL by fanout_last_error().
+ *   page_table   dev int32 [B][max_pages_per_branch], grown already.
+ *   suffix_lens, add_lens  dev int32 [B]: private tokens without the drafted ones, and T_b.
+ *   masks        dev uint32 [n_rows][mask_words], written: bit u of row t (word u / 32) says
+ *                that u is t or an ancestor of t; with window >= 1 one less than `window`
+ *                levels above it. T_b <= 32 * mask_words <= 1024.
+ *   positions    dev int32 [n_rows], written: n_b + the number of t's ancestors.
+ *   slots        dev int64 [n_rows], 8-byte aligned, written: page * page_size + place in
+ *                it of key n_b + t, as in fanout_extend_device (a negative page id: -1 and
+ *                FANOUT_EINVAL).
+ * Rows behind the last token get no bits, position 0 and slot -1, and so do all rows when a
+ * length is not valid (a negative one, more than n_rows tokens, T_b past the mask, a row
+ * of the table too short; reported as FANOUT_EINVAL). Arrays that are written share no
+ * byte with another (FANOUT_EINVAL). No workspace; can be captured (first call on a
+ * device outside a capture).
+ */
+FANOUT_API int fanout_tree_rows(const int32_t *parents, const int32_t *page_table,
+                int32_t num_branches, int32_t max_pages_per_branch, int32_t prefix_len,
+                const int32_t *suffix_lens, const int32_t *add_lens, int32_t page_size,
+                int64_t n_rows, int32_t mask_words, int32_t window, uint32_t *masks,
+                int32_t *positions, int64_t *slots, fanout_stream_t stream);
+
+/*
+ * fanout_tree_accept -- the path through each branch's drafted tokens that the model's
+ * own tokens follow (device). From no node on: the child that was drafted as the token
+ * picked at its parent -- first_tokens[b] before any, target_tokens of the node after it --
+ * and of several the one of lowest index, until there is none. (A tree whose root is the
+ * branch's last committed token: first_tokens[b] = that token.)
+ *   parents, draft_tokens, target_tokens  dev int32, int64, int64 [n_rows], by branch.
+ *   first_tokens  dev int64 [B];  add_lens  dev int32 [B]: T_b.
+ *   path          dev int32 [n_rows], written: of each branch's rows the first counts[b]
+ *                 hold the accepted tokens' indices in it, ascending, the others -1.
+ *   counts        dev int32 [B], written: accepted tokens.
+ *   next_tokens   dev int64 [B], written: the token picked behind the path.
+ * Lengths that are not valid (negative, past 1024, more than n_rows in all) are reported as
+ * FANOUT_EINVAL; then nothing is accepted: path and next_tokens -1, counts 0. Arrays that
+ * are written share no byte with another (FANOUT_EINVAL). Can be captured.
+ */
+FANOUT_API int fanout_tree_accept(const int32_t *parents, const int64_t *draft_tokens,
+                const int64_t *target_tokens, const int64_t *first_tokens,
+                const int32_t *add_lens, int32_t num_branches, int64_t n_rows, int32_t *path,
+                int32_t *counts, int64_t *next_tokens, fanout_stream_t stream);
+
+/* What a pool holds a value in. */
+enum fanout_kv_type { FANOUT_KV_BF16 = 0, FANOUT_KV_Q4 = 1, FANOUT_KV_Q8 = 2 };
+
+/*
+ * fanout_kv_keep -- move the accepted rows of each branch together (device): for i <
+ * counts[b], the K and V rows at key n_b + path[i] of the branch, of every KV head, are
+ * copied to key n_b + i, as the bytes they are. Keys from n_b + counts[b] on keep rows of
+ * the draft.
+ *   kv_type        fanout_kv_type of the pools;  path, counts  as fanout_tree_accept.
+ *   suffix_lens, add_lens  dev int32 [B], as fanout_tree_rows. H_kv * B < 2^31; d = 128.
+ * A branch whose path does not ascend inside its T_b tokens is left as it was, a row whose
+ * page is outside the pools is skipped, and with lengths that are not valid nothing is
+ * moved; each is reported as FANOUT_EINVAL. No two branches may share the pages of their
+ * drafted rows. Can be captured.
+ */
+FANOUT_API int fanout_kv_keep(void *k_pages, void *v_pages, int32_t kv_type,
+                const int32_t *page_table, int32_t num_branches, int32_t max_pages_per_branch,
+                int32_t prefix_len, const int32_t *suffix_lens, const int32_t *add_lens,
+                const int32_t *path, const int32_t *counts, int64_t n_rows, int32_t num_pages,
+                int32_t H_kv, int32_t d, int32_t page_size, fanout_stream_t stream);
+
+/*
  * fanout_attn -- batched shared-prefix fan-out attention.
  * "AHBM Agentic Runtime Architecture" sections 3.2-3.5; "ADR-0060" TL;DR,
  * sections 3, 4, 5.2 and 5.4.
@@ -373,6 +473,47 @@ FANOUT_API int fanout_attn_q4(const void *q, const void *k_pages, const void *v_
                 int32_t d, int32_t page_size, float scale, int32_t causal, float k_scale,
                 float v_scale, int32_t window, int32_t sinks, void *out, int32_t out_dtype,
                 float *lse, fanout_stream_t stream);
+
+/*
+ * fanout_attn_q8 -- fanout_attn_q4 over 8-bit pools (see there for the scales, window,
+ * sinks, page ids, capturing and plans). A row of q with an infinity or a NaN gives NaN.
+ * Bytes of keys that no row sees are never used; a key that a row of the call sees must
+ * not hold 0x7f or 0xff.
+ */
+FANOUT_API int fanout_attn_q8(const void *q, const void *k_pages, const void *v_pages,
+                const int32_t *page_table, int32_t prefix_len, const int32_t *suffix_lens,
+                const int32_t *q_rows_per_branch, int32_t num_branches,
+                int32_t max_pages_per_branch, int32_t num_pages, int32_t H_q, int32_t H_kv,
+                int32_t d, int32_t page_size, float scale, int32_t causal, float k_scale,
+                float v_scale, int32_t window, int32_t sinks, void *out, int32_t out_dtype,
+                float *lse, fanout_stream_t stream);
+
+/*
+ * fanout_attn_tree -- attention for trees of drafted tokens over the cache. As in
+ * fanout_attn a branch's new rows are the tail of its suffix: with T_b =
+ * q_rows_per_branch[b] <= suffix_lens[b] and n_b = prefix_len + suffix_lens[b] - T_b keys
+ * before them, row t of branch b sees
+ *   key j < n_b      iff window == 0, or j > positions[row] - window, or j < sinks;
+ *   key n_b + u      iff u == t or bit u of masks[row] is set (u < T_b).
+ * (suffix_lens counts the drafted tokens here, as the other attention calls do.)
+ *   kv_type     fanout_kv_type of the pools; layouts and scales as fanout_attn,
+ *               fanout_attn_q4 and fanout_attn_q8 (scales not used with bf16).
+ *   masks       dev uint32 [R][mask_words], 4-byte aligned, T_b <= 32 * mask_words, any
+ *               bits (fanout_tree_rows gives a tree's); T_b <= 1024, else FANOUT_EUNSUPPORTED.
+ *   positions   dev int32 [R] or NULL: read with window >= 1 only, and needed then; n_b ..
+ *               n_b + 1023 (a value outside counts as the nearest of these).
+ *   window, sinks  0, 0: every key before the draft; sinks without a window is FANOUT_EINVAL.
+ * The drafted tokens' rows must all be finite. Everything else as fanout_attn_window: page
+ * ids, hidden keys, capturing, plans, errors.
+ */
+FANOUT_API int fanout_attn_tree(const void *q, const void *k_pages, const void *v_pages,
+                int32_t kv_type, const int32_t *page_table, int32_t prefix_len,
+                const int32_t *suffix_lens, const int32_t *q_rows_per_branch,
+                int32_t num_branches, int32_t max_pages_per_branch, int32_t num_pages,
+                int32_t H_q, int32_t H_kv, int32_t d, int32_t page_size, float scale,
+                const uint32_t *masks, int32_t mask_words, const int32_t *positions,
+                int32_t window, int32_t sinks, float k_scale, float v_scale, void *out,
+                int32_t out_dtype, float *lse, fanout_stream_t stream);
 
 /*
  * fanout_lse_merge -- the log-sum-exp merge of split partials on its own

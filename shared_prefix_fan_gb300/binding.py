@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_HERE, "lib", "libfanout.so")
 
 OK, EINVAL, EUNSUPPORTED, ECUDA, ENOMEM, ETIMEOUT = range(6)
 OUT_F32, OUT_BF16 = 0, 1
+KV_BF16, KV_Q4, KV_Q8 = 0, 1, 2
 OPT_SPLITS, OPT_VALIDATE_TABLE, OPT_WAIT_LIMIT_NS, OPT_NUM_SMS, OPT_FUSED_MERGE = 1, 2, 3, 4, 5
 
 # The C ABI (include/fanout.h): name -> (restype, argtypes)
@@ -54,6 +55,22 @@ ABI = {
     "fanout_attn_q4": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32,
                                       _i32, _i32, _i32, _i32, _f32, _i32, _f32, _f32, _i32, _i32,
                                       _vp, _i32, _vp, _vp]),
+    "fanout_kv_append_q8": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _i32, _i32, _i32,
+                                           _i32, _i32, _f32, _f32, _vp]),
+    "fanout_kv_read_q8": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _f32, _f32,
+                                         _vp, _vp, _i64, _i64, _vp]),
+    "fanout_attn_q8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32,
+                                      _i32, _i32, _i32, _i32, _f32, _i32, _f32, _f32, _i32, _i32,
+                                      _vp, _i32, _vp, _vp]),
+    "fanout_tree_rows": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _vp, _vp, _i32, _i64, _i32,
+                                        _i32, _vp, _vp, _vp, _vp]),
+    "fanout_tree_accept": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _vp, _vp, _vp,
+                                          _vp]),
+    "fanout_kv_keep": (ctypes.c_int, [_vp, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
+                                      _i64, _i32, _i32, _i32, _i32, _vp]),
+    "fanout_attn_tree": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _i32, _i32,
+                                        _i32, _i32, _i32, _i32, _f32, _vp, _i32, _vp, _i32, _i32,
+                                        _f32, _f32, _vp, _i32, _vp, _vp]),
     "fanout_lse_merge": (ctypes.c_int, [_vp, _vp, _i32, _i64, _i32, _vp, _i32, _vp, _vp]),
     "fanout_last_error": (ctypes.c_int, [_vp]),
     "fanout_last_error_detail": (ctypes.c_int, [_vp, _i32p, _i32p]),
@@ -414,6 +431,185 @@ def copy_pages_q4(k_pages, v_pages, pairs, page_size: int, stream=None) -> None:
                  page_size // 2)
 
 
+def q8_pool(num_pages: int, h_kv: int, page_size: int, device="cuda"):
+    """A zeroed 8-bit pool: float8_e4m3fn [num_pages, H_kv, page_size, 128]."""
+    import torch
+    shape = (int(num_pages), int(h_kv), int(page_size), 128)
+    return torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+
+
+def _q8_pools(k_pages, v_pages, dev):
+    """(num_pages, H_kv, page_size, d) of a pair of 8-bit pools."""
+    import torch
+    shape = k_pages.shape
+    _need("k_pages", k_pages, torch.float8_e4m3fn, dev)
+    _need("v_pages", v_pages, torch.float8_e4m3fn, dev, shape)
+    if len(shape) != 4:
+        raise ValueError("k_pages / v_pages must be [num_pages, H_kv, page_size, d]")
+    return shape
+
+
+def kv_append_q8(k_new, v_new, k_pages, v_pages, slots, k_scale: float = 1.0,
+                 v_scale: float = 1.0, stream=None) -> None:
+    """Write new K/V rows (bf16 [R, H_kv, 128], rows may be strided) into 8-bit
+    pools at `slots` (int64 [R]; negative: the row is skipped)."""
+    import torch
+    dev, n = k_pages.device, slots.numel()
+    num_pages, h_kv, page_size, d = _q8_pools(k_pages, v_pages, dev)
+    _need("slots", slots, torch.int64, dev, (n,))
+    ks, vs = _rows_of("k_new", k_new, n, h_kv, dev), _rows_of("v_new", v_new, n, h_kv, dev)
+    if k_new.shape[2] != d or v_new.shape[2] != d:
+        raise ValueError(f"k_new / v_new rows must hold the pools' {d} values")
+    _device_call("fanout_kv_append_q8", dev, stream, k_new.data_ptr(), v_new.data_ptr(), ks, vs,
+                 k_pages.data_ptr(), v_pages.data_ptr(), slots.data_ptr(), n, num_pages, h_kv, d,
+                 page_size, k_scale, v_scale)
+
+
+def kv_read_q8(k_pages, v_pages, slots, k_scale: float = 1.0, v_scale: float = 1.0, k_out=None,
+               v_out=None, stream=None):
+    """The bf16 rows [R, H_kv, 128] that `slots` of 8-bit pools stand for: (k, v).
+    Rows with a negative slot are left as they were (undefined when allocated here)."""
+    import torch
+    dev, n = k_pages.device, slots.numel()
+    num_pages, h_kv, page_size, d = _q8_pools(k_pages, v_pages, dev)
+    _need("slots", slots, torch.int64, dev, (n,))
+    empty = torch.empty if stream is None else _empty_on(dev, stream)
+    if k_out is None:
+        k_out = empty((n, h_kv, d), dtype=torch.bfloat16, device=dev)
+    if v_out is None:
+        v_out = empty((n, h_kv, d), dtype=torch.bfloat16, device=dev)
+    ks, vs = _rows_of("k_out", k_out, n, h_kv, dev), _rows_of("v_out", v_out, n, h_kv, dev)
+    if k_out.shape[2] != d or v_out.shape[2] != d:
+        raise ValueError(f"k_out / v_out rows must hold the pools' {d} values")
+    _device_call("fanout_kv_read_q8", dev, stream, k_pages.data_ptr(), v_pages.data_ptr(),
+                 slots.data_ptr(), n, num_pages, h_kv, d, page_size, k_scale, v_scale,
+                 k_out.data_ptr(), v_out.data_ptr(), ks, vs)
+    return k_out, v_out
+
+
+def copy_pages_q8(k_pages, v_pages, pairs, rows: int, stream=None) -> None:
+    """copy_pages for 8-bit pools: token slots [0, rows) of page pairs (int32 [n, 2])."""
+    import torch
+    dev = k_pages.device
+    num_pages, h_kv, page_size, d = _q8_pools(k_pages, v_pages, dev)
+    _need("pairs", pairs, torch.int32, dev, (pairs.shape[0], 2))
+    # a row of d bytes as d / 2 16-bit values
+    _device_call("fanout_copy_pages", dev, stream, k_pages.data_ptr(), v_pages.data_ptr(),
+                 pairs.data_ptr(), pairs.shape[0], rows, num_pages, h_kv, d // 2, page_size)
+
+
+def _pools(k_pages, v_pages, page_size: int, h_kv: int, dev):
+    """(what the pools hold, num_pages, H_kv) of a pair of pools of any kind."""
+    import torch
+    if k_pages.dtype is torch.uint8:
+        kind, shape = KV_Q4, _q4_pools(k_pages, v_pages, page_size, dev)
+    else:
+        if k_pages.dtype is torch.float8_e4m3fn:
+            kind, shape = KV_Q8, _q8_pools(k_pages, v_pages, dev)
+        else:
+            kind, shape = KV_BF16, k_pages.shape
+            _need("k_pages", k_pages, torch.bfloat16, dev)
+            _need("v_pages", v_pages, torch.bfloat16, dev, shape)
+        if len(shape) != 4 or shape[2] != page_size or shape[3] != 128:
+            raise ValueError("k_pages / v_pages must be [num_pages, H_kv, page_size, 128]")
+    if h_kv and shape[1] != h_kv:
+        raise ValueError(f"pools hold {shape[1]} KV heads, not {h_kv}")
+    return kind, shape[0], shape[1]
+
+
+def tree_rows(parents, page_table, prefix_len: int, suffix_lens, add_lens, page_size: int,
+              max_nodes: int, window: int = 0, masks=None, positions=None, slots=None, stream=None):
+    """What a step's drafted rows need: (masks int32 [R, words], positions int32 [R],
+    slots int64 [R]).
+
+    parents (int32 [R], rows grouped by branch): each drafted token's parent in its
+    branch, or -1; suffix_lens / add_lens (int32 [B]): private tokens before the draft, and
+    drafted ones, at most max_nodes (<= 1024) each. Bit u of a token's mask is set for
+    itself and its ancestors (with a window, those less than `window` levels above it);
+    its position is prefix + suffix + its depth; its slot is where its K/V row belongs.
+    Rows behind the last token get no bits, position 0 and slot -1."""
+    import torch
+    i32, dev, R = torch.int32, parents.device, parents.numel()
+    if max_nodes < 1 or max_nodes > 1024:
+        raise ValueError("max_nodes must be 1 .. 1024")
+    B, width = page_table.shape
+    words = -(-max_nodes // 32)
+    for name, v in (("prefix_len", prefix_len), ("page_size", page_size)):
+        if v >> 31:
+            _fit32(name, v)
+    if window >> 31:
+        window = max(-1, min(window, _I32_MAX))
+    _need("parents", parents, i32, dev, (R,))
+    _need("page_table", page_table, i32, dev)
+    _need("suffix_lens", suffix_lens, i32, dev, (B,))
+    _need("add_lens", add_lens, i32, dev, (B,))
+    empty = torch.empty if stream is None else _empty_on(dev, stream)
+    if masks is None:
+        masks = empty((R, words), dtype=i32, device=dev)
+    else:
+        _need("masks", masks, i32, dev, (R, words))
+    if positions is None:
+        positions = empty((R,), dtype=i32, device=dev)
+    else:
+        _need("positions", positions, i32, dev, (R,))
+    if slots is None:
+        slots = empty((R,), dtype=torch.int64, device=dev)
+    else:
+        _need("slots", slots, torch.int64, dev, (R,))
+    _device_call("fanout_tree_rows", dev, stream, parents.data_ptr(), page_table.data_ptr(), B,
+                 width, prefix_len, suffix_lens.data_ptr(), add_lens.data_ptr(), page_size, R,
+                 words, window, masks.data_ptr(), positions.data_ptr(), slots.data_ptr())
+    return masks, positions, slots
+
+
+def tree_accept(parents, draft_tokens, target_tokens, first_tokens, add_lens, stream=None):
+    """The drafted tokens that the model agrees with: (path int32 [R], counts int32
+    [B], next_tokens int64 [B]).
+
+    draft_tokens / target_tokens (int64 [R]): each node's token, and the one the model
+    picked behind it; first_tokens (int64 [B]): the one picked behind the context. Of each
+    branch's rows of `path` the first counts[b] hold the accepted nodes, the others -1."""
+    import torch
+    i32, i64, dev = torch.int32, torch.int64, parents.device
+    R, B = parents.numel(), add_lens.numel()
+    _need("parents", parents, i32, dev, (R,))
+    _need("draft_tokens", draft_tokens, i64, dev, (R,))
+    _need("target_tokens", target_tokens, i64, dev, (R,))
+    _need("first_tokens", first_tokens, i64, dev, (B,))
+    _need("add_lens", add_lens, i32, dev, (B,))
+    empty = torch.empty if stream is None else _empty_on(dev, stream)
+    path = empty((R,), dtype=i32, device=dev)
+    counts = empty((B,), dtype=i32, device=dev)
+    after = empty((B,), dtype=i64, device=dev)
+    _device_call("fanout_tree_accept", dev, stream, parents.data_ptr(), draft_tokens.data_ptr(),
+                 target_tokens.data_ptr(), first_tokens.data_ptr(), add_lens.data_ptr(), B, R,
+                 path.data_ptr(), counts.data_ptr(), after.data_ptr())
+    return path, counts, after
+
+
+def kv_keep(k_pages, v_pages, page_table, prefix_len: int, suffix_lens, add_lens, path, counts,
+            page_size: int, stream=None) -> None:
+    """Move the accepted rows together in pools of any kind: drafted row path[i] of a
+    branch becomes its row i (path, counts as tree_accept gives them; suffix_lens without
+    the drafted tokens)."""
+    import torch
+    i32, dev = torch.int32, k_pages.device
+    B, width = page_table.shape
+    for name, v in (("prefix_len", prefix_len), ("page_size", page_size)):
+        if v >> 31:
+            _fit32(name, v)
+    kind, num_pages, h_kv = _pools(k_pages, v_pages, page_size, 0, dev)
+    _need("page_table", page_table, i32, dev)
+    _need("suffix_lens", suffix_lens, i32, dev, (B,))
+    _need("add_lens", add_lens, i32, dev, (B,))
+    _need("path", path, i32, dev, (path.numel(),))
+    _need("counts", counts, i32, dev, (B,))
+    _device_call("fanout_kv_keep", dev, stream, k_pages.data_ptr(), v_pages.data_ptr(), kind,
+                 page_table.data_ptr(), B, width, prefix_len, suffix_lens.data_ptr(),
+                 add_lens.data_ptr(), path.data_ptr(), counts.data_ptr(), path.numel(), num_pages,
+                 h_kv, 128, page_size)
+
+
 def plan(suffix_lens, q_rows, prefix_len: int, h_q: int, h_kv: int, page_size: int,
          causal: bool, num_sms: int = 152) -> Tuple[np.ndarray, np.ndarray, int]:
     """The work plan fanout_attn would run: (units [n, 8], cta_first [n_cta+1], n_parts)."""
@@ -593,6 +789,65 @@ def attn_q4(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q_row
                  page_table.shape[1], num_pages, h_q, h_kv, q.shape[-1], page_size, scale,
                  1 if causal else 0, k_scale, v_scale, window, sinks, out.data_ptr(), code,
                  _ptr_or_none(lse))
+    return out, lse
+
+
+def attn_q8(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q_rows, h_q: int,
+            h_kv: int, page_size: int, scale: float, causal: bool, k_scale: float = 1.0,
+            v_scale: float = 1.0, window: int = 0, sinks: int = 0, out=None, lse=None,
+            out_dtype: str = "f32", want_lse: bool = True, stream=None):
+    """attn() over 8-bit pools (float8_e4m3fn [num_pages, H_kv, page_size, 128]); window
+    and sinks as in attn_window (0, 0: none)."""
+    import torch
+    if window >> 31 or sinks >> 31:
+        window, sinks = max(-1, min(window, _I32_MAX)), max(-1, min(sinks, _I32_MAX))
+    if prefix_len >> 31:
+        _fit32("prefix_len", prefix_len)
+    held, lens, B, R = _lens(suffix_lens, q_rows)
+    code, out, lse = _attn_out(q, page_table, R, B, h_q, out, lse, out_dtype, want_lse,
+                               stream)
+    dev, d = q.device, q.shape[-1]
+    pool = (k_pages.shape[0], h_kv, page_size, d)
+    _need("k_pages", k_pages, torch.float8_e4m3fn, dev, pool)
+    _need("v_pages", v_pages, torch.float8_e4m3fn, dev, pool)
+    _device_call("fanout_attn_q8", dev, stream, q.data_ptr(), k_pages.data_ptr(),
+                 v_pages.data_ptr(), page_table.data_ptr(), prefix_len, lens, lens + 4 * B, B,
+                 page_table.shape[1], pool[0], h_q, h_kv, d, page_size, scale,
+                 1 if causal else 0, k_scale, v_scale, window, sinks, out.data_ptr(), code,
+                 _ptr_or_none(lse))
+    return out, lse
+
+
+def attn_tree(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q_rows, h_q: int,
+              h_kv: int, page_size: int, scale: float, masks, positions=None, window: int = 0,
+              sinks: int = 0, k_scale: float = 1.0, v_scale: float = 1.0, out=None, lse=None,
+              out_dtype: str = "f32", want_lse: bool = True, stream=None):
+    """attn() for trees of drafted tokens, the last q_rows[b] <= 1024 tokens of a branch's
+    suffix (suffix_lens counts them): a row sees the keys before its branch's draft (with
+    a window those past position - window and the first `sinks`), itself, and the drafted
+    tokens that its mask names (masks int32 [R, words], positions int32 [R]: tree_rows
+    gives them; positions are read with a window only). Pools of any kind: bf16, 4 bits
+    (uint8), 8 bits (float8_e4m3fn)."""
+    import torch
+    if window >> 31 or sinks >> 31:
+        window, sinks = max(-1, min(window, _I32_MAX)), max(-1, min(sinks, _I32_MAX))
+    if prefix_len >> 31:
+        _fit32("prefix_len", prefix_len)
+    held, lens, B, R = _lens(suffix_lens, q_rows)
+    code, out, lse = _attn_out(q, page_table, R, B, h_q, out, lse, out_dtype, want_lse,
+                               stream)
+    dev, d = q.device, q.shape[-1]
+    kind, num_pages, _ = _pools(k_pages, v_pages, page_size, h_kv, dev)
+    if masks.dim() != 2 or masks.shape[0] != R:
+        raise ValueError(f"masks must be [{R}, words]")
+    _need("masks", masks, torch.int32, dev)
+    if positions is not None:
+        _need("positions", positions, torch.int32, dev, (R,))
+    _device_call("fanout_attn_tree", dev, stream, q.data_ptr(), k_pages.data_ptr(),
+                 v_pages.data_ptr(), kind, page_table.data_ptr(), prefix_len, lens, lens + 4 * B,
+                 B, page_table.shape[1], num_pages, h_q, h_kv, d, page_size, scale,
+                 masks.data_ptr(), masks.shape[1], _ptr_or_none(positions), window, sinks,
+                 k_scale, v_scale, out.data_ptr(), code, _ptr_or_none(lse))
     return out, lse
 
 

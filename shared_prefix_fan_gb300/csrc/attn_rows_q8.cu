@@ -1,0 +1,13 @@
+// attn_rows_q8.cu -- attn_rows.cuh over 8-bit pools, tokens in causal order.
+#include "attn_rows.cuh"
+
+namespace fanout {
+
+cudaError_t launch_attn_rows_q8(const RowParams& p, const CUtensorMap& tm_q,
+                                const CUtensorMap& tm_k, int grid, cudaStream_t stream) {
+    const CUtensorMap none{};
+    return p.nq == 2 ? launch_nq<2, Pool::q8, false>(p, tm_q, tm_k, none, grid, stream)
+                     : launch_nq<1, Pool::q8, false>(p, tm_q, tm_k, none, grid, stream);
+}
+
+}  // namespace fanout

@@ -46,7 +46,17 @@ struct Workspace {
     bool plan_ready = false;
     uint32_t epoch = 0;  // flag value of the last call (fused merge)
 };
-enum AttnKind { kFull = 0, kWindow = 1, kQ4 = 2, kQ4Window = 3 };
+// kFull is fanout_attn's; the others add what the pools hold, a window and a tree.
+enum AttnKind { kFull = 0, kRows = 1 };
+constexpr int kind_of(Pool pool, bool window, bool tree) {
+    return kRows + 4 * static_cast<int>(pool) + (window ? 2 : 0) + (tree ? 1 : 0);
+}
+// A drafted tree's arguments; none: tokens in causal order, or all keys.
+struct TreeArgs {
+    const uint32_t* masks = nullptr;
+    int32_t words = 0;
+    const int32_t* positions = nullptr;
+};
 std::map<std::tuple<int, cudaStream_t, int>, Workspace*> g_ws;
 
 int status_from_cuda(cudaError_t e) {
@@ -85,17 +95,28 @@ cudaError_t launch_stream_read(const void* buf, int64_t bytes, uint32_t* xor_out
 
 namespace {
 
-// The call behind fanout_attn, fanout_attn_window and fanout_attn_q4: checks,
-// the (device, stream, kind) workspace, the plan, its upload and the launches.
+// A pool's scales, and their product with the softmax scale: the softmax scale of the held
+// values, which is normal as its inverse is (the kernel keeps it so when a row's own
+// power of two comes in).
+bool scales_ok(Pool pool, float scale, float k_scale, float v_scale) {
+    if (pool == Pool::bf16) return true;
+    return pool_scale_ok(k_scale) && pool_scale_ok(v_scale) && scale * k_scale >= 1e-37f &&
+           scale * k_scale <= 1e37f;
+}
+
+// The call behind fanout_attn, fanout_attn_window, fanout_attn_q4, fanout_attn_q8 and
+// fanout_attn_tree: checks, the (device, stream, kind) workspace, the plan, its upload and
+// the launches. full: fanout_attn itself, else a row plan over what `pool` names.
 // window > 0 (causal only): rows see keys > pos - window and keys < sinks.
-int attn_call(AttnKind kind, const void* q, const void* k_pages, const void* v_pages,
+int attn_call(bool full, Pool pool, const TreeArgs& tree, const void* q, const void* k_pages, const void* v_pages,
               const int32_t* page_table, int32_t prefix_len, const int32_t* suffix_lens,
               const int32_t* q_rows_per_branch, int32_t num_branches,
               int32_t max_pages_per_branch, int32_t num_pages, int32_t H_q, int32_t H_kv,
               int32_t d, int32_t page_size, float scale, int32_t causal, int32_t window,
               int32_t sinks, float k_scale, float v_scale, void* out, int32_t out_dtype,
               float* lse, fanout_stream_t stream_) {
-    const bool rows = kind != kFull, q4 = kind == kQ4 || kind == kQ4Window;
+    const bool rows = !full, is_tree = tree.masks != nullptr;
+    const int kind = full ? kFull : kind_of(pool, window > 0, is_tree);
     int st = validate_shape(suffix_lens, q_rows_per_branch, num_branches, prefix_len, H_q, H_kv,
                             d, page_size, causal);
     if (st != FANOUT_OK) return st;
@@ -185,7 +206,8 @@ int attn_call(AttnKind kind, const void* q, const void* k_pages, const void* v_p
     in.rows = rows;
     in.window = window;
     in.sinks = sinks;
-    if (q4) in.row_bytes = 2 * kQ4RowBytes;
+    in.tree = is_tree;
+    if (pool != Pool::bf16) in.row_bytes = 2 * (pool == Pool::q4 ? kQ4RowBytes : kHD);
     bool patched = false;
     if (ws->plan_ready && key != ws->key && key.size() == ws->key.size() &&
         std::equal(key.begin(), key.begin() + fixed, ws->key.begin()) &&
@@ -238,8 +260,9 @@ int attn_call(AttnKind kind, const void* q, const void* k_pages, const void* v_p
     if (++ws->epoch == 0) ws->epoch = 1;  // 0 is the flags' initial value
     CallArgs a{q, k_pages, v_pages, page_table, max_pages_per_branch, num_pages, H_q, H_kv,
                page_size, out_dtype == FANOUT_OUT_BF16, scale, out, lse, R, wait_limit_ns,
-               window, sinks, q4, k_scale, v_scale,
-               rows ? 0 : static_cast<int32_t>(fused_merge), ws->epoch};
+               window, sinks, static_cast<int32_t>(pool), k_scale, v_scale,
+               rows ? 0 : static_cast<int32_t>(fused_merge), ws->epoch, tree.masks,
+               tree.positions, tree.words};
     return launch_plan(a, ws->plan, ws->layout, static_cast<uint8_t*>(ws->buf), stream,
                        ev_before, ev_after);
 }
@@ -521,7 +544,7 @@ int fanout_attn(const void* q, const void* k_pages, const void* v_pages,
                 int32_t d, int32_t page_size, float scale, int32_t causal, void* out,
                 int32_t out_dtype, float* lse, fanout_stream_t stream) {
     try {
-        return attn_call(kFull, q, k_pages, v_pages, page_table, prefix_len, suffix_lens,
+        return attn_call(true, Pool::bf16, {}, q, k_pages, v_pages, page_table, prefix_len, suffix_lens,
                          q_rows_per_branch, num_branches, max_pages_per_branch, num_pages, H_q,
                          H_kv, d, page_size, scale, causal, 0, 0, 1.f, 1.f, out, out_dtype, lse,
                          stream);
@@ -539,7 +562,7 @@ int fanout_attn_window(const void* q, const void* k_pages, const void* v_pages,
                        fanout_stream_t stream) {
     if (window < 1 || sinks < 0) return FANOUT_EINVAL;
     try {
-        return attn_call(kWindow, q, k_pages, v_pages, page_table, prefix_len, suffix_lens,
+        return attn_call(false, Pool::bf16, {}, q, k_pages, v_pages, page_table, prefix_len, suffix_lens,
                          q_rows_per_branch, num_branches, max_pages_per_branch, num_pages, H_q,
                          H_kv, d, page_size, scale, 1, std::min(window, kNoCausal),
                          std::min(sinks, kNoCausal), 1.f, 1.f, out, out_dtype, lse, stream);
@@ -557,16 +580,70 @@ int fanout_attn_q4(const void* q, const void* k_pages, const void* v_pages,
                    float* lse, fanout_stream_t stream) {
     if (window < 0 || sinks < 0 || (window > 0 && !causal) || (window == 0 && sinks > 0))
         return FANOUT_EINVAL;
-    if (!q4_scale_ok(k_scale) || !q4_scale_ok(v_scale)) return FANOUT_EINVAL;
-    // their product is the softmax scale of the held values: it and its inverse normal (the
-    // kernel keeps it so when a row's own power of two comes in)
-    if (!(scale * k_scale >= 1e-37f && scale * k_scale <= 1e37f)) return FANOUT_EINVAL;
+    if (!scales_ok(Pool::q4, scale, k_scale, v_scale)) return FANOUT_EINVAL;
     try {
-        return attn_call(window > 0 ? kQ4Window : kQ4, q, k_pages, v_pages, page_table,
-                         prefix_len, suffix_lens, q_rows_per_branch, num_branches,
+        return attn_call(false, Pool::q4, {}, q, k_pages, v_pages, page_table, prefix_len,
+                         suffix_lens, q_rows_per_branch, num_branches,
                          max_pages_per_branch, num_pages, H_q, H_kv, d, page_size, scale, causal,
                          std::min(window, kNoCausal), std::min(sinks, kNoCausal), k_scale,
                          v_scale, out, out_dtype, lse, stream);
+    } catch (const std::bad_alloc&) {
+        return FANOUT_ENOMEM;
+    }
+}
+
+int fanout_attn_q8(const void* q, const void* k_pages, const void* v_pages,
+                   const int32_t* page_table, int32_t prefix_len, const int32_t* suffix_lens,
+                   const int32_t* q_rows_per_branch, int32_t num_branches,
+                   int32_t max_pages_per_branch, int32_t num_pages, int32_t H_q, int32_t H_kv,
+                   int32_t d, int32_t page_size, float scale, int32_t causal, float k_scale,
+                   float v_scale, int32_t window, int32_t sinks, void* out, int32_t out_dtype,
+                   float* lse, fanout_stream_t stream) {
+    if (window < 0 || sinks < 0 || (window > 0 && !causal) || (window == 0 && sinks > 0))
+        return FANOUT_EINVAL;
+    if (!scales_ok(Pool::q8, scale, k_scale, v_scale)) return FANOUT_EINVAL;
+    try {
+        return attn_call(false, Pool::q8, {}, q, k_pages, v_pages, page_table, prefix_len,
+                         suffix_lens, q_rows_per_branch, num_branches, max_pages_per_branch,
+                         num_pages, H_q, H_kv, d, page_size, scale, causal,
+                         std::min(window, kNoCausal), std::min(sinks, kNoCausal), k_scale,
+                         v_scale, out, out_dtype, lse, stream);
+    } catch (const std::bad_alloc&) {
+        return FANOUT_ENOMEM;
+    }
+}
+
+int fanout_attn_tree(const void* q, const void* k_pages, const void* v_pages, int32_t kv_type,
+                     const int32_t* page_table, int32_t prefix_len, const int32_t* suffix_lens,
+                     const int32_t* q_rows_per_branch, int32_t num_branches,
+                     int32_t max_pages_per_branch, int32_t num_pages, int32_t H_q, int32_t H_kv,
+                     int32_t d, int32_t page_size, float scale, const uint32_t* masks,
+                     int32_t mask_words, const int32_t* positions, int32_t window,
+                     int32_t sinks, float k_scale, float v_scale, void* out, int32_t out_dtype,
+                     float* lse, fanout_stream_t stream) {
+    if (kv_type != FANOUT_KV_BF16 && kv_type != FANOUT_KV_Q4 && kv_type != FANOUT_KV_Q8)
+        return FANOUT_EINVAL;
+    const Pool pool = static_cast<Pool>(kv_type);
+    if (window < 0 || sinks < 0 || (window == 0 && sinks > 0)) return FANOUT_EINVAL;
+    if (!scales_ok(pool, scale, k_scale, v_scale)) return FANOUT_EINVAL;
+    if (mask_words <= 0 || num_branches < 0) return FANOUT_EINVAL;
+    if (num_branches > 0 && !q_rows_per_branch) return FANOUT_EINVAL;
+    bool any = false;
+    for (int32_t b = 0; b < num_branches; ++b) {
+        if (q_rows_per_branch[b] > kMaxTreeTokens) return FANOUT_EUNSUPPORTED;
+        if (q_rows_per_branch[b] > 32LL * mask_words) return FANOUT_EINVAL;
+        any = any || q_rows_per_branch[b] > 0;
+    }
+    if (any && (!masks || (window > 0 && !positions))) return FANOUT_EINVAL;
+    if ((reinterpret_cast<uintptr_t>(masks) | reinterpret_cast<uintptr_t>(positions)) & 3u)
+        return FANOUT_EINVAL;
+    try {
+        return attn_call(false, pool, {masks, mask_words, window > 0 ? positions : nullptr}, q,
+                         k_pages, v_pages, page_table, prefix_len, suffix_lens,
+                         q_rows_per_branch, num_branches, max_pages_per_branch, num_pages, H_q,
+                         H_kv, d, page_size, scale, 1, std::min(window, kNoCausal),
+                         std::min(sinks, kNoCausal), pool == Pool::bf16 ? 1.f : k_scale,
+                         pool == Pool::bf16 ? 1.f : v_scale, out, out_dtype, lse, stream);
     } catch (const std::bad_alloc&) {
         return FANOUT_ENOMEM;
     }

@@ -1,0 +1,138 @@
+// kv_q8.cu -- rows into the 8-bit KV cache and back.
+//
+// A cached row is 128 e4m3 codes: with the pool's scale gs
+//   code = e4m3(x / gs), value = code * gs,
+// the quotient in fp32, rounded to nearest, ties to even, saturating at 448. A pool is
+// [num_pages][H_kv][page][128] bytes, so a page of a KV head is a tile of 128-byte rows,
+// which the attention kernel's products read as they are.
+//
+// A lane owns 16 values (32 bytes of bf16, 16 of codes); 8 lanes make a K row, 8 its V
+// row, so a warp handles two (row, KV head) pairs, without exchanges, and its stores are
+// whole 128-byte lines. Bound by HBM when rows are many (384 bytes a row and direction),
+// by a launch and one dependent chain (slot, row, store) when they are few.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ptx_fp8.cuh"
+#include "ptx_sm100.cuh"
+#include "row_values.cuh"
+#include "rows.h"
+
+namespace fanout {
+namespace {
+
+constexpr int kErrInval = 1;  // FANOUT_EINVAL
+constexpr int kWarps = 8;
+
+// The (row, head) pair of this half-warp and the byte of the pools its row starts at;
+// false when there is nothing to do.
+__device__ __forceinline__ bool item_of(const Q8RowParams& p, uint32_t& r, uint32_t& h,
+                                        int64_t& at) {
+    const uint32_t item = blockIdx.x * (2 * kWarps) + (threadIdx.x >> 4);  // < 2^31 + 16 (host check)
+    r = item / static_cast<uint32_t>(p.H_kv);
+    h = item - r * static_cast<uint32_t>(p.H_kv);
+    if (r >= static_cast<uint32_t>(p.n_rows)) return false;
+    const int64_t slot = __ldg(p.slots + r);
+    if (slot < 0) return false;  // a padded row
+    if (slot >= p.n_slots) {
+        if ((threadIdx.x & 15) == 0) atomicCAS(p.err, 0, kErrInval);
+        return false;
+    }
+    const int64_t page = slot >> p.page_shift;
+    const int32_t in_page = static_cast<int32_t>(slot) & ((1 << p.page_shift) - 1);
+    at = ((((page * p.H_kv + h) << p.page_shift) + in_page) * kHD);
+    return true;
+}
+
+__global__ void __launch_bounds__(32 * kWarps) append_q8_kernel(const Q8RowParams p) {
+    const int part = threadIdx.x & 7;
+    const bool is_v = threadIdx.x & 8;
+    uint32_t r, h;
+    int64_t at;
+    if (!item_of(p, r, h, at)) return;
+    const __nv_bfloat16* src = is_v ? p.v_rows + static_cast<int64_t>(r) * p.v_stride
+                                    : p.k_rows + static_cast<int64_t>(r) * p.k_stride;
+    uint32_t raw[8];
+    src += h * kHD + part * 16;
+    if (p.align32) {  // one load of a whole sector
+        ptx::ld_global_v8(src, raw);
+    } else {
+        const uint4* from = reinterpret_cast<const uint4*>(src);
+        const uint4 a = __ldg(from), b = __ldg(from + 1);
+        raw[0] = a.x, raw[1] = a.y, raw[2] = a.z, raw[3] = a.w;
+        raw[4] = b.x, raw[5] = b.y, raw[6] = b.z, raw[7] = b.w;
+    }
+    uint32_t top2 = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top2 = ptx::max_nan_bf16x2(top2, raw[i] & 0x7fff7fffu);
+    if ((top2 & 0x7fffu) > 0x7f80u || (top2 >> 16) > 0x7f80u) {
+        // a NaN is recorded, and held as 0: it must not reach other rows
+        atomicCAS(p.err, 0, kErrInval);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if ((raw[i] & 0x7fffu) > 0x7f80u) raw[i] &= 0xffff0000u;
+            if ((raw[i] & 0x7fff0000u) > 0x7f800000u) raw[i] &= 0xffffu;
+        }
+    }
+    const float gs = is_v ? p.v_scale : p.k_scale, rcp = is_v ? p.v_rcp : p.k_rcp;
+    const float most = 512.f * gs;  // (codes saturate at 448, so 512 stands for what is larger)
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float y[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t v = raw[2 * i + (c >> 1)];
+            const float x = __uint_as_float(c & 1 ? v & 0xffff0000u : v << 16);
+            // (a zero's sign does not pass the correction)
+            y[c] = copysignf(quotient(fminf(fmaxf(x, -most), most), gs, rcp), x);
+        }
+        w[i] = e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16;
+    }
+    *reinterpret_cast<uint4*>((is_v ? p.v_pool : p.k_pool) + at + part * 16) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__global__ void __launch_bounds__(32 * kWarps) read_q8_kernel(const Q8RowParams p) {
+    const int part = threadIdx.x & 7;
+    const bool is_v = threadIdx.x & 8;
+    uint32_t r, h;
+    int64_t at;
+    if (!item_of(p, r, h, at)) return;
+    const uint4 c = __ldg(
+        reinterpret_cast<const uint4*>((is_v ? p.v_pool : p.k_pool) + at + part * 16));
+    const float gs = is_v ? p.v_scale : p.k_scale;
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    uint32_t out[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t a, b;
+        ptx::f16x2_of_e4m3x4(w[i], a, b);
+        out[2 * i] = ptx::pack_bf16x2(lo_f16_f32(a) * gs, hi_f16_f32(a) * gs);
+        out[2 * i + 1] = ptx::pack_bf16x2(lo_f16_f32(b) * gs, hi_f16_f32(b) * gs);
+    }
+    __nv_bfloat16* dst = is_v ? p.v_out + static_cast<int64_t>(r) * p.v_stride
+                              : p.k_out + static_cast<int64_t>(r) * p.k_stride;
+    dst += h * kHD + part * 16;
+    if (p.align32) {
+        ptx::st_global_v8(dst, out);
+    } else {
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(out[0], out[1], out[2], out[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(out[4], out[5], out[6], out[7]);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_q8_rows(const Q8RowParams& p, bool read, cudaStream_t stream) {
+    const int64_t items = static_cast<int64_t>(p.n_rows) * p.H_kv;
+    if (items <= 0) return cudaSuccess;
+    const unsigned grid = static_cast<unsigned>((items + 2 * kWarps - 1) / (2 * kWarps));
+    if (read) read_q8_kernel<<<grid, 32 * kWarps, 0, stream>>>(p);
+    else append_q8_kernel<<<grid, 32 * kWarps, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace fanout

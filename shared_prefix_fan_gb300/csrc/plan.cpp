@@ -13,7 +13,7 @@
 //     branch's private suffix [P, P + S_b) is a key range for tiles of that
 //     branch's rows only.
 //   * Otherwise every branch's tiles take its whole context [0, P + S_b).
-//   * Row plans (windowed or 4-bit attention) trim each range to the keys its
+//   * Row plans (windowed, 4-bit, 8-bit and tree attention) trim each range to the keys its
 //     rows see: it starts at the page of the first row's oldest key, and the
 //     first keys that stay visible are swept as extra tiles in front of it, so
 //     that a windowed row block is still one unit (make_row_ranges).
@@ -383,7 +383,8 @@ void make_row_ranges(const PlanInput& in, bool share, std::vector<Range>& ranges
     bool reaches = false;  // some row's window holds shared keys
     for (int32_t b = 0; b < B; ++b)
         for (int32_t t = tok0[b]; t < tok0[b + 1]; ++t) {
-            if (in.causal) tok_pos[t] = P + in.suffix_lens[b] + tail - tok0[b + 1] + t;
+            if (in.causal)
+                tok_pos[t] = P + in.suffix_lens[b] + tail - tok0[b + 1] + (in.tree ? tok0[b] : t);
             reaches = reaches || oldest(t) < P;
         }
     const bool shared = share && active >= 2 && P > 0 && reaches;
@@ -427,13 +428,19 @@ void make_row_ranges(const PlanInput& in, bool share, std::vector<Range>& ranges
             const int32_t end = P + in.suffix_lens[b] + tail, base = split_at;
             for (int32_t t = tok0[b]; t < tok0[b + 1]; t += tpt) {
                 const int32_t n = std::min(tpt, tok0[b + 1] - t);
-                const int32_t hi = in.causal ? std::min(end, tok_pos[t + n - 1] + 1) : end;
+                const int32_t hi =
+                    in.causal && !in.tree ? std::min(end, tok_pos[t + n - 1] + 1) : end;
                 bool complete = true;
                 for (int32_t i = t; i < t + n; ++i) complete = complete && !in_shared[i];
                 emit(h, b, t, n, base, oldest(t), hi, W > 0 ? std::min(in.sinks, hi) : 0,
                      complete);
             }
         }
+    }
+    if (in.tree) {
+        tok_pos.resize(2 * static_cast<size_t>(R));
+        for (int32_t b = 0; b < B; ++b)
+            for (int32_t t = tok0[b]; t < tok0[b + 1]; ++t) tok_pos[R + t] = tok_pos[t] + t - tok0[b];
     }
 }
 

@@ -5,6 +5,7 @@
 #include <vector>
 
 #include "fanout_internal.h"
+#include "rows.h"
 
 namespace fanout {
 
@@ -25,6 +26,9 @@ struct PlanInput {
     int32_t window = 0;    // > 0: a row at pos sees keys > pos - window ...
     int32_t sinks = 0;     // ... and keys < sinks
     int32_t row_bytes = 2 * 2 * kHD;  // K and V of one token and KV head
+    // Row plans of drafted trees (causal): a branch's new tokens all sit behind the same
+    // keys, and any of them may see any other.
+    int32_t tree = 0;
 };
 
 // A key range of the plan: the rows of n_tok tokens from tok_begin (one KV
@@ -52,7 +56,9 @@ struct Plan {
     int32_t tpt = 0;                 // tokens per 128-row query tile
     int32_t nq = 1;                  // query tiles per unit (1 or 2)
     bool need_merge = false;
-    std::vector<int32_t> tok_pos;    // row plans: absolute position of every token
+    // row plans: absolute position of every token; drafted trees: the number of keys before
+    // its branch's drafted tokens, then (as many again) every token's own key
+    std::vector<int32_t> tok_pos;
     int32_t split_at = 0;            // keys below are the shared range's (0: no shared range)
     std::vector<PlanRange> ranges;   // the key ranges the units were cut from
     std::vector<int32_t> unit_range; // per unit: its range
@@ -83,10 +89,13 @@ struct CallArgs {
     int64_t R;
     unsigned long long wait_limit_ns;
     int32_t window, sinks;   // see PlanInput
-    int32_t q4;              // 1: 4-bit pools
-    float k_scale, v_scale;  // their scales
+    int32_t pool;            // a Pool
+    float k_scale, v_scale;  // its scales (bf16: 1)
     int32_t fused_merge;     // 1: merge inside the attention kernel when the grid fits
     uint32_t epoch;          // this call's flag value (never 0; distinct from the last call's)
+    const uint32_t* masks = nullptr;  // drafted trees: see RowParams
+    const int32_t* positions = nullptr;
+    int32_t mask_words = 0;
 };
 
 // Device layout of a plan inside one scratch buffer.
@@ -114,7 +123,7 @@ int validate_call(const void* q, const void* k, const void* v, const int32_t* pa
                   const int32_t* suffix_lens, int32_t B, int32_t P, int32_t max_pages,
                   int32_t num_pages, int32_t page_size, float scale, int32_t out_dtype,
                   const void* out);
-// Whether a 4-bit pool's scale is in the supported range.
-bool q4_scale_ok(float gs);
+// Whether a 4-bit or 8-bit pool's scale is in the supported range.
+bool pool_scale_ok(float gs);
 
 }  // namespace fanout

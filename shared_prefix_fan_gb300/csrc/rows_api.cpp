@@ -1,5 +1,6 @@
-// rows_api.cpp -- the C entry points of the device page tables and of the
-// 4-bit rows: argument checks and launches (kernels in tables.cu, kv_q4.cu).
+// rows_api.cpp -- the C entry points of the device page tables, of the 4-bit and 8-bit
+// rows and of drafted trees: argument checks and launches (kernels in tables.cu,
+// kv_q4.cu, kv_q8.cu, tree.cu).
 #include <cuda_runtime.h>
 
 #include <cstddef>
@@ -106,7 +107,7 @@ int check_rows(const void* k_rows, const void* v_rows, const void* k_pages, cons
     if (d != kHD) return FANOUT_EUNSUPPORTED;
     if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
         return FANOUT_EUNSUPPORTED;
-    if (!q4_scale_ok(k_scale) || !q4_scale_ok(v_scale)) return FANOUT_EINVAL;
+    if (!pool_scale_ok(k_scale) || !pool_scale_ok(v_scale)) return FANOUT_EINVAL;
     if (static_cast<int64_t>(n_rows) * H_kv >= (1LL << 31)) return FANOUT_EUNSUPPORTED;
     if (n_rows == 0) return FANOUT_OK;
     const int64_t row = static_cast<int64_t>(H_kv) * d;
@@ -131,12 +132,45 @@ int run_rows(Q4RowParams& p, bool read, int32_t page_size, fanout_stream_t strea
     return status_from_cuda(launch_q4_rows(p, read, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+int run_rows_q8(Q8RowParams& p, bool read, int32_t page_size, fanout_stream_t stream) {
+    const void* k = read ? static_cast<const void*>(p.k_out) : p.k_rows;
+    const void* v = read ? static_cast<const void*>(p.v_out) : p.v_rows;
+    p.align32 = aligned(k, 32) && aligned(v, 32) && p.k_stride % 16 == 0 && p.v_stride % 16 == 0;
+    p.k_rcp = 1.0f / p.k_scale;
+    p.v_rcp = 1.0f / p.v_scale;
+    p.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+    const cudaError_t ce = err_word_ptr(&p.err);
+    if (ce != cudaSuccess) return status_from_cuda(ce);
+    return status_from_cuda(launch_q8_rows(p, read, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Whether every array is there when the call has rows (`any`) and starts where its type does.
+struct Typed {
+    const void* at;
+    uintptr_t align;
+    bool needed;
+};
+template <size_t N>
+bool arrays_ok(const Typed (&arrays)[N]) {
+    for (const Typed& a : arrays)
+        if ((a.needed && !a.at) || !aligned(a.at, a.align)) return false;
+    return true;
+}
+template <size_t N>
+bool any_overlap_among(const Array (&written)[N]) {
+    for (size_t i = 0; i < N; ++i)
+        for (size_t j = i + 1; j < N; ++j)
+            if (overlap(written[i].at, written[i].bytes, written[j].at, written[j].bytes))
+                return true;
+    return false;
+}
+
 }  // namespace
 
 namespace fanout {
 // Quotients by 6 gs and sc gs (sc from 2^-9 to 448) and the values themselves
 // stay normal fp32 numbers inside these bounds.
-bool q4_scale_ok(float gs) { return gs >= 1e-30f && gs <= 1e30f; }
+bool pool_scale_ok(float gs) { return gs >= 1e-30f && gs <= 1e30f; }
 }  // namespace fanout
 
 extern "C" {
@@ -254,6 +288,175 @@ int fanout_kv_read_q4(const void* k_pages, const void* v_pages, const int64_t* s
     p.k_scale = k_scale;
     p.v_scale = v_scale;
     return run_rows(p, true, page_size, stream);
+}
+
+int fanout_kv_append_q8(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
+                        void* k_pages, void* v_pages, const int64_t* slots, int32_t n_rows,
+                        int32_t num_pages, int32_t H_kv, int32_t d, int32_t page_size,
+                        float k_scale, float v_scale, fanout_stream_t stream) {
+    const int st = check_rows(k_new, v_new, k_pages, v_pages, slots, n_rows, k_stride, v_stride,
+                              num_pages, H_kv, d, page_size, k_scale, v_scale);
+    if (st != FANOUT_OK || n_rows == 0) return st;
+    Q8RowParams p{};
+    p.k_rows = static_cast<const __nv_bfloat16*>(k_new);
+    p.v_rows = static_cast<const __nv_bfloat16*>(v_new);
+    p.k_pool = static_cast<uint8_t*>(k_pages);
+    p.v_pool = static_cast<uint8_t*>(v_pages);
+    p.slots = slots;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.n_slots = static_cast<int64_t>(num_pages) * page_size;
+    p.n_rows = n_rows;
+    p.H_kv = H_kv;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    return run_rows_q8(p, false, page_size, stream);
+}
+
+int fanout_kv_read_q8(const void* k_pages, const void* v_pages, const int64_t* slots,
+                      int32_t n_rows, int32_t num_pages, int32_t H_kv, int32_t d,
+                      int32_t page_size, float k_scale, float v_scale, void* k_out, void* v_out,
+                      int64_t k_stride, int64_t v_stride, fanout_stream_t stream) {
+    const int st = check_rows(k_out, v_out, k_pages, v_pages, slots, n_rows, k_stride, v_stride,
+                              num_pages, H_kv, d, page_size, k_scale, v_scale);
+    if (st != FANOUT_OK || n_rows == 0) return st;
+    Q8RowParams p{};
+    p.k_out = static_cast<__nv_bfloat16*>(k_out);
+    p.v_out = static_cast<__nv_bfloat16*>(v_out);
+    p.k_pool = static_cast<uint8_t*>(const_cast<void*>(k_pages));
+    p.v_pool = static_cast<uint8_t*>(const_cast<void*>(v_pages));
+    p.slots = slots;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.n_slots = static_cast<int64_t>(num_pages) * page_size;
+    p.n_rows = n_rows;
+    p.H_kv = H_kv;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    return run_rows_q8(p, true, page_size, stream);
+}
+
+int fanout_tree_rows(const int32_t* parents, const int32_t* page_table, int32_t num_branches,
+                     int32_t max_pages_per_branch, int32_t prefix_len, const int32_t* suffix_lens,
+                     const int32_t* add_lens, int32_t page_size, int64_t n_rows,
+                     int32_t mask_words, int32_t window, uint32_t* masks, int32_t* positions,
+                     int64_t* slots, fanout_stream_t stream) {
+    if (num_branches < 0 || max_pages_per_branch < 0 || prefix_len < 0 || page_size <= 0 ||
+        n_rows < 0 || mask_words <= 0 || window < 0)
+        return FANOUT_EINVAL;
+    if (num_branches > kMaxTableBranches || mask_words > kMaxTreeTokens / 32 || n_rows > 0x7fffffff)
+        return FANOUT_EUNSUPPORTED;
+    if (n_rows == 0) return FANOUT_OK;
+    const bool some = num_branches > 0;
+    const Typed arrays[] = {{parents, 4, some},     {page_table, 4, some && max_pages_per_branch > 0},
+                            {suffix_lens, 4, some}, {add_lens, 4, some},
+                            {masks, 4, true},       {positions, 4, true},
+                            {slots, 8, true}};
+    if (!arrays_ok(arrays)) return FANOUT_EINVAL;
+    const Array read[] = {{parents, 4 * n_rows},
+                          {page_table, 4LL * num_branches * max_pages_per_branch},
+                          {suffix_lens, 4LL * num_branches},
+                          {add_lens, 4LL * num_branches}};
+    const Array written[] = {{masks, 4 * n_rows * mask_words}, {positions, 4 * n_rows}, {slots, 8 * n_rows}};
+    if (any_overlap(read, written) || any_overlap_among(written)) return FANOUT_EINVAL;
+    TreeParams p{};
+    p.parents = parents;
+    p.page_table = page_table;
+    p.suffix_lens = suffix_lens;
+    p.lens = add_lens;
+    p.masks = masks;
+    p.positions = positions;
+    p.slots = slots;
+    p.num_branches = num_branches;
+    p.R = static_cast<int32_t>(n_rows);
+    p.words = mask_words;
+    p.window = window;
+    p.prefix_len = prefix_len;
+    p.page_size = page_size;
+    p.max_pages = max_pages_per_branch;
+    const cudaError_t ce = err_word_ptr(&p.err);
+    if (ce != cudaSuccess) return status_from_cuda(ce);
+    return status_from_cuda(launch_tree_rows(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int fanout_tree_accept(const int32_t* parents, const int64_t* draft_tokens,
+                       const int64_t* target_tokens, const int64_t* first_tokens,
+                       const int32_t* add_lens, int32_t num_branches, int64_t n_rows,
+                       int32_t* path, int32_t* counts, int64_t* next_tokens,
+                       fanout_stream_t stream) {
+    if (num_branches < 0 || n_rows < 0) return FANOUT_EINVAL;
+    if (num_branches > kMaxTableBranches || n_rows > 0x7fffffff) return FANOUT_EUNSUPPORTED;
+    if (n_rows == 0 && num_branches == 0) return FANOUT_OK;
+    const bool some = num_branches > 0, rows = n_rows > 0;
+    const Typed arrays[] = {{parents, 4, rows},       {draft_tokens, 8, rows},
+                            {target_tokens, 8, rows}, {first_tokens, 8, some},
+                            {add_lens, 4, some},      {path, 4, rows},
+                            {counts, 4, some},        {next_tokens, 8, some}};
+    if (!arrays_ok(arrays)) return FANOUT_EINVAL;
+    const Array read[] = {{parents, 4 * n_rows},
+                          {draft_tokens, 8 * n_rows},
+                          {target_tokens, 8 * n_rows},
+                          {first_tokens, 8LL * num_branches},
+                          {add_lens, 4LL * num_branches}};
+    const Array written[] = {{path, 4 * n_rows}, {counts, 4LL * num_branches}, {next_tokens, 8LL * num_branches}};
+    if (any_overlap(read, written) || any_overlap_among(written)) return FANOUT_EINVAL;
+    TreeParams p{};
+    p.parents = parents;
+    p.draft = draft_tokens;
+    p.target = target_tokens;
+    p.first = first_tokens;
+    p.lens = add_lens;
+    p.path = path;
+    p.counts = counts;
+    p.next = next_tokens;
+    p.num_branches = num_branches;
+    p.R = static_cast<int32_t>(n_rows);
+    const cudaError_t ce = err_word_ptr(&p.err);
+    if (ce != cudaSuccess) return status_from_cuda(ce);
+    return status_from_cuda(launch_tree_accept(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int fanout_kv_keep(void* k_pages, void* v_pages, int32_t kv_type, const int32_t* page_table,
+                   int32_t num_branches, int32_t max_pages_per_branch, int32_t prefix_len,
+                   const int32_t* suffix_lens, const int32_t* add_lens, const int32_t* path,
+                   const int32_t* counts, int64_t n_rows, int32_t num_pages, int32_t H_kv,
+                   int32_t d, int32_t page_size, fanout_stream_t stream) {
+    if (kv_type != FANOUT_KV_BF16 && kv_type != FANOUT_KV_Q4 && kv_type != FANOUT_KV_Q8)
+        return FANOUT_EINVAL;
+    if (num_branches < 0 || max_pages_per_branch < 0 || prefix_len < 0 || n_rows < 0 ||
+        num_pages <= 0 || H_kv <= 0 || d <= 0 || page_size <= 0)
+        return FANOUT_EINVAL;
+    if (d != kHD) return FANOUT_EUNSUPPORTED;
+    if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
+        return FANOUT_EUNSUPPORTED;
+    if (num_branches > kMaxTableBranches || n_rows > 0x7fffffff ||
+        static_cast<int64_t>(num_branches) * H_kv > 0x7fffffff)
+        return FANOUT_EUNSUPPORTED;
+    if (n_rows == 0 || num_branches == 0) return FANOUT_OK;
+    const Typed arrays[] = {{k_pages, 16, true}, {v_pages, 16, true},
+                            {page_table, 4, max_pages_per_branch > 0},
+                            {suffix_lens, 4, true}, {add_lens, 4, true},
+                            {path, 4, true}, {counts, 4, true}};
+    if (!arrays_ok(arrays)) return FANOUT_EINVAL;
+    TreeParams p{};
+    p.page_table = page_table;
+    p.suffix_lens = suffix_lens;
+    p.lens = add_lens;
+    p.path = const_cast<int32_t*>(path);
+    p.counts = const_cast<int32_t*>(counts);
+    p.k_pool = static_cast<uint8_t*>(k_pages);
+    p.v_pool = static_cast<uint8_t*>(v_pages);
+    p.pool = static_cast<Pool>(kv_type);
+    p.num_branches = num_branches;
+    p.R = static_cast<int32_t>(n_rows);
+    p.prefix_len = prefix_len;
+    p.page_size = page_size;
+    p.max_pages = max_pages_per_branch;
+    p.num_pages = num_pages;
+    p.H_kv = H_kv;
+    const cudaError_t ce = err_word_ptr(&p.err);
+    if (ce != cudaSuccess) return status_from_cuda(ce);
+    return status_from_cuda(launch_kv_keep(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

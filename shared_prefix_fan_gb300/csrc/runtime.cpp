@@ -52,6 +52,21 @@ int map_pool(CUtensorMap* m, const void* base, int64_t rows, int32_t box_rows) {
                : FANOUT_ECUDA;
 }
 
+// 8-bit pool viewed as [num_pages * H_kv * page][128] bytes; a box is one page of one KV
+// head, whose rows are one swizzle span.
+int map_pool_q8(CUtensorMap* m, const void* base, int64_t rows, int32_t box_rows) {
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(kHD), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(kHD)};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(kHD), static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t es[2] = {1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides,
+                       box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? FANOUT_OK
+               : FANOUT_ECUDA;
+}
+
 // q viewed as [R][H_q][128] bf16; a box is 128/G tokens x the G heads of one
 // KV head x 64 columns: one half of a 128-row tile, token-major.
 int map_q(CUtensorMap* m, const void* q, int64_t R, int32_t H_q, int32_t G, int32_t tpt) {
@@ -167,7 +182,10 @@ int launch_plan(const CallArgs& a, const Plan& pl, const Layout& L, uint8_t* bas
     const int64_t pool_rows = static_cast<int64_t>(a.num_pages) * a.H_kv * a.page_size;
     int st;
     if ((st = map_q(&tm_q, a.q, a.R, a.H_q, G, pl.tpt)) != FANOUT_OK) return st;
-    if (!a.q4) {
+    const Pool pool = static_cast<Pool>(a.pool);
+    if (pool == Pool::q8) {
+        if ((st = map_pool_q8(&tm_k, a.k, pool_rows, a.page_size)) != FANOUT_OK) return st;
+    } else if (pool == Pool::bf16) {
         if ((st = map_pool(&tm_k, a.k, pool_rows, a.page_size)) != FANOUT_OK) return st;
         if ((st = map_pool(&tm_v, a.v, pool_rows, a.page_size)) != FANOUT_OK) return st;
     }
@@ -175,7 +193,7 @@ int launch_plan(const CallArgs& a, const Plan& pl, const Layout& L, uint8_t* bas
     cudaError_t ce = err_word_ptr(&err);
     if (ce != cudaSuccess) return status_of(ce);
 
-    SplitParams p;
+    RowParams p;
     p.page_table = a.page_table;
     p.units = reinterpret_cast<const Unit*>(base + L.units);
     p.cta_first = reinterpret_cast<const int32_t*>(base + L.cta);
@@ -198,7 +216,7 @@ int launch_plan(const CallArgs& a, const Plan& pl, const Layout& L, uint8_t* bas
     // Formed in 64 bits, where neither a scale at the end of fp32's range nor k_scale moves
     // it out of range before their product is there; without k_scale the bits of one fp32
     // product.
-    const double scale_log2 = static_cast<double>(a.scale) * (a.q4 ? a.k_scale : 1.0f) *
+    const double scale_log2 = static_cast<double>(a.scale) * (pool != Pool::bf16 ? a.k_scale : 1.0f) *
                               static_cast<double>(1.4426950408889634f);
     p.scale_log2 = static_cast<float>(
         std::min(scale_log2, static_cast<double>(std::numeric_limits<float>::max())));
@@ -209,6 +227,9 @@ int launch_plan(const CallArgs& a, const Plan& pl, const Layout& L, uint8_t* bas
     p.k_pool = static_cast<const uint8_t*>(a.k);
     p.v_pool = static_cast<const uint8_t*>(a.v);
     p.o_scale = a.v_scale;
+    p.masks = a.masks;
+    p.positions = a.positions;
+    p.mask_words = a.mask_words;
     // No shorter than copies in flight may take to land: attn_fwd.cu bounds its drain by it too.
     p.wait_limit_ns = std::max(a.wait_limit_ns, 1000000ull);
     MergeParams& m = p.merge;
@@ -239,8 +260,11 @@ int launch_plan(const CallArgs& a, const Plan& pl, const Layout& L, uint8_t* bas
 
     if (ev_before) cudaEventRecord(ev_before, stream);
     p.fused_merge = fuse ? 1 : 0;
-    ce = p.tok_pos ? launch_attn_rows(p, tm_q, tm_k, tm_v, a.q4 != 0, pl.n_cta(), stream)
-                   : launch_split_attn(p, tm_q, tm_k, tm_v, pl.n_cta(), fuse, stream);
+    ce = !p.tok_pos          ? launch_split_attn(p, tm_q, tm_k, tm_v, pl.n_cta(), fuse, stream)
+         : p.masks           ? launch_attn_tree(p, tm_q, tm_k, tm_v, pool, pl.n_cta(), stream)
+         : pool == Pool::q8  ? launch_attn_rows_q8(p, tm_q, tm_k, pl.n_cta(), stream)
+         : pool == Pool::q4  ? launch_attn_rows_q4(p, tm_q, pl.n_cta(), stream)
+                             : launch_attn_rows(p, tm_q, tm_k, tm_v, pl.n_cta(), stream);
     if (ce != cudaSuccess && fuse) {
         (void)cudaGetLastError();  // refused as a cooperative launch: merge separately
         p.fused_merge = 0;
