@@ -113,7 +113,7 @@ struct Cfg {
                                kRegsLaunch * kThreads,
                   "register split");
     // K and V tiles that the products read (8-bit pools: K as it is cached), raw ones.
-    static constexpr int kKStages = !kQ8 ? 2 : NQ == 1 ? 4 : 3, kVStages = 2;
+    static constexpr int kKStages = !kQ8 ? 2 : NQ == 1 ? 4 : 2, kVStages = 2;
     static constexpr int kStages = kKStages + kVStages;
     static constexpr int kKBytes = kQ8 ? kBN * kHD : kTileBytes;
     static constexpr int kRaw = kQ4 ? (NQ == 1 ? 6 : 2) : kQ8 ? (NQ == 1 ? 3 : 2) : 0;
@@ -254,7 +254,7 @@ __device__ void producer_warp(const RowParams& p, const Smem<NQ, F>& sm, const C
     const int lane = threadIdx.x & 31;
     volatile int* abort = sm.abort_flag();
     const int ps = p.page_size;
-    const int64_t block = static_cast<int64_t>(ps) * (C::kQ4 ? kQ4RowBytes : kHD);
+    const int64_t block = static_cast<int64_t>(ps) * kQ4RowBytes;
     // the barriers of tile `pos` in the ring this warp fills: raw tiles (8-bit pools: V
     // only), or the tiles that the products read
     auto is_raw = [](uint32_t pos) { return C::kQ4 || (C::kQ8 && (pos & 1u)); };
@@ -384,7 +384,7 @@ __device__ void producer_warp(const RowParams& p, const Smem<NQ, F>& sm, const C
                     ok = wait_for(empty, parity_of(it) ^ 1u, 2);
                     if (!ok) break;
                     const uint32_t full = full_of(it);
-                    if (is_raw(it)) {
+                    if (C::kQ4) {
                         if (lane == 0)
                             ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(n_pg) *
                                                                  static_cast<uint32_t>(block));
@@ -396,12 +396,16 @@ __device__ void producer_warp(const RowParams& p, const Smem<NQ, F>& sm, const C
                                            static_cast<uint32_t>(block), full);
                     } else if (C::kQ8) {
                         // a row is one swizzled line; scores of rows past the pages are masked
+                        const uint32_t dst =
+                            kv == 0 ? sm.tile(it)
+                                    : sm.base + C::kSmemRaw + C::raw_stage(it) * C::kRawBytes;
                         if (lane == 0)
                             ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(n_pg * ps) * 128u);
                         __syncwarp();
                         if (lane < n_pg)
-                            ptx::tma_load_2d(sm.tile(it) + static_cast<uint32_t>(lane * ps) * 128u,
-                                             tm_k, full, 0, static_cast<int>(head * ps));
+                            ptx::tma_load_2d(dst + static_cast<uint32_t>(lane * ps) * 128u,
+                                             kv == 0 ? tm_k : tm_v, full, 0,
+                                             static_cast<int>(head * ps));
                     } else {
                         const bool partial = kv == 1 && (n_valid < kBN || front > 0);
                         const uint32_t bar = partial ? sm.bar(C::BAR_AUX) : full;
@@ -695,18 +699,20 @@ __device__ void widen_warp(const RowParams& p, const Smem<NQ, Pool::q4>& sm, int
     }
 }
 
-// 8-bit pools: four warps widen every V tile to f16 (exact), 32 rows each. Eight lanes
-// take a row, 16 values each, so loads are contiguous; lanes of the upper 64 columns
-// store their two pieces in the other order, so that the 8 lanes of a store phase cover
-// all 8 sixteen-byte columns. Rows that no row of the unit sees become zeros.
+// 8-bit pools: four warps widen every V tile to f16 (exact), 32 rows each. A lane takes 16
+// values of a row; the raw tile and the 16-bit one are swizzled alike, and 8 lanes that
+// load or store together take 64 values of a row r and of r ^ 5: those differ in the bits
+// that keep their loads (of 4 neighbouring pieces) and their stores (of every second) out
+// of each other's banks, so that nothing has to be selected. Rows that no row of the unit
+// sees become zeros.
 template <int NQ>
 __device__ void widen_warp_e4m3(const RowParams& p, const Smem<NQ, Pool::q8>& sm, int w) {
     using C = Cfg<NQ, Pool::q8>;
     const int lane = threadIdx.x & 31;
-    const int part = lane & 7, swap = part >> 2;
-    const int row0 = w * 32 + (lane >> 3);
-    const uint32_t from = row0 * 128 + part * 16;
-    const uint32_t to = (part >> 2) * kHalfBytes + row0 * 128;
+    // lane: piece of the half row, row or its partner, half of the row, one of two row pairs
+    const int part = lane & 3, half = (lane >> 3) & 1;
+    // rows 0 5, 1 4 (of a group of 8) in the first step, 2 7, 3 6 in the second
+    const int row0 = w * 32 + ((lane >> 4) ^ (lane & 4 ? 5 : 0));
     uint32_t it = 1;  // ring position of the next V tile
     const int ui_end = p.cta_first[blockIdx.x + 1];
     for (int ui = p.cta_first[blockIdx.x]; ui < ui_end; ++ui) {
@@ -717,45 +723,46 @@ __device__ void widen_warp_e4m3(const RowParams& p, const Smem<NQ, Pool::q8>& sm
             tl.tile(j, kt, last, front);
             const uint32_t rs = C::raw_stage(it), stage = C::stage(it);
             if (!warp_wait<NQ, Pool::q8>(p, sm, sm.bar(C::BAR_RFULL + rs), C::raw_parity(it), 40)) return;
-            const uint32_t raw = sm.base + C::kSmemRaw + rs * C::kRawBytes + from;
-            uint4 c[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                c[i] = ptx::ld_shared_v4(raw + i * 512);
-                const int r = row0 + 4 * i;
-                if (r < front || kt + r >= last) c[i] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            // (the raw stage is free once its words are in registers: see widen_warp)
-            uint32_t seen = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) seen ^= c[i].x ^ c[i].y ^ c[i].z ^ c[i].w;
-            const bool late = __all_sync(0xffffffffu, seen == 0x9e3779b9u);
-            if (lane == 0 && !late) ptx::mbar_arrive(sm.bar(C::BAR_REMPTY + rs));
             if (!warp_wait<NQ, Pool::q8>(p, sm, sm.bar(C::BAR_EMPTY + stage), C::parity(it) ^ 1u, 41))
                 return;
-            const uint32_t dst = sm.tile(it) + to;
+            const uint32_t raw = sm.base + C::kSmemRaw + rs * C::kRawBytes;
+            const uint32_t dst = sm.tile(it) + half * kHalfBytes;
+            const bool border = front > 0 || last - kt < kBN;
+#pragma unroll 1
+            for (int g = 0; g < 2; ++g) {  // two groups of 8 rows at a time
+                uint4 c[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                uint32_t o[8];
-                ptx::f16x2_of_e4m3x4(c[i].x, o[0], o[1]);
-                ptx::f16x2_of_e4m3x4(c[i].y, o[2], o[3]);
-                ptx::f16x2_of_e4m3x4(c[i].z, o[4], o[5]);
-                ptx::f16x2_of_e4m3x4(c[i].w, o[6], o[7]);
-                const uint32_t line = dst + i * 512;
-                const uint32_t key = static_cast<uint32_t>((row0 + 4 * i) & 7);
+                for (int i = 0; i < 4; ++i) {
+                    const int r = row0 ^ (i & 1 ? 2 : 0), line = (r + 16 * g + 8 * (i >> 1)) * 128;
+                    c[i] = ptx::ld_shared_v4(raw + line + ((((half << 2) + part) ^ (r & 7)) << 4));
+                }
+                if (border) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int q = h ^ swap;
-                    const uint32_t at = line + ((((part & 3) * 2 + q) ^ key) << 4);
-                    ptx::st_shared_v4(at, q ? o[4] : o[0], q ? o[5] : o[1], q ? o[6] : o[2],
-                                      q ? o[7] : o[3]);
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = (row0 ^ (i & 1 ? 2 : 0)) + 16 * g + 8 * (i >> 1);
+                        if (r < front || kt + r >= last) c[i] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = row0 ^ (i & 1 ? 2 : 0);
+                    const uint32_t at = dst + (r + 16 * g + 8 * (i >> 1)) * 128;
+                    const uint32_t p0 = static_cast<uint32_t>((2 * part) ^ (r & 7)) << 4;
+                    uint32_t o[8];
+                    ptx::f16x2_of_e4m3x4(c[i].x, o[0], o[1]);
+                    ptx::f16x2_of_e4m3x4(c[i].y, o[2], o[3]);
+                    ptx::f16x2_of_e4m3x4(c[i].z, o[4], o[5]);
+                    ptx::f16x2_of_e4m3x4(c[i].w, o[6], o[7]);
+                    ptx::st_shared_v4(at + p0, o[0], o[1], o[2], o[3]);
+                    ptx::st_shared_v4(at + (p0 ^ 16u), o[4], o[5], o[6], o[7]);
                 }
             }
+            // (every word has been used by now, so the raw stage is free)
             ptx::fence_proxy_async_smem();  // the MMAs read the tile
             __syncwarp();
             if (lane == 0) {
+                ptx::mbar_arrive(sm.bar(C::BAR_REMPTY + rs));
                 ptx::mbar_arrive(sm.bar(C::BAR_FULL + stage));
-                if (late) ptx::mbar_arrive(sm.bar(C::BAR_REMPTY + rs));
             }
         }
     }
@@ -1343,7 +1350,7 @@ __global__ void __launch_bounds__(Cfg<NQ, F>::kThreads, 1)
     if (warp == 0 && lane == 0) {
         ptx::prefetch_tmap(&tm_q);
         if (!C::kQ4) ptx::prefetch_tmap(&tm_k);
-        if (!C::kF16) ptx::prefetch_tmap(&tm_v);
+        if (!C::kQ4) ptx::prefetch_tmap(&tm_v);
     }
     if (warp == 1) {
         ptx::tmem_alloc(ptx::smem_u32(sm.tmem_slot()), kTmemCols);

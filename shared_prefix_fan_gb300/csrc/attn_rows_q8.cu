@@ -4,10 +4,10 @@
 namespace fanout {
 
 cudaError_t launch_attn_rows_q8(const RowParams& p, const CUtensorMap& tm_q,
-                                const CUtensorMap& tm_k, int grid, cudaStream_t stream) {
-    const CUtensorMap none{};
-    return p.nq == 2 ? launch_nq<2, Pool::q8, false>(p, tm_q, tm_k, none, grid, stream)
-                     : launch_nq<1, Pool::q8, false>(p, tm_q, tm_k, none, grid, stream);
+                                const CUtensorMap& tm_k, const CUtensorMap& tm_v, int grid,
+                                cudaStream_t stream) {
+    return p.nq == 2 ? launch_nq<2, Pool::q8, false>(p, tm_q, tm_k, tm_v, grid, stream)
+                     : launch_nq<1, Pool::q8, false>(p, tm_q, tm_k, tm_v, grid, stream);
 }
 
 }  // namespace fanout

@@ -68,7 +68,8 @@ cudaError_t launch_attn_rows(const RowParams& p, const CUtensorMap& tm_q, const 
 cudaError_t launch_attn_rows_q4(const RowParams& p, const CUtensorMap& tm_q, int grid,
                                 cudaStream_t stream);
 cudaError_t launch_attn_rows_q8(const RowParams& p, const CUtensorMap& tm_q,
-                                const CUtensorMap& tm_k, int grid, cudaStream_t stream);
+                                const CUtensorMap& tm_k, const CUtensorMap& tm_v, int grid,
+                                cudaStream_t stream);
 cudaError_t launch_attn_tree(const RowParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                              const CUtensorMap& tm_v, Pool pool, int grid, cudaStream_t stream);
 cudaError_t launch_q8_rows(const Q8RowParams& p, bool read, cudaStream_t stream);

@@ -185,6 +185,7 @@ int launch_plan(const CallArgs& a, const Plan& pl, const Layout& L, uint8_t* bas
     const Pool pool = static_cast<Pool>(a.pool);
     if (pool == Pool::q8) {
         if ((st = map_pool_q8(&tm_k, a.k, pool_rows, a.page_size)) != FANOUT_OK) return st;
+        if ((st = map_pool_q8(&tm_v, a.v, pool_rows, a.page_size)) != FANOUT_OK) return st;
     } else if (pool == Pool::bf16) {
         if ((st = map_pool(&tm_k, a.k, pool_rows, a.page_size)) != FANOUT_OK) return st;
         if ((st = map_pool(&tm_v, a.v, pool_rows, a.page_size)) != FANOUT_OK) return st;
@@ -262,7 +263,7 @@ int launch_plan(const CallArgs& a, const Plan& pl, const Layout& L, uint8_t* bas
     p.fused_merge = fuse ? 1 : 0;
     ce = !p.tok_pos          ? launch_split_attn(p, tm_q, tm_k, tm_v, pl.n_cta(), fuse, stream)
          : p.masks           ? launch_attn_tree(p, tm_q, tm_k, tm_v, pool, pl.n_cta(), stream)
-         : pool == Pool::q8  ? launch_attn_rows_q8(p, tm_q, tm_k, pl.n_cta(), stream)
+         : pool == Pool::q8  ? launch_attn_rows_q8(p, tm_q, tm_k, tm_v, pl.n_cta(), stream)
          : pool == Pool::q4  ? launch_attn_rows_q4(p, tm_q, pl.n_cta(), stream)
                              : launch_attn_rows(p, tm_q, tm_k, tm_v, pl.n_cta(), stream);
     if (ce != cudaSuccess && fuse) {
