@@ -98,6 +98,9 @@ constexpr int kQWarps = 2;
 constexpr int kWarpSoftmax = 4;  // first softmax warp
 constexpr int kWarpWiden = 12;   // first widening warp
 constexpr int kFacBufs = 4;      // units whose row factors are held
+// Barriers of a softmax group: S there; the first half of P there (and O rescaled), all of
+// it; a unit's last product done; two for the join.
+enum { SFULL = 0, PHALF = 1, PFULL = 2, ODONE = 3, JOIN = 4, kGroupBars = 6 };
 
 // What differs between the pools: threads, registers a thread at launch and after the
 // warpgroups' split (whose sum must not exceed what the block was launched with), rings.
@@ -118,6 +121,11 @@ struct Cfg {
     static constexpr int kKBytes = kQ8 ? kBN * kHD : kTileBytes;
     static constexpr int kRaw = kQ4 ? (NQ == 1 ? 6 : 2) : kQ8 ? (NQ == 1 ? 3 : 2) : 0;
     static constexpr int kRawBytes = kQ4 ? kBN * kQ4RowBytes : kBN * kHD;
+    // The product over P's first half starts while the softmax works on its second. (bf16
+    // pools, window prefill 164 -> 158 us, window over 32 branches 99 -> 97; 8 bits, prefill
+    // 1411 -> 1400; 4 bits, prefill 1449 -> 1428, but 32 branches over 65536 keys 823 -> 846,
+    // so not there.)
+    static constexpr bool kEarlyP = !kQ4;
     // P is 2^lift times the probability's numerator
     static constexpr float kLiftLog2 = kF16 ? 7.0f : 0.0f, kUnlift = kF16 ? 0.0078125f : 1.0f;
     static constexpr uint32_t kIdescQK = kQ8   ? ptx::idesc_e4m3_f32(kBM, kBN)
@@ -144,8 +152,8 @@ struct Cfg {
     static constexpr int BAR_OFREE = BAR_QREADY + NQ;
     static constexpr int BAR_AUX = BAR_OFREE + 1;
     static constexpr int BAR_DRAIN = BAR_AUX + 1;
-    static constexpr int BAR_GROUP = BAR_DRAIN + 1;  // + 5 x + {SFULL, PFULL, ODONE, JOIN, JOIN + 1}
-    static constexpr int kNumBars = BAR_GROUP + 10;
+    static constexpr int BAR_GROUP = BAR_DRAIN + 1;  // + kGroupBars x + {SFULL, ...}
+    static constexpr int kNumBars = BAR_GROUP + 2 * kGroupBars;
     static constexpr int kSmemMisc = kSmemBar + kNumBars * 8;
     static constexpr int kSmemJoin = (kSmemMisc + 16 + 15) & ~15;  // float2 [2][2][128]
     static constexpr int kSmemFac = kSmemJoin + 2 * 2 * kBM * 8;  // uint8 [kFacBufs][NQ][128]
@@ -173,7 +181,6 @@ struct Cfg {
 };
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;
-enum { SFULL = 0, PFULL = 1, ODONE = 2, JOIN = 3 };
 
 template <int NQ, Pool F>
 struct Smem {
@@ -181,7 +188,7 @@ struct Smem {
     uint32_t base;  // shared-window address of the 1024-aligned base
     uint8_t* ptr;   // generic pointer to the same place
     __device__ uint32_t bar(int i) const { return base + C::kSmemBar + 8u * i; }
-    __device__ uint32_t gbar(int x, int which) const { return bar(C::BAR_GROUP + 5 * x + which); }
+    __device__ uint32_t gbar(int x, int which) const { return bar(C::BAR_GROUP + kGroupBars * x + which); }
     __device__ uint32_t* tmem_slot() const { return reinterpret_cast<uint32_t*>(ptr + C::kSmemMisc); }
     __device__ volatile int* abort_flag() const {
         return reinterpret_cast<volatile int*>(ptr + C::kSmemMisc + 4);
@@ -830,9 +837,10 @@ struct Issuer {
     }
     // P written (and O rescaled), V widened or loaded, O free; and the tile at `next`,
     // which the S product that follows reads (any tile of the ring that is there, if
-    // none does).
+    // none does). The product over P's first half runs while the softmax still works on
+    // its second.
     __device__ __forceinline__ bool issue_pv(const PvOp& op, uint32_t next) {
-        const uint32_t pf = sm.gbar(op.x, PFULL);
+        const uint32_t pf = sm.gbar(op.x, C::kEarlyP ? PHALF : PFULL);
         const bool of = op.first && op.k > 0;
         if (!wait(pf, op.t & 1u, full(op.pos), full_par(op.pos), of ? sm.bar(C::BAR_OFREE) : pf,
                   of ? (op.k - 1) & 1u : op.t & 1u, full(next), full_par(next), 14))
@@ -842,9 +850,17 @@ struct Issuer {
         const uint32_t d = kColO + 128u * op.x;
         const uint64_t dv = ptx::sdesc_sw128(sm.tile(op.pos), kHalfBytes, 1024);
 #pragma unroll
-        for (int kk = 0; kk < kBN / 16; ++kk)
+        for (int kk = 0; kk < kBN / 32; ++kk)
             ptx::mma_f16_ts_if(d, a + 8u * kk, dv + 128u * kk, C::kIdescPV,
                                (!op.first || kk > 0) ? 1u : 0u, leader);
+        issued_any = true;
+        if (C::kEarlyP) {
+            if (!warp_wait<NQ, F>(p, sm, sm.gbar(op.x, PFULL), op.t & 1u, 15)) return false;
+            ptx::tc_fence_after();
+        }
+#pragma unroll
+        for (int kk = kBN / 32; kk < kBN / 16; ++kk)
+            ptx::mma_f16_ts_if(d, a + 8u * kk, dv + 128u * kk, C::kIdescPV, 1u, leader);
         if (op.last) commit(sm.gbar(op.x, ODONE));
         return true;
     }
@@ -1047,11 +1063,27 @@ struct Running {
     }
 };
 
-// One tile's softmax of this thread's row: P over the first 64 columns of S. Returns
-// the rescale factor. (One pass with the reference of the tiles before, starting over
-// when it must be raised, was slower: a prefill 1661 us against 1583.)
-template <bool kF16>
-__device__ __forceinline__ float softmax_tile(uint32_t colS, float sl2, Running& run) {
+// O's 128 columns times corr, in place.
+__device__ __forceinline__ void rescale(uint32_t colO, float corr, uint32_t (&r)[32]) {
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        __syncwarp();
+        ptx::tmem_ld32(colO + 32 * c, r);
+        ptx::tmem_ld_wait(r);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * corr);
+        ptx::tmem_st32(colO + 32 * c, r);
+    }
+}
+
+// One tile's softmax of this thread's row: P over the first 64 columns of S; `half` runs
+// once O is rescaled (where `held`: it holds products) and P's first half is written: the
+// product over it need not wait for the rest of the exponentials. (One pass with the
+// reference of the tiles before, starting over when it must be raised, was slower: a
+// prefill 1661 us against 1583.)
+template <bool kF16, typename Half>
+__device__ __forceinline__ void softmax_tile(uint32_t colS, uint32_t colO, float sl2, bool held,
+                                             bool row_valid, Running& run, Half half) {
     constexpr float kLift = Cfg<1, kF16 ? Pool::q4 : Pool::bf16>::kLiftLog2;
     const uint64_t sl2p = ptx::f32x2(sl2, sl2);
     uint64_t l[2] = {0ull, 0ull};
@@ -1075,10 +1107,18 @@ __device__ __forceinline__ float softmax_tile(uint32_t colS, float sl2, Running&
     mx = max32(s0, mx);
     const float corr = run.raise(mx * sl2, kLift, neg);
     const uint64_t negm = ptx::f32x2(neg, neg);
+    // O is rescaled in place: this S was issued after the group's previous product, so
+    // that one has completed. (Of a lane without a row nothing is used.)
+    if (held && __any_sync(0xffffffffu, row_valid && corr != 1.f)) {
+        ptx::tmem_ld_wait(s1);
+        rescale(colO, corr, s1);
+        ptx::tmem_ld32(colS + 32, s1);
+    }
     exp32<kF16>(s0, colS, sl2p, negm, l);
     ptx::tmem_ld_wait(s1);
     ptx::tmem_ld32(colS + 64, s0);
     exp32<kF16>(s1, colS + 16, sl2p, negm, l);
+    half();
     ptx::tmem_ld_wait(s0);
     ptx::tmem_ld32(colS + 96, s1);
     exp32<kF16>(s0, colS + 32, sl2p, negm, l);
@@ -1086,7 +1126,6 @@ __device__ __forceinline__ float softmax_tile(uint32_t colS, float sl2, Running&
     exp32<kF16>(s1, colS + 48, sl2p, negm, l);
     const uint64_t sum = ptx::add_f32x2(l[0], l[1]);
     run.l = run.l * corr + (ptx::lo_f32(sum) + ptx::hi_f32(sum));
-    return corr;
 }
 
 // 32 columns of a finished row to out (direct) or to its partial block; from 4-bit
@@ -1200,7 +1239,13 @@ __device__ void softmax_group(const RowParams& p, const Smem<NQ, F>& sm, uint32_
                 sl2 = fmaxf(fminf(sl2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23), 3e38f),
                             1.2e-38f);
             }
-            float corr = 1.f;
+            auto half = [&]() {
+                if (!C::kEarlyP) return;
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(sm.gbar(x, PHALF));
+            };
             if (active) {
                 if constexpr (Tree) {
                     if (!full)
@@ -1209,22 +1254,9 @@ __device__ void softmax_group(const RowParams& p, const Smem<NQ, F>& sm, uint32_
                 } else {
                     if (!full) mask_tile<C::kQ4>(colS, lim, lo, sink);
                 }
-                corr = softmax_tile<C::kF16>(colS, sl2, run);
-                if (!row_valid) corr = 1.f;  // nothing of this lane is used
-            }
-            // O is rescaled in place: this S was issued after the group's previous
-            // product, so that one has completed.
-            if (j > j0 && __any_sync(0xffffffffu, corr != 1.f)) {
-                uint32_t r[32];
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    __syncwarp();
-                    ptx::tmem_ld32(colO + 32 * c, r);
-                    ptx::tmem_ld_wait(r);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * corr);
-                    ptx::tmem_st32(colO + 32 * c, r);
-                }
+                softmax_tile<C::kF16>(colS, colO, sl2, j > j0, row_valid, run, half);
+            } else {
+                half();
             }
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
@@ -1338,6 +1370,7 @@ __global__ void __launch_bounds__(Cfg<NQ, F>::kThreads, 1)
         ptx::mbar_init(sm.bar(C::BAR_DRAIN), 1);
         for (int x = 0; x < 2; ++x) {
             ptx::mbar_init(sm.gbar(x, SFULL), 1);
+            ptx::mbar_init(sm.gbar(x, PHALF), kGroupWarps);
             ptx::mbar_init(sm.gbar(x, PFULL), kGroupWarps);
             ptx::mbar_init(sm.gbar(x, ODONE), 1);
             ptx::mbar_init(sm.gbar(x, JOIN), kGroupWarps);
