@@ -93,8 +93,6 @@ constexpr int kErrTimeout = 5;        // FANOUT_ETIMEOUT
 constexpr int kErrCuda = 3;           // FANOUT_ECUDA
 constexpr uint64_t kLingerNs = 1000000;  // a CTA's stay after a wait has given up
 constexpr int kGroupWarps = 4;
-constexpr int kWarpQ = 2;        // first warp of the Q conversion
-constexpr int kQWarps = 2;
 constexpr int kWarpSoftmax = 4;  // first softmax warp
 constexpr int kWarpWiden = 12;   // first widening warp
 constexpr int kFacBufs = 4;      // units whose row factors are held
@@ -471,150 +469,95 @@ __device__ void producer_warp(const RowParams& p, const Smem<NQ, F>& sm, const C
 }
 
 // ------------------------------------------------------------------ Q tiles
-// Two warps turn the rows of a loaded Q tile into f16 in place: a thread finds its
-// row's largest exponent, scales by a power of two and stores the 8 values of each
-// 16-byte piece in the order the widened K tiles have. Rows behind the unit's last
-// are left as they are (their scores are never used).
-template <int NQ>
-__device__ void q_warp(const RowParams& p, const Smem<NQ, Pool::q4>& sm, int w) {
-    using C = Cfg<NQ, Pool::q4>;
-    const int lane = threadIdx.x & 31;
-    uint32_t loads[2] = {0, 0};
-    const int ui_end = p.cta_first[blockIdx.x + 1];
-    for (int ui = p.cta_first[blockIdx.x]; ui < ui_end; ++ui) {
-        const Unit u = p.units[ui];
-        const int nq = unit_nq<NQ>(u, p.tpt);
-        for (int x = 0; x < nq; ++x) {
-            const uint32_t n = x == 0 ? loads[0]++ : loads[1]++;
-            if (!warp_wait<NQ, Pool::q4>(p, sm, sm.bar(C::BAR_QFULL + x), n & 1u, 50)) return;
-            const int rows = min(p.tpt, u.n_tok - x * p.tpt) * p.G;
-            for (int row = w * 32 + lane; row < rows; row += 32 * kQWarps) {
-                const uint32_t at = sm.base + C::kSmemQ + x * kQBytes + row * 128;
-                const uint32_t swz = static_cast<uint32_t>(row & 7) << 4;
-                auto piece = [&](int c) { return at + (c >> 3) * kHalfBytes + (((c & 7) << 4) ^ swz); };
-                uint32_t top[4] = {0, 0, 0, 0};
+// The warps that widen V tiles turn a unit's loaded Q tiles into what the products take,
+// in place, before its first V tile (which S, and so Q, comes before): 4 lanes a row, 32
+// values each, in pieces of 16 bytes. They find the row's largest exponent, scale by a
+// power of two and store. Rows behind the unit's last are left as they are (their scores
+// are never used).
+//
+// 4-bit pools: f16, the 8 values of a piece in the order the widened K tiles have.
+//
+// 8-bit pools: K stays in e4m3, so Q goes to the product in two e4m3 parts: a bf16 value
+// has 8 significant bits, e4m3 four, and x = upper + lower with upper = x rounded to e4m3
+// and lower the exact rest, whose own 4 bits hold it. A row's largest element goes into
+// [2^7, 2^8); elements below 2^-9 of that lose bits, each at most half of e4m3's smallest
+// step of 2^-9, 2^-17 of the row's largest. A step of the product takes 32 values: their
+// upper parts replace the first two of the four pieces that held them, their lower parts
+// the last two, and the step runs over the same 32 values of K twice. A row with an
+// infinity or a NaN is NaN.
+template <int NQ, Pool F>
+__device__ __forceinline__ bool convert_q(const RowParams& p, const Smem<NQ, F>& sm, const Unit& u, int w,
+                                          uint32_t (&loads)[2]) {
+    using C = Cfg<NQ, F>;
+    const int lane = threadIdx.x & 31, q = (lane & 3) * 4;
+    const int nq = unit_nq<NQ>(u, p.tpt);
+    for (int x = 0; x < nq; ++x) {
+        const uint32_t n = x == 0 ? loads[0]++ : loads[1]++;
+        if (!warp_wait<NQ, F>(p, sm, sm.bar(C::BAR_QFULL + x), n & 1u, 50)) return false;
+        const int rows = min(p.tpt, u.n_tok - x * p.tpt) * p.G;
+        // (whole warps go round: a row's lanes exchange its largest exponent)
 #pragma unroll 1
-                for (int q = 0; q < 16; q += 4) {
-                    uint4 v[4];
+        for (int row0 = w * 8; row0 < rows; row0 += 8 * kGroupWarps) {
+            const int row = row0 + (lane >> 2);
+            const uint32_t at = sm.base + C::kSmemQ + x * kQBytes + row * 128;
+            const uint32_t swz = static_cast<uint32_t>(row & 7) << 4;
+            auto piece = [&](int c) { return at + (c >> 3) * kHalfBytes + (((c & 7) << 4) ^ swz); };
+            uint4 v[4];
+            uint32_t t = 0;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) v[c] = ptx::ld_shared_v4(piece(q + c));
+            for (int c = 0; c < 4; ++c) v[c] = ptx::ld_shared_v4(piece(q + c));
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        top[0] = ptx::max_abs_bf16x2(top[0], v[c].x);
-                        top[1] = ptx::max_abs_bf16x2(top[1], v[c].y);
-                        top[2] = ptx::max_abs_bf16x2(top[2], v[c].z);
-                        top[3] = ptx::max_abs_bf16x2(top[3], v[c].w);
-                    }
-                }
-                const uint32_t t = ptx::max_abs_bf16x2(ptx::max_abs_bf16x2(top[0], top[1]),
-                                                       ptx::max_abs_bf16x2(top[2], top[3]));
-                const int e = max((t >> 7) & 0xff, (t >> 23) & 0xff);
-                // largest element to [2^14, 2^15); infinities stay, tiny rows at most 2^100
-                const int k = e == 255 ? 0 : min(141 - e, 100);
-                const float f = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-                auto lo = [f](uint32_t b) { return __uint_as_float(b << 16) * f; };
-                auto hi = [f](uint32_t b) { return __uint_as_float(b & 0xffff0000u) * f; };
-#pragma unroll 1
-                for (int q = 0; q < 16; q += 4) {
-                    uint4 v[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) v[c] = ptx::ld_shared_v4(piece(q + c));
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        v[c] = make_uint4(ptx::pack_f16x2(lo(v[c].x), lo(v[c].y)),
-                                          ptx::pack_f16x2(lo(v[c].z), lo(v[c].w)),
-                                          ptx::pack_f16x2(hi(v[c].x), hi(v[c].y)),
-                                          ptx::pack_f16x2(hi(v[c].z), hi(v[c].w)));
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        ptx::st_shared_v4(piece(q + c), v[c].x, v[c].y, v[c].z, v[c].w);
-                }
-                *sm.fac(n, x, row) = static_cast<uint8_t>(k + 127);
+            for (int c = 0; c < 4; ++c) {
+                t = ptx::max_nan_bf16x2(t, v[c].x & 0x7fff7fffu);
+                t = ptx::max_nan_bf16x2(t, v[c].y & 0x7fff7fffu);
+                t = ptx::max_nan_bf16x2(t, v[c].z & 0x7fff7fffu);
+                t = ptx::max_nan_bf16x2(t, v[c].w & 0x7fff7fffu);
             }
-            ptx::fence_proxy_async_smem();  // the MMAs read the tile
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(sm.bar(C::BAR_QREADY + x));
-        }
-    }
-}
-
-// The same for 8-bit pools. K stays in e4m3, so Q goes to the product in two e4m3 parts:
-// a bf16 value has 8 significant bits, e4m3 four, and x = upper + lower with upper = x
-// rounded to e4m3 and lower the exact rest, whose own 4 bits hold it. A row is scaled by
-// the power of two that brings its largest element into [2^7, 2^8); elements below 2^-9 of
-// that lose bits, each at most 2^-10 of e4m3's smallest step of 2^-9, 2^-17 of the row's
-// largest. A step of the product takes 32 values: their upper parts replace the first two
-// of the four 16-byte pieces that held them, their lower parts the last two, and the step
-// runs over the same 32 values of K twice. A row with an infinity or a NaN is NaN.
-template <int NQ>
-__device__ void q_warp_e4m3(const RowParams& p, const Smem<NQ, Pool::q8>& sm, int w) {
-    using C = Cfg<NQ, Pool::q8>;
-    const int lane = threadIdx.x & 31;
-    uint32_t loads[2] = {0, 0};
-    const int ui_end = p.cta_first[blockIdx.x + 1];
-    for (int ui = p.cta_first[blockIdx.x]; ui < ui_end; ++ui) {
-        const Unit u = p.units[ui];
-        const int nq = unit_nq<NQ>(u, p.tpt);
-        for (int x = 0; x < nq; ++x) {
-            const uint32_t n = x == 0 ? loads[0]++ : loads[1]++;
-            if (!warp_wait<NQ, Pool::q8>(p, sm, sm.bar(C::BAR_QFULL + x), n & 1u, 50)) return;
-            const int rows = min(p.tpt, u.n_tok - x * p.tpt) * p.G;
-            for (int row = w * 32 + lane; row < rows; row += 32 * kQWarps) {
-                const uint32_t at = sm.base + C::kSmemQ + x * kQBytes + row * 128;
-                const uint32_t swz = static_cast<uint32_t>(row & 7) << 4;
-                auto piece = [&](int c) { return at + (c >> 3) * kHalfBytes + (((c & 7) << 4) ^ swz); };
-                uint32_t top[4] = {0, 0, 0, 0};
-#pragma unroll 1
-                for (int q = 0; q < 16; q += 4) {
-                    uint4 v[4];
+            t = ptx::max_nan_bf16x2(t, __shfl_xor_sync(0xffffffffu, t, 1));
+            t = ptx::max_nan_bf16x2(t, __shfl_xor_sync(0xffffffffu, t, 2));
+            const int e = max((t >> 7) & 0xff, (t >> 23) & 0xff);
+            // f16: largest element to [2^14, 2^15); tiny rows times at most 2^100
+            const int k = e == 255 ? 0 : min((C::kQ8 ? 134 : 141) - e, 100);
+            const float f = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+            auto lo = [f](uint32_t b) { return __uint_as_float(b << 16) * f; };
+            auto hi = [f](uint32_t b) { return __uint_as_float(b & 0xffff0000u) * f; };
+            if (row >= rows) continue;
+            if constexpr (C::kQ8) {
+                uint32_t up[8], rest[8];  // 4 values each
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) v[c] = ptx::ld_shared_v4(piece(q + c));
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        top[0] = ptx::max_nan_bf16x2(top[0], v[c].x & 0x7fff7fffu);
-                        top[1] = ptx::max_nan_bf16x2(top[1], v[c].y & 0x7fff7fffu);
-                        top[2] = ptx::max_nan_bf16x2(top[2], v[c].z & 0x7fff7fffu);
-                        top[3] = ptx::max_nan_bf16x2(top[3], v[c].w & 0x7fff7fffu);
-                    }
+                for (int c = 0; c < 4; ++c) {
+                    // (f16 holds the scaled values' 8 bits down to 2^-17)
+                    ptx::split_e4m3x4(ptx::pack_f16x2(lo(v[c].x), hi(v[c].x)),
+                                      ptx::pack_f16x2(lo(v[c].y), hi(v[c].y)), up[2 * c], rest[2 * c]);
+                    ptx::split_e4m3x4(ptx::pack_f16x2(lo(v[c].z), hi(v[c].z)),
+                                      ptx::pack_f16x2(lo(v[c].w), hi(v[c].w)), up[2 * c + 1],
+                                      rest[2 * c + 1]);
                 }
-                const uint32_t t = ptx::max_nan_bf16x2(ptx::max_nan_bf16x2(top[0], top[1]),
-                                                       ptx::max_nan_bf16x2(top[2], top[3]));
-                const int e = max((t >> 7) & 0xff, (t >> 23) & 0xff);
-                const bool bad = e == 255;
-                const int k = bad ? 0 : min(134 - e, 100);
-                const float f = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-                auto lo = [f](uint32_t b) { return __uint_as_float(b << 16) * f; };
-                auto hi = [f](uint32_t b) { return __uint_as_float(b & 0xffff0000u) * f; };
-#pragma unroll 1
-                for (int q = 0; q < 16; q += 4) {
-                    uint32_t up[8], rest[8];  // 4 values each
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint4 v = ptx::ld_shared_v4(piece(q + c));
-                        // (f16 holds the scaled values' 8 bits down to 2^-17)
-                        ptx::split_e4m3x4(ptx::pack_f16x2(lo(v.x), hi(v.x)),
-                                          ptx::pack_f16x2(lo(v.y), hi(v.y)), up[2 * c], rest[2 * c]);
-                        ptx::split_e4m3x4(ptx::pack_f16x2(lo(v.z), hi(v.z)),
-                                          ptx::pack_f16x2(lo(v.w), hi(v.w)), up[2 * c + 1],
-                                          rest[2 * c + 1]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (bad) up[i] = 0x7f7f7f7fu;
-                        if (bad) rest[i] = 0u;
-                    }
-                    ptx::st_shared_v4(piece(q), up[0], up[1], up[2], up[3]);
-                    ptx::st_shared_v4(piece(q + 1), up[4], up[5], up[6], up[7]);
-                    ptx::st_shared_v4(piece(q + 2), rest[0], rest[1], rest[2], rest[3]);
-                    ptx::st_shared_v4(piece(q + 3), rest[4], rest[5], rest[6], rest[7]);
+                for (int i = 0; i < 8; ++i) {
+                    if (e == 255) up[i] = 0x7f7f7f7fu;
+                    if (e == 255) rest[i] = 0u;
                 }
-                *sm.fac(n, x, row) = static_cast<uint8_t>(k + 127);
+                ptx::st_shared_v4(piece(q), up[0], up[1], up[2], up[3]);
+                ptx::st_shared_v4(piece(q + 1), up[4], up[5], up[6], up[7]);
+                ptx::st_shared_v4(piece(q + 2), rest[0], rest[1], rest[2], rest[3]);
+                ptx::st_shared_v4(piece(q + 3), rest[4], rest[5], rest[6], rest[7]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    ptx::st_shared_v4(piece(q + c), ptx::pack_f16x2(lo(v[c].x), lo(v[c].y)),
+                                      ptx::pack_f16x2(lo(v[c].z), lo(v[c].w)),
+                                      ptx::pack_f16x2(hi(v[c].x), hi(v[c].y)),
+                                      ptx::pack_f16x2(hi(v[c].z), hi(v[c].w)));
             }
-            ptx::fence_proxy_async_smem();  // the MMAs read the tile
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(sm.bar(C::BAR_QREADY + x));
+            if ((lane & 3) == 0) *sm.fac(n, x, row) = static_cast<uint8_t>(k + 127);
         }
+        __syncwarp();
+        ptx::fence_proxy_async_smem();  // the MMAs read the tile
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(sm.bar(C::BAR_QREADY + x));
     }
+    return true;
 }
 
 // ------------------------------------------------------------------ widening
@@ -652,9 +595,11 @@ __device__ void widen_warp(const RowParams& p, const Smem<NQ, Pool::q4>& sm, int
     const uint32_t col =
         static_cast<uint32_t>(((piece & 1) * 4) ^ (upper ? 2 : 0) ^ (row0 & 7)) << 4;
     uint32_t it = is_v ? 1u : 0u;  // ring position of these warps' next tile
+    uint32_t loads[2] = {0, 0};
     const int ui_end = p.cta_first[blockIdx.x + 1];
     for (int ui = p.cta_first[blockIdx.x]; ui < ui_end; ++ui) {
         const Unit u = p.units[ui];
+        if (is_v && !convert_q<NQ, Pool::q4>(p, sm, u, w, loads)) return;
         const Tiles tl(p, u);
         for (int j = 0; j < tl.n; ++j, it += 2) {
             int kt, last, front;
@@ -721,9 +666,11 @@ __device__ void widen_warp_e4m3(const RowParams& p, const Smem<NQ, Pool::q8>& sm
     // rows 0 5, 1 4 (of a group of 8) in the first step, 2 7, 3 6 in the second
     const int row0 = w * 32 + ((lane >> 4) ^ (lane & 4 ? 5 : 0));
     uint32_t it = 1;  // ring position of the next V tile
+    uint32_t loads[2] = {0, 0};
     const int ui_end = p.cta_first[blockIdx.x + 1];
     for (int ui = p.cta_first[blockIdx.x]; ui < ui_end; ++ui) {
         const Unit u = p.units[ui];
+        if (!convert_q<NQ, Pool::q8>(p, sm, u, w, loads)) return;
         const Tiles tl(p, u);
         for (int j = 0; j < tl.n; ++j, it += 2) {
             int kt, last, front;
@@ -1363,7 +1310,7 @@ __global__ void __launch_bounds__(Cfg<NQ, F>::kThreads, 1)
         for (int x = 0; x < NQ; ++x) {
             ptx::mbar_init(sm.bar(C::BAR_QFULL + x), 1);
             ptx::mbar_init(sm.bar(C::BAR_QFREE + x), 1);
-            ptx::mbar_init(sm.bar(C::BAR_QREADY + x), kQWarps);
+            ptx::mbar_init(sm.bar(C::BAR_QREADY + x), kGroupWarps);
         }
         ptx::mbar_init(sm.bar(C::BAR_OFREE), 2 * kGroupWarps);
         ptx::mbar_init(sm.bar(C::BAR_AUX), 1);
@@ -1404,8 +1351,7 @@ __global__ void __launch_bounds__(Cfg<NQ, F>::kThreads, 1)
         mma_warp<NQ, F>(p, sm);
         __syncwarp();
     } else if (warp < kWarpSoftmax) {
-        if constexpr (C::kQ4) q_warp<NQ>(p, sm, warp - kWarpQ);
-        if constexpr (C::kQ8) q_warp_e4m3<NQ>(p, sm, warp - kWarpQ);
+        // (only there to make a warpgroup)
     } else if (warp < kWarpWiden) {
         if (C::kF16) ptx::regs_inc<C::kRegsSoftmax>();
         softmax_group<NQ, F, Tree>(p, sm, tmem, (warp - kWarpSoftmax) / kGroupWarps);
