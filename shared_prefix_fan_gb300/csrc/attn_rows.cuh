@@ -724,8 +724,22 @@ __device__ void widen_warp_e4m3(const RowParams& p, const Smem<NQ, Pool::q8>& sm
 
 // ------------------------------------------------------------------ MMA issuer
 // Descriptors: see attn_fwd.cu (the same tile layouts).
-__device__ __forceinline__ uint64_t kmajor_step(int kk) {
-    return static_cast<uint64_t>((kk >> 2) * (kHalfBytes >> 4) + (kk & 3) * 2);
+__device__ __forceinline__ uint32_t kmajor_step(int kk) {
+    return static_cast<uint32_t>((kk >> 2) * (kHalfBytes >> 4) + (kk & 3) * 2);
+}
+
+// A value that is the same in all lanes, as the compiler can see: it then keeps what comes
+// of it in uniform registers, where a product's operands have to be.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+    return __ballot_sync(0xffffffffu, (v >> (threadIdx.x & 31)) & 1u);
+}
+// A descriptor from its lower word (uniform) and constants: see ptx::sdesc_sw128.
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+    constexpr uint32_t hi = (1024u >> 4) | 1u << 14 | 2u << 29;
+    return static_cast<uint64_t>(hi) << 32 | lo;
+}
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+    return uniform(((saddr & 0x3FFFFu) >> 4) | (lbo >> 4) << 16);
 }
 
 // One P.V product: group x's P of its t-th tile times the V tile at ring position
@@ -768,16 +782,17 @@ struct Issuer {
     // S of group x = Q tile qx times the K tile at pos.
     __device__ __forceinline__ void issue_s(int x, int qx, uint32_t pos) {
         ptx::tc_fence_after();
-        const uint64_t dq = ptx::sdesc_sw128(sm.base + C::kSmemQ + qx * kQBytes, 16, 1024);
-        const uint64_t dk = ptx::sdesc_sw128(sm.tile(pos), 16, 1024);
+        const uint32_t dq = desc_lo(sm.base + C::kSmemQ + qx * kQBytes, 16);
+        const uint32_t dk = desc_lo(sm.tile(pos), 16);
+        const uint32_t d = uniform(128u * x);
 #pragma unroll
         for (int kk = 0; kk < kHD / 16; ++kk) {
             if constexpr (C::kQ8)  // 32 values of K times their upper, then their lower parts of Q
-                ptx::mma_e4m3_ss_if(128u * x, dq + kmajor_step(kk), dk + 2u * (kk >> 1), C::kIdescQK,
-                                    kk > 0, leader);
+                ptx::mma_e4m3_ss_if(d, desc_of(dq + kmajor_step(kk)), desc_of(dk + 2u * (kk >> 1)),
+                                    C::kIdescQK, kk > 0, leader);
             else
-                ptx::mma_f16_ss_if(128u * x, dq + kmajor_step(kk), dk + kmajor_step(kk), C::kIdescQK,
-                                   kk > 0, leader);
+                ptx::mma_f16_ss_if(d, desc_of(dq + kmajor_step(kk)), desc_of(dk + kmajor_step(kk)),
+                                   C::kIdescQK, kk > 0, leader);
         }
         commit(sm.gbar(x, SFULL));
         issued_any = true;
@@ -793,12 +808,12 @@ struct Issuer {
                   of ? (op.k - 1) & 1u : op.t & 1u, full(next), full_par(next), 14))
             return false;
         ptx::tc_fence_after();
-        const uint32_t a = 128u * op.x;  // P: 64 columns of 16-bit pairs
-        const uint32_t d = kColO + 128u * op.x;
-        const uint64_t dv = ptx::sdesc_sw128(sm.tile(op.pos), kHalfBytes, 1024);
+        const uint32_t a = uniform(128u * op.x);  // P: 64 columns of 16-bit pairs
+        const uint32_t d = kColO + a;
+        const uint32_t dv = desc_lo(sm.tile(op.pos), kHalfBytes);
 #pragma unroll
         for (int kk = 0; kk < kBN / 32; ++kk)
-            ptx::mma_f16_ts_if(d, a + 8u * kk, dv + 128u * kk, C::kIdescPV,
+            ptx::mma_f16_ts_if(d, a + 8u * kk, desc_of(dv + 128u * kk), C::kIdescPV,
                                (!op.first || kk > 0) ? 1u : 0u, leader);
         issued_any = true;
         if (C::kEarlyP) {
@@ -807,7 +822,7 @@ struct Issuer {
         }
 #pragma unroll
         for (int kk = kBN / 32; kk < kBN / 16; ++kk)
-            ptx::mma_f16_ts_if(d, a + 8u * kk, dv + 128u * kk, C::kIdescPV, 1u, leader);
+            ptx::mma_f16_ts_if(d, a + 8u * kk, desc_of(dv + 128u * kk), C::kIdescPV, 1u, leader);
         if (op.last) commit(sm.gbar(op.x, ODONE));
         return true;
     }
@@ -1347,7 +1362,7 @@ __global__ void __launch_bounds__(Cfg<NQ, F>::kThreads, 1)
         if (threadIdx.x == 0) atomicCAS(p.err, 0, kErrCuda);
     } else if (warp == 0) {
         producer_warp<NQ, F>(p, sm, &tm_q, &tm_k, &tm_v);
-    } else if (warp == 1) {
+    } else if (warp == 3) {
         mma_warp<NQ, F>(p, sm);
         __syncwarp();
     } else if (warp < kWarpSoftmax) {
