@@ -326,8 +326,8 @@ FANOUT_API int fanout_kv_read_q8(const void *k_pages, const void *v_pages, const
  * Rows behind the last token get no bits, position 0 and slot -1, and so do all rows when a
  * length is not valid (a negative one, more than n_rows tokens, T_b past the mask, a row
  * of the table too short; reported as FANOUT_EINVAL). Arrays that are written share no
- * byte with another (FANOUT_EINVAL). No workspace; can be captured (first call on a
- * device outside a capture).
+ * byte with another (FANOUT_EINVAL). n_rows == 0 does nothing. No workspace; can be
+ * captured (first call on a device outside a capture).
  */
 FANOUT_API int fanout_tree_rows(const int32_t *parents, const int32_t *page_table,
                 int32_t num_branches, int32_t max_pages_per_branch, int32_t prefix_len,
@@ -369,7 +369,7 @@ enum fanout_kv_type { FANOUT_KV_BF16 = 0, FANOUT_KV_Q4 = 1, FANOUT_KV_Q8 = 2 };
  * A branch whose path does not ascend inside its T_b tokens is left as it was, a row whose
  * page is outside the pools is skipped, and with lengths that are not valid nothing is
  * moved; each is reported as FANOUT_EINVAL. No two branches may share the pages of their
- * drafted rows. Can be captured.
+ * drafted rows. n_rows == 0 does nothing. Can be captured.
  */
 FANOUT_API int fanout_kv_keep(void *k_pages, void *v_pages, int32_t kv_type,
                 const int32_t *page_table, int32_t num_branches, int32_t max_pages_per_branch,

@@ -208,7 +208,7 @@ def _device_call(name: str, dev, stream, *args) -> None:
     idx = dev.index
     handle = torch._C._cuda_getCurrentRawStream(idx) if stream is None else _stream_handle(stream)
     fn = getattr(_lib or load(), name)
-    if torch.cuda.current_device() == idx:
+    if torch._C._cuda_getDevice() == idx:
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(idx):
@@ -534,9 +534,9 @@ def tree_rows(parents, page_table, prefix_len: int, suffix_lens, add_lens, page_
         raise ValueError("max_nodes must be 1 .. 1024")
     B, width = page_table.shape
     words = -(-max_nodes // 32)
-    for name, v in (("prefix_len", prefix_len), ("page_size", page_size)):
-        if v >> 31:
-            _fit32(name, v)
+    if prefix_len >> 31 or page_size >> 31:
+        _fit32("prefix_len", prefix_len)
+        _fit32("page_size", page_size)
     if window >> 31:
         window = max(-1, min(window, _I32_MAX))
     _need("parents", parents, i32, dev, (R,))
@@ -595,9 +595,9 @@ def kv_keep(k_pages, v_pages, page_table, prefix_len: int, suffix_lens, add_lens
     import torch
     i32, dev = torch.int32, k_pages.device
     B, width = page_table.shape
-    for name, v in (("prefix_len", prefix_len), ("page_size", page_size)):
-        if v >> 31:
-            _fit32(name, v)
+    if prefix_len >> 31 or page_size >> 31:
+        _fit32("prefix_len", prefix_len)
+        _fit32("page_size", page_size)
     kind, num_pages, h_kv = _pools(k_pages, v_pages, page_size, 0, dev)
     _need("page_table", page_table, i32, dev)
     _need("suffix_lens", suffix_lens, i32, dev, (B,))

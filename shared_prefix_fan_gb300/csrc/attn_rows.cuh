@@ -1,6 +1,7 @@
-// attn_rows.cu -- fan-out attention of row plans, for sm_103a: over bf16 pools with a
-// sliding window and first keys that stay visible, and over pools held in 4 bits
-// (with or without a window).
+// attn_rows.cuh -- fan-out attention of row plans, for sm_103a: over bf16 pools with a
+// sliding window and first keys that stay visible, over pools held in 4 or 8 bits (with or
+// without a window), and for trees of drafted tokens over any of them. Instances:
+// attn_rows.cu, attn_rows_q8.cu, attn_tree.cu.
 //
 // Units, tiles and the online softmax are those of attn_fwd.cu (128 query rows x
 // 128 keys, base 2, the reference maximum m raised only when a row's maximum passes
@@ -11,17 +12,22 @@
 // GB300 mapping, one persistent CTA per SM:
 //   warp 0      producer. bf16 pools: TMA boxes, a page of a KV head each, into a
 //               ring of 32 KB tiles. 4-bit pools: page blocks by cp.async.bulk into
-//               a ring of raw tiles (9 KB: 128 rows of 72 bytes). Q by TMA as soon as
-//               its buffer is free. Page ids are checked before they are read through;
-//   warp 1      TMEM owner and tcgen05 issuer: the whole warp runs the issue loop, so
-//               that its addresses stay warp-uniform, and one elected lane issues;
-//   warps 2-3   4-bit pools only: turn loaded Q tiles into f16 in place;
+//               a ring of raw tiles (9 KB: 128 rows of 72 bytes). 8-bit pools: TMA boxes
+//               of 128-byte rows, K into the ring that the products read, V into one of
+//               raw tiles. Q by TMA as soon as its buffer is free. Page ids are checked
+//               before they are read through;
+//   warp 1      TMEM owner;
+//   warp 3      tcgen05 issuer: the whole warp runs the issue loop, so that its
+//               addresses stay warp-uniform, and one elected lane issues. (An issuer
+//               for each group lets the groups' softmaxes coincide: a bf16 prefill of
+//               2048 tokens took 1755 us, not 1243.);
 //   warps 4-11  two softmax groups of 4 warps, thread = row;
-//   warps 12-19 4-bit pools only: widen raw tiles into the swizzled 16-bit ring (4
-//               warps the K tiles, 4 the V tiles): with 4 warps for both, a decode
-//               step waited for them (35 us against 31 with 8).
+//   warps 12-19 4-bit pools: turn Q tiles into f16 and widen raw tiles into the swizzled
+//               16-bit ring (4 warps the K tiles, 4 Q and the V tiles): with 4 warps for
+//               both, a decode step waited for them (35 us against 31 with 8). 8-bit
+//               pools: warps 12-15, Q and the V tiles.
 // Keys of a tile that no row of the unit sees are zeros in shared memory, whatever
-// the pool holds there.
+// the pool holds there (K tiles of 8 bits: their scores are masked).
 //
 // A unit of two query tiles gives each group one of them. A unit of one query
 // tile (decode) is split over the groups by keys instead: even tiles (counted over
@@ -51,24 +57,43 @@
 // The codes of a word come out as values 0 2 4 6 1 3 5 7 of its 8; K and Q keep
 // that order (it is summed over), V's columns are put back when O is stored.
 //
+// 8-bit pools. The rows are e4m3 codes (kv_q8.cu), and a row of 128 is one line of a
+// swizzled K-major tile, so K goes to the tensor core as it is cached: S is an e4m3
+// product, Q in two e4m3 parts (convert_q), over twice the values at twice f16's rate. It
+// accumulates in fp32 (sums of 128 products over all of e4m3's range: off by at most 2^-20
+// of the sum of their magnitudes, measured). V is widened to f16 (exact) for the product with P, which
+// needs f16's range: in e4m3 a P below 2^-18 of its row's largest would be lost, and
+// behind a first key that takes most of a row there may be thousands of such.
+//
+// Drafted trees. A row sees the keys before its branch's drafted tokens as in a window,
+// and of the drafted ones those of its mask, read as 32 bits for 32 columns in the one to
+// nine tiles that hold them; every other tile is the same as without a tree.
+//
 // What bounds it (GB300, L2 flushed, whole calls). Two query tiles: the chain of a
-// group, S product (512 cycles), softmax (1650: its maximum 500, exponentials 850,
-// P's store 300), hand-off (400), P.V product (512); P lies over S, and two S and
-// two O are all of TMEM, so S cannot be doubled, and a key tile takes about 3250
-// cycles a pair where its products are 2048. A boundary between units costs about
-// 10000 cycles (epilogue, next Q, masked tiles).
-//   4-bit prefill, 2048 rows x 64 heads over 32768 keys: 1442 us, 1478 TFLOP/s
-//   4-bit, 32 branches of 1..32 tokens over 65536 shared keys: 836 us, 1194 TFLOP/s
-//   bf16, the same over 16384 keys, window 2048: 102 us, 2060 GB/s, 356 TFLOP/s
-//   bf16 prefill, 4096 rows x 64 heads, window 1024: 166 us, 832 TFLOP/s
-// One query tile (decode), 8 rows x 64 heads over 32768 keys: 33 us for 42.5 MB in 4
-// bits (bf16 pools through attn_fwd.cu: 45 us for 151 MB): 15 tiles a CTA of 1900
-// cycles each, and 6600 cycles until the first S (35100 of the 44400 cycles counted; the
-// rest is not accounted for). A tile moves 200 KB through shared memory (raw rows in
-// and out 36, widened 64, the products' operands K, V and Q 96), 1570 cycles at 128 bytes
-// a cycle by reckoning; shorter chains gained little there
-// (rows copied into a tile's idle half, so that a row's keys were split over two warps,
-// gained nothing). Window 4096: 20.5 us, four tiles a CTA, start and epilogue.
+// group, S product (512 cycles), softmax, hand-off (400), P.V product (512); P lies over
+// S, and two S and two O are all of TMEM, so S cannot be doubled. Cycles a key tile and
+// pair of query tiles, whose products are 2048: bf16 2750 (softmax 1300), 8 bits 2900,
+// 4 bits 3150 (softmax 1600: the widening warps take issue slots). Products keep
+// their 512 cycles beside 60 bytes a cycle of other shared-memory traffic and full TMEM
+// reading (measured), so neither is the bound. Halving S to double it (64 keys each) was
+// slower: a product of 64 keys takes 384 cycles, not 256, as Q is read twice, and with
+// both groups' softmaxes always running each took twice as long (1714 us against 1461 of
+// an 8-bit prefill then). A boundary between units costs about 10000 cycles (epilogue,
+// next Q, masked tiles).
+//   4-bit prefill, 2048 rows x 64 heads over 32768 keys: 1440 us, 1480 TFLOP/s
+//   8-bit, the same: 1300 us (in a row of calls, power-limited, 1350), 1640 TFLOP/s
+//   4-bit, 32 branches of 1..32 tokens over 65536 shared keys: 825 us, 1210 TFLOP/s
+//   8-bit, 32 branches of 1..64 drafted tokens over 65536 shared keys: 1500 us, 1505 TFLOP/s
+//   bf16, 8 branches of 32 drafted tokens over 32768 shared keys: 206 us, 1354 TFLOP/s
+//   bf16, 32 branches of 1..32 tokens over 16384 keys, window 2048: 97 us, 375 TFLOP/s
+//   bf16 prefill, 4096 rows x 64 heads, window 1024: 158 us, 874 TFLOP/s
+// One query tile (decode), 8 rows x 64 heads over 32768 keys: 31 us for 42.5 MB in 4
+// bits, 27 us in a row of calls for 76 MB in 8 (bf16 pools through attn_fwd.cu: 45 us for
+// 151 MB): of 41000 cycles a CTA 6000 pass until the first S and 6000 behind the last P;
+// its 18 tiles take 1575 each, two groups in turn (softmax 1400, wait for the products
+// 1450). Shorter chains gained little there (rows copied into a tile's idle half, so that
+// a row's keys were split over two warps, gained nothing). Window 4096: 20.5 us, four tiles
+// a CTA, start and epilogue.
 // Every wait is bounded, as in attn_fwd.cu.
 #pragma once
 
@@ -922,13 +947,6 @@ __device__ void mma_warp(const RowParams& p, const Smem<NQ, F>& sm) {
 }
 
 // ------------------------------------------------------------------ softmax
-__device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&a)[32], uint32_t (&b)[32]) {
-    ptx::tmem_ld32(taddr, a);
-    ptx::tmem_ld32(taddr + 32, b);
-    ptx::tmem_ld_wait(a);
-    ptx::reg_touch(b);
-}
-
 // Scores a row does not see become -inf in TMEM (tiles at a mask's border only,
 // so that the common path carries no masks): it sees columns below lim, and not
 // [sink, lo), a bit each of 32. (bf16 pools: 102 us, with two comparisons a column

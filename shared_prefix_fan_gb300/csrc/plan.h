@@ -19,7 +19,7 @@ struct PlanInput {
     int32_t num_sms;       // persistent CTAs: at most one per SM
     int32_t force_splits;  // >0: cut every key range into this many chunks
     int32_t tail_cuts = 1; // 0: never cut a direct range to even out the last wave
-    // Row plans (windowed or 4-bit attention): every token's position goes to the
+    // Row plans (windowed, 4-bit, 8-bit and tree attention): every token's position goes to the
     // device (Plan::tok_pos), and a unit may sweep some first keys before its own
     // range (Unit::pos_base, see there).
     int32_t rows = 0;

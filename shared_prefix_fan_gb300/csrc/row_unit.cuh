@@ -1,5 +1,5 @@
-// row_unit.cuh -- a unit of a row plan (windowed or 4-bit attention) as attn_rows.cu
-// reads it: the first keys it sweeps in front of its own range, where that range's
+// row_unit.cuh -- a unit of a row plan (windowed, 4-bit, 8-bit or tree attention) as
+// attn_rows.cuh reads it: the first keys it sweeps in front of its own range, where that range's
 // tiles begin, and the check of a page id before it is read through.
 #pragma once
 
