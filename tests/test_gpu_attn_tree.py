@@ -176,3 +176,34 @@ def test_capture_is_refused():
             prob.run(out=out)
         out.add_(0.0)
     assert e.value.code == binding.EUNSUPPORTED
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_pools_past_32_bit_offsets(kind):
+    trees = trees_of([9, 5])
+    prob = tree_ref.Problem([300, 40], [9, 5], 100, 8, 8, 128, kind=kind, trees=trees, seed=12, spare=0)
+    q, k, v, table, *rest = prob.args()
+    n = {"bf16": 17000, "q4": 62000, "q8": 34000}[kind]
+    big = [torch.empty((n, *x.shape[1:]), dtype=x.dtype, device="cuda") for x in (k, v)]
+    assert big[0].numel() * big[0].element_size() > 2 ** 32
+    for x, y in zip(big, (k, v)):
+        x.view(torch.uint8)[-y.shape[0]:] = y.view(torch.uint8)
+    prob.dev[1:4] = [*big, table + (n - k.shape[0])]
+    out, lse = prob.run()
+    assert binding.last_error() == binding.OK
+    prob.check(out, lse)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_on_another_stream_and_into_given_outputs(kind):
+    prob = tree_ref.Problem([30, 28], [5, 9], 1024, 32, 4, 16, kind=kind, trees=trees_of([5, 9]), seed=9)
+    here, lse = prob.run("bf16")
+    prob.check(here, lse)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    # an output that starts on 16 bytes only
+    flat = torch.zeros(14 * 32 * 128 + 8, dtype=torch.bfloat16, device="cuda")
+    out = flat[8:].view(14, 32, 128)
+    got, none = prob.run("bf16", stream=s, out=out, want_lse=False)
+    torch.cuda.current_stream().wait_stream(s)
+    assert none is None and got is out and torch.equal(out, here) and not flat[:8].any()

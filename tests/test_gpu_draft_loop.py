@@ -42,8 +42,10 @@ def test_drafting_steps(kind):
             return tree_ref.decode8(tree_ref.encode8(x.float().numpy(), gs), gs)
         return ref.decode(*ref.encode(x.float().numpy(), gs), gs)
 
-    def append(k, v, slots):
-        if kind == "bf16":
+    def append(k, v, slots, T=None):
+        if kind == "bf16" and T is not None:
+            binding.kv_append(k.cuda(), v.cuda(), *pools, table, P, S, T, page)
+        elif kind == "bf16":
             for pool, x in zip(pools, (k, v)):
                 pool[slots // page, :, slots % page] = x.cuda()
         else:
@@ -81,7 +83,7 @@ def test_drafting_steps(kind):
         masks, positions, slots = binding.tree_rows(parents, table, P, suffix, add, page, t_max)
         k, v = (to_bf16(rng.standard_normal((R, hkv, 128))) for _ in range(2))
         q = to_bf16(rng.standard_normal((R, hq, 128)) * 1.5)
-        append(k, v, slots)
+        append(k, v, slots, T)
         out, lse = binding.attn_tree(q.cuda(), *pools, table, P, [s + t for s, t in zip(S, T)], T, hq, hkv,
                                      page, 128 ** -0.5, masks, positions, 0, 0, gs, gs)
         draft = rng.integers(0, 4, size=R)
@@ -121,3 +123,50 @@ def test_drafting_steps(kind):
         assert suffix.tolist() == S
     assert accepted > B
     assert int(used) <= free.numel() and sum(reserved.tolist()) >= sum(S)
+
+
+def test_two_threads_on_two_streams():
+    """Both run whole steps at once; each gets what it got alone."""
+    import threading
+
+    def inputs(seed):
+        rng = np.random.default_rng(seed)
+        T = [12, 5, 30]
+        trees = [tree_ref.random_tree(rng, t) for t in T]
+        prob = tree_ref.Problem([40, 61, 7], T, 300, 16, 2, 16, kind="q8", trees=trees, seed=seed)
+        prob.args()
+        flat = torch.tensor([p for t in trees for p in t], dtype=torch.int32, device="cuda")
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        tok = [torch.from_numpy(rng.integers(0, 3, size=47)).cuda() for _ in range(2)]
+        return prob, flat, i32([40, 61, 7]), i32(T), tok, torch.from_numpy(rng.integers(0, 3, size=3)).cuda()
+
+    def step(x, stream):
+        prob, flat, S, T, (draft, target), first = x
+        m, p, s = binding.tree_rows(flat, prob.dev[3], prob.P, S, T, 16, 30, stream=stream)
+        out, lse = binding.attn_tree(*prob.dev[:4], prob.P, prob.S, prob.T, 16, 2, 16, prob.scale, m, p,
+                                     stream=stream)
+        return (m, p, s, out, lse) + tuple(binding.tree_accept(flat, draft, target, first, T,
+                                                               stream=stream))
+    work = [inputs(1), inputs(2)]
+    alone = [step(x, None) for x in work]
+    torch.cuda.synchronize()
+    streams, got, errors = [torch.cuda.Stream() for _ in work], [None, None], []
+
+    def run(i):
+        try:
+            for _ in range(40):
+                got[i] = step(work[i], streams[i])
+            streams[i].synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    torch.cuda.synchronize()
+    for a, b in zip(alone, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+    assert binding.last_error() == binding.OK

@@ -282,3 +282,23 @@ def test_on_another_stream():
     rows = binding.tree_rows(args[0], i32(table), 37, i32(S), args[4], 16, 12)
     torch.cuda.current_stream().wait_stream(s)
     assert all(torch.equal(x, y) for x, y in zip(here, there)) and len(rows) == 3
+
+
+def test_kept_rows_past_32_bit_offsets():
+    pages, hkv, page = 34000, 8, 128
+    pools = [torch.zeros((pages, hkv, page, 128), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for x in pools:
+        x[-2:] = torch.randint(0, 256, (2, hkv, page, 128), dtype=torch.uint8, device="cuda")
+    want = [x[-2:].cpu().numpy().copy() for x in pools]
+    table = np.array([[pages - 1, pages - 2]], np.int32)
+    for x in want:  # rows 126, 127 of the first page, 0 and on of the second
+        x[1, :, 127], x[0, :, 0] = x[0, :, 0].copy(), x[0, :, 3].copy()
+    _, _, slots = binding.tree_rows(i32([-1, 0, 1, 2, 3, 4]), i32(table), 100, i32([26]), i32([6]), page, 6)
+    assert slots.tolist() == [(pages - 1) * page + 126, (pages - 1) * page + 127] + \
+        [(pages - 2) * page + i for i in range(4)]
+    binding.kv_keep(pools[0].view(torch.float8_e4m3fn), pools[1].view(torch.float8_e4m3fn), i32(table), 100,
+                    i32([26]), i32([6]), i32([0, 2, 5, -1, -1, -1]), i32([3]), page)
+    assert binding.last_error() == binding.OK
+    for x, w in zip(pools, want):
+        assert np.array_equal(x[-2:].cpu().numpy(), w)
+        assert not x[0].any() and not x[:-2:1000].any()
