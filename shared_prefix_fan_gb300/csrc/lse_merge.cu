@@ -20,14 +20,19 @@ __device__ int32_t g_err_word[4];
 namespace {
 
 // One warp per output row at a time; kMergeBatch partials per pass: 24 for
-// rows with many partials (decode), 8 when every row has few. Blocks of two
-// warps: small enough to be resident beside an attention CTA (which leaves
-// ~27 K registers and 2 KB of shared memory of an SM free), so part of the
-// grid starts, and runs its dry pass, while the attention kernel is still
-// working. The grid is at most what the device holds at once (the rest of it
-// starts the moment the attention CTAs leave, in one wave), and warps loop
-// over rows with the merge index read one row ahead, so after the wait a row
-// costs one memory round trip (its partials).
+// rows with many partials (decode), fewer when every row has few, because a
+// pass loads kMergeBatch of them whatever the row has (merge_row.cuh). With
+// 39360 rows of two partials each (attention over 8-bit keys, a window), the
+// call takes 106 us with 8 a pass and 97 with 2; two or four rows a warp at
+// once instead took 107 and 127 (more registers a block, so fewer blocks fit
+// beside the attention kernel). Blocks of two warps: small enough to be
+// resident beside an attention CTA (which leaves ~27 K registers and 2 KB of
+// shared memory of an SM free), so part of the grid starts, and runs its dry
+// pass, while the attention kernel is still working. The grid is at most what
+// the device holds at once (the rest of it starts the moment the attention
+// CTAs leave, in one wave), and warps loop over rows with the merge index read
+// one row ahead, so after the wait a row costs one memory round trip (its
+// partials).
 constexpr int kMergeThreads = 64;
 template <int kMergeBatch>
 __global__ void __launch_bounds__(kMergeThreads, 1) lse_merge_kernel(const MergeParams p) {
@@ -67,6 +72,27 @@ int merge_blocks_per_sm() {
     return occ;
 }
 
+template <int kMergeBatch>
+cudaError_t launch_batch(const MergeParams& p, int sms, cudaStream_t stream) {
+    const int64_t rows_per_block = kMergeThreads / 32;
+    const int64_t blocks_needed = (p.n_out + rows_per_block - 1) / rows_per_block;
+    const int grid = static_cast<int>(std::min<int64_t>(
+        blocks_needed, static_cast<int64_t>(sms) * merge_blocks_per_sm<kMergeBatch>()));
+    // Programmatic dependent launch: the merge grid may start while the
+    // attention kernel finishes; griddepcontrol.wait orders the reads.
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.dynamicSmemBytes = 0;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, lse_merge_kernel<kMergeBatch>, p);
+}
+
 // One thread waits on a barrier that nothing will ever complete; the bounded
 // wait must give up and report FANOUT_ETIMEOUT.
 __global__ void wait_selftest_kernel(int32_t* err, unsigned long long limit_ns) {
@@ -87,26 +113,11 @@ cudaError_t launch_lse_merge(const MergeParams& p, cudaStream_t stream) {
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int32_t most = p.merge_cnt ? p.merge_stride : p.n_parts;  // partials of the fullest row
-    const bool few = most <= 8;
-    const int64_t rows_per_block = kMergeThreads / 32;
-    const int64_t blocks_needed = (p.n_out + rows_per_block - 1) / rows_per_block;
-    const int per_sm = few ? merge_blocks_per_sm<8>() : merge_blocks_per_sm<24>();
-    const int grid = static_cast<int>(
-        std::min<int64_t>(blocks_needed, static_cast<int64_t>(sms) * per_sm));
-    // Programmatic dependent launch: the merge grid may start while the
-    // attention kernel finishes; griddepcontrol.wait orders the reads.
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kMergeThreads);
-    cfg.dynamicSmemBytes = 0;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (few) return cudaLaunchKernelEx(&cfg, lse_merge_kernel<8>, p);
-    return cudaLaunchKernelEx(&cfg, lse_merge_kernel<24>, p);
+    if (most <= 2) return launch_batch<2>(p, sms, stream);
+    if (most <= 4) return launch_batch<4>(p, sms, stream);
+    if (most <= 6) return launch_batch<6>(p, sms, stream);
+    if (most <= 8) return launch_batch<8>(p, sms, stream);
+    return launch_batch<24>(p, sms, stream);
 }
 
 // Device address of this device's error word (the symbol's host-side name is
