@@ -1,4 +1,5 @@
-"""Python binding of libfanout.so (ctypes): argument marshalling only.
+"""Python binding of libfanout.so: argument marshalling only (ctypes, and for the small
+calls of the 8-bit cache and of drafted trees the extension module _host_calls).
 
 Every step of the attention path runs in the library's CUDA kernels; this
 module turns torch tensors into pointers, checks dtypes/devices/shapes, calls
@@ -16,6 +17,7 @@ import numpy as np
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libfanout.so")
+HOST_PATH = os.path.join(_HERE, "lib", "_host_calls.so")
 
 OK, EINVAL, EUNSUPPORTED, ECUDA, ENOMEM, ETIMEOUT = range(6)
 OUT_F32, OUT_BF16 = 0, 1
@@ -112,6 +114,33 @@ def load(path: Optional[str] = None):
     if path is None:
         _lib = lib
     return lib
+
+
+_host = None
+
+
+def _host_calls():
+    """The extension module behind the small calls (csrc/host_calls.c), set up with torch's
+    functions. Raises if it has not been built."""
+    global _host
+    if _host is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch
+        load()
+        if not os.path.exists(HOST_PATH):
+            raise RuntimeError(f"_host_calls not built ({HOST_PATH}); run "
+                               "shared_prefix_fan_gb300.build.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_host_calls", HOST_PATH)
+        module = importlib.util.module_from_spec(
+            importlib.util.spec_from_loader("_host_calls", loader))
+        loader.exec_module(module)
+        module.setup((torch.bfloat16, torch.float8_e4m3fn, torch.uint8, torch.int32, torch.int64),
+                     torch.empty, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice,
+                     torch.cuda.device, _empty_on, _stream_handle, _check)
+        _host = module
+    return _host
 
 
 def strerror(code: int) -> str:
@@ -453,38 +482,16 @@ def kv_append_q8(k_new, v_new, k_pages, v_pages, slots, k_scale: float = 1.0,
                  v_scale: float = 1.0, stream=None) -> None:
     """Write new K/V rows (bf16 [R, H_kv, 128], rows may be strided) into 8-bit
     pools at `slots` (int64 [R]; negative: the row is skipped)."""
-    import torch
-    dev, n = k_pages.device, slots.numel()
-    num_pages, h_kv, page_size, d = _q8_pools(k_pages, v_pages, dev)
-    _need("slots", slots, torch.int64, dev, (n,))
-    ks, vs = _rows_of("k_new", k_new, n, h_kv, dev), _rows_of("v_new", v_new, n, h_kv, dev)
-    if k_new.shape[2] != d or v_new.shape[2] != d:
-        raise ValueError(f"k_new / v_new rows must hold the pools' {d} values")
-    _device_call("fanout_kv_append_q8", dev, stream, k_new.data_ptr(), v_new.data_ptr(), ks, vs,
-                 k_pages.data_ptr(), v_pages.data_ptr(), slots.data_ptr(), n, num_pages, h_kv, d,
-                 page_size, k_scale, v_scale)
+    (_host or _host_calls()).kv_append_q8(k_new, v_new, k_pages, v_pages, slots, k_scale, v_scale,
+                                          stream)
 
 
 def kv_read_q8(k_pages, v_pages, slots, k_scale: float = 1.0, v_scale: float = 1.0, k_out=None,
                v_out=None, stream=None):
     """The bf16 rows [R, H_kv, 128] that `slots` of 8-bit pools stand for: (k, v).
     Rows with a negative slot are left as they were (undefined when allocated here)."""
-    import torch
-    dev, n = k_pages.device, slots.numel()
-    num_pages, h_kv, page_size, d = _q8_pools(k_pages, v_pages, dev)
-    _need("slots", slots, torch.int64, dev, (n,))
-    empty = torch.empty if stream is None else _empty_on(dev, stream)
-    if k_out is None:
-        k_out = empty((n, h_kv, d), dtype=torch.bfloat16, device=dev)
-    if v_out is None:
-        v_out = empty((n, h_kv, d), dtype=torch.bfloat16, device=dev)
-    ks, vs = _rows_of("k_out", k_out, n, h_kv, dev), _rows_of("v_out", v_out, n, h_kv, dev)
-    if k_out.shape[2] != d or v_out.shape[2] != d:
-        raise ValueError(f"k_out / v_out rows must hold the pools' {d} values")
-    _device_call("fanout_kv_read_q8", dev, stream, k_pages.data_ptr(), v_pages.data_ptr(),
-                 slots.data_ptr(), n, num_pages, h_kv, d, page_size, k_scale, v_scale,
-                 k_out.data_ptr(), v_out.data_ptr(), ks, vs)
-    return k_out, v_out
+    return (_host or _host_calls()).kv_read_q8(k_pages, v_pages, slots, k_scale, v_scale, k_out,
+                                               v_out, stream)
 
 
 def copy_pages_q8(k_pages, v_pages, pairs, rows: int, stream=None) -> None:
@@ -528,38 +535,13 @@ def tree_rows(parents, page_table, prefix_len: int, suffix_lens, add_lens, page_
     itself and its ancestors (with a window, those less than `window` levels above it);
     its position is prefix + suffix + its depth; its slot is where its K/V row belongs.
     Rows behind the last token get no bits, position 0 and slot -1."""
-    import torch
-    i32, dev, R = torch.int32, parents.device, parents.numel()
     if max_nodes < 1 or max_nodes > 1024:
         raise ValueError("max_nodes must be 1 .. 1024")
-    B, width = page_table.shape
-    words = -(-max_nodes // 32)
-    if prefix_len >> 31 or page_size >> 31:
-        _fit32("prefix_len", prefix_len)
-        _fit32("page_size", page_size)
     if window >> 31:
         window = max(-1, min(window, _I32_MAX))
-    _need("parents", parents, i32, dev, (R,))
-    _need("page_table", page_table, i32, dev)
-    _need("suffix_lens", suffix_lens, i32, dev, (B,))
-    _need("add_lens", add_lens, i32, dev, (B,))
-    empty = torch.empty if stream is None else _empty_on(dev, stream)
-    if masks is None:
-        masks = empty((R, words), dtype=i32, device=dev)
-    else:
-        _need("masks", masks, i32, dev, (R, words))
-    if positions is None:
-        positions = empty((R,), dtype=i32, device=dev)
-    else:
-        _need("positions", positions, i32, dev, (R,))
-    if slots is None:
-        slots = empty((R,), dtype=torch.int64, device=dev)
-    else:
-        _need("slots", slots, torch.int64, dev, (R,))
-    _device_call("fanout_tree_rows", dev, stream, parents.data_ptr(), page_table.data_ptr(), B,
-                 width, prefix_len, suffix_lens.data_ptr(), add_lens.data_ptr(), page_size, R,
-                 words, window, masks.data_ptr(), positions.data_ptr(), slots.data_ptr())
-    return masks, positions, slots
+    return (_host or _host_calls()).tree_rows(parents, page_table, prefix_len, suffix_lens, add_lens,
+                                              page_size, (max_nodes + 31) // 32, window, masks,
+                                              positions, slots, stream)
 
 
 def tree_accept(parents, draft_tokens, target_tokens, first_tokens, add_lens, stream=None):
@@ -569,22 +551,8 @@ def tree_accept(parents, draft_tokens, target_tokens, first_tokens, add_lens, st
     draft_tokens / target_tokens (int64 [R]): each node's token, and the one the model
     picked behind it; first_tokens (int64 [B]): the one picked behind the context. Of each
     branch's rows of `path` the first counts[b] hold the accepted nodes, the others -1."""
-    import torch
-    i32, i64, dev = torch.int32, torch.int64, parents.device
-    R, B = parents.numel(), add_lens.numel()
-    _need("parents", parents, i32, dev, (R,))
-    _need("draft_tokens", draft_tokens, i64, dev, (R,))
-    _need("target_tokens", target_tokens, i64, dev, (R,))
-    _need("first_tokens", first_tokens, i64, dev, (B,))
-    _need("add_lens", add_lens, i32, dev, (B,))
-    empty = torch.empty if stream is None else _empty_on(dev, stream)
-    path = empty((R,), dtype=i32, device=dev)
-    counts = empty((B,), dtype=i32, device=dev)
-    after = empty((B,), dtype=i64, device=dev)
-    _device_call("fanout_tree_accept", dev, stream, parents.data_ptr(), draft_tokens.data_ptr(),
-                 target_tokens.data_ptr(), first_tokens.data_ptr(), add_lens.data_ptr(), B, R,
-                 path.data_ptr(), counts.data_ptr(), after.data_ptr())
-    return path, counts, after
+    return (_host or _host_calls()).tree_accept(parents, draft_tokens, target_tokens, first_tokens,
+                                                add_lens, stream)
 
 
 def kv_keep(k_pages, v_pages, page_table, prefix_len: int, suffix_lens, add_lens, path, counts,
@@ -592,22 +560,8 @@ def kv_keep(k_pages, v_pages, page_table, prefix_len: int, suffix_lens, add_lens
     """Move the accepted rows together in pools of any kind: drafted row path[i] of a
     branch becomes its row i (path, counts as tree_accept gives them; suffix_lens without
     the drafted tokens)."""
-    import torch
-    i32, dev = torch.int32, k_pages.device
-    B, width = page_table.shape
-    if prefix_len >> 31 or page_size >> 31:
-        _fit32("prefix_len", prefix_len)
-        _fit32("page_size", page_size)
-    kind, num_pages, h_kv = _pools(k_pages, v_pages, page_size, 0, dev)
-    _need("page_table", page_table, i32, dev)
-    _need("suffix_lens", suffix_lens, i32, dev, (B,))
-    _need("add_lens", add_lens, i32, dev, (B,))
-    _need("path", path, i32, dev, (path.numel(),))
-    _need("counts", counts, i32, dev, (B,))
-    _device_call("fanout_kv_keep", dev, stream, k_pages.data_ptr(), v_pages.data_ptr(), kind,
-                 page_table.data_ptr(), B, width, prefix_len, suffix_lens.data_ptr(),
-                 add_lens.data_ptr(), path.data_ptr(), counts.data_ptr(), path.numel(), num_pages,
-                 h_kv, 128, page_size)
+    (_host or _host_calls()).kv_keep(k_pages, v_pages, page_table, prefix_len, suffix_lens, add_lens,
+                                     path, counts, page_size, stream)
 
 
 def plan(suffix_lens, q_rows, prefix_len: int, h_q: int, h_kv: int, page_size: int,

@@ -155,6 +155,8 @@ def test_negative_windows_stay_negative(monkeypatch, window, sinks):
     binding.attn_q8(q, pool, pool, table, 16, [4], [2], 1, 1, 16, 1.0, True, 1.0, 1.0, window, sinks)
     binding.attn_tree(q, pool, pool, table, 16, [4], [2], 1, 1, 16, 1.0, masks, None, window, sinks)
     if not sinks:
+        monkeypatch.setattr(binding, "_host", type("Host", (), {
+            "tree_rows": lambda self, *a: c.calls.append(a)})())
         binding.tree_rows(i, table, 0, i, i, 16, 4, window)
     for args in c.calls:
         ints = [a for a in args if isinstance(a, int) and a < 0]
