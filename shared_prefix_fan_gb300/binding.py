@@ -1,5 +1,5 @@
-"""Python binding of libfanout.so: argument marshalling only (ctypes, and for the small
-calls of the 8-bit cache and of drafted trees the extension module _host_calls).
+"""Python binding of libfanout.so: argument marshalling only (ctypes, and for the calls of
+the 8-bit cache and of drafted trees the extension module _host_calls).
 
 Every step of the attention path runs in the library's CUDA kernels; this
 module turns torch tensors into pointers, checks dtypes/devices/shapes, calls
@@ -21,7 +21,6 @@ HOST_PATH = os.path.join(_HERE, "lib", "_host_calls.so")
 
 OK, EINVAL, EUNSUPPORTED, ECUDA, ENOMEM, ETIMEOUT = range(6)
 OUT_F32, OUT_BF16 = 0, 1
-KV_BF16, KV_Q4, KV_Q8 = 0, 1, 2
 OPT_SPLITS, OPT_VALIDATE_TABLE, OPT_WAIT_LIMIT_NS, OPT_NUM_SMS, OPT_FUSED_MERGE = 1, 2, 3, 4, 5
 
 # The C ABI (include/fanout.h): name -> (restype, argtypes)
@@ -120,7 +119,7 @@ _host = None
 
 
 def _host_calls():
-    """The extension module behind the small calls (csrc/host_calls.c), set up with torch's
+    """The extension module behind those calls (csrc/host_calls.c), set up with torch's
     functions. Raises if it has not been built."""
     global _host
     if _host is None:
@@ -136,9 +135,10 @@ def _host_calls():
         module = importlib.util.module_from_spec(
             importlib.util.spec_from_loader("_host_calls", loader))
         loader.exec_module(module)
-        module.setup((torch.bfloat16, torch.float8_e4m3fn, torch.uint8, torch.int32, torch.int64),
-                     torch.empty, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice,
-                     torch.cuda.device, _empty_on, _stream_handle, _check)
+        types = (torch.bfloat16, torch.float8_e4m3fn, torch.uint8, torch.int32, torch.int64,
+                 torch.float32)
+        module.setup(types, torch.empty, torch._C._cuda_getCurrentRawStream,
+                     torch._C._cuda_getDevice, torch.cuda.device, _empty_on, _stream_handle, _check)
         _host = module
     return _host
 
@@ -505,25 +505,6 @@ def copy_pages_q8(k_pages, v_pages, pairs, rows: int, stream=None) -> None:
                  pairs.data_ptr(), pairs.shape[0], rows, num_pages, h_kv, d // 2, page_size)
 
 
-def _pools(k_pages, v_pages, page_size: int, h_kv: int, dev):
-    """(what the pools hold, num_pages, H_kv) of a pair of pools of any kind."""
-    import torch
-    if k_pages.dtype is torch.uint8:
-        kind, shape = KV_Q4, _q4_pools(k_pages, v_pages, page_size, dev)
-    else:
-        if k_pages.dtype is torch.float8_e4m3fn:
-            kind, shape = KV_Q8, _q8_pools(k_pages, v_pages, dev)
-        else:
-            kind, shape = KV_BF16, k_pages.shape
-            _need("k_pages", k_pages, torch.bfloat16, dev)
-            _need("v_pages", v_pages, torch.bfloat16, dev, shape)
-        if len(shape) != 4 or shape[2] != page_size or shape[3] != 128:
-            raise ValueError("k_pages / v_pages must be [num_pages, H_kv, page_size, 128]")
-    if h_kv and shape[1] != h_kv:
-        raise ValueError(f"pools hold {shape[1]} KV heads, not {h_kv}")
-    return kind, shape[0], shape[1]
-
-
 def tree_rows(parents, page_table, prefix_len: int, suffix_lens, add_lens, page_size: int,
               max_nodes: int, window: int = 0, masks=None, positions=None, slots=None, stream=None):
     """What a step's drafted rows need: (masks int32 [R, words], positions int32 [R],
@@ -746,30 +727,26 @@ def attn_q4(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q_row
     return out, lse
 
 
+def _bf16_out(out_dtype: str) -> bool:
+    if out_dtype not in ("f32", "bf16"):
+        raise ValueError("out_dtype must be 'f32' or 'bf16'")
+    return out_dtype == "bf16"
+
+
 def attn_q8(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q_rows, h_q: int,
             h_kv: int, page_size: int, scale: float, causal: bool, k_scale: float = 1.0,
             v_scale: float = 1.0, window: int = 0, sinks: int = 0, out=None, lse=None,
             out_dtype: str = "f32", want_lse: bool = True, stream=None):
     """attn() over 8-bit pools (float8_e4m3fn [num_pages, H_kv, page_size, 128]); window
     and sinks as in attn_window (0, 0: none)."""
-    import torch
     if window >> 31 or sinks >> 31:
         window, sinks = max(-1, min(window, _I32_MAX)), max(-1, min(sinks, _I32_MAX))
     if prefix_len >> 31:
         _fit32("prefix_len", prefix_len)
     held, lens, B, R = _lens(suffix_lens, q_rows)
-    code, out, lse = _attn_out(q, page_table, R, B, h_q, out, lse, out_dtype, want_lse,
-                               stream)
-    dev, d = q.device, q.shape[-1]
-    pool = (k_pages.shape[0], h_kv, page_size, d)
-    _need("k_pages", k_pages, torch.float8_e4m3fn, dev, pool)
-    _need("v_pages", v_pages, torch.float8_e4m3fn, dev, pool)
-    _device_call("fanout_attn_q8", dev, stream, q.data_ptr(), k_pages.data_ptr(),
-                 v_pages.data_ptr(), page_table.data_ptr(), prefix_len, lens, lens + 4 * B, B,
-                 page_table.shape[1], pool[0], h_q, h_kv, d, page_size, scale,
-                 1 if causal else 0, k_scale, v_scale, window, sinks, out.data_ptr(), code,
-                 _ptr_or_none(lse))
-    return out, lse
+    return (_host or _host_calls()).attn_q8(
+        q, k_pages, v_pages, page_table, prefix_len, lens, B, R, h_q, h_kv, page_size, scale, causal,
+        window, sinks, k_scale, v_scale, out, lse, _bf16_out(out_dtype), want_lse, stream)
 
 
 def attn_tree(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q_rows, h_q: int,
@@ -782,27 +759,14 @@ def attn_tree(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q_r
     tokens that its mask names (masks int32 [R, words], positions int32 [R]: tree_rows
     gives them; positions are read with a window only). Pools of any kind: bf16, 4 bits
     (uint8), 8 bits (float8_e4m3fn)."""
-    import torch
     if window >> 31 or sinks >> 31:
         window, sinks = max(-1, min(window, _I32_MAX)), max(-1, min(sinks, _I32_MAX))
     if prefix_len >> 31:
         _fit32("prefix_len", prefix_len)
     held, lens, B, R = _lens(suffix_lens, q_rows)
-    code, out, lse = _attn_out(q, page_table, R, B, h_q, out, lse, out_dtype, want_lse,
-                               stream)
-    dev, d = q.device, q.shape[-1]
-    kind, num_pages, _ = _pools(k_pages, v_pages, page_size, h_kv, dev)
-    if masks.dim() != 2 or masks.shape[0] != R:
-        raise ValueError(f"masks must be [{R}, words]")
-    _need("masks", masks, torch.int32, dev)
-    if positions is not None:
-        _need("positions", positions, torch.int32, dev, (R,))
-    _device_call("fanout_attn_tree", dev, stream, q.data_ptr(), k_pages.data_ptr(),
-                 v_pages.data_ptr(), kind, page_table.data_ptr(), prefix_len, lens, lens + 4 * B,
-                 B, page_table.shape[1], num_pages, h_q, h_kv, d, page_size, scale,
-                 masks.data_ptr(), masks.shape[1], _ptr_or_none(positions), window, sinks,
-                 k_scale, v_scale, out.data_ptr(), code, _ptr_or_none(lse))
-    return out, lse
+    return (_host or _host_calls()).attn_tree(
+        q, k_pages, v_pages, page_table, prefix_len, lens, B, R, h_q, h_kv, page_size, scale, masks,
+        positions, window, sinks, k_scale, v_scale, out, lse, _bf16_out(out_dtype), want_lse, stream)
 
 
 # Fixed scratch of fanout_attn_noalloc (FANOUT_NOALLOC_SCRATCH_BYTES in include/fanout.h).

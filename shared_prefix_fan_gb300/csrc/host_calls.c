@@ -1,10 +1,11 @@
-/* host_calls.c -- the host side of the small serving calls, as a CPython extension module.
+/* host_calls.c -- the host side of the calls of the 8-bit cache and of drafted trees, as a
+ * CPython extension module.
  *
- * The kernels behind these calls take 2 to 4 us in a drafting step, and a call through
- * ctypes with its checks in Python took 8 to 16 us of host time. Here the same checks, output
- * tensors and calls take 4 to 10, of which the launch is 2.5 and an output tensor made and
- * freed 1.9. The module holds no state of calls: it is handed torch's own
- * functions and types once (setup), and every call looks at its tensors again.
+ * Most kernels behind these calls take 2 to 4 us in a drafting step, and a call through
+ * ctypes with its checks in Python took 8 to 21 us of host time. Here the same checks, output
+ * tensors and calls take 4 to 14, of which the launch is 2.5 and an output tensor made and
+ * freed 1.9. The module holds no state of calls: it is handed torch's own functions and types
+ * once (setup), and every call looks at its tensors again.
  *
  * Checks are binding.py's: every tensor contiguous, of its type and shape, on the CUDA device
  * of the call's first one; integers that do not fit 32 bits are refused. Results of a call on
@@ -18,7 +19,7 @@
 #include "../../include/fanout.h"
 
 /* What setup() is given; owned for the life of the process. */
-enum { BF16, F8, U8, I32, I64, N_TYPES };
+enum { BF16, F8, U8, I32, I64, F32, N_TYPES };
 static PyObject *g_type[N_TYPES];
 static PyObject *g_empty, *g_raw_stream, *g_get_device, *g_device_guard, *g_empty_on, *g_handle_of,
     *g_raise;
@@ -428,7 +429,7 @@ done:
     return result;
 }
 
-/* A pair of pools of any kind, of pages of page_size tokens. */
+/* A pair of pools of any kind, of pages of page_size tokens (*h_kv < 0: any number of heads). */
 static int any_pools(const Call *c, PyObject *k, PyObject *v, int32_t page_size, int32_t *kind,
                      int32_t *pages, int32_t *h_kv, void **kp, void **vp) {
     PyObject *dtype = PyObject_GetAttr(k, s_dtype);
@@ -437,7 +438,7 @@ static int any_pools(const Call *c, PyObject *k, PyObject *v, int32_t page_size,
     Py_DECREF(dtype);
     *kind = type == U8 ? FANOUT_KV_Q4 : type == F8 ? FANOUT_KV_Q8 : FANOUT_KV_BF16;
     const int nd = type == U8 ? 3 : 4;
-    Py_ssize_t shape[4] = {-1, -1, type == U8 ? (Py_ssize_t)page_size * FANOUT_Q4_ROW_BYTES : page_size, 128};
+    Py_ssize_t shape[4] = {-1, *h_kv, type == U8 ? (Py_ssize_t)page_size * FANOUT_Q4_ROW_BYTES : page_size, 128};
     if (need(c, "k_pages", k, type, nd, shape, kp) < 0 || sizes(k, shape, 4) < 0 ||
         need(c, "v_pages", v, type, nd, shape, vp) < 0)
         return -1;
@@ -448,7 +449,7 @@ static int any_pools(const Call *c, PyObject *k, PyObject *v, int32_t page_size,
  *         page_size, stream) */
 static PyObject *kv_keep(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     if (arity("kv_keep", n, 10) < 0) return NULL;
-    int32_t kind, pages, h_kv, prefix_len, page_size, B = 0, width = 0;
+    int32_t kind, pages, h_kv = -1, prefix_len, page_size, B = 0, width = 0;
     if (int32_of(a[3], "prefix_len", &prefix_len) < 0 || int32_of(a[8], "page_size", &page_size) < 0)
         return NULL;
     Call c;
@@ -468,6 +469,120 @@ static PyObject *kv_keep(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         fanout_kv_keep(kp, vp, kind, tp, B, width, prefix_len, s, l, path, counts, rows[0], pages, h_kv, 128,
                        page_size, stream));
     result = Py_NewRef(Py_None);
+done:
+    drop(&c);
+    return result;
+}
+
+/* What the two attention calls share. Host lengths: the address of int32 [2, B] (binding._lens). */
+typedef struct {
+    int32_t prefix_len, B, width, h_q, h_kv, d, page_size, window, sinks, code;
+    const int32_t *lens;
+    Py_ssize_t R;
+    void *q, *table, *out, *lse;
+    PyObject *out_t, *lse_t;
+    float scale, k_scale, v_scale;
+} Attn;
+
+/* a: q .. scale as the calls below have them; tail: window, sinks, k_scale, v_scale, out, lse, bf16 out, want lse */
+static int attn_of(Call *c, Attn *x, PyObject *const *a, PyObject *const *tail) {
+    Py_ssize_t shape[3] = {0};
+    int want, nd;
+    if (int32_of(a[4], "prefix_len", &x->prefix_len) < 0 || int32_of(a[6], "branches", &x->B) < 0 ||
+        int32_of(a[8], "h_q", &x->h_q) < 0 || int32_of(a[9], "h_kv", &x->h_kv) < 0 ||
+        int32_of(a[10], "page_size", &x->page_size) < 0 || float_of(a[11], &x->scale) < 0 ||
+        int32_of(tail[0], "window", &x->window) < 0 || int32_of(tail[1], "sinks", &x->sinks) < 0 ||
+        float_of(tail[2], &x->k_scale) < 0 || float_of(tail[3], &x->v_scale) < 0)
+        return -1;
+    x->lens = PyLong_AsVoidPtr(a[5]);
+    x->R = PyLong_AsSsize_t(a[7]);
+    if (PyErr_Occurred() || (nd = sizes(a[0], shape, 3)) < 0) return -1;
+    if (nd != 3) {
+        PyErr_SetString(PyExc_ValueError, "q must be [R, H_q, d]");
+        return -1;
+    }
+    if (x->R < 0 || x->h_q < 0 || x->h_kv < 0) {  // (a size below 0 would stand for any)
+        PyErr_SetString(PyExc_ValueError, "rows and heads must not be negative");
+        return -1;
+    }
+    Py_ssize_t rows[3] = {x->R, x->h_q, shape[2]}, table[2] = {x->B, -1};
+    if (size32(shape[2], "d", &x->d) < 0 || need(c, "q", a[0], BF16, 3, rows, &x->q) < 0 ||
+        need(c, "page_table", a[3], I32, 2, table, &x->table) < 0 || sizes(a[3], table, 2) < 0 ||
+        size32(table[1], "page_table", &x->width) < 0 || (x->code = PyObject_IsTrue(tail[6])) < 0 ||
+        (want = PyObject_IsTrue(tail[7])) < 0)
+        return -1;
+    const int type = x->code ? BF16 : F32;
+    x->code = x->code ? FANOUT_OUT_BF16 : FANOUT_OUT_F32;
+    x->out_t = tail[4];
+    x->lse_t = tail[5];
+    x->lse = NULL;
+    if (x->out_t == Py_None) {
+        const int at = make(c, type, 3, rows, &x->out);
+        if (at < 0) return -1;
+        x->out_t = c->held[at];
+    } else if (need(c, "out", x->out_t, type, 3, rows, &x->out) < 0) {
+        return -1;
+    }
+    if (x->lse_t != Py_None) return need(c, "lse", x->lse_t, F32, 2, rows, &x->lse);
+    if (want) {
+        const int at = make(c, F32, 2, rows, &x->lse);
+        if (at < 0) return -1;
+        x->lse_t = c->held[at];
+    }
+    return 0;
+}
+
+/* attn_q8(q, k_pages, v_pages, page_table, prefix_len, lens, B, R, h_q, h_kv, page_size, scale,
+ *         causal, window, sinks, k_scale, v_scale, out, lse, bf16 out, want lse, stream)
+ *   -> (out, lse) */
+static PyObject *attn_q8(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    if (arity("attn_q8", n, 22) < 0) return NULL;
+    Call c;
+    if (begin(&c, a[0], "q", a[21]) < 0) return NULL;
+    PyObject *result = NULL;
+    Attn x;
+    int32_t pages = 0;
+    void *kp, *vp;
+    const int causal = PyObject_IsTrue(a[12]);
+    if (causal < 0 || attn_of(&c, &x, a, a + 13) < 0) goto done;
+    Py_ssize_t pool[4] = {-1, x.h_kv, x.page_size < 0 ? 0 : x.page_size, x.d};
+    if (need(&c, "k_pages", a[1], F8, 4, pool, &kp) < 0 || sizes(a[1], pool, 4) < 0 ||
+        need(&c, "v_pages", a[2], F8, 4, pool, &vp) < 0 || size32(pool[0], "num_pages", &pages) < 0)
+        goto done;
+    RUN(c, "fanout_attn_q8",
+        fanout_attn_q8(x.q, kp, vp, x.table, x.prefix_len, x.lens, x.lens + x.B, x.B, x.width, pages, x.h_q,
+                       x.h_kv, x.d, x.page_size, x.scale, causal, x.k_scale, x.v_scale, x.window, x.sinks,
+                       x.out, x.code, x.lse, stream));
+    result = PyTuple_Pack(2, x.out_t, x.lse_t);
+done:
+    drop(&c);
+    return result;
+}
+
+/* attn_tree(q, k_pages, v_pages, page_table, prefix_len, lens, B, R, h_q, h_kv, page_size, scale,
+ *           masks, positions, window, sinks, k_scale, v_scale, out, lse, bf16 out, want lse, stream)
+ *   -> (out, lse) */
+static PyObject *attn_tree(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    if (arity("attn_tree", n, 23) < 0) return NULL;
+    Call c;
+    if (begin(&c, a[0], "q", a[22]) < 0) return NULL;
+    PyObject *result = NULL;
+    Attn x;
+    int32_t kind, pages, words = 0;
+    void *kp, *vp, *masks, *positions = NULL;
+    if (attn_of(&c, &x, a, a + 14) < 0 ||
+        any_pools(&c, a[1], a[2], x.page_size, &kind, &pages, &x.h_kv, &kp, &vp) < 0)
+        goto done;
+    Py_ssize_t mask[2] = {x.R, -1};
+    if (need(&c, "masks", a[12], I32, 2, mask, &masks) < 0 || sizes(a[12], mask, 2) < 0 ||
+        size32(mask[1], "masks", &words) < 0 ||
+        (a[13] != Py_None && need(&c, "positions", a[13], I32, 1, mask, &positions) < 0))
+        goto done;
+    RUN(c, "fanout_attn_tree",
+        fanout_attn_tree(x.q, kp, vp, kind, x.table, x.prefix_len, x.lens, x.lens + x.B, x.B, x.width,
+                         pages, x.h_q, x.h_kv, x.d, x.page_size, x.scale, masks, words, positions, x.window,
+                         x.sinks, x.k_scale, x.v_scale, x.out, x.code, x.lse, stream));
+    result = PyTuple_Pack(2, x.out_t, x.lse_t);
 done:
     drop(&c);
     return result;
@@ -497,6 +612,8 @@ static PyMethodDef methods[] = {
     {"tree_rows", (PyCFunction)(void (*)(void))tree_rows, METH_FASTCALL, NULL},
     {"tree_accept", (PyCFunction)(void (*)(void))tree_accept, METH_FASTCALL, NULL},
     {"kv_keep", (PyCFunction)(void (*)(void))kv_keep, METH_FASTCALL, NULL},
+    {"attn_q8", (PyCFunction)(void (*)(void))attn_q8, METH_FASTCALL, NULL},
+    {"attn_tree", (PyCFunction)(void (*)(void))attn_tree, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_host_calls", NULL, -1, methods, NULL, NULL,
                                     NULL, NULL};

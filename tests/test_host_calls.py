@@ -1,16 +1,18 @@
-"""The extension module behind the small serving calls, on the CPU: which arguments it refuses,
+"""The extension module behind the calls of the 8-bit cache and of drafts, on the CPU: which arguments it refuses,
 what it hands to the library, which device and stream it uses, and that no object is kept.
 
 Its tensors here are stand-ins with the attributes that it reads; their addresses are made up,
 and every call is refused or has no rows, so nothing is launched."""
 import sys
 
+import numpy as np
 import pytest
 import torch
 
 from shared_prefix_fan_gb300 import binding
 
-BF16, F8, U8, I32, I64 = (torch.bfloat16, torch.float8_e4m3fn, torch.uint8, torch.int32, torch.int64)
+BF16, F8, U8, I32, I64, F32 = TYPES = (torch.bfloat16, torch.float8_e4m3fn, torch.uint8, torch.int32,
+                                       torch.int64, torch.float32)
 DEV, OTHER = torch.device("cuda", 0), torch.device("cuda", 1)
 
 
@@ -78,7 +80,7 @@ def built():
 @pytest.fixture
 def host(built):
     module, fake = binding._host_calls(), Torch()
-    module.setup((BF16, F8, U8, I32, I64), fake.empty, fake.raw_stream, fake.get_device, fake.guard,
+    module.setup(TYPES, fake.empty, fake.raw_stream, fake.get_device, fake.guard,
                  fake.empty_on, fake.handle_of, binding._check)
     yield module, fake
     binding._host = None  # the next call sets it up with torch's own
@@ -117,7 +119,26 @@ def keep(n=0, B=2, dtype=BF16, **kw):
     return {**d, **kw}
 
 
-CALLS = {"kv_append_q8": append, "kv_read_q8": read, "tree_rows": rows, "tree_accept": accept,
+LENS = np.zeros((2, 3), dtype=np.int32)  # three branches of no rows
+
+
+def attn(R=0, **kw):
+    d = dict(q=Fake(BF16, R, 4, 128), k_pages=Fake(F8, 9, 2, 16, 128), v_pages=Fake(F8, 9, 2, 16, 128),
+             page_table=Fake(I32, 3, 8), prefix_len=0, lens=LENS.ctypes.data, B=3, R=R, h_q=4, h_kv=2,
+             page_size=16, scale=1.0, causal=True, window=0, sinks=0, k_scale=1.0, v_scale=1.0, out=None,
+             lse=None, bf16=False, want_lse=True, stream=None)
+    return {**d, **kw}
+
+
+def tree(R=0, dtype=BF16, **kw):
+    shape = (9, 2, 16 * 72) if dtype is U8 else (9, 2, 16, 128)
+    d = attn(R, k_pages=Fake(dtype, *shape), v_pages=Fake(dtype, *shape))
+    tail = {k: d.pop(k) for k in list(d)[list(d).index("causal"):]}
+    del tail["causal"]
+    return {**d, "masks": Fake(I32, R, 1), "positions": Fake(I32, R), **tail, **kw}
+
+
+CALLS = {"attn_q8": attn, "attn_tree": tree, "kv_append_q8": append, "kv_read_q8": read, "tree_rows": rows, "tree_accept": accept,
          "kv_keep": keep}
 
 
@@ -136,6 +157,13 @@ def test_no_rows_is_no_work(host):
     assert (path.dtype, counts.dtype, after.dtype) == (I32, I32, I64)
     for dtype in (BF16, F8, U8):
         assert module.kv_keep(*keep(dtype=dtype).values()) is None
+        out, lse = module.attn_tree(*tree(dtype=dtype).values())
+        assert (out.shape, out.dtype, lse.shape, lse.dtype) == ((0, 4, 128), F32, (0, 4), F32)
+    out, lse = module.attn_q8(*attn(bf16=True).values())
+    assert (out.shape, out.dtype, lse.shape, lse.dtype) == ((0, 4, 128), BF16, (0, 4), F32)
+    to = attn(out=Fake(F32, 0, 4, 128), lse=Fake(F32, 0, 4), want_lse=False)
+    assert module.attn_q8(*to.values()) == (to["out"], to["lse"])
+    assert module.attn_tree(*tree(want_lse=False, positions=None).values())[1] is None
 
 
 @pytest.mark.parametrize("name", CALLS)
@@ -157,7 +185,9 @@ def test_refused_by_the_library(host):
     fake.device = 1
     for name, args in (("kv_append_q8", append(k_scale=0.0)), ("kv_read_q8", read(v_scale=-1.0)),
                        ("tree_rows", rows(page_size=0)), ("tree_accept", accept(B=5000)),
-                       ("kv_keep", keep(prefix_len=-1))):
+                       ("kv_keep", keep(prefix_len=-1)), ("attn_q8", attn(scale=0.0)),
+                       ("attn_q8", attn(window=4, causal=False)), ("attn_tree", tree(sinks=1)),
+                       ("attn_tree", tree(scale=float("inf")))):
         fake.log.clear()
         with pytest.raises(binding.FanoutError):
             getattr(module, name)(*args.values())
@@ -197,6 +227,19 @@ REFUSED = [
     ("kv_keep", keep(dtype=U8, page_size=32)), ("kv_keep", keep(v_pages=Fake(F8, 9, 2, 16, 128))),
     ("kv_keep", keep(v_pages=Fake(BF16, 9, 4, 16, 128))), ("kv_keep", keep(counts=Fake(I32, 3))),
     ("kv_keep", keep(path=Fake(I64, 0))), ("kv_keep", keep(prefix_len=1 << 32)),
+    ("attn_q8", attn(q=Fake(F32, 0, 4, 128))), ("attn_q8", attn(q=Fake(BF16, 4, 128))),
+    ("attn_q8", attn(R=2, q=Fake(BF16, 1, 4, 128))), ("attn_q8", attn(h_q=8)),
+    ("attn_q8", {**attn(), "R": -1}), ("attn_q8", attn(h_kv=-1)), ("attn_q8", attn(h_kv=4)),
+    ("attn_q8", attn(page_size=32)), ("attn_q8", attn(page_size=-1)), ("attn_q8", attn(B=2)),
+    ("attn_q8", attn(page_table=Fake(I32, 24))), ("attn_q8", attn(window=1 << 31)),
+    ("attn_q8", attn(k_pages=Fake(BF16, 9, 2, 16, 128))), ("attn_q8", attn(out=Fake(BF16, 0, 4, 128))),
+    ("attn_q8", attn(bf16=True, out=Fake(F32, 0, 4, 128))), ("attn_q8", attn(lse=Fake(F32, 1, 4))),
+    ("attn_q8", attn(v_pages=Fake(F8, 8, 2, 16, 128))), ("attn_q8", attn(prefix_len=1 << 31)),
+    ("attn_tree", tree(masks=Fake(I32, 1, 1))), ("attn_tree", tree(masks=Fake(I64, 0, 1))),
+    ("attn_tree", tree(masks=Fake(I32, 0))), ("attn_tree", tree(positions=Fake(I32, 1))),
+    ("attn_tree", tree(positions=Fake(I32, 0, device=OTHER))), ("attn_tree", tree(h_kv=1)),
+    ("attn_tree", tree(dtype=U8, page_size=32)), ("attn_tree", tree(v_pages=Fake(F8, 9, 2, 16, 128))),
+    ("attn_tree", tree(out=Fake(F32, 0, 4, 64))), ("attn_tree", tree(sinks=-(1 << 40))),
     ("kv_keep", keep(dtype=F8, k_pages=Fake(F8, 9, 2, 16, 64), v_pages=Fake(F8, 9, 2, 16, 64))),
 ]
 
@@ -212,11 +255,13 @@ def test_refusals(host, name, args):
 @pytest.mark.parametrize("name", CALLS)
 def test_wrong_kinds_of_objects(host, name):
     module, fake = host
-    args = list(CALLS[name]().values())
+    names, args = list(CALLS[name]()), list(CALLS[name]().values())
     for bad in (args[:-1], args + [None], [None] + args[1:]):
         with pytest.raises((TypeError, AttributeError)):
             getattr(module, name)(*bad)
     for i in range(len(args)):  # any one argument of a type it cannot be
+        if names[i] in ("causal", "bf16", "want_lse"):  # (truth values: anything has one)
+            continue
         with pytest.raises((TypeError, AttributeError, ValueError)):
             getattr(module, name)(*args[:i], object(), *args[i + 1:])
 
@@ -229,7 +274,7 @@ def test_nothing_is_kept(host, name):
     good = list(CALLS[name](stream=1 << 20).values())
     bad = [a for n, a in REFUSED if n == name]
     held = good + [x for a in bad for x in a.values()] + [
-        DEV, OTHER, BF16, F8, U8, I32, I64, fake.empty.__func__, ()]
+        DEV, OTHER, *TYPES, fake.empty.__func__, ()]
 
     def run(times):
         for _ in range(times):

@@ -147,7 +147,10 @@ def test_integers_past_32_bits_are_refused(monkeypatch, big):
 
 @pytest.mark.parametrize("window,sinks", [(-2 ** 32 + 5, 0), (4, -2 ** 32 + 1)])
 def test_negative_windows_stay_negative(monkeypatch, window, sinks):
-    c = Calls(monkeypatch)
+    calls = []
+    record = lambda self, *a: calls.append(a)  # noqa: E731
+    monkeypatch.setattr(binding, "_host", type("Host", (), {
+        "tree_rows": record, "attn_q8": record, "attn_tree": record})())
     i, table = torch.zeros(1, dtype=torch.int32), torch.zeros((1, 4), dtype=torch.int32)
     q = torch.zeros((2, 1, 128), dtype=torch.bfloat16)
     pool = torch.zeros((4, 1, 16, 128), dtype=torch.uint8).view(torch.float8_e4m3fn)
@@ -155,10 +158,9 @@ def test_negative_windows_stay_negative(monkeypatch, window, sinks):
     binding.attn_q8(q, pool, pool, table, 16, [4], [2], 1, 1, 16, 1.0, True, 1.0, 1.0, window, sinks)
     binding.attn_tree(q, pool, pool, table, 16, [4], [2], 1, 1, 16, 1.0, masks, None, window, sinks)
     if not sinks:
-        monkeypatch.setattr(binding, "_host", type("Host", (), {
-            "tree_rows": lambda self, *a: c.calls.append(a)})())
         binding.tree_rows(i, table, 0, i, i, 16, 4, window)
-    for args in c.calls:
+    assert len(calls) == (2 if sinks else 3)
+    for args in calls:
         ints = [a for a in args if isinstance(a, int) and a < 0]
         assert ints and all(a >= -2 ** 31 for a in ints)
 
