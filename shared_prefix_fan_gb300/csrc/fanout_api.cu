@@ -207,6 +207,7 @@ int attn_call(bool full, Pool pool, const TreeArgs& tree, const void* q, const v
     in.window = window;
     in.sinks = sinks;
     in.tree = is_tree;
+    in.own_cuts = is_tree || pool == Pool::q8;
     if (pool != Pool::bf16) in.row_bytes = 2 * (pool == Pool::q4 ? kQ4RowBytes : kHD);
     bool patched = false;
     if (ws->plan_ready && key != ws->key && key.size() == ws->key.size() &&

@@ -29,6 +29,7 @@ struct PlanInput {
     // Row plans of drafted trees (causal): a branch's new tokens all sit behind the same
     // keys, and any of them may see any other.
     int32_t tree = 0;
+    int32_t own_cuts = 0;  // 1: row plans whose branches sweep the prefix themselves may be cut
 };
 
 // A key range of the plan: the rows of n_tok tokens from tok_begin (one KV

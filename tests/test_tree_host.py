@@ -59,7 +59,8 @@ def shim(tmp_path_factory):
     return ctypes.CDLL(so).tree_plan
 
 
-def plan(shim, S, T, P, hq, hkv, page, window=0, sinks=0, prev=None, splits=0, row_bytes=256):
+def plan(shim, S, T, P, hq, hkv, page, window=0, sinks=0, prev=None, splits=0, row_bytes=256,
+         tree=1):
     """S counts the drafted tokens, as the attention calls do."""
     S, T = np.asarray(S, np.int32), np.asarray(T, np.int32)
     prev = None if prev is None else np.asarray(prev, np.int32)
@@ -67,7 +68,7 @@ def plan(shim, S, T, P, hq, hkv, page, window=0, sinks=0, prev=None, splits=0, r
     units, R = np.zeros((50000, 8), np.int32), int(T.sum())
     pos, info = np.zeros(max(2 * R, 1), np.int32), np.zeros(6, np.int32)
     n = shim(ptr(prev), ptr(S), ptr(T), len(S), P, hq, hkv, page, window, sinks, splits, row_bytes,
-             ptr(units), len(units), ptr(pos), ptr(info))
+             tree, ptr(units), len(units), ptr(pos), ptr(info))
     assert 0 <= n <= len(units)
     return units[:n], pos[:R], pos[R:2 * R], info
 
@@ -116,6 +117,45 @@ def test_tree_plans_sweep_every_key_once(shim, seed):
     window, sinks = (0, 0) if seed % 3 == 0 else (int(rng.integers(1, 400)), int(rng.integers(0, 40)))
     check_plan(shim, S.tolist(), T.tolist(), P, hq, hkv, page, window, sinks,
                splits=int(rng.choice([0, 0, 1, 3])))
+
+
+CUT = [  # (S, T, P, H_q, H_kv, page, window, sinks): row blocks that hold one branch only
+    ([100 + 40 * b for b in range(8)], [32] * 8, 16384, 64, 8, 64, 0, 0),
+    ([700, 90, 333], [64, 32, 31], 5000, 16, 2, 16, 0, 0),
+    ([100 + 40 * b for b in range(8)], [32] * 8, 16384, 64, 8, 64, 8192, 4),
+    ([40, 900], [96, 160], 9000, 32, 4, 128, 3000, 300)]
+
+
+@pytest.mark.parametrize("case", CUT)
+def test_branches_that_sweep_the_prefix_themselves_are_cut(shim, case):
+    units, info = check_plan(shim, [s + t for s, t in zip(case[0], case[1])], *case[1:])
+    assert info[0] == 0 and info[3] > 0  # no shared range, and partials
+    moved = [s + t + 1 for s, t in zip(case[0], case[1])]
+    check_plan(shim, moved, *case[1:], prev=[s - 1 for s in moved])
+
+
+@pytest.mark.parametrize("case", CUT)
+def test_cut_causal_plans_sweep_every_key_once(shim, case):
+    S, T, P, hq, hkv, page, window, sinks = case
+    S = [s + t for s, t in zip(S, T)]
+    kept = 0
+    for prev in [None] + [[s - i for s in S] for i in (1, 2, 3, 5, 8)]:
+        units, pos, _, info = plan(shim, S, T, P, hq, hkv, page, window, sinks, prev=prev, tree=0)
+        kept += int(info[4])
+        assert info[0] == 0 and info[3] > 0
+        swept = np.zeros((sum(T), hkv, P + max(S)), np.int32)
+        rows = [(b, i) for b, t in enumerate(T) for i in range(t)]
+        for h, b, t0, nt, kb, ke, first_end, _ in units.tolist():
+            assert all(rows[r][0] == b for r in range(t0, t0 + nt))
+            swept[t0:t0 + nt, h, kb:ke] += 1
+            swept[t0:t0 + nt, h, :first_end] += 1
+        for r, (b, i) in enumerate(rows):
+            assert pos[r] == P + S[b] - T[b] + i
+            j = np.arange(P + max(S))
+            may = (j <= pos[r]) & ((j > pos[r] - window) | (j < sinks) if window else True)
+            assert (swept[r, :, may] == 1).all() and (swept[r] <= 1).all()
+            assert not swept[r, :, P + S[b]:].any()
+    assert kept > 0
 
 
 @pytest.mark.parametrize("window,sinks", [(0, 0), (64, 4)])
