@@ -102,6 +102,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "launch_after.cuh"
 #include "ptx_fp8.cuh"
 #include "ptx_sm100.cuh"
 #include "row_unit.cuh"
@@ -391,7 +392,7 @@ __device__ void producer_warp(const RowParams& p, const Smem<NQ, F>& sm, const C
             // page ids, 32 per window, loaded one window ahead
             auto load_window = [&](int w) -> int {
                 const int idx = w * 32 + lane;
-                return idx < n_pages ? __ldg(table + begin / ps + idx) : 0;
+                return idx < n_pages ? table[begin / ps + idx] : 0;
             };
             int win = 0, win_cur = load_window(0), win_nxt = load_window(1);
             for (int j = 0; j < n_tiles && ok; ++j) {
@@ -986,8 +987,8 @@ __device__ __forceinline__ void mask_tree_tile(uint32_t taddr, int last, int lo,
         uint32_t see = below(ub) & (below(sink) | ~below(lo));
         if (ub < c0 + 32) {  // (a lane without a row has no mask)
             const int bit = c0 - ub, w = bit >> 5;
-            const uint32_t a = mask && w >= 0 && w < words ? __ldg(mask + w) : 0u;
-            const uint32_t b = mask && w >= -1 && w + 1 < words ? __ldg(mask + w + 1) : 0u;
+            const uint32_t a = mask && w >= 0 && w < words ? mask[w] : 0u;
+            const uint32_t b = mask && w >= -1 && w + 1 < words ? mask[w + 1] : 0u;
             uint32_t bits = __funnelshift_r(a, b, bit & 31);
             if (self >= c0 && self < c0 + 32) bits |= 1u << (self - c0);
             see |= bits & ~below(ub);
@@ -1181,7 +1182,7 @@ __device__ void softmax_group(const RowParams& p, const Smem<NQ, F>& sm, uint32_
         // (a drafted token's position is at most a tree's depth past the keys before it)
         int row_pos1 = row_end + (Tree ? 1 : 0);
         if (Tree && row_valid && p.positions)
-            row_pos1 = min(max(__ldg(p.positions + tok), row_end), row_end + kMaxTreeTokens - 1) + 1;
+            row_pos1 = min(max(p.positions[tok], row_end), row_end + kMaxTreeTokens - 1) + 1;
         const int self = Tree && row_valid ? p.tok_pos[p.R + tok] : 0;
         const uint32_t* const mask =
             Tree && row_valid ? p.masks + static_cast<int64_t>(tok) * p.mask_words : nullptr;
@@ -1373,6 +1374,7 @@ __global__ void __launch_bounds__(Cfg<NQ, F>::kThreads, 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *sm.tmem_slot();
+    wait_for_previous();  // up to here nothing of global memory was touched
 
     if (C::kF16 && warp < kWarpSoftmax) ptx::regs_dec<C::kRegsOther>();
     if (tmem != 0 || (sm.base & 1023u) != 0) {
@@ -1441,9 +1443,8 @@ cudaError_t launch_nq(const RowParams& p, const CUtensorMap& tm_q, const CUtenso
             if (known) attr_set[dev].store(true, std::memory_order_release);
         }
     }
-    attn_rows_kernel<NQ, F, Tree><<<grid, Cfg<NQ, F>::kThreads, Cfg<NQ, F>::kSmemAlloc, stream>>>(
-        p, tm_q, tm_k, tm_v);
-    return cudaGetLastError();
+    return launch_after(attn_rows_kernel<NQ, F, Tree>, grid, Cfg<NQ, F>::kThreads, Cfg<NQ, F>::kSmemAlloc,
+                        stream, p, tm_q, tm_k, tm_v);
 }
 
 }  // namespace

@@ -18,6 +18,7 @@
 
 #include <cstdint>
 
+#include "launch_after.cuh"
 #include "ptx_fp8.cuh"
 #include "ptx_sm100.cuh"
 #include "row_values.cuh"
@@ -29,6 +30,16 @@ namespace {
 constexpr int kErrInval = 1;  // FANOUT_EINVAL
 constexpr int kWarps = 8;
 constexpr int kRows = 2;  // (row, head) pairs of a half-warp
+
+// 256-bit load (address 32-byte aligned). An ordinary one: the rows may have been written
+// while this kernel started up (launch_after.cuh).
+__device__ __forceinline__ void load_v8(const void* ptr, uint32_t (&r)[8]) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                   "=r"(r[7])
+                 : "l"(ptr)
+                 : "memory");
+}
 
 // Pair k of this half-warp; false behind the last one.
 __device__ __forceinline__ bool row_of(const Q8RowParams& p, int k, uint32_t& r, uint32_t& h) {
@@ -53,6 +64,7 @@ __device__ __forceinline__ bool place_of(const Q8RowParams& p, int64_t slot, uin
 }
 
 __global__ void __launch_bounds__(32 * kWarps) append_q8_kernel(const Q8RowParams p) {
+    after_previous();
     const int part = threadIdx.x & 7;
     const bool is_v = threadIdx.x & 8;
     uint32_t raws[kRows][8], hs[kRows];
@@ -62,15 +74,15 @@ __global__ void __launch_bounds__(32 * kWarps) append_q8_kernel(const Q8RowParam
         uint32_t r;
         slot[k] = -1;
         if (!row_of(p, k, r, hs[k])) continue;
-        slot[k] = __ldg(p.slots + r);
+        slot[k] = __ldcg(p.slots + r);
         const __nv_bfloat16* src = is_v ? p.v_rows + static_cast<int64_t>(r) * p.v_stride
                                         : p.k_rows + static_cast<int64_t>(r) * p.k_stride;
         src += hs[k] * kHD + part * 16;
         if (p.align32) {  // one load of a whole sector
-            ptx::ld_global_v8(src, raws[k]);
+            load_v8(src, raws[k]);
         } else {
             const uint4* from = reinterpret_cast<const uint4*>(src);
-            const uint4 a = __ldg(from), b = __ldg(from + 1);
+            const uint4 a = __ldcg(from), b = __ldcg(from + 1);
             raws[k][0] = a.x, raws[k][1] = a.y, raws[k][2] = a.z, raws[k][3] = a.w;
             raws[k][4] = b.x, raws[k][5] = b.y, raws[k][6] = b.z, raws[k][7] = b.w;
         }
@@ -113,6 +125,7 @@ __global__ void __launch_bounds__(32 * kWarps) append_q8_kernel(const Q8RowParam
 }
 
 __global__ void __launch_bounds__(32 * kWarps) read_q8_kernel(const Q8RowParams p) {
+    after_previous();
     const int part = threadIdx.x & 7;
     const bool is_v = threadIdx.x & 8;
     int64_t slot[kRows], at[kRows];
@@ -122,13 +135,13 @@ __global__ void __launch_bounds__(32 * kWarps) read_q8_kernel(const Q8RowParams 
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
         slot[k] = -1;
-        if (row_of(p, k, rs[k], hs[k])) slot[k] = __ldg(p.slots + rs[k]);
+        if (row_of(p, k, rs[k], hs[k])) slot[k] = __ldcg(p.slots + rs[k]);
     }
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
         on[k] = place_of(p, slot[k], hs[k], at[k]);
         if (on[k])
-            cs[k] = __ldg(reinterpret_cast<const uint4*>((is_v ? p.v_pool : p.k_pool) + at[k] +
+            cs[k] = __ldcg(reinterpret_cast<const uint4*>((is_v ? p.v_pool : p.k_pool) + at[k] +
                                                          part * 16));
     }
     const float gs = is_v ? p.v_scale : p.k_scale;
@@ -161,10 +174,8 @@ __global__ void __launch_bounds__(32 * kWarps) read_q8_kernel(const Q8RowParams 
 cudaError_t launch_q8_rows(const Q8RowParams& p, bool read, cudaStream_t stream) {
     const int64_t items = static_cast<int64_t>(p.n_rows) * p.H_kv;
     if (items <= 0) return cudaSuccess;
-    const unsigned grid = static_cast<unsigned>((items + 2 * kWarps * kRows - 1) / (2 * kWarps * kRows));
-    if (read) read_q8_kernel<<<grid, 32 * kWarps, 0, stream>>>(p);
-    else append_q8_kernel<<<grid, 32 * kWarps, 0, stream>>>(p);
-    return cudaGetLastError();
+    const int grid = static_cast<int>((items + 2 * kWarps * kRows - 1) / (2 * kWarps * kRows));
+    return launch_after(read ? read_q8_kernel : append_q8_kernel, grid, 32 * kWarps, 0, stream, p);
 }
 
 }  // namespace fanout

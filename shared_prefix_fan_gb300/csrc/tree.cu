@@ -22,6 +22,7 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "launch_after.cuh"
 #include "rows.h"
 
 namespace fanout {
@@ -45,10 +46,10 @@ __device__ bool sum_rows(const TreeParams& p, Sums& sm, int32_t b_first, bool pl
     before = all = 0;
     bool ok = true;
     for (int b = threadIdx.x; b < p.num_branches; b += kThreads) {
-        const int32_t n = __ldg(p.lens + b);
+        const int32_t n = __ldcg(p.lens + b);
         ok &= n >= 0 && n <= kMaxTreeTokens && (p.words == 0 || n <= 32 * p.words);
         if (place) {
-            const int32_t s = __ldg(p.suffix_lens + b);
+            const int32_t s = __ldcg(p.suffix_lens + b);
             const int64_t end = static_cast<int64_t>(p.prefix_len) + s + n;
             ok &= s >= 0 && end <= kMaxTokens &&
                   end <= static_cast<int64_t>(p.max_pages) * p.page_size;
@@ -85,6 +86,7 @@ __device__ __forceinline__ void run_of(int32_t items, int32_t& i0, int32_t& i1) 
 
 // ------------------------------------------------------------ masks, positions, slots
 __global__ void __launch_bounds__(kThreads) tree_rows_kernel(const TreeParams p) {
+    after_previous();
     __shared__ Sums sums;
     __shared__ int32_t parent[kMaxTreeTokens];
     int32_t b0, b1;
@@ -102,10 +104,10 @@ __global__ void __launch_bounds__(kThreads) tree_rows_kernel(const TreeParams p)
     }
     if (!ok) return;
     for (int32_t b = b0; b < b1; ++b) {
-        const int32_t T = __ldg(p.lens + b), n = p.prefix_len + __ldg(p.suffix_lens + b);
+        const int32_t T = __ldcg(p.lens + b), n = p.prefix_len + __ldcg(p.suffix_lens + b);
         __syncthreads();
         for (int t = threadIdx.x; t < T; t += kThreads) {
-            int32_t up = __ldg(p.parents + row + t);
+            int32_t up = __ldcg(p.parents + row + t);
             if (up < -1 || up >= t) {  // reported, and taken as none
                 atomicCAS(p.err, 0, kErrInval);
                 up = -1;
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(kThreads) tree_rows_kernel(const TreeParams p)
             const int32_t key = n + t;
             const int32_t i = static_cast<int32_t>(static_cast<uint32_t>(key) /
                                                    static_cast<uint32_t>(p.page_size));
-            const int32_t page = __ldg(p.page_table + static_cast<int64_t>(b) * p.max_pages + i);
+            const int32_t page = __ldcg(p.page_table + static_cast<int64_t>(b) * p.max_pages + i);
             if (page < 0) atomicCAS(p.err, 0, kErrInval);
             p.slots[row + t] =
                 page < 0 ? -1 : static_cast<int64_t>(page) * p.page_size + (key - i * p.page_size);
@@ -139,6 +141,7 @@ __global__ void __launch_bounds__(kThreads) tree_rows_kernel(const TreeParams p)
 
 // ------------------------------------------------------------ the accepted path
 __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const TreeParams p) {
+    after_previous();
     __shared__ Sums sums;
     __shared__ int32_t parent[kMaxTreeTokens];
     __shared__ int64_t draft[kMaxTreeTokens];
@@ -160,15 +163,15 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const TreeParams 
             }
             continue;
         }
-        const int32_t T = __ldg(p.lens + b);
+        const int32_t T = __ldcg(p.lens + b);
         __syncthreads();
         for (int t = threadIdx.x; t < T; t += kThreads) {
-            parent[t] = __ldg(p.parents + row + t);
-            draft[t] = __ldg(p.draft + row + t);
+            parent[t] = __ldcg(p.parents + row + t);
+            draft[t] = __ldcg(p.draft + row + t);
         }
         __syncthreads();
         if (threadIdx.x < 32) {
-            int64_t want = __ldg(p.first + b);
+            int64_t want = __ldcg(p.first + b);
             int32_t at = -1, count = 0;
             // (a child comes behind its parent, so the search goes on behind it)
             for (int base = 0; base < T;) {
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const TreeParams 
                     continue;
                 }
                 at = base + __ffs(hit) - 1;
-                want = __ldg(p.target + row + at);
+                want = __ldcg(p.target + row + at);
                 if (lane == 0) p.path[row + count] = at;
                 ++count;
                 base = at + 1;
@@ -223,6 +226,7 @@ constexpr int kMoves = 4;                     // rows read before any is written
 
 template <Pool F>
 __global__ void __launch_bounds__(kThreads) kv_keep_kernel(const TreeParams p) {
+    after_previous();
     using Row = RowOf<F>;
     __shared__ Sums sums;
     const int32_t groups = (p.H_kv + kHeadsPerItem - 1) / kHeadsPerItem;
@@ -239,18 +243,18 @@ __global__ void __launch_bounds__(kThreads) kv_keep_kernel(const TreeParams p) {
     int32_t last = i0 / groups;
     for (int32_t item = i0; item < i1; ++item) {
         const int32_t b = item / groups;
-        if (b != last) row += __ldg(p.lens + last);
+        if (b != last) row += __ldcg(p.lens + last);
         last = b;
         const int32_t h = (item - b * groups) * kHeadsPerItem + (threadIdx.x >> 5);
         if (h >= p.H_kv) continue;
-        const int32_t T = __ldg(p.lens + b), count = __ldg(p.counts + b);
-        const int32_t n = p.prefix_len + __ldg(p.suffix_lens + b);
+        const int32_t T = __ldcg(p.lens + b), count = __ldcg(p.counts + b);
+        const int32_t n = p.prefix_len + __ldcg(p.suffix_lens + b);
         const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
         // a path that does not ascend inside the branch moves nothing
         bool good = count >= 0 && count <= T;
         for (int i = lane; good && i < count; i += 32) {
-            const int32_t from = __ldg(p.path + row + i);
-            const int32_t before = i > 0 ? __ldg(p.path + row + i - 1) : -1;
+            const int32_t from = __ldcg(p.path + row + i);
+            const int32_t before = i > 0 ? __ldcg(p.path + row + i - 1) : -1;
             good = from > before && from < T;
         }
         if (!__all_sync(0xffffffffu, good)) {
@@ -262,11 +266,11 @@ __global__ void __launch_bounds__(kThreads) kv_keep_kernel(const TreeParams p) {
             int32_t from = 0, slot_s = 0, slot_d = 0, page_s = -1, page_d = -1;
             const int32_t to = c0 + lane;
             if (to < count) {
-                from = __ldg(p.path + row + to);
+                from = __ldcg(p.path + row + to);
                 auto place = [&](int32_t key, int32_t& page, int32_t& slot) {
                     const int32_t i = static_cast<int32_t>(static_cast<uint32_t>(key) /
                                                            static_cast<uint32_t>(p.page_size));
-                    page = __ldg(table + i);
+                    page = __ldcg(table + i);
                     slot = key - i * p.page_size;
                     if (page < 0 || page >= p.num_pages) {
                         atomicCAS(p.err, 0, kErrInval);
@@ -313,22 +317,20 @@ int grid_for(int64_t items) {
 }  // namespace
 
 cudaError_t launch_tree_rows(const TreeParams& p, cudaStream_t stream) {
-    tree_rows_kernel<<<grid_for(p.num_branches), kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_after(tree_rows_kernel, grid_for(p.num_branches), kThreads, 0, stream, p);
 }
 
 cudaError_t launch_tree_accept(const TreeParams& p, cudaStream_t stream) {
-    tree_accept_kernel<<<grid_for(p.num_branches), kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_after(tree_accept_kernel, grid_for(p.num_branches), kThreads, 0, stream, p);
 }
 
 cudaError_t launch_kv_keep(const TreeParams& p, cudaStream_t stream) {
     const int groups = (p.H_kv + kHeadsPerItem - 1) / kHeadsPerItem;
     const int grid = grid_for(static_cast<int64_t>(p.num_branches) * groups);
-    if (p.pool == Pool::bf16) kv_keep_kernel<Pool::bf16><<<grid, kThreads, 0, stream>>>(p);
-    else if (p.pool == Pool::q4) kv_keep_kernel<Pool::q4><<<grid, kThreads, 0, stream>>>(p);
-    else kv_keep_kernel<Pool::q8><<<grid, kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    auto* kernel = p.pool == Pool::bf16 ? kv_keep_kernel<Pool::bf16>
+                   : p.pool == Pool::q4 ? kv_keep_kernel<Pool::q4>
+                                        : kv_keep_kernel<Pool::q8>;
+    return launch_after(kernel, grid, kThreads, 0, stream, p);
 }
 
 }  // namespace fanout

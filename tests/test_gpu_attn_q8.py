@@ -194,3 +194,12 @@ def test_pools_past_32_bit_offsets():
     out, lse = prob.run()
     assert binding.last_error() == binding.OK
     prob.check(out, lse)
+
+
+@pytest.mark.parametrize("causal,window,sinks", [(True, 0, 0), (True, 2500, 200), (False, 0, 0)])
+def test_branches_that_sweep_the_prefix_themselves(causal, window, sinks):
+    """Branches of a unit's rows and more: their own sweeps are cut, and the plan moves with
+    the suffixes."""
+    for more in (0, 1, 2, 130):
+        run([364 + more, 52 + more, 164], [64, 32, 31], 3000, 16, 2, 16, causal=causal, window=window,
+            sinks=sinks, seed=more)

@@ -207,3 +207,13 @@ def test_on_another_stream_and_into_given_outputs(kind):
     got, none = prob.run("bf16", stream=s, out=out, want_lse=False)
     torch.cuda.current_stream().wait_stream(s)
     assert none is None and got is out and torch.equal(out, here) and not flat[:8].any()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (2500, 200)])
+def test_branches_that_sweep_the_prefix_themselves(kind, window, sinks):
+    """Branches of a unit's rows and more: their own sweeps are cut, and the plan moves with
+    the suffixes."""
+    for more in (0, 1, 2, 130):
+        run([300 + more, 20 + more, 133], trees_of([64, 32, 31], seed=more), 3000, 16, 2, 16, kind=kind,
+            window=window, sinks=sinks, out_dtype="bf16", seed=more)
