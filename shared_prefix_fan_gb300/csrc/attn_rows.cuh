@@ -81,18 +81,18 @@
 // an 8-bit prefill then). A boundary between units costs about 10000 cycles (epilogue,
 // next Q, masked tiles).
 //   4-bit prefill, 2048 rows x 64 heads over 32768 keys: 1440 us, 1480 TFLOP/s
-//   8-bit, the same: 1300 us (in a row of calls, power-limited, 1350), 1640 TFLOP/s
-//   4-bit, 32 branches of 1..32 tokens over 65536 shared keys: 825 us, 1210 TFLOP/s
+//   8-bit, the same: 1310 us (in a row of calls, power-limited, 1366), 1630 TFLOP/s
+//   4-bit, 32 branches of 1..32 tokens over 65536 shared keys: 829 us, 1205 TFLOP/s
 //   8-bit, 32 branches of 1..64 drafted tokens over 65536 shared keys: 1500 us, 1505 TFLOP/s
-//   bf16, 8 branches of 32 drafted tokens over 32768 shared keys: 206 us, 1354 TFLOP/s
-//   bf16, 32 branches of 1..32 tokens over 16384 keys, window 2048: 97 us, 375 TFLOP/s
+//   bf16, 8 branches of 32 drafted tokens over 32768 shared keys: 200 us, 1394 TFLOP/s
+//   bf16, 32 branches of 1..32 tokens over 16384 keys, window 2048: 94 us, 387 TFLOP/s
 //   bf16 prefill, 4096 rows x 64 heads, window 1024: 158 us, 874 TFLOP/s
-// One query tile (decode), 8 rows x 64 heads over 32768 keys: 31 us for 42.5 MB in 4
-// bits, 27 us in a row of calls for 76 MB in 8 (bf16 pools through attn_fwd.cu: 45 us for
+// One query tile (decode), 8 rows x 64 heads over 32768 keys: 28 us for 42.5 MB in 4
+// bits, 25 us for 76 MB in 8, in a row of calls (bf16 pools through attn_fwd.cu: 45 us for
 // 151 MB): of 41000 cycles a CTA 6000 pass until the first S and 6000 behind the last P;
 // its 18 tiles take 1575 each, two groups in turn (softmax 1400, wait for the products
 // 1450). Shorter chains gained little there (rows copied into a tile's idle half, so that
-// a row's keys were split over two warps, gained nothing). Window 4096: 20.5 us, four tiles
+// a row's keys were split over two warps, gained nothing). Window 4096: 21 us, four tiles
 // a CTA, start and epilogue.
 // Every wait is bounded, as in attn_fwd.cu.
 #pragma once

@@ -10,9 +10,10 @@
 // row, so a half-warp handles a (row, KV head) pair without exchanges and its stores are
 // whole 128-byte lines. It takes two pairs at once, so that twice the bytes are under way
 // (one: 26.5 us for 8192 rows of 8 heads in and out; four: 26.1, fewer warps fit), and loads
-// a new row beside its slot. Two: 24.5 us for 101 MB (4.1 TB/s, the rows just written read
-// from L2); the chain of slot, row and store and two ramps are what is left. 8 rows: a
-// launch each, 1.9 and 1.7 us back to back in a graph.
+// a new row beside its slot. Two: 23.1 us for 101 MB (4.4 TB/s, the rows just written read
+// from L2); the chain of slot, row and store and two ramps are what is left, and one call
+// behind another, where those overlap (launch_after.cuh), it takes 16.2 (6.2 TB/s). 8 rows:
+// a launch each, 2.0 us back to back in a graph.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

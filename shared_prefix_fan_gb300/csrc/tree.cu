@@ -15,8 +15,9 @@
 // tables.cu does): no CTA waits for another and all come to the same verdict on the
 // lengths. All three are a launch and a chain of dependent reads (lengths, parents, steps
 // up or down a tree in shared memory, table, rows), which is what bounds them: back to back
-// in a graph 2.8, 3.4 and 3.2 us for 8 branches of 32 drafted tokens (8 KV heads). A call
-// costs the host 9 to 16 us from Python, so a step's five calls are bound by the host.
+// in a graph 2.7, 3.1 and 3.2 us for 8 branches of 32 drafted tokens (8 KV heads). A call
+// costs the host 5 to 11 us from Python, so a step's calls issued one by one are bound by the
+// host.
 #include <cuda_runtime.h>
 
 #include <algorithm>
