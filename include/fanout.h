@@ -286,8 +286,9 @@ FANOUT_API int fanout_kv_read_q4(const void *k_pages, const void *v_pages, const
  *
  * fanout_kv_append_q8, fanout_kv_read_q8 -- as fanout_kv_append_q4 and
  * fanout_kv_read_q4, into and from 8-bit pools: infinities are held as 448 gs, a NaN as
- * 0 (reported). A byte 0x7f or 0xff, which an append never writes, reads as NaN. Both can
- * be captured.
+ * 0 (reported). A byte 0x7f or 0xff, which an append never writes, reads as NaN. What is
+ * written (the pools; the rows) shares no byte with what is read, nor the pools of an append
+ * with each other (FANOUT_EINVAL). Both can be captured.
  */
 FANOUT_API int fanout_kv_append_q8(const void *k_new, const void *v_new, int64_t k_stride,
                 int64_t v_stride, void *k_pages, void *v_pages, const int64_t *slots,
@@ -369,7 +370,8 @@ enum fanout_kv_type { FANOUT_KV_BF16 = 0, FANOUT_KV_Q4 = 1, FANOUT_KV_Q8 = 2 };
  * A branch whose path does not ascend inside its T_b tokens is left as it was, a row whose
  * page is outside the pools is skipped, and with lengths that are not valid nothing is
  * moved; each is reported as FANOUT_EINVAL. No two branches may share the pages of their
- * drafted rows. n_rows == 0 does nothing. Can be captured.
+ * drafted rows. The pools share no byte with another array or each other (FANOUT_EINVAL).
+ * n_rows == 0 does nothing. Can be captured.
  */
 FANOUT_API int fanout_kv_keep(void *k_pages, void *v_pages, int32_t kv_type,
                 const int32_t *page_table, int32_t num_branches, int32_t max_pages_per_branch,

@@ -132,9 +132,23 @@ int run_rows(Q4RowParams& p, bool read, int32_t page_size, fanout_stream_t strea
     return status_from_cuda(launch_q4_rows(p, read, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// A size in bytes, where arguments may be such that its product passes 64 bits (exact up to
+// 2^53).
+int64_t bytes_of(double n) { return n < 9e18 ? static_cast<int64_t>(n) : INT64_MAX; }
+
 int run_rows_q8(Q8RowParams& p, bool read, int32_t page_size, fanout_stream_t stream) {
     const void* k = read ? static_cast<const void*>(p.k_out) : p.k_rows;
     const void* v = read ? static_cast<const void*>(p.v_out) : p.v_rows;
+    // (k_out and v_out may be rows of one array that lie between each other)
+    const double row = static_cast<double>(p.H_kv) * kHD, last = p.n_rows - 1;
+    const int64_t pool = bytes_of(row * static_cast<double>(p.n_slots));
+    const Array pools[] = {{p.k_pool, pool}, {p.v_pool, pool}};
+    const Array rows[] = {{k, bytes_of(2 * (last * static_cast<double>(p.k_stride) + row))},
+                          {v, bytes_of(2 * (last * static_cast<double>(p.v_stride) + row))}};
+    const Array slots[] = {{p.slots, 8LL * p.n_rows}};
+    if (any_overlap(rows, pools) || (read ? any_overlap(slots, rows) : any_overlap(slots, pools)) ||
+        (!read && overlap(p.k_pool, pool, p.v_pool, pool)))
+        return FANOUT_EINVAL;
     p.align32 = aligned(k, 32) && aligned(v, 32) && p.k_stride % 16 == 0 && p.v_stride % 16 == 0;
     p.k_rcp = 1.0f / p.k_scale;
     p.v_rcp = 1.0f / p.v_scale;
@@ -438,6 +452,15 @@ int fanout_kv_keep(void* k_pages, void* v_pages, int32_t kv_type, const int32_t*
                             {suffix_lens, 4, true}, {add_lens, 4, true},
                             {path, 4, true}, {counts, 4, true}};
     if (!arrays_ok(arrays)) return FANOUT_EINVAL;
+    const double row = kv_type == FANOUT_KV_BF16 ? 2 * kHD : kv_type == FANOUT_KV_Q4 ? kQ4RowBytes : kHD;
+    const int64_t pool = bytes_of(row * num_pages * H_kv * page_size);
+    const Array read[] = {{page_table, 4LL * num_branches * max_pages_per_branch},
+                          {suffix_lens, 4LL * num_branches},
+                          {add_lens, 4LL * num_branches},
+                          {path, 4 * n_rows},
+                          {counts, 4LL * num_branches}};
+    const Array written[] = {{k_pages, pool}, {v_pages, pool}};
+    if (any_overlap(read, written) || any_overlap_among(written)) return FANOUT_EINVAL;
     TreeParams p{};
     p.page_table = page_table;
     p.suffix_lens = suffix_lens;

@@ -149,3 +149,38 @@ def test_captured_chain():
         for x, y in zip(got, want):
             assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), i
     assert binding.last_error() == binding.OK
+
+
+def test_behind_another_stream_and_behind_copies():
+    """What lies between two calls (an event of another stream, a copy from the host, a kernel of
+    another kind) is waited for as ever."""
+    R, hkv = 512, 4
+    pools = [binding.q8_pool(R // 64, hkv, 64) for _ in range(2)]
+    slots = torch.arange(R, device="cuda")
+    new = torch.zeros((2, R, hkv, 128), dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros((30, 2, R, hkv, 128), dtype=torch.bfloat16, device="cuda")
+    host = torch.zeros_like(new, device="cpu").pin_memory()
+    big = torch.randn((4096, 4096), device="cuda")
+    side, main = torch.cuda.Stream(), torch.cuda.current_stream()
+    for i in range(30):
+        binding.kv_read_q8(*pools, slots)
+        if i % 3 == 0:
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                for _ in range(4):
+                    big = torch.tanh(big @ big)
+                new.fill_(i + 1)
+            main.wait_stream(side)
+        elif i % 3 == 1:
+            torch.cuda.synchronize()
+            host.fill_(i + 1)
+            big = torch.tanh(big @ big)
+            binding.kv_read_q8(*pools, slots)
+            new.copy_(host, non_blocking=True)
+        else:
+            new.fill_(i + 1)
+        binding.kv_append_q8(new[0], new[1], *pools, slots)
+        binding.kv_read_q8(*pools, slots, k_out=out[i, 0], v_out=out[i, 1])
+    torch.cuda.synchronize()
+    want = (torch.arange(30, device="cuda") + 1).to(torch.float8_e4m3fn).bfloat16()
+    assert torch.equal(out, want.view(30, 1, 1, 1, 1).expand_as(out))

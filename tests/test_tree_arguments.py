@@ -58,7 +58,12 @@ def test_tree_accept_refusals(lib, kw, rc):
     (dict(d=64), U_), (dict(ps=24), U_), (dict(B=4097), U_), (dict(R=1 << 31), U_),
     (dict(hkv=1 << 30), U_), (dict(k=None), E_), (dict(v=None), E_), (dict(k=0x100008), E_),
     (dict(table=None), E_), (dict(S=None), E_), (dict(A=None), E_), (dict(path=None), E_),
-    (dict(counts=None), E_), (dict(path=0x50002), E_), (dict(R=0), OK), (dict(B=0), OK)])
+    (dict(counts=None), E_), (dict(path=0x50002), E_), (dict(R=0), OK), (dict(B=0), OK),
+    # arrays inside the pools (9 pages of 2 heads x 16 rows of 128 bytes), pools over each other
+    (dict(table=0x108ffc), E_), (dict(S=0x200000), E_), (dict(A=0x200004), E_),
+    (dict(path=0x100000 - 20), E_), (dict(counts=0x208ff8), E_), (dict(v=0x108ff0), E_),
+    (dict(k=0x200000), E_), (dict(kv=0, path=0x111ffc), E_), (dict(kv=1, path=0x1050fc), E_),
+    (dict(pages=2 ** 31 - 1, hkv=2 ** 29), E_)])
 def test_kv_keep_refusals(lib, kw, rc):
     assert lib.fanout_kv_keep(*{**KEEP, **kw}.values()) == rc
 
@@ -76,6 +81,17 @@ def test_8_bit_row_refusals(lib, name, kw, rc):
         a = {k: a[k] for k in ("kp", "vp", "slots", "n", "pages", "hkv", "d", "ps", "kscale",
                                "vscale", "k", "v", "ks", "vs", "stream")}
     assert getattr(lib, f"fanout_kv_{name}_q8")(*a.values()) == rc
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("append", dict(vp=0x108ff0)), ("append", dict(kp=0x200000)),
+    ("append", dict(k=0x108ff0)), ("append", dict(v=0x200000 - 0x710)),
+    ("append", dict(slots=0x208ff8)), ("append", dict(slots=0x100000 - 24)),
+    ("read", dict(k=0x108ff0)), ("read", dict(v=0x200000 - 0x7f0)), ("read", dict(slots=0x1000)),
+    ("read", dict(slots=0x27f8)), ("read", dict(ks=1 << 40)),
+    ("append", dict(pages=2 ** 31 - 1, hkv=2 ** 28, ks=2 ** 60, vs=2 ** 60))])
+def test_8_bit_rows_over_pools_are_refused(lib, name, kw):
+    test_8_bit_row_refusals(lib, name, kw, E_)
 
 
 def attn(lib, tree, **kw):
