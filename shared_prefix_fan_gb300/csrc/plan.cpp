@@ -224,8 +224,10 @@ void make_streamk(const std::vector<Range>& ranges, int32_t max_cta, double unit
 // CTA above the balanced load is cut there and its remainder goes back into
 // the queue. The leading waves keep the lockstep order of the whole-range plan
 // (the CTAs' first units read the same key chunks at about the same time) and
-// only the cut pieces become partials.
-void make_lpt_cut(const std::vector<Range>& ranges, int32_t max_cta, double unit_ovh, Cand& c) {
+// only the cut pieces become partials. slack: the load that pieces are cut at lies above
+// the balanced one by this part of it.
+void make_lpt_cut(const std::vector<Range>& ranges, int32_t max_cta, double unit_ovh, Cand& c,
+                  double slack = 0) {
     struct Piece {
         int64_t work;  // its tiles, those of the range's first keys among them
         int32_t range;
@@ -241,7 +243,7 @@ void make_lpt_cut(const std::vector<Range>& ranges, int32_t max_cta, double unit
     }
     const int32_t n_cta = static_cast<int32_t>(std::min<int64_t>(max_cta, total));
     const double target = (static_cast<double>(total) +
-                           unit_ovh * static_cast<double>(ranges.size() + n_cta)) / n_cta;
+                           unit_ovh * static_cast<double>(ranges.size() + n_cta)) / n_cta * (1 + slack);
     auto later = [](const Piece& a, const Piece& b) {
         return std::make_tuple(-b.work, b.k_lo, b.kv_head, b.branch, b.tok_begin) <
                std::make_tuple(-a.work, a.k_lo, a.kv_head, a.branch, a.tok_begin);
@@ -476,15 +478,39 @@ int build_plan(const PlanInput& in, Plan& plan) {
     // Chunk size from the cost model (or the forced split count).
     const int32_t max_cta = std::max(1, in.num_sms);
     const double ovh = plan.nq == 1 ? kUnitOverhead1 : in.rows ? kUnitOverheadRows2 : kUnitOverhead2;
-    Cand best, cand, cand2;
-    // The cheapest way to cut the ranges.
-    auto search = [&](const std::vector<Range>& ranges, Cand& best) {
+    Cand best, cand, cand2, own_best;
+    // The cheapest way to cut the ranges (first: best holds none to beat yet).
+    auto search = [&](const std::vector<Range>& ranges, Cand& best, bool first) {
+        auto take_if_below = [&](double part) {
+            if (first || cand.cost < best.cost * part) {
+                std::swap(best, cand);
+                first = false;
+            }
+        };
+        // Tail cuts when every range is written directly (long prefill): the
+        // cut pieces are then the only partials. With split ranges the
+        // equal-chunk plans below already balance, and measured faster: the
+        // cuts' remainders pile onto the CTAs that hold many short units.
+        auto tail_cuts = [&]() {
+            for (const Range& r : ranges)
+                if (!r.complete) return;
+            if (!in.tail_cuts) return;
+            make_lpt_cut(ranges, max_cta, ovh, cand);
+            if (!in.own_cuts) return take_if_below(0.995);
+            // A little room spares the last cuts' scraps, each a unit of its own. (Not for
+            // less than 2 %: one wave of 128 whole units of 69 tiles takes 119 us, cut at an
+            // estimate 0.6 % lower 125.)
+            for (double slack : {0.005, 0.01, 0.02}) {
+                make_lpt_cut(ranges, max_cta, ovh, cand2, slack);
+                if (cand2.cost < cand.cost) std::swap(cand, cand2);
+            }
+            take_if_below(0.98);
+        };
         int64_t max_nkt = 1;
         for (const Range& r : ranges) max_nkt = std::max(max_nkt, cdiv(r.hi - r.lo, kBN));
         // keep the plan (and host planning time) bounded
         const int64_t max_units =
             std::max<int64_t>(16LL * max_cta, static_cast<int64_t>(ranges.size()));
-        bool first = true;
         for (int64_t chunk : {0LL, 1024LL, 512LL, 384LL, 256LL, 192LL, 128LL, 96LL, 64LL, 48LL,
                               40LL, 32LL, 28LL, 24LL, 20LL, 18LL, 16LL, 14LL, 12LL, 10LL, 8LL, 6LL,
                               4LL, 3LL, 2LL}) {
@@ -497,21 +523,10 @@ int build_plan(const PlanInput& in, Plan& plan) {
             if (!first && candidate_cost_bound(ranges, chunk, max_cta, ovh) >= best.cost * 0.995)
                 continue;  // could not replace the best
             make_candidate(ranges, chunk, 0, max_cta, ovh, cand);
-            if (first || cand.cost < best.cost * 0.995) {
-                std::swap(best, cand);
-                first = false;
-            }
+            take_if_below(0.995);
+            if (chunk == 0 && in.own_cuts) tail_cuts();  // often the best: spares the others
         }
-        // Tail cuts when every range is written directly (long prefill): the
-        // cut pieces are then the only partials. With split ranges the
-        // equal-chunk plans above already balance, and measured faster: the
-        // cuts' remainders pile onto the CTAs that hold many short units.
-        bool all_complete = true;
-        for (const Range& r : ranges) all_complete = all_complete && r.complete;
-        if (all_complete && in.tail_cuts) {
-            make_lpt_cut(ranges, max_cta, ovh, cand);
-            if (cand.cost < best.cost * 0.995) std::swap(best, cand);
-        }
+        if (!in.own_cuts) tail_cuts();
         // Exact balance scatters CTAs over different key offsets; use it only
         // when the whole KV fits in L2 (otherwise the lockstep waves of the
         // equal-chunk plan are what keeps a large shared prefix in L2).
@@ -526,13 +541,36 @@ int build_plan(const PlanInput& in, Plan& plan) {
         const int64_t kv_bytes = kv_tokens * in.H_kv * in.row_bytes;
         if (kv_bytes <= (100LL << 20)) {
             make_streamk(ranges, max_cta, ovh, cand, in.own_cuts != 0);
-            if (cand.cost < best.cost * 0.97) std::swap(best, cand);
+            take_if_below(0.97);
         }
     };
     if (in.force_splits > 0) {
         make_candidate(ranges, 0, in.force_splits, max_cta, ovh, best);
     } else {
-        search(ranges, best);
+        // Where the shared range's row blocks hold no block of two branches anyway, units of a
+        // branch that sweeps all of its keys itself have as many tiles, fewer boundaries and
+        // partials, and no short units for the suffixes. 8 branches of 32 drafted tokens over
+        // 65536 keys: 330 us against 400 in bf16, 351 against 430 in 8 bits; over 32768: 179
+        // against 205 and 191 against 210. (4-bit pools and windows without drafts keep the
+        // plans, and so the bits, that they had, here and above.)
+        std::vector<Range> own;
+        int32_t own_split_at = 0;
+        bool own_fits = false;
+        if (in.own_cuts && plan.split_at > 0) {
+            int32_t nq = 0, tpt = 0;
+            make_row_ranges(in, false, own, R, nq, tpt, plan.tok_pos, own_split_at);
+            own_fits = nq == plan.nq && own.size() * 2 <= ranges.size();
+        }
+        if (own_fits) {
+            search(own, own_best, true);
+            best.cost = own_best.cost;
+        }
+        search(ranges, best, !own_fits);
+        if (own_fits && best.units.empty()) {  // nothing beat it
+            std::swap(best, own_best);
+            std::swap(ranges, own);
+            plan.split_at = own_split_at;
+        }
         // A short context: every branch sweeps all of its keys in a unit of its own,
         // which needs no merge, where one wave of such units is the shorter by what the
         // model puts a merge's launch at (short calls hide most of it): 8 branches of a
@@ -550,21 +588,6 @@ int build_plan(const PlanInput& in, Plan& plan) {
                     std::swap(ranges, own);
                     plan.nq = nq;
                     plan.tpt = tpt;
-                    plan.split_at = split_at;
-                }
-            }
-            // Where the shared range's row blocks hold no block of two branches anyway, such
-            // units have as many tiles, fewer boundaries and partials, and no short units for
-            // the suffixes; they may be cut too. 8 branches of 32 drafted tokens over 65536
-            // keys: 345 us against 400 in bf16, 365 against 430 in 8 bits; over 32768: 201
-            // against 205 and 195 against 210. (4-bit pools and windows without drafts keep
-            // the plans, and so the bits, that they had, here and in make_streamk.)
-            if (in.own_cuts && plan.split_at > 0 && nq == plan.nq &&
-                own.size() * 2 <= ranges.size()) {
-                search(own, cand2);
-                if (cand2.cost <= best.cost) {
-                    std::swap(best, cand2);
-                    std::swap(ranges, own);
                     plan.split_at = split_at;
                 }
             }
