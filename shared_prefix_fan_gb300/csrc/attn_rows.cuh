@@ -81,10 +81,10 @@
 // an 8-bit prefill then). A boundary between units costs about 10000 cycles (epilogue,
 // next Q, masked tiles).
 //   4-bit prefill, 2048 rows x 64 heads over 32768 keys: 1440 us, 1480 TFLOP/s
-//   8-bit, the same: 1310 us (in a row of calls, power-limited, 1366), 1630 TFLOP/s
+//   8-bit, the same: 1300 us (in a row of calls, power-limited, 1366), 1640 TFLOP/s
 //   4-bit, 32 branches of 1..32 tokens over 65536 shared keys: 829 us, 1205 TFLOP/s
 //   8-bit, 32 branches of 1..64 drafted tokens over 65536 shared keys: 1500 us, 1505 TFLOP/s
-//   bf16, 8 branches of 32 drafted tokens over 32768 shared keys: 200 us, 1394 TFLOP/s
+//   bf16, 8 branches of 32 drafted tokens over 32768 shared keys: 184 us, 1516 TFLOP/s
 //   bf16, 32 branches of 1..32 tokens over 16384 keys, window 2048: 94 us, 387 TFLOP/s
 //   bf16 prefill, 4096 rows x 64 heads, window 1024: 158 us, 874 TFLOP/s
 // One query tile (decode), 8 rows x 64 heads over 32768 keys: 28 us for 42.5 MB in 4
