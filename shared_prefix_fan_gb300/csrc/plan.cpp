@@ -312,6 +312,13 @@ void make_lpt_cut(const std::vector<Range>& ranges, int32_t max_cta, double unit
     c.cost = makespan + (n_parts > 0 ? kMergeLaunch + kMergePerPart * n_parts / c.n_cta : 0.0);
 }
 
+// Tiles of all ranges.
+int64_t tiles_of(const std::vector<Range>& ranges) {
+    int64_t n = 0;
+    for (const Range& r : ranges) n += cdiv(r.hi - r.lo, kBN) + r.first_tiles;
+    return n;
+}
+
 // The key ranges of a problem (rows x keys before any split-KV cut), and the
 // row geometry: R tokens, nq query tiles per unit, tpt tokens per tile.
 void make_ranges(const PlanInput& in, std::vector<Range>& ranges, int32_t& R, int32_t& nq,
@@ -547,19 +554,22 @@ int build_plan(const PlanInput& in, Plan& plan) {
     if (in.force_splits > 0) {
         make_candidate(ranges, 0, in.force_splits, max_cta, ovh, best);
     } else {
-        // Where the shared range's row blocks hold no block of two branches anyway, units of a
-        // branch that sweeps all of its keys itself have as many tiles, fewer boundaries and
-        // partials, and no short units for the suffixes. 8 branches of 32 drafted tokens over
-        // 65536 keys: 330 us against 400 in bf16, 351 against 430 in 8 bits; over 32768: 179
-        // against 205 and 191 against 210. (4-bit pools and windows without drafts keep the
-        // plans, and so the bits, that they had, here and above.)
+        // Where the shared range packs few branches into a row block (each fills its own, or
+        // their windows reach little of the prefix), units of a branch that sweeps all of its
+        // keys itself have about as many tiles, fewer boundaries and partials, and no short
+        // units for the suffixes. 8 branches of 32 drafted tokens over 65536 keys: 330 us
+        // against 400 in bf16, 351 against 430 in 8 bits; over 32768: 179 against 205 and 191
+        // against 210; 32 branches of 1..32 tokens, window 2048 over 8 bits, 78 against 94;
+        // of 1..64 drafts, window 4096, 197 against 228, with 1.2 times the tiles. (4-bit
+        // and bf16 pools without drafts keep the plans, and so the bits, that they had, here
+        // and above.)
         std::vector<Range> own;
         int32_t own_split_at = 0;
         bool own_fits = false;
         if (in.own_cuts && plan.split_at > 0) {
             int32_t nq = 0, tpt = 0;
             make_row_ranges(in, false, own, R, nq, tpt, plan.tok_pos, own_split_at);
-            own_fits = nq == plan.nq && own.size() * 2 <= ranges.size();
+            own_fits = nq == plan.nq && 4 * tiles_of(own) <= 5 * tiles_of(ranges);
         }
         if (own_fits) {
             search(own, own_best, true);

@@ -168,3 +168,12 @@ def test_tree_plans_move_with_the_suffixes(shim, window, sinks):
         _, info = check_plan(shim, S, [8, 20], 256, 8, 1, 16, window, sinks, prev=prev)
         kept += int(info[4])
     assert kept > 0
+
+
+def test_ragged_windows_are_swept_whole(shim):
+    """Windows that reach little of the prefix: no shared range, and no partials."""
+    rng = np.random.default_rng(2)
+    T = rng.integers(1, 33, size=32).tolist()
+    S = [int(t + s) for t, s in zip(T, rng.integers(64, 4096, size=32))]
+    units, info = check_plan(shim, S, T, 16384, 64, 8, 16, 2048, 16)
+    assert info[0] == 0 and info[3] == 0
