@@ -22,10 +22,10 @@ namespace {
 // One warp per output row at a time; kMergeBatch partials per pass: 24 for
 // rows with many partials (decode), fewer when every row has few, because a
 // pass loads kMergeBatch of them whatever the row has (merge_row.cuh). With
-// 39360 rows of two partials each (attention over 8-bit keys, a window), the
-// call takes 106 us with 8 a pass and 97 with 2; two or four rows a warp at
-// once instead took 107 and 127 (more registers a block, so fewer blocks fit
-// beside the attention kernel). Blocks of two warps: small enough to be
+// 39360 rows of two partials each (a window over 8-bit keys, cut so), the call
+// took 106 us with 8 a pass and 97 with 2; two or four rows a warp at once
+// instead took 107 and 127 (more registers a block, so fewer blocks fit beside
+// the attention kernel). Blocks of two warps: small enough to be
 // resident beside an attention CTA (which leaves ~27 K registers and 2 KB of
 // shared memory of an SM free), so part of the grid starts, and runs its dry
 // pass, while the attention kernel is still working. The grid is at most what
