@@ -15,9 +15,12 @@
 // tables.cu does): no CTA waits for another and all come to the same verdict on the
 // lengths. All three are a launch and a chain of dependent reads (lengths, parents, steps
 // up or down a tree in shared memory, table, rows), which is what bounds them: back to back
-// in a graph 2.7, 3.1 and 3.2 us for 8 branches of 32 drafted tokens (8 KV heads). A call
-// costs the host 5 to 11 us from Python, so a step's calls issued one by one are bound by the
-// host.
+// in a graph 2.7, 2.6 and 3.2 us for 8 branches of 32 drafted tokens (8 KV heads). Masks are
+// found a word of 32 tokens at a time, so that a token steps from word to word and not from
+// parent to parent; of every token's children the accepted one is found at once, so that the
+// path is a step a token in shared memory. (A chain of 64 tokens: 3.3 and 4.1 us, not 10 and
+// 15; of 1024: 28 and 33, not 660 and 200.) A call costs the host 5 to 11 us from Python, so
+// a step's calls issued one by one are bound by the host.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -89,7 +92,10 @@ __device__ __forceinline__ void run_of(int32_t items, int32_t& i0, int32_t& i1) 
 __global__ void __launch_bounds__(kThreads) tree_rows_kernel(const TreeParams p) {
     after_previous();
     __shared__ Sums sums;
-    __shared__ int32_t parent[kMaxTreeTokens];
+    // of every token: its ancestors (and itself) in its word of 32 tokens, and the first
+    // ancestor in a word below (-1: none)
+    __shared__ uint32_t family[kMaxTreeTokens];
+    __shared__ int32_t below[kMaxTreeTokens];
     int32_t b0, b1;
     run_of(p.num_branches, b0, b1);
     int64_t row, all;
@@ -107,26 +113,46 @@ __global__ void __launch_bounds__(kThreads) tree_rows_kernel(const TreeParams p)
     for (int32_t b = b0; b < b1; ++b) {
         const int32_t T = __ldcg(p.lens + b), n = p.prefix_len + __ldcg(p.suffix_lens + b);
         __syncthreads();
-        for (int t = threadIdx.x; t < T; t += kThreads) {
-            int32_t up = __ldcg(p.parents + row + t);
+        for (int t = threadIdx.x; (t & ~31) < T; t += kThreads) {  // a warp a word
+            int32_t up = t < T ? __ldcg(p.parents + row + t) : -1;
             if (up < -1 || up >= t) {  // reported, and taken as none
                 atomicCAS(p.err, 0, kErrInval);
                 up = -1;
             }
-            parent[t] = up;
+            // A run of ancestors in the word, from the token up, is doubled five times:
+            // its tokens, the next one in the word (-1: none) or else the one below.
+            uint32_t run = 1u << (t & 31);
+            int32_t next = up >= (t & ~31) ? up & 31 : -1, out = up;
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                const int from = max(next, 0);
+                const uint32_t r = __shfl_sync(0xffffffffu, run, from);
+                const int32_t o = __shfl_sync(0xffffffffu, out, from);
+                const int32_t x = __shfl_sync(0xffffffffu, next, from);
+                if (next >= 0) {
+                    run |= r;
+                    out = o;
+                    next = x;
+                }
+            }
+            family[t] = run;
+            below[t] = out;
         }
         __syncthreads();
         for (int t = threadIdx.x; t < T; t += kThreads) {
             uint32_t* mask = p.masks + (row + t) * p.words;
             for (int w = (t >> 5) + 1; w < p.words; ++w) mask[w] = 0u;
             int depth = 0, word = t >> 5;
-            uint32_t bits = 0;
-            for (int u = t; u >= 0; u = parent[u], ++depth) {
-                if (p.window > 0 && depth >= p.window) continue;
-                for (; word > (u >> 5); --word, bits = 0) mask[word] = bits;
-                bits |= 1u << (u & 31);
+            for (int u = t; u >= 0; u = below[u]) {  // ancestors come in descending order
+                uint32_t bits = family[u];
+                const int count = __popc(bits), left = p.window - depth;
+                if (p.window > 0 && count > left)  // the `left` nearest: the highest
+                    bits = left <= 0 ? 0u : bits & (~0u << __fns(bits, 0, count - left + 1));
+                depth += count;
+                for (; word > (u >> 5); --word) mask[word] = 0u;
+                mask[word--] = bits;
             }
-            for (; word >= 0; --word, bits = 0) mask[word] = bits;
+            for (; word >= 0; --word) mask[word] = 0u;
             p.positions[row + t] = n + depth - 1;
             const int32_t key = n + t;
             const int32_t i = static_cast<int32_t>(static_cast<uint32_t>(key) /
@@ -144,8 +170,9 @@ __global__ void __launch_bounds__(kThreads) tree_rows_kernel(const TreeParams p)
 __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const TreeParams p) {
     after_previous();
     __shared__ Sums sums;
-    __shared__ int32_t parent[kMaxTreeTokens];
-    __shared__ int64_t draft[kMaxTreeTokens];
+    __shared__ int64_t target[kMaxTreeTokens];
+    __shared__ int32_t child[kMaxTreeTokens + 1];  // behind each token (0: behind none) the accepted one
+    __shared__ int32_t list[kMaxTreeTokens];
     __shared__ int32_t taken;
     int32_t b0, b1;
     run_of(p.num_branches, b0, b1);
@@ -155,7 +182,6 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const TreeParams 
     for (int64_t r = (ok ? all : 0) + static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; r < p.R;
          r += static_cast<int64_t>(gridDim.x) * kThreads)
         p.path[r] = -1;
-    const int lane = threadIdx.x & 31;
     for (int32_t b = b0; b < b1; ++b) {
         if (!ok) {
             if (threadIdx.x == 0) {
@@ -165,38 +191,31 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const TreeParams 
             continue;
         }
         const int32_t T = __ldcg(p.lens + b);
+        const int64_t first = __ldcg(p.first + b);
+        __syncthreads();
+        for (int t = threadIdx.x; t <= T; t += kThreads) {
+            child[t] = kMaxTreeTokens;
+            if (t < T) target[t] = __ldcg(p.target + row + t);
+        }
         __syncthreads();
         for (int t = threadIdx.x; t < T; t += kThreads) {
-            parent[t] = __ldcg(p.parents + row + t);
-            draft[t] = __ldcg(p.draft + row + t);
+            const int32_t up = __ldcg(p.parents + row + t);
+            if (up < -1 || up >= t) continue;  // no token's child
+            if (__ldcg(p.draft + row + t) == (up < 0 ? first : target[up])) atomicMin(child + up + 1, t);
         }
         __syncthreads();
-        if (threadIdx.x < 32) {
-            int64_t want = __ldcg(p.first + b);
+        if (threadIdx.x == 0) {
             int32_t at = -1, count = 0;
-            // (a child comes behind its parent, so the search goes on behind it)
-            for (int base = 0; base < T;) {
-                const int t = base + lane;
-                const unsigned hit = __ballot_sync(
-                    0xffffffffu, t < T && t > at && parent[t] == at && draft[t] == want);
-                if (hit == 0) {
-                    base += 32;
-                    continue;
-                }
-                at = base + __ffs(hit) - 1;
-                want = __ldcg(p.target + row + at);
-                if (lane == 0) p.path[row + count] = at;
-                ++count;
-                base = at + 1;
+            for (int32_t t = child[0]; t < kMaxTreeTokens; t = child[t + 1]) {
+                list[count++] = t;
+                at = t;
             }
-            if (lane == 0) {
-                p.counts[b] = count;
-                p.next[b] = want;
-                taken = count;
-            }
+            p.counts[b] = count;
+            p.next[b] = at < 0 ? first : target[at];
+            taken = count;
         }
         __syncthreads();
-        for (int t = taken + threadIdx.x; t < T; t += kThreads) p.path[row + t] = -1;
+        for (int t = threadIdx.x; t < T; t += kThreads) p.path[row + t] = t < taken ? list[t] : -1;
         row += T;
     }
 }
@@ -252,12 +271,13 @@ __global__ void __launch_bounds__(kThreads) kv_keep_kernel(const TreeParams p) {
         const int32_t n = p.prefix_len + __ldcg(p.suffix_lens + b);
         const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
         // a path that does not ascend inside the branch moves nothing
-        bool good = count >= 0 && count <= T;
-        for (int i = lane; good && i < count; i += 32) {
+        bool good = count >= 0 && count <= T, ascends = true;
+        for (int i = lane; i < (good ? count : 0); i += 32) {
             const int32_t from = __ldcg(p.path + row + i);
             const int32_t before = i > 0 ? __ldcg(p.path + row + i - 1) : -1;
-            good = from > before && from < T;
+            ascends = ascends && from > before && from < T;
         }
+        good = good && ascends;
         if (!__all_sync(0xffffffffu, good)) {
             if (lane == 0) atomicCAS(p.err, 0, kErrInval);
             continue;
@@ -283,6 +303,7 @@ __global__ void __launch_bounds__(kThreads) kv_keep_kernel(const TreeParams p) {
                     place(n + to, page_d, slot_d);
                 }
             }
+            if (!__any_sync(0xffffffffu, page_s >= 0)) continue;  // all in place
             const int32_t moves = min(32, count - c0);
             for (int32_t m = 0; m < moves; m += kMoves) {
                 typename Row::Piece v[kMoves];

@@ -302,3 +302,30 @@ def test_kept_rows_past_32_bit_offsets():
     for x, w in zip(pools, want):
         assert np.array_equal(x[-2:].cpu().numpy(), w)
         assert not x[0].any() and not x[:-2:1000].any()
+
+
+@pytest.mark.parametrize("window", [0, 1, 5, 31, 32, 33, 70, 1023])
+def test_masks_of_deep_trees(window):
+    """Ancestors over many words of 32 tokens, windows that end inside and at a word."""
+    rng = np.random.default_rng(window)
+    deep = [-1] + [t - 1 - int(rng.integers(0, 3)) if t > 3 else t - 1 for t in range(1, 900)]
+    trees = [list(range(-1, 1023)), deep, [-1] * 40, [-1] + [0] * 99, list(range(-1, 63))]
+    T, S = [len(t) for t in trees], [3, 0, 17, 5, 40]
+    i32 = lambda a: torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")  # noqa: E731
+    width = 1200 // 16
+    table = i32(rng.permutation(5 * width).reshape(5, width))
+    masks, positions, _ = binding.tree_rows(i32(np.concatenate(trees)), table, 32, i32(S), i32(T), 16,
+                                            1024, window)
+    words = masks.cpu().numpy().view(np.uint32).reshape(-1, 32)
+    bits = np.unpackbits(words.view(np.uint8), axis=1, bitorder="little").astype(bool)
+    row = 0
+    for tree, s in zip(trees, S):
+        for t in range(len(tree)):
+            up, line = t, []
+            while up >= 0:
+                line.append(up)
+                up = tree[up]
+            want = np.zeros(1024, bool)
+            want[line[:window] if window else line] = True
+            assert np.array_equal(bits[row], want) and int(positions[row]) == 32 + s + len(line) - 1
+            row += 1
