@@ -329,12 +329,23 @@ FANOUT_API int fanout_kv_read_q8(const void *k_pages, const void *v_pages, const
  * of the table too short; reported as FANOUT_EINVAL). Arrays that are written share no
  * byte with another (FANOUT_EINVAL). n_rows == 0 does nothing. No workspace; can be
  * captured (first call on a device outside a capture).
+ *
+ * fanout_tree_rows_sinks -- the same for a layer whose first `sinks` keys stay visible behind
+ * its window: an ancestor at a position below `sinks` keeps its bit, however many levels
+ * above. Where a context is shorter than `sinks`, drafted tokens are among those first keys;
+ * a chain then sees what fanout_attn_window shows its tokens. sinks == 0 is
+ * fanout_tree_rows; sinks without a window is FANOUT_EINVAL.
  */
 FANOUT_API int fanout_tree_rows(const int32_t *parents, const int32_t *page_table,
                 int32_t num_branches, int32_t max_pages_per_branch, int32_t prefix_len,
                 const int32_t *suffix_lens, const int32_t *add_lens, int32_t page_size,
                 int64_t n_rows, int32_t mask_words, int32_t window, uint32_t *masks,
                 int32_t *positions, int64_t *slots, fanout_stream_t stream);
+FANOUT_API int fanout_tree_rows_sinks(const int32_t *parents, const int32_t *page_table,
+                int32_t num_branches, int32_t max_pages_per_branch, int32_t prefix_len,
+                const int32_t *suffix_lens, const int32_t *add_lens, int32_t page_size,
+                int64_t n_rows, int32_t mask_words, int32_t window, int32_t sinks,
+                uint32_t *masks, int32_t *positions, int64_t *slots, fanout_stream_t stream);
 
 /*
  * fanout_tree_accept -- the path through each branch's drafted tokens that the model's
@@ -505,6 +516,8 @@ FANOUT_API int fanout_attn_q8(const void *q, const void *k_pages, const void *v_
  *   positions   dev int32 [R] or NULL: read with window >= 1 only, and needed then; n_b ..
  *               n_b + 1023 (a value outside counts as the nearest of these).
  *   window, sinks  0, 0: every key before the draft; sinks without a window is FANOUT_EINVAL.
+ *               (Among the drafted tokens the masks alone say what is seen: with first keys
+ *               they come from fanout_tree_rows_sinks.)
  * The drafted tokens' rows must all be finite. Everything else as fanout_attn_window: page
  * ids, hidden keys, capturing, plans, errors.
  */

@@ -65,6 +65,8 @@ ABI = {
                                       _vp, _i32, _vp, _vp]),
     "fanout_tree_rows": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _vp, _vp, _i32, _i64, _i32,
                                         _i32, _vp, _vp, _vp, _vp]),
+    "fanout_tree_rows_sinks": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _vp, _vp, _i32, _i64,
+                                              _i32, _i32, _i32, _vp, _vp, _vp, _vp]),
     "fanout_tree_accept": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _vp, _vp, _vp,
                                           _vp]),
     "fanout_kv_keep": (ctypes.c_int, [_vp, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
@@ -506,23 +508,28 @@ def copy_pages_q8(k_pages, v_pages, pairs, rows: int, stream=None) -> None:
 
 
 def tree_rows(parents, page_table, prefix_len: int, suffix_lens, add_lens, page_size: int,
-              max_nodes: int, window: int = 0, masks=None, positions=None, slots=None, stream=None):
+              max_nodes: int, window: int = 0, masks=None, positions=None, slots=None, stream=None,
+              sinks: int = 0):
     """What a step's drafted rows need: (masks int32 [R, words], positions int32 [R],
     slots int64 [R]).
 
     parents (int32 [R], rows grouped by branch): each drafted token's parent in its
     branch, or -1; suffix_lens / add_lens (int32 [B]): private tokens before the draft, and
     drafted ones, at most max_nodes (<= 1024) each. Bit u of a token's mask is set for
-    itself and its ancestors (with a window, those less than `window` levels above it);
+    itself and its ancestors (with a window, those less than `window` levels above it and
+    those at positions below `sinks`: give what the layer's attention is given);
     its position is prefix + suffix + its depth; its slot is where its K/V row belongs.
     Rows behind the last token get no bits, position 0 and slot -1."""
     if max_nodes < 1 or max_nodes > 1024:
         raise ValueError("max_nodes must be 1 .. 1024")
-    if window >> 31:
-        window = max(-1, min(window, _I32_MAX))
-    return (_host or _host_calls()).tree_rows(parents, page_table, prefix_len, suffix_lens, add_lens,
-                                              page_size, (max_nodes + 31) // 32, window, masks,
-                                              positions, slots, stream)
+    if window >> 31 or sinks >> 31:
+        window, sinks = max(-1, min(window, _I32_MAX)), max(-1, min(sinks, _I32_MAX))
+    host, words = _host or _host_calls(), (max_nodes + 31) // 32
+    if sinks:
+        return host.tree_rows_sinks(parents, page_table, prefix_len, suffix_lens, add_lens, page_size,
+                                    words, window, sinks, masks, positions, slots, stream)
+    return host.tree_rows(parents, page_table, prefix_len, suffix_lens, add_lens, page_size, words,
+                          window, masks, positions, slots, stream)
 
 
 def tree_accept(parents, draft_tokens, target_tokens, first_tokens, add_lens, stream=None):

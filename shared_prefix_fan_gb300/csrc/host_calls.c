@@ -360,17 +360,15 @@ done:
     return result;
 }
 
-/* tree_rows(parents, page_table, prefix_len, suffix_lens, add_lens, page_size, words, window,
- *           masks, positions, slots, stream) -> (masks, positions, slots) */
-static PyObject *tree_rows(PyObject *self, PyObject *const *a, Py_ssize_t n) {
-    if (arity("tree_rows", n, 12) < 0) return NULL;
+/* tail: masks, positions, slots, stream */
+static PyObject *tree_rows_of(PyObject *const *a, int32_t sinks, PyObject *const *tail) {
     int32_t prefix_len, page_size, words, window, B = 0, width = 0;
     if (int32_of(a[2], "prefix_len", &prefix_len) < 0 || int32_of(a[5], "page_size", &page_size) < 0 ||
         int32_of(a[6], "mask words", &words) < 0 || int32_of(a[7], "window", &window) < 0)
         return NULL;
     Call c;
-    if (begin(&c, a[0], "parents", a[11]) < 0) return NULL;
-    PyObject *result = NULL, *out[3] = {a[8], a[9], a[10]};
+    if (begin(&c, a[0], "parents", tail[3]) < 0) return NULL;
+    PyObject *result = NULL, *out[3] = {tail[0], tail[1], tail[2]};
     static const Py_ssize_t any[2] = {-1, -1};
     static const char *const names[3] = {"masks", "positions", "slots"};
     static const int types[3] = {I32, I32, I64};
@@ -394,12 +392,25 @@ static PyObject *tree_rows(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         }
     }
     RUN(c, "fanout_tree_rows",
-        fanout_tree_rows(parents, tp, B, width, prefix_len, s, l, page_size, rows[0], words, window, to[0],
-                         to[1], to[2], stream));
+        fanout_tree_rows_sinks(parents, tp, B, width, prefix_len, s, l, page_size, rows[0], words, window,
+                               sinks, to[0], to[1], to[2], stream));
     result = PyTuple_Pack(3, out[0], out[1], out[2]);
 done:
     drop(&c);
     return result;
+}
+
+/* tree_rows(parents, page_table, prefix_len, suffix_lens, add_lens, page_size, words, window,
+ *           masks, positions, slots, stream) -> (masks, positions, slots) */
+static PyObject *tree_rows(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    return arity("tree_rows", n, 12) < 0 ? NULL : tree_rows_of(a, 0, a + 8);
+}
+
+/* the same with first keys: sinks behind window */
+static PyObject *tree_rows_sinks(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    int32_t sinks;
+    if (arity("tree_rows_sinks", n, 13) < 0 || int32_of(a[8], "sinks", &sinks) < 0) return NULL;
+    return tree_rows_of(a, sinks, a + 9);
 }
 
 /* tree_accept(parents, draft_tokens, target_tokens, first_tokens, add_lens, stream)
@@ -610,6 +621,7 @@ static PyMethodDef methods[] = {
     {"kv_append_q8", (PyCFunction)(void (*)(void))kv_append_q8, METH_FASTCALL, NULL},
     {"kv_read_q8", (PyCFunction)(void (*)(void))kv_read_q8, METH_FASTCALL, NULL},
     {"tree_rows", (PyCFunction)(void (*)(void))tree_rows, METH_FASTCALL, NULL},
+    {"tree_rows_sinks", (PyCFunction)(void (*)(void))tree_rows_sinks, METH_FASTCALL, NULL},
     {"tree_accept", (PyCFunction)(void (*)(void))tree_accept, METH_FASTCALL, NULL},
     {"kv_keep", (PyCFunction)(void (*)(void))kv_keep, METH_FASTCALL, NULL},
     {"attn_q8", (PyCFunction)(void (*)(void))attn_q8, METH_FASTCALL, NULL},

@@ -59,7 +59,7 @@ struct TreeParams {
     uint8_t* k_pool;
     uint8_t* v_pool;
     int32_t* err;
-    int32_t num_branches, R, words, window, prefix_len, page_size, max_pages, num_pages, H_kv;
+    int32_t num_branches, R, words, window, sinks, prefix_len, page_size, max_pages, num_pages, H_kv;
     Pool pool;
 };
 

@@ -355,8 +355,19 @@ int fanout_tree_rows(const int32_t* parents, const int32_t* page_table, int32_t 
                      const int32_t* add_lens, int32_t page_size, int64_t n_rows,
                      int32_t mask_words, int32_t window, uint32_t* masks, int32_t* positions,
                      int64_t* slots, fanout_stream_t stream) {
+    return fanout_tree_rows_sinks(parents, page_table, num_branches, max_pages_per_branch, prefix_len,
+                                  suffix_lens, add_lens, page_size, n_rows, mask_words, window, 0,
+                                  masks, positions, slots, stream);
+}
+
+int fanout_tree_rows_sinks(const int32_t* parents, const int32_t* page_table, int32_t num_branches,
+                           int32_t max_pages_per_branch, int32_t prefix_len,
+                           const int32_t* suffix_lens, const int32_t* add_lens, int32_t page_size,
+                           int64_t n_rows, int32_t mask_words, int32_t window, int32_t sinks,
+                           uint32_t* masks, int32_t* positions, int64_t* slots,
+                           fanout_stream_t stream) {
     if (num_branches < 0 || max_pages_per_branch < 0 || prefix_len < 0 || page_size <= 0 ||
-        n_rows < 0 || mask_words <= 0 || window < 0)
+        n_rows < 0 || mask_words <= 0 || window < 0 || sinks < 0 || (window == 0 && sinks > 0))
         return FANOUT_EINVAL;
     if (num_branches > kMaxTableBranches || mask_words > kMaxTreeTokens / 32 || n_rows > 0x7fffffff)
         return FANOUT_EUNSUPPORTED;
@@ -385,6 +396,7 @@ int fanout_tree_rows(const int32_t* parents, const int32_t* page_table, int32_t 
     p.R = static_cast<int32_t>(n_rows);
     p.words = mask_words;
     p.window = window;
+    p.sinks = sinks;
     p.prefix_len = prefix_len;
     p.page_size = page_size;
     p.max_pages = max_pages_per_branch;

@@ -5,7 +5,8 @@
 // Branch b drafted T_b tokens; token t has parent[t] < t (-1: none) and sits in the cache
 // at key n_b + t, n_b = prefix_len + suffix_lens[b].
 //   depth(t) = 0 without a parent, depth(parent[t]) + 1 else; position = n_b + depth(t);
-//   bit u of t's mask: u is t or an ancestor of t less than `window` levels above it;
+//   bit u of t's mask: u is t or an ancestor of t less than `window` levels above it, or one
+//   at a position below `sinks`;
 //   accepted: from no node on, the child of lowest index that was drafted as the token
 //   picked at its parent (first[b] at none), until there is none;
 //   kept: row n_b + i := row n_b + path[i]. A path ascends, so path[i] >= i, and a row is
@@ -142,12 +143,23 @@ __global__ void __launch_bounds__(kThreads) tree_rows_kernel(const TreeParams p)
         for (int t = threadIdx.x; t < T; t += kThreads) {
             uint32_t* mask = p.masks + (row + t) * p.words;
             for (int w = (t >> 5) + 1; w < p.words; ++w) mask[w] = 0u;
+            // of the tokens from t up, those from the `far`-th on are among the first keys
+            int far = 1 << 30;
+            if (p.window > 0 && p.sinks > n) {
+                far = n - p.sinks;
+                for (int u = t; u >= 0; u = below[u]) far += __popc(family[u]);
+            }
             int depth = 0, word = t >> 5;
             for (int u = t; u >= 0; u = below[u]) {  // ancestors come in descending order
                 uint32_t bits = family[u];
                 const int count = __popc(bits), left = p.window - depth;
-                if (p.window > 0 && count > left)  // the `left` nearest: the highest
-                    bits = left <= 0 ? 0u : bits & (~0u << __fns(bits, 0, count - left + 1));
+                const int low = depth + count - max(depth, far);
+                if (p.window > 0 && count > left && count > low) {
+                    // the `left` nearest: the highest; the `low` nearest the root: the lowest
+                    uint32_t keep = left <= 0 ? 0u : ~0u << __fns(bits, 0, count - left + 1);
+                    if (low > 0) keep |= (1u << __fns(bits, 0, low + 1)) - 1u;
+                    bits &= keep;
+                }
                 depth += count;
                 for (; word > (u >> 5); --word) mask[word] = 0u;
                 mask[word--] = bits;
