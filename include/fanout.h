@@ -353,7 +353,8 @@ FANOUT_API int fanout_tree_rows_sinks(const int32_t *parents, const int32_t *pag
  * picked at its parent -- first_tokens[b] before any, target_tokens of the node after it --
  * and of several the one of lowest index, until there is none. (A tree whose root is the
  * branch's last committed token: first_tokens[b] = that token.)
- *   parents, draft_tokens, target_tokens  dev int32, int64, int64 [n_rows], by branch.
+ *   parents, draft_tokens, target_tokens  dev int32, int64, int64 [n_rows], by branch. A
+ *                 parent out of range counts as -1 and is reported, as in fanout_tree_rows.
  *   first_tokens  dev int64 [B];  add_lens  dev int32 [B]: T_b.
  *   path          dev int32 [n_rows], written: of each branch's rows the first counts[b]
  *                 hold the accepted tokens' indices in it, ascending, the others -1.

@@ -211,8 +211,11 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const TreeParams 
         }
         __syncthreads();
         for (int t = threadIdx.x; t < T; t += kThreads) {
-            const int32_t up = __ldcg(p.parents + row + t);
-            if (up < -1 || up >= t) continue;  // no token's child
+            int32_t up = __ldcg(p.parents + row + t);
+            if (up < -1 || up >= t) {  // reported, and taken as none
+                atomicCAS(p.err, 0, kErrInval);
+                up = -1;
+            }
             if (__ldcg(p.draft + row + t) == (up < 0 ? first : target[up])) atomicMin(child + up + 1, t);
         }
         __syncthreads();
