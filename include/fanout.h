@@ -269,7 +269,8 @@ FANOUT_API int fanout_kv_append_q4(const void *k_new, const void *v_new, int64_t
 
 /*
  * fanout_kv_read_q4 -- the values that slots of 4-bit pools stand for, rounded to
- * bf16, into k_out / v_out (strides as the appended rows'). A row whose slot is
+ * bf16, into k_out / v_out (strides as the appended rows'; rows of one may lie between
+ * those of the other, but share no byte with them: FANOUT_EINVAL). A row whose slot is
  * negative, or outside the pools (reported), is left as it was. Can be captured.
  */
 FANOUT_API int fanout_kv_read_q4(const void *k_pages, const void *v_pages, const int64_t *slots,
@@ -287,8 +288,8 @@ FANOUT_API int fanout_kv_read_q4(const void *k_pages, const void *v_pages, const
  * fanout_kv_append_q8, fanout_kv_read_q8 -- as fanout_kv_append_q4 and
  * fanout_kv_read_q4, into and from 8-bit pools: infinities are held as 448 gs, a NaN as
  * 0 (reported). A byte 0x7f or 0xff, which an append never writes, reads as NaN. What is
- * written (the pools; the rows) shares no byte with what is read, nor the pools of an append
- * with each other (FANOUT_EINVAL). Both can be captured.
+ * written (the pools; the rows) shares no byte with what is read, nor the pools of an append,
+ * or the K and V rows of a read, with each other (FANOUT_EINVAL). Both can be captured.
  */
 FANOUT_API int fanout_kv_append_q8(const void *k_new, const void *v_new, int64_t k_stride,
                 int64_t v_stride, void *k_pages, void *v_pages, const int64_t *slots,

@@ -63,6 +63,24 @@ struct TreeParams {
     Pool pool;
 };
 
+// Whether two arrays of n >= 1 rows share a byte. A row is `row` values of 2 bytes, the next
+// one starts a_stride (b_stride) >= row values behind it; rows of one array may lie between
+// those of the other.
+inline bool rows_overlap(const void* a, int64_t a_stride, const void* b, int64_t b_stride, int64_t n,
+                         int64_t row) {
+    using Wide = __int128;  // (n strides may pass 64 bits)
+    const Wide as = 2 * static_cast<Wide>(a_stride), bs = 2 * static_cast<Wide>(b_stride), len = 2 * row;
+    const Wide a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    if (a0 >= b0 + (n - 1) * bs + len || b0 >= a0 + (n - 1) * as + len) return false;
+    for (Wide i = 0, j = 0; i < n && j < n;) {  // past the rows that end first
+        const Wide x = a0 + i * as, y = b0 + j * bs;
+        if (x + len <= y) i += (y - len - x) / as + 1;
+        else if (y + len <= x) j += (x - len - y) / bs + 1;
+        else return true;
+    }
+    return false;
+}
+
 cudaError_t launch_attn_rows(const RowParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                              const CUtensorMap& tm_v, int grid, cudaStream_t stream);
 cudaError_t launch_attn_rows_q4(const RowParams& p, const CUtensorMap& tm_q, int grid,

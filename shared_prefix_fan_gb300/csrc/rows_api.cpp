@@ -123,6 +123,8 @@ int check_rows(const void* k_rows, const void* v_rows, const void* k_pages, cons
 int run_rows(Q4RowParams& p, bool read, int32_t page_size, fanout_stream_t stream) {
     const void* k = read ? static_cast<const void*>(p.k_out) : p.k_rows;
     const void* v = read ? static_cast<const void*>(p.v_out) : p.v_rows;
+    if (read && rows_overlap(k, p.k_stride, v, p.v_stride, p.n_rows, static_cast<int64_t>(p.H_kv) * kHD))
+        return FANOUT_EINVAL;
     p.align32 = aligned(k, 32) && aligned(v, 32) && p.k_stride % 16 == 0 && p.v_stride % 16 == 0;
     p.k_rcp6 = 1.0f / (6.0f * p.k_scale);
     p.v_rcp6 = 1.0f / (6.0f * p.v_scale);
@@ -139,7 +141,6 @@ int64_t bytes_of(double n) { return n < 9e18 ? static_cast<int64_t>(n) : INT64_M
 int run_rows_q8(Q8RowParams& p, bool read, int32_t page_size, fanout_stream_t stream) {
     const void* k = read ? static_cast<const void*>(p.k_out) : p.k_rows;
     const void* v = read ? static_cast<const void*>(p.v_out) : p.v_rows;
-    // (k_out and v_out may be rows of one array that lie between each other)
     const double row = static_cast<double>(p.H_kv) * kHD, last = p.n_rows - 1;
     const int64_t pool = bytes_of(row * static_cast<double>(p.n_slots));
     const Array pools[] = {{p.k_pool, pool}, {p.v_pool, pool}};
@@ -147,7 +148,8 @@ int run_rows_q8(Q8RowParams& p, bool read, int32_t page_size, fanout_stream_t st
                           {v, bytes_of(2 * (last * static_cast<double>(p.v_stride) + row))}};
     const Array slots[] = {{p.slots, 8LL * p.n_rows}};
     if (any_overlap(rows, pools) || (read ? any_overlap(slots, rows) : any_overlap(slots, pools)) ||
-        (!read && overlap(p.k_pool, pool, p.v_pool, pool)))
+        (!read && overlap(p.k_pool, pool, p.v_pool, pool)) ||
+        (read && rows_overlap(k, p.k_stride, v, p.v_stride, p.n_rows, static_cast<int64_t>(p.H_kv) * kHD)))
         return FANOUT_EINVAL;
     p.align32 = aligned(k, 32) && aligned(v, 32) && p.k_stride % 16 == 0 && p.v_stride % 16 == 0;
     p.k_rcp = 1.0f / p.k_scale;
