@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sysconfig
 from array import array
 from typing import Optional, Sequence, Tuple
 
@@ -17,7 +18,7 @@ import numpy as np
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libfanout.so")
-HOST_PATH = os.path.join(_HERE, "lib", "_host_calls.so")
+HOST_PATH = os.path.join(_HERE, "lib", "_host_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 OK, EINVAL, EUNSUPPORTED, ECUDA, ENOMEM, ETIMEOUT = range(6)
 OUT_F32, OUT_BF16 = 0, 1
