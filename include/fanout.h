@@ -516,12 +516,14 @@ FANOUT_API int fanout_attn_q8(const void *q, const void *k_pages, const void *v_
  *   masks       dev uint32 [R][mask_words], 4-byte aligned, T_b <= 32 * mask_words, any
  *               bits (fanout_tree_rows gives a tree's); T_b <= 1024, else FANOUT_EUNSUPPORTED.
  *   positions   dev int32 [R] or NULL: read with window >= 1 only, and needed then; n_b ..
- *               n_b + 1023 (a value outside counts as the nearest of these).
+ *               n_b + 1023 (a value outside counts as the nearest of these). The call is
+ *               planned without them, for tokens at n_b: keys past n_b - window must be
+ *               finite and on good pages even where every position hides them.
  *   window, sinks  0, 0: every key before the draft; sinks without a window is FANOUT_EINVAL.
  *               (Among the drafted tokens the masks alone say what is seen: with first keys
  *               they come from fanout_tree_rows_sinks.)
- * The drafted tokens' rows must all be finite. Everything else as fanout_attn_window: page
- * ids, hidden keys, capturing, plans, errors.
+ * The drafted tokens' rows must all be finite. Everything else as fanout_attn_window with
+ * every token at n_b: page ids, hidden keys, capturing, plans, errors.
  */
 FANOUT_API int fanout_attn_tree(const void *q, const void *k_pages, const void *v_pages,
                 int32_t kv_type, const int32_t *page_table, int32_t prefix_len,

@@ -765,7 +765,8 @@ def attn_tree(q, k_pages, v_pages, page_table, prefix_len: int, suffix_lens, q_r
     suffix (suffix_lens counts them): a row sees the keys before its branch's draft (with
     a window those past position - window and the first `sinks`), itself, and the drafted
     tokens that its mask names (masks int32 [R, words], positions int32 [R]: tree_rows
-    gives them; positions are read with a window only). Pools of any kind: bf16, 4 bits
+    gives them; positions are read with a window only, and keys that a token right behind the
+    context would see must be good whatever they say). Pools of any kind: bf16, 4 bits
     (uint8), 8 bits (float8_e4m3fn)."""
     if window >> 31 or sinks >> 31:
         window, sinks = max(-1, min(window, _I32_MAX)), max(-1, min(sinks, _I32_MAX))
