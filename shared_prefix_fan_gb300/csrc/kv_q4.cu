@@ -81,6 +81,7 @@ __device__ __forceinline__ bool item_of(const Q4RowParams& p, uint32_t& r, uint3
     return true;
 }
 
+template <bool kSmall>
 __global__ void __launch_bounds__(32 * kWarps) append_q4_kernel(const Q4RowParams p) {
     const int group = threadIdx.x & 7;
     const bool is_v = threadIdx.x & 8;
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(32 * kWarps) append_q4_kernel(const Q4RowParam
     const float gs = is_v ? p.v_scale : p.k_scale;
     // (from 448 on the scale saturates, so 512 stands for whatever is larger)
     const float c6 = 6.0f * gs;
-    const float most = quotient(fminf(top, 512.f * c6), c6, is_v ? p.v_rcp6 : p.k_rcp6);
+    const float most = quotient<kSmall>(fminf(top, 512.f * c6), c6, is_v ? p.v_rcp6 : p.k_rcp6);
     const uint32_t sc = e4m3x2(most, 0.f) & 0xffu;
     const float den = e4m3_f32(sc) * gs;
     uint32_t w[2] = {0u, 0u};
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(32 * kWarps) append_q4_kernel(const Q4RowParam
             for (int i = 0; i < 8; ++i) {
                 const uint32_t v = raw[4 * half + (i >> 1)];
                 const float x = __uint_as_float(i & 1 ? v & 0xffff0000u : v << 16);
-                y[i] = quotient(x, den, rcp);
+                y[i] = quotient<kSmall>(x, den, rcp);
             }
             w[half] = e2m1_word(y);
         }
@@ -193,7 +194,8 @@ cudaError_t launch_q4_rows(const Q4RowParams& p, bool read, cudaStream_t stream)
     if (items <= 0) return cudaSuccess;
     const unsigned grid = static_cast<unsigned>((items + 2 * kWarps - 1) / (2 * kWarps));
     if (read) read_q4_kernel<<<grid, 32 * kWarps, 0, stream>>>(p);
-    else append_q4_kernel<<<grid, 32 * kWarps, 0, stream>>>(p);
+    else if (small_scales(p.k_scale, p.v_scale)) append_q4_kernel<true><<<grid, 32 * kWarps, 0, stream>>>(p);
+    else append_q4_kernel<false><<<grid, 32 * kWarps, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -64,6 +64,7 @@ __device__ __forceinline__ bool place_of(const Q8RowParams& p, int64_t slot, uin
     return true;
 }
 
+template <bool kSmall>
 __global__ void __launch_bounds__(32 * kWarps) append_q8_kernel(const Q8RowParams p) {
     after_previous();
     const int part = threadIdx.x & 7;
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(32 * kWarps) append_q8_kernel(const Q8RowParam
                 const uint32_t v = raw[2 * i + (c >> 1)];
                 const float x = __uint_as_float(c & 1 ? v & 0xffff0000u : v << 16);
                 // (a zero's sign does not pass the correction)
-                y[c] = copysignf(quotient(fminf(fmaxf(x, -most), most), gs, rcp), x);
+                y[c] = copysignf(quotient<kSmall>(fminf(fmaxf(x, -most), most), gs, rcp), x);
             }
             w[i] = e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16;
         }
@@ -176,7 +177,10 @@ cudaError_t launch_q8_rows(const Q8RowParams& p, bool read, cudaStream_t stream)
     const int64_t items = static_cast<int64_t>(p.n_rows) * p.H_kv;
     if (items <= 0) return cudaSuccess;
     const int grid = static_cast<int>((items + 2 * kWarps * kRows - 1) / (2 * kWarps * kRows));
-    return launch_after(read ? read_q8_kernel : append_q8_kernel, grid, 32 * kWarps, 0, stream, p);
+    auto* kernel = read                                 ? read_q8_kernel
+                   : small_scales(p.k_scale, p.v_scale) ? append_q8_kernel<true>
+                                                        : append_q8_kernel<false>;
+    return launch_after(kernel, grid, 32 * kWarps, 0, stream, p);
 }
 
 }  // namespace fanout
