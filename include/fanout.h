@@ -439,7 +439,9 @@ FANOUT_API int fanout_kv_keep(void *k_pages, void *v_pages, int32_t kv_type,
  * ceil((prefix_len + suffix_lens[b]) / page_size) entries for every branch,
  * and a branch with query rows must have at least one key (FANOUT_EINVAL).
  * The library keeps a grow-only device workspace per (device, stream) for
- * split partials and the work plan; it is freed by fanout_release().
+ * split partials and the work plan; it is freed by fanout_release(). (The calls below
+ * keep one each beside it, by what the pools hold, with or without a window, with or
+ * without drafts: as many as the stream makes kinds of calls.)
  */
 FANOUT_API int fanout_attn(const void *q, const void *k_pages, const void *v_pages,
                 const int32_t *page_table, int32_t prefix_len, const int32_t *suffix_lens,

@@ -21,11 +21,13 @@ namespace {
 
 // One warp per output row at a time; kMergeBatch partials per pass: 24 for
 // rows with many partials (decode), fewer when every row has few, because a
-// pass loads kMergeBatch of them whatever the row has (merge_row.cuh). With
-// 39360 rows of two partials each (a window over 8-bit keys, cut so), the call
-// took 106 us with 8 a pass and 97 with 2; two or four rows a warp at once
-// instead took 107 and 127 (more registers a block, so fewer blocks fit beside
-// the attention kernel). Blocks of two warps: small enough to be
+// pass loads kMergeBatch of them whatever the row has (merge_row.cuh). By itself, 16384
+// rows of 2, 4 and 6 partials take 5.3, 6.2 and 7.5 us with as many a pass, 8.3, 8.4 and
+// 8.5 with 8; 39360 rows 9.3, 14.8 and 27 against 16.3, 19.9 and 31. Whole calls with
+// two to four partials a row: 32 ragged branches in a bf16 window 86.9 us against 93.6
+// with 8, a drafting step on 8 bits 89.3 against 92.9, 8 branches of 32 drafts 180.6
+// against 183.2. Two or four rows a warp at once instead were slower (more registers a
+// block, so fewer blocks fit beside the attention kernel). Blocks of two warps: small enough to be
 // resident beside an attention CTA (which leaves ~27 K registers and 2 KB of
 // shared memory of an SM free), so part of the grid starts, and runs its dry
 // pass, while the attention kernel is still working. The grid is at most what
