@@ -1,5 +1,5 @@
-"""README's drafting loop, run against a stand-in of the binding that records its calls (CPU
-only): every call fits its signature, and masks are made for what attention is given."""
+"""The drafting loop that users are shown, run against a stand-in of the binding that records its
+calls (CPU only): every call fits its signature, and masks are made for what attention is given."""
 import inspect
 import os
 import re
